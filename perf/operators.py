@@ -325,8 +325,8 @@ def _round_e4m3(v):
 
 
 def _exact_quantize(x, kind):
-    """(q, s, q * s) in doubles; every input here is finite.  The factor 448 / amax is by definition
-    an fp32 number (in doubles other elements would lie on a tie); nothing else is rounded."""
+    """(q, s, q * s) in doubles; every input here is finite.  x * 448 is exact and its quotient
+    rounded once, so an element that lies on a tie between two e4m3 values is seen as one."""
     br, bc = _SHAPE[kind]
     x = x.double()
     R, C = x.shape
@@ -335,7 +335,7 @@ def _exact_quantize(x, kind):
     tiles = pad.reshape(_ceil(R, br), br, _ceil(C, bc), bc)
     amax = tiles.abs().amax(3, keepdim=True).amax(1, keepdim=True).clamp_min(AMAX_MIN)
     s = amax / E4M3_MAX
-    q = _round_e4m3(tiles * (E4M3_MAX / amax).float().double())
+    q = _round_e4m3(tiles * E4M3_MAX / amax)
     back = (q * s).reshape(pad.shape)[:R, :C]
     return q.reshape(pad.shape)[:R, :C], s.reshape(s.shape[0], s.shape[2]), back
 
