@@ -1,4 +1,4 @@
-"""ctypes binding of include/gemm.h: the same names, argument marshalling only.
+"""ctypes binding of include/gemm.h and gemm_fp8.h: the same names, argument marshalling only.
 
 Every computation happens in the CUDA library; if the library is missing this
 module raises instead of falling back to anything else.
@@ -45,6 +45,33 @@ class gemm_plan_t(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+# ---- include/gemm_fp8.h
+GEMM_BF16 = 2
+GEMM_FP8_ROW, GEMM_FP8_COL, GEMM_FP8_TILE = range(3)
+GEMM_MOE_MAX_TOKENS, GEMM_MOE_MAX_EXPERTS, GEMM_MOE_MAX_TOP_K = 64, 512, 16
+
+
+class gemm_fp8_matrix_t(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("ld", c_int64), ("scale", c_void_p),
+                ("scale_stride_r", c_int64), ("scale_stride_c", c_int64), ("blocks", c_int32),
+                ("reserved", c_int32)]
+
+
+class gemm_fp8_experts_t(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("ld", c_int64), ("expert_stride", c_int64),
+                ("scale", c_void_p), ("scale_stride_e", c_int64), ("scale_stride_r", c_int64),
+                ("scale_stride_c", c_int64)]
+
+
+class gemm_moe_fp8_t(ctypes.Structure):
+    _fields_ = [("tokens", c_int64), ("hidden", c_int64), ("inner", c_int64),
+                ("experts", c_int64), ("top_k", c_int32), ("renormalize", c_int32),
+                ("dtype", c_int32), ("reserved", c_int32), ("x", c_void_p), ("ld_x", c_int64),
+                ("router", c_void_p), ("ld_router", c_int64), ("gate", gemm_fp8_experts_t),
+                ("up", gemm_fp8_experts_t), ("down", gemm_fp8_experts_t), ("out", c_void_p),
+                ("ld_out", c_int64), ("ids", c_void_p), ("gates", c_void_p)]
 
 
 class GemmError(RuntimeError):
@@ -96,6 +123,13 @@ def load(build_if_missing: bool = True):
         "gemm_set_trace": (c_int, [c_void_p, c_void_p, c_int64]),
         "gemm_run_noalloc": (c_int, [c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                      c_void_p, gemm_layout_t, c_void_p, c_void_p]),
+        "gemm_fp8_quantize": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int,
+                                      P(gemm_fp8_matrix_t), P(gemm_fp8_matrix_t), c_void_p]),
+        "gemm_fp8_run": (c_int, [c_void_p, c_int64, c_int64, c_int64, P(gemm_fp8_matrix_t),
+                                 P(gemm_fp8_matrix_t), c_void_p, c_void_p, c_int64, c_int, c_int,
+                                 c_int, c_void_p]),
+        "gemm_moe_fp8_workspace": (c_int, [c_void_p, P(gemm_moe_fp8_t), P(c_int64)]),
+        "gemm_moe_fp8": (c_int, [c_void_p, P(gemm_moe_fp8_t), c_void_p, c_int64, c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -215,6 +249,28 @@ def gemm_set_trace(h, dev_buf_ptr, ctas: int) -> int:
     """Points the handle's tensor-core launches at a device buffer of
     ctas x 8 uint64 phase stamps (None / 0 turns tracing off)."""
     return load().gemm_set_trace(c_void_p(h), c_void_p(dev_buf_ptr), int(ctas))
+
+
+def gemm_fp8_quantize(h, rows, cols, src_ptr, ld_src, src_dtype, out, out2, stream_ptr) -> int:
+    return load().gemm_fp8_quantize(c_void_p(h), rows, cols, src_ptr, ld_src, src_dtype,
+                                    ctypes.byref(out),
+                                    ctypes.byref(out2) if out2 is not None else None, stream_ptr)
+
+
+def gemm_fp8_run(h, M, N, K, A, Bm, bias_ptr, C_ptr, ldc, a_major, b_major, out_dtype,
+                 stream_ptr) -> int:
+    return load().gemm_fp8_run(c_void_p(h), M, N, K, ctypes.byref(A), ctypes.byref(Bm), bias_ptr,
+                               C_ptr, ldc, a_major, b_major, out_dtype, stream_ptr)
+
+
+def gemm_moe_fp8_workspace(h, layer: gemm_moe_fp8_t):
+    n = c_int64()
+    rc = load().gemm_moe_fp8_workspace(c_void_p(h), ctypes.byref(layer), ctypes.byref(n))
+    return rc, n.value
+
+
+def gemm_moe_fp8(h, layer: gemm_moe_fp8_t, ws_ptr, ws_bytes, stream_ptr) -> int:
+    return load().gemm_moe_fp8(c_void_p(h), ctypes.byref(layer), ws_ptr, ws_bytes, stream_ptr)
 
 
 TRACE_PHASES = ("start", "first_load", "first_data", "mma_done", "last_accum", "end")

@@ -16,9 +16,10 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdgemm_gb300.so")
 SOURCES = ["api.cu", "simt.cu", "simt_f16.cu", "selftest.cu", "noalloc.cu", "tc2.cu",
-           "tc_n256.cu", "tc_n128.cu", "tc_small.cu", "tc_narrow.cu", "tc64.cu"]
+           "tc_n256.cu", "tc_n128.cu", "tc_small.cu", "tc_narrow.cu", "tc64.cu",
+           "fp8_api.cu", "fp8_quant.cu", "fp8_simt.cu", "fp8_moe.cu"]
 HEADERS = ["ptx.cuh", "work.cuh", "tc_kernel.cuh", "tc2_kernel.cuh", "tc64_kernel.cuh",
-           "tc_launch.cuh", "simt_kernel.cuh", "internal.h"]
+           "tc_launch.cuh", "simt_kernel.cuh", "internal.h", "context.h", "fp8.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-I", os.path.join(ROOT, "include")]
@@ -33,7 +34,7 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files.append(os.path.join(ROOT, "include", "gemm.h"))
+    files += [os.path.join(ROOT, "include", h) for h in ("gemm.h", "gemm_fp8.h")]
     return files
 
 

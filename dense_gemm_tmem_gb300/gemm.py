@@ -2,11 +2,15 @@
 the current CUDA stream.  PyTorch supplies device memory and streams only."""
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import binding as B
+from .fp8 import Fp8Matrix
 
 _DT = {torch.float16: B.GEMM_F16, torch.float32: B.GEMM_F32}
+_DT8 = {**_DT, torch.bfloat16: B.GEMM_BF16}  # the 8-bit operators' other types
 ROW, COL = B.GEMM_ROW_MAJOR, B.GEMM_COL_MAJOR
 
 
@@ -42,7 +46,8 @@ class Gemm:
             dev = torch.device("cuda", 0)
         self.device = dev
         self.handle = B.gemm_create(dev.index)
-        self._run = B.load().gemm_run  # argument types set once by the binding
+        self._lib = B.load()
+        self._run = self._lib.gemm_run  # argument types set once by the binding
 
     def close(self):
         if getattr(self, "handle", None):
@@ -137,3 +142,126 @@ class Gemm:
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_query_plan")
         return p.as_dict()
+
+    # ---- block-scaled 8-bit operators (include/gemm_fp8.h)
+    def fp8_quantize(self, x: torch.Tensor, blocks: str = "row", stream=None):
+        """x (rows, cols; float16, bfloat16 or float32, unit stride along its
+        rows) as an Fp8Matrix with "row", "col" or "tile" blocks, or, for
+        "row+col", a pair of them from one pass over x."""
+        code = _DT8.get(x.dtype)
+        if code is None:
+            raise TypeError("x must be float16, bfloat16 or float32, got %s" % x.dtype)
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D")
+        if x.get_device() != self.device.index:
+            raise ValueError("tensor on %s, handle on %s" % (x.device, self.device))
+        rows, cols = x.shape
+        sr, sc = x.stride()
+        if cols > 1 and sc != 1:
+            raise ValueError("rows of x must be contiguous")
+        if rows > 1 and sr < cols:
+            raise ValueError("rows of x overlap")
+        both = blocks == "row+col"
+        out = Fp8Matrix.empty(rows, cols, "row" if both else blocks, self.device)
+        out2 = Fp8Matrix.empty(rows, cols, "col", self.device) if both else None
+        rc = self._lib.gemm_fp8_quantize(self.handle, rows, cols, x.data_ptr(), max(sr, cols),
+                                         code, out.ref, out2.ref if both else None,
+                                         self._stream(stream))
+        if rc != B.GEMM_OK:
+            raise B.GemmError(rc, "gemm_fp8_quantize")
+        return (out, out2) if both else out
+
+    def fp8_run(self, A: Fp8Matrix, Bm: Fp8Matrix, C: torch.Tensor, bias=None, a_major=ROW,
+                b_major=ROW, stream=None) -> None:
+        """Enqueues C = A·B (+bias) of block-scaled matrices into C (M, N;
+        float16, bfloat16 or float32, unit stride along its rows).  A is stored
+        (M, K) row-major or (K, M) column-major, B (K, N) or (N, K); the blocks
+        of each must run along K."""
+        if len(A.shape) != 2 or len(Bm.shape) != 2:
+            raise ValueError("A and B must be 2-D")
+        M, K = A.shape if a_major == ROW else A.shape[::-1]
+        Kb, N = Bm.shape if b_major == ROW else Bm.shape[::-1]
+        if K != Kb:
+            raise ValueError("inner dimensions differ: %d vs %d" % (K, Kb))
+        idx = self.device.index
+        if A.device_index != idx or Bm.device_index != idx or C.get_device() != idx:
+            raise ValueError("operands must be on the handle's device, %s" % self.device)
+        code = _DT8.get(C.dtype)
+        if code is None:
+            raise TypeError("C must be float16, bfloat16 or float32, got %s" % C.dtype)
+        if C.dim() != 2 or C.shape[0] != M or C.shape[1] != N:
+            raise ValueError("C has shape %s, expected (%d, %d)" % (tuple(C.shape), M, N))
+        sr, sc = C.stride()
+        if (N > 1 and sc != 1) or (M > 1 and sr < N):
+            raise ValueError("rows of C must be contiguous and not overlap")
+        bias_ptr = None
+        if bias is not None:
+            if (bias.dtype != torch.float32 or tuple(bias.shape) != (N,)
+                    or not bias.is_contiguous()):
+                raise ValueError("bias must be contiguous float32 of shape (N,)")
+            if bias.get_device() != idx:
+                raise ValueError("tensor on %s, handle on %s" % (bias.device, self.device))
+            bias_ptr = bias.data_ptr()
+        rc = self._lib.gemm_fp8_run(self.handle, M, N, K, A.ref, Bm.ref, bias_ptr, C.data_ptr(),
+                                    max(sr, N), a_major, b_major, code, self._stream(stream))
+        if rc != B.GEMM_OK:
+            raise B.GemmError(rc, "gemm_fp8_run")
+
+    def fp8_matmul(self, A: Fp8Matrix, Bm: Fp8Matrix, bias=None, a_major=ROW, b_major=ROW,
+                   out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+        """A·B (+bias) as a new tensor (see fp8_run)."""
+        M = A.shape[0] if a_major == ROW else A.shape[1]
+        N = Bm.shape[1] if b_major == ROW else Bm.shape[0]
+        C = torch.empty((M, N), dtype=out_dtype, device=self.device)
+        self.fp8_run(A, Bm, C, bias, a_major, b_major, stream)
+        return C
+
+    def moe_fp8(self, x: torch.Tensor, router: torch.Tensor, gate: Fp8Matrix, up: Fp8Matrix,
+                down: Fp8Matrix, top_k: int, renormalize: bool = True, stream=None):
+        """A mixture-of-experts layer on a few tokens: x (tokens, hidden) and
+        router (experts, hidden) float16 or bfloat16, gate and up Fp8Matrix
+        (experts, inner, hidden), down (experts, hidden, inner).  Returns out
+        (tokens, hidden), ids (tokens, top_k) int32 and gates (tokens, top_k)
+        float32; the arithmetic is that of gemm_moe_fp8."""
+        if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
+            raise ValueError("x must be (tokens, hidden), router (experts, hidden)")
+        T, H = x.shape
+        E = router.shape[0]
+        if len(gate.shape) != 3 or len(up.shape) != 3 or len(down.shape) != 3:
+            raise ValueError("gate, up and down must be (experts, rows, cols)")
+        I = gate.shape[1]
+        if (tuple(gate.shape) != (E, I, H) or tuple(up.shape) != (E, I, H)
+                or tuple(down.shape) != (E, H, I)):
+            raise ValueError("weights have shapes %s, %s and %s, expected gate and up (%d, inner, "
+                             "%d), down (%d, %d, inner)" % (tuple(gate.shape), tuple(up.shape),
+                                                            tuple(down.shape), E, H, E, H))
+        if x.dtype != router.dtype or x.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("x and router: both float16 or both bfloat16")
+        if not 1 <= top_k <= E:
+            raise ValueError("top_k must be 1 ... %d, got %d" % (E, top_k))
+        idx = self.device.index
+        for d in (x.get_device(), router.get_device(), gate.device_index, up.device_index,
+                  down.device_index):
+            if d != idx:
+                raise ValueError("operands must be on the handle's device, %s" % self.device)
+        for t in (x, router):
+            if (H > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < H):
+                raise ValueError("rows of x and router must be contiguous")
+        out = torch.empty((T, H), dtype=x.dtype, device=self.device)
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=self.device)
+        gates = torch.empty((T, top_k), dtype=torch.float32, device=self.device)
+        L = B.gemm_moe_fp8_t(T, H, I, E, top_k, 1 if renormalize else 0, _DT8[x.dtype], 0,
+                             x.data_ptr(), max(x.stride(0), H), router.data_ptr(),
+                             max(router.stride(0), H), gate.desc, up.desc, down.desc,
+                             out.data_ptr(), H, ids.data_ptr(), gates.data_ptr())
+        rc, n = B.gemm_moe_fp8_workspace(self.handle, L)
+        if rc != B.GEMM_OK:
+            raise B.GemmError(rc, "gemm_moe_fp8_workspace")
+        s = self._stream(stream)
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        if stream is not None:
+            ws.record_stream(stream)
+        rc = self._lib.gemm_moe_fp8(self.handle, ctypes.byref(L), ws.data_ptr(), n, s)
+        if rc != B.GEMM_OK:
+            raise B.GemmError(rc, "gemm_moe_fp8")
+        return out, ids, gates
