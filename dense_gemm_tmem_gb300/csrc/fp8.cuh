@@ -70,9 +70,9 @@ cudaError_t launch_fp8_quantize(int64_t rows, int64_t cols, const void* src, int
                                 const gemm_fp8_matrix_t* out2, cudaStream_t stream);
 // CUDA-core product: any strides, any alignment (fp8_simt.cu).
 cudaError_t launch_fp8_simt(const Fp8Product& p, cudaStream_t stream);
-// Tensor-core product on CTA pairs (fp8_pair.cu), where fp8_pair_runs.
-bool fp8_pair_runs(const Fp8Product& p);
-cudaError_t launch_fp8_pair(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream);
+// Tensor-core product (fp8_tc.cu), where fp8_tc_runs.
+bool fp8_tc_runs(const Fp8Product& p);
+cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream);
 
 // Mixture-of-experts layer (fp8_moe.cu).
 int64_t moe_workspace_bytes(const gemm_moe_fp8_t& L);

@@ -99,7 +99,7 @@ int gemm_fp8_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp
   return dg::on_device(h->device, [&]() -> int {
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
-        dg::fp8_pair_runs(p) ? dg::launch_fp8_pair(h, p, s) : dg::launch_fp8_simt(p, s);
+        dg::fp8_tc_runs(p) ? dg::launch_fp8_tc(h, p, s) : dg::launch_fp8_simt(p, s);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
   });
 }

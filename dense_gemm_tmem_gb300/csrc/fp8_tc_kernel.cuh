@@ -1,0 +1,746 @@
+// fp8_tc_kernel.cuh: the block-scaled product on the tensor cores
+// (tcgen05.mma.kind::f8f6f4).
+//
+//   C[m, n] = sum over kb of sa[m, kb] sb[n, kb] P_kb[m, n],
+//   P_kb[m, n] = sum over the 128 k of block kb of a[m, k] b[n, k]
+//
+// The scales change every 128 k, so no accumulator may run past a block: each
+// k-block's P is its own short MMA chain (4 x K = 32) into a TMEM buffer, and
+// the sum over k-blocks is kept in fp32 registers.  A k-block of 128 bytes is
+// one 128-byte swizzle row, so the ring is that of the 16-bit kernel with twice
+// the k per block.  Per CTA (persistent, one per SM, 128 x BN tiles):
+//   warp 0, one lane   TMA producer: 128 rows of A and BN rows of B, kGroup
+//                      k-blocks per stage, into an S-stage ring.
+//   warp 1, one lane   4 MMAs of 128 x BN x 32 per k-block into the next of the
+//                      TMEM buffers; commits free the stage and hand the buffer
+//                      to the epilogue.
+//   warps 2-3          the scales of the k-blocks ahead, by 4-byte asynchronous
+//                      copies (any stride) into a ring of two slots of
+//                      kScaleGroup k-blocks each: read straight from global memory
+//                      by the epilogue, two k-blocks ahead, their latency cost 180
+//                      of 656 us at 8192^3.
+//   warps 4-11         epilogue, two warpgroups of BN / 2 columns: TMEM ->
+//                      registers, acc += (sa sb) * P, and the buffer goes back.
+//                      A 128 x 256 tile keeps 128 fp32 sums a thread.
+// What bounds it: a buffer's round trip (512 cycles of MMA for 128 x 256 x 128,
+// its commit, 128 KB of TMEM reads and 32768 FMAs, the hand-back) against two
+// buffers of 256 columns, all the TMEM there is: 8192^3 takes 567 us (1939
+// TFLOP/s), 397 without the FMAs.  That round trip is why the tile belongs to
+// one SM: on CTA pairs (cta_group::2, 256 x 256) each hand-over crosses SMs,
+// and the same epilogue without the scale ring took 727 us against 656.
+// For skinny problems (TRANS: operands swapped, C stored transposed) the bound
+// is the stream of the weights.
+// Small problems split the k-blocks of all tiles evenly over the CTAs; the last
+// CTA to finish a tile adds the fp32 partials in ascending k order, so the sum
+// does not depend on who is last and no CTA waits for another.
+#pragma once
+
+#include "fp8.cuh"
+#include "tc_kernel.cuh"
+
+namespace dg {
+
+constexpr int kF8EpiWarps = 8;
+constexpr int kF8RoleWarps = 4;  // producer, MMA issuer, two scale loaders: one warpgroup
+constexpr int kF8ScaleThreads = 64;
+constexpr int kF8Threads = 32 * (kF8RoleWarps + kF8EpiWarps);
+// Registers a thread: 3 warpgroups launch with 168 each (504 in all); for a
+// 256-wide tile, whose epilogue threads keep 128 sums, the role warpgroup gives
+// up all but 40 and the epilogue's two take 232 each (40 + 2 * 232 = 504).
+constexpr int kF8RoleRegs = 40, kF8EpiRegs = 232;
+
+template <int BN>
+struct Fp8TcConfig {
+  // k-blocks per stage and TMA copy: an SM's TMA unit takes about as long for a
+  // copy of 32 KiB as for one of 16
+  static constexpr int kGroup = BN == 256 ? 1 : 2;
+  static constexpr int kABytes = kBM * kFp8Block;  // per k-block
+  static constexpr int kBBytes = BN * kFp8Block;
+  static constexpr int kStageBytes = kGroup * (kABytes + kBBytes);
+  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
+  static constexpr int kBuffers = BN == 256 ? 2 : 4;      // TMEM accumulators
+  static constexpr int kTmemCols = BN * kBuffers;         // a power of two >= 32
+  static constexpr int kHalf = BN / 2;                    // columns per warpgroup
+  static constexpr int kChunk = kHalf < 32 ? kHalf : 32;  // columns per TMEM load
+  static constexpr int kStoreLd = 16 + 4;                 // staged store: 64 bytes a row, in floats
+  static constexpr int kEpiBytes = kF8EpiWarps * 32 * kStoreLd * 4;
+  // scales of one k-block: the tile's rows, then its columns
+  static constexpr int kScaleGroup = 4;  // k-blocks per ring slot
+  static constexpr int kScaleRing = 2;
+  static constexpr int kScaleFloats = kBM + BN;
+  static constexpr int kScaleBytes = kScaleRing * kScaleGroup * kScaleFloats * 4;
+  static constexpr int kBarBytes = 384;
+  static constexpr int kSmemBytes =
+      1024 + kStages * kStageBytes + kEpiBytes + kScaleBytes + kBarBytes;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert((2 * kStages + 2 * kBuffers + 1 + 2 * kScaleRing) * 8 + 16 <= kBarBytes, "barrier area");
+};
+
+// One operand's scales in the MMA view: row (or column) r of k-block kb at
+// p[(r >> shift) * stride + kb * kb_stride].
+struct Fp8Scales {
+  const float* p;
+  int64_t stride, kb_stride;
+  int32_t shift;
+};
+
+struct Fp8TcArgs {
+  WorkSpec work;
+  int32_t Mm, Nm;      // MMA-view extents
+  Fp8Scales row, col;  // of the MMA-view A and B operands
+  void* C;             // row-major in the problem's view
+  int64_t ldc;
+  const float* bias;   // NULL or one per column of C
+  int32_t out_dtype;
+  int32_t c_vec;       // 1: C's base is 16-byte aligned, its pitch a multiple of 16 bytes
+  int32_t a_mn, b_mn;  // 1: the operand is MN-major (b_mn: BN a multiple of 128)
+  int32_t k_full;      // whole k-blocks of K
+  float* workspace;
+  int* tickets;
+  int* status;
+  uint64_t wait_limit_ns;
+  uint32_t idesc;
+};
+
+// Whether the phase has completed, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One lane of the warp, the same on every call.
+__device__ __forceinline__ bool f8_elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// D[tmem] (+)= A[smem desc] · B[smem desc]ᵀ, e4m3 x e4m3 -> fp32, one CTA.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Barrier among the 256 epilogue threads.
+__device__ __forceinline__ void f8_epi_sync() {
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// d += a * b, two lanes; as two scalar FMAs: the packed form needs register
+// pairs that the TMEM loads do not give (8192^3: 590 us packed, 571 scalar).
+__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
+  d.x = fmaf(a.x, b.x, d.x);
+  d.y = fmaf(a.y, b.y, d.y);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  return make_float2(a.x * b.x, a.y * b.y);
+}
+
+// An operand's two tensor maps: `group` brings kGroup whole k-blocks in one
+// box (K-major: {128 k, rows}, or for kGroup > 1 the view {128 k, rows,
+// k-block}; MN-major: {128 rows, 128 k x kGroup}), `one` a single k-block of a
+// K-major operand, zeros past K.
+struct Fp8Maps {
+  CUtensorMap group, one;
+};
+
+// One operand's part of a stage.  A K-major group that reaches into the ragged
+// last k-block comes block by block; blocks past K read as zeros.  An MN-major
+// operand comes in boxes of 128 rows.
+template <int ROWS, int G>
+__device__ __forceinline__ void f8_load(const Fp8Maps& m, uint32_t dst, uint32_t bar, int32_t mn,
+                                        int32_t row, int32_t kb, int32_t k_full) {
+  if (mn) {
+#pragma unroll
+    for (int i = 0; i < ROWS / 128; ++i)
+      tma_load_2d(dst + i * G * 128 * kFp8Block, &m.group, bar, row + i * 128, kb * kFp8Block);
+  } else if (G > 1 && kb + G <= k_full) {
+    tma_load_3d(dst, &m.group, bar, 0, row, kb);
+  } else {
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+      tma_load_2d(dst + j * ROWS * kFp8Block, &m.one, bar, (kb + j) * kFp8Block, row);
+  }
+}
+
+// TMA producer (one thread).  Returns how many stages it filled.
+template <int BN>
+__device__ __forceinline__ uint32_t f8_producer(const Fp8Maps& mA, const Fp8Maps& mB,
+                                                const Fp8TcArgs& args, uint8_t* sA, uint8_t* sB,
+                                                uint64_t* full, uint64_t* empty,
+                                                const WaitCtl& wc) {
+  using Cfg = Fp8TcConfig<BN>;
+  constexpr int G = Cfg::kGroup;
+  const WorkSpec& W = args.work;
+  WorkIter it;
+  it.init(W, int32_t(blockIdx.x));
+  Unit u;
+  int s = 0;
+  uint32_t ph = 0, filled = 0;
+  pdl_wait_prerequisites();
+  while (it.next(W, u)) {
+    int32_t tm, tn;
+    tile_coords(W, u.tile, tm, tn);
+    for (int32_t kb = u.kb0; kb < u.kb1; kb += G) {
+      if (!wait_bounded(smem_u32(&empty[s]), ph ^ 1, wc, kSiteProducer)) return filled;
+      const uint32_t fb = smem_u32(&full[s]);
+      mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
+      f8_load<kBM, G>(mA, smem_u32(sA + s * G * Cfg::kABytes), fb, args.a_mn, tm * kBM, kb,
+                      args.k_full);
+      f8_load<BN, G>(mB, smem_u32(sB + s * G * Cfg::kBBytes), fb, args.b_mn, tn * BN, kb,
+                     args.k_full);
+      ++filled;
+      if (++s == Cfg::kStages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+  }
+  return filled;
+}
+
+// 4 bytes global -> shared, asynchronously.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Scale loaders (64 threads): rows t and t + 64 of the tile and columns t, t +
+// 64, ..., rows and columns past the matrix clamped to its last.  A thread
+// arrives on a ring slot's barrier when its copies into it have landed.  Where
+// 128 columns share a scale only the first of each is needed.
+template <int BN, bool COLVEC>
+__device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, uint32_t ring, uint64_t* sc_full,
+                                          uint64_t* sc_empty, const WaitCtl& wc) {
+  using Cfg = Fp8TcConfig<BN>;
+  constexpr int kCols = COLVEC ? (BN + kF8ScaleThreads - 1) / kF8ScaleThreads : 1;
+  const int t = int(threadIdx.x) - 64;
+  const WorkSpec& W = args.work;
+  WorkIter it;
+  it.init(W, int32_t(blockIdx.x));
+  Unit u;
+  uint32_t slot = 0, ph = 0;
+  bool ok = true;
+  pdl_wait_prerequisites();
+  while (ok && it.next(W, u)) {
+    int32_t tm, tn;
+    tile_coords(W, u.tile, tm, tn);
+    const float* src[2 + kCols];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int32_t r = min(tm * kBM + t + i * kF8ScaleThreads, args.Mm - 1);
+      src[i] = args.row.p + int64_t(r >> args.row.shift) * args.row.stride +
+               u.kb0 * args.row.kb_stride;
+    }
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      // uniform columns: threads 0 and 1 fetch the two warpgroups' scales
+      const int32_t c = COLVEC ? t + i * kF8ScaleThreads : (t & 1) * Cfg::kHalf;
+      const int32_t n = min(tn * BN + c, args.Nm - 1);
+      src[2 + i] = args.col.p + int64_t(n >> args.col.shift) * args.col.stride +
+                   u.kb0 * args.col.kb_stride;
+    }
+    for (int32_t kb = u.kb0; kb < u.kb1; kb += Cfg::kScaleGroup) {
+      if (!wait_bounded(smem_u32(&sc_empty[slot]), ph ^ 1, wc, kSiteProducer)) {
+        ok = false;
+        break;
+      }
+      uint32_t dst = ring + slot * (Cfg::kScaleGroup * Cfg::kScaleFloats * 4);
+#pragma unroll 1
+      for (int j = 0; j < Cfg::kScaleGroup && kb + j < u.kb1; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          cp_async4(dst + (t + i * kF8ScaleThreads) * 4, src[i]);
+          src[i] += args.row.kb_stride;
+        }
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          const int c = t + i * kF8ScaleThreads;
+          if (c < (COLVEC ? BN : 2)) cp_async4(dst + (kBM + c) * 4, src[2 + i]);
+          src[2 + i] += args.col.kb_stride;
+        }
+        dst += Cfg::kScaleFloats * 4;
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                       smem_u32(&sc_full[slot]))
+                   : "memory");
+      if (++slot == uint32_t(Cfg::kScaleRing)) {
+        slot = 0;
+        ph ^= 1;
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// MMA issuer: the whole warp runs the loop, so that addresses and descriptors
+// stay in uniform registers; one lane issues.  Buffer j of a unit's k-block j
+// modulo kBuffers; `phases` holds each buffer's parity.
+template <int BN>
+__device__ __forceinline__ void f8_mma(const Fp8TcArgs& args, uint32_t sA, uint32_t sB,
+                                       uint32_t full, uint32_t empty, uint32_t acc_full,
+                                       uint32_t acc_empty, uint32_t drain, const WaitCtl& wc,
+                                       uint32_t tmem_base) {
+  using Cfg = Fp8TcConfig<BN>;
+  constexpr int G = Cfg::kGroup, NB = Cfg::kBuffers;
+  const WorkSpec& W = args.work;
+  WorkIter it;
+  it.init(W, int32_t(blockIdx.x));
+  Unit u;
+  uint32_t s = 0, ph = 0, phases = (1u << NB) - 1;
+  bool ok = true, any = false;
+  const bool leader = f8_elect();
+  // K = 32 steps: 32 bytes along a K-major row, 32 rows of 128 bytes MN-major;
+  // k-block j of a group: a block of rows K-major, 128 rows of k MN-major; the
+  // 128-row boxes of an MN-major B of 256 rows lie kGroup k-blocks apart
+  const uint32_t a_step = args.a_mn ? (4096u >> 4) : (32u >> 4);
+  const uint32_t b_step = args.b_mn ? (4096u >> 4) : (32u >> 4);
+  const uint32_t b_blk = args.b_mn ? 128u * kFp8Block : uint32_t(Cfg::kBBytes);
+  const uint32_t b_lbo = args.b_mn ? uint32_t(G) * 128u * kFp8Block : 16u;
+  const uint64_t adesc0 = make_sdesc_sw128(sA, 16, 1024);
+  const uint64_t bdesc0 = make_sdesc_sw128(sB, b_lbo, 1024);
+  while (ok && it.next(W, u)) {
+    uint32_t b = 0;
+    for (int32_t kb = u.kb0; ok && kb < u.kb1; kb += G) {
+      if (!mbar_test(full + 8 * s, ph)) ok = wait_bounded(full + 8 * s, ph, wc, kSiteMmaFull);
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        if (kb + j >= u.kb1) break;  // the unit ends inside the group
+        if (!mbar_test(acc_empty + 8 * b, (phases >> b) & 1))
+          ok = ok && wait_bounded(acc_empty + 8 * b, (phases >> b) & 1, wc, kSiteMmaAccum);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t adesc = adesc0 + ((s * G * Cfg::kABytes + j * Cfg::kABytes) >> 4);
+          const uint64_t bdesc = bdesc0 + ((s * G * Cfg::kBBytes + j * b_blk) >> 4);
+          const uint32_t d = tmem_base + b * BN;
+#pragma unroll
+          for (int kk = 0; kk < kFp8Block / 32; ++kk)
+            tc_mma_f8(d, adesc + uint64_t(kk * a_step), bdesc + uint64_t(kk * b_step),
+                      args.idesc, kk > 0 ? 1u : 0u);
+          // the stage's commit first: the epilogue's last wait then covers it
+          if (j == G - 1 || kb + j + 1 >= u.kb1) tc_commit(empty + 8 * s);
+          tc_commit(acc_full + 8 * b);
+        }
+        __syncwarp();
+        any = true;
+        phases ^= 1u << b;
+        b = b + 1 == NB ? 0 : b + 1;
+      }
+      if (++s == uint32_t(Cfg::kStages)) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+  }
+  if (!ok && any && leader) {  // every MMA issued so far must finish before TMEM is freed
+    tc_commit(drain);
+    wait_drain(drain, 0, wc);
+  }
+  __syncwarp();
+}
+
+// Row-major store of a warp's 32 rows x HC columns (lane i holds row mrow0 + i),
+// 64 bytes of each row at a time through the warp's shared rows, so that 4 lanes
+// store a row's 64 bytes and an instruction 8 rows.  SIZE: bytes an element.
+// The bias is added in fp32 before the one rounding.
+template <int HC, int SIZE>
+__device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float2 (&acc)[HC / 2],
+                                              float* stage_w, int32_t mrow0, int lane,
+                                              int32_t nn0) {
+  constexpr int PER = 64 / SIZE;               // columns a pass
+  constexpr int VEC = 16 / SIZE;               // columns a lane stores
+  constexpr int LD = 20;                       // floats a staged row
+  static_assert(HC % 16 == 0, "whole passes, or half of one");
+  const bool f16 = a.out_dtype == GEMM_F16;
+  const int piece = lane & 3, rs = lane >> 2;
+#pragma unroll
+  for (int c = 0; c < HC; c += PER) {
+    __syncwarp();                              // the previous pass has been read
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if constexpr (SIZE == 4) {
+        const float2 x = acc[(c + j) / 2];
+        const float b = a.bias && nn0 + c + j < a.Nm ? __ldg(a.bias + nn0 + c + j) : 0.f;
+        w[j] = __float_as_uint((j & 1 ? x.y : x.x) + b);
+      } else {
+        w[j] = 0;
+        if (c + 2 * j < HC) {
+          float2 x = acc[(c + 2 * j) / 2];
+          if (a.bias) {
+            const int32_t n = nn0 + c + 2 * j;
+            if (n < a.Nm) x.x += __ldg(a.bias + n);
+            if (n + 1 < a.Nm) x.y += __ldg(a.bias + n + 1);
+          }
+          if (f16) {
+            const __half2 h = __floats2half2_rn(x.x, x.y);
+            __builtin_memcpy(&w[j], &h, 4);
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+            __builtin_memcpy(&w[j], &h, 4);
+          }
+        }
+      }
+    }
+    uint4* own = reinterpret_cast<uint4*>(stage_w + lane * LD);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      own[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    __syncwarp();
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = *reinterpret_cast<const uint4*>(stage_w + (i * 8 + rs) * LD + 4 * piece);
+    const int32_t n = nn0 + c + piece * VEC;
+    int32_t valid = a.Nm - n;                  // columns of this lane's 16 bytes inside C
+    if (HC - c < PER && HC - c - piece * VEC < valid) valid = HC - c - piece * VEC;
+    if (valid <= 0) continue;
+    const int32_t r0 = mrow0 + rs;
+    uint8_t* p = static_cast<uint8_t*>(a.C) + (int64_t(r0) * a.ldc + n) * SIZE;
+    const int64_t step = a.ldc * (8 * SIZE);
+    if (valid >= VEC && a.c_vec) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i, p += step)
+        if (r0 + 8 * i < a.Mm) *reinterpret_cast<uint4*>(p) = x[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i, p += step) {
+        if (r0 + 8 * i >= a.Mm) break;
+        const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          if (j >= valid) break;
+          if constexpr (SIZE == 4)
+            reinterpret_cast<uint32_t*>(p)[j] = xw[j];
+          else
+            reinterpret_cast<uint16_t*>(p)[j] = uint16_t(xw[j / 2] >> (16 * (j & 1)));
+        }
+      }
+    }
+  }
+}
+
+// CW consecutive fp32 columns of this thread's TMEM lane; the registers may be
+// read after tmem_wait.
+template <int CW>
+__device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&r)[CW]) {
+  if constexpr (CW == 32) {
+    tmem_ld32(taddr, r);
+  } else {
+    static_assert(CW == 16, "chunk width");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+  }
+}
+template <int CW>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[CW]) {
+  if constexpr (CW == 32) {
+    tmem_wait_ld32(r);
+  } else {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+  }
+}
+
+template <int BN, bool TRANS, bool COLVEC>
+__device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_full,
+                                            uint32_t acc_empty, uint32_t sc_full,
+                                            uint32_t sc_empty, const WaitCtl& wc,
+                                            uint32_t tmem_base, float* stage, const float* ring,
+                                            volatile int* last_flag) {
+  using Cfg = Fp8TcConfig<BN>;
+  constexpr int HC = Cfg::kHalf, CW = Cfg::kChunk;
+  const WorkSpec& W = args.work;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3;               // TMEM lane quarter this warp may access
+  const int wg = (warp - kF8RoleWarps) >> 2;       // which half of the columns
+  const int row = q * 32 + lane;
+  float* stage_w = stage + (warp - kF8RoleWarps) * 32 * Cfg::kStoreLd;
+  WorkIter it;
+  const int32_t cta = int32_t(blockIdx.x);
+  it.init(W, cta);
+  pdl_wait_prerequisites();
+  Unit u;
+  // buffer j % kBuffers holds the unit's k-block j; `phases`: each buffer's parity
+  uint32_t phases = 0, slot = 0, sph = 0;
+  bool ok = true;
+  const uint32_t tlane = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(wg * HC);
+  // After a wait gave up the units run on without waiting or storing, so that
+  // every warp still meets every barrier of the split tiles below.
+  while (it.next(W, u)) {
+    int32_t tm, tn;
+    tile_coords(W, u.tile, tm, tn);
+    const int32_t mrow0 = tm * kBM;
+    const int32_t mm = mrow0 + row;
+    const int32_t nn0 = tn * BN + wg * HC;
+    float2 acc[HC / 2];
+#pragma unroll
+    for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+    // kScaleGroup k-blocks a turn, unrolled, so that buffers and chunks are
+    // constants.  Chunk c + 1 of a buffer is loaded while chunk c is added, and
+    // so is chunk 0 of the next buffer if its product is there by then (asked
+    // for a chunk ahead, so the answer costs no wait).
+    constexpr int NC = HC / CW, NB = Cfg::kBuffers, SG = Cfg::kScaleGroup;
+    static_assert(SG % NB == 0 && (NC == 1 || NC % 2 == 0), "constant buffers and chunks");
+    uint32_t v[2][CW];
+    // true once buffer i's product is there; its first chunk is then on its way
+    auto begin = [&](int i) {
+      if (!mbar_test(acc_full + 8 * i, (phases >> i) & 1))
+        ok = wait_bounded(acc_full + 8 * i, (phases >> i) & 1, wc, kSiteEpilogue);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        tmem_issue<CW>(tlane + uint32_t(i * BN), v[0]);
+      }
+    };
+    begin(0);
+    for (int32_t kb = u.kb0; ok && kb < u.kb1; kb += SG) {
+      ok = __all_sync(0xffffffffu, wait_bounded(sc_full + 8 * slot, sph, wc, kSiteEpilogue));
+      if (!ok) break;
+      const float* sc = ring + slot * (SG * Cfg::kScaleFloats);
+      float rs[SG];
+#pragma unroll
+      for (int j = 0; j < SG; ++j) {
+        rs[j] = sc[j * Cfg::kScaleFloats + row];
+        if (!COLVEC) rs[j] *= sc[j * Cfg::kScaleFloats + kBM + wg];
+      }
+#pragma unroll
+      for (int j = 0; j < SG; ++j) {
+        if (!ok || kb + j >= u.kb1) break;
+        const int i = j % NB, next = (j + 1) % NB;
+        const bool more = kb + j + 1 < u.kb1;
+        const float2 rs2 = make_float2(rs[j], rs[j]);
+        phases ^= 1u << i;
+        bool ready = false;
+        tmem_wait<CW>(v[0]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          if (c + 1 < NC) {
+            tmem_issue<CW>(tlane + uint32_t(i * BN + (c + 1) * CW), v[(c + 1) & 1]);
+            if (c + 2 == NC && more) ready = mbar_test(acc_full + 8 * next, (phases >> next) & 1);
+          } else {  // the buffer's last read is done: back to the MMA issuer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + 8 * i);
+            if (NC > 1 && more) {
+              ready = __all_sync(0xffffffffu, ready);
+              if (ready) {
+                tc_fence_after();
+                tmem_issue<CW>(tlane + uint32_t(next * BN), v[0]);
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < CW / 2; ++e) {
+            const float2 p2 = make_float2(__uint_as_float(v[c & 1][2 * e]),
+                                          __uint_as_float(v[c & 1][2 * e + 1]));
+            if constexpr (COLVEC) {
+              const float2 cs = *reinterpret_cast<const float2*>(
+                  sc + j * Cfg::kScaleFloats + kBM + wg * HC + c * CW + 2 * e);
+              fma2(acc[c * (CW / 2) + e], mul2(cs, rs2), p2);
+            } else {
+              fma2(acc[c * (CW / 2) + e], rs2, p2);
+            }
+          }
+          if (c + 1 < NC) tmem_wait<CW>(v[(c + 1) & 1]);
+        }
+        if (more && !ready) begin(next);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sc_empty + 8 * slot);
+      if (++slot == uint32_t(Cfg::kScaleRing)) {
+        slot = 0;
+        sph ^= 1;
+      }
+    }
+
+    // Split tile: this CTA's fp32 partial goes to the workspace (128 rows x BN,
+    // float4 j of row r at j * 128 + r); the last CTA to arrive adds them all.
+    bool mine = true;
+    int32_t first = cta, last = cta;
+    const int32_t st = u.tile - W.dp_tiles;
+    const bool partial = unit_is_partial(W, u);
+    auto part_of = [&](int32_t p) {
+      return reinterpret_cast<float4*>(args.workspace) +
+             size_t(split_slot(W, p, st)) * (size_t(kBM) * BN / 4) + size_t(wg) * (HC / 4) * kBM +
+             row;
+    };
+    if (partial) {
+      float4* dst = part_of(cta);
+#pragma unroll
+      for (int j = 0; j < HC / 4; ++j)
+        __stcg(dst + j * kBM, make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x,
+                                          acc[2 * j + 1].y));
+      __threadfence();
+      f8_epi_sync();
+      split_contributors(W, st, first, last);
+      if (threadIdx.x == 32 * kF8RoleWarps) {
+        const int old = atomicAdd(args.tickets + st, 1);
+        *last_flag = (old == last - first) ? 1 : 0;
+        if (old == last - first) atomicExch(args.tickets + st, 0);  // for the next launch
+      }
+      f8_epi_sync();
+      mine = *last_flag != 0;
+      if (mine) __threadfence();
+    }
+    if (!mine || !ok) continue;
+    const float* bias = args.bias;
+    if (partial) {
+      // the sum of all partials replaces this CTA's own
+#pragma unroll
+      for (int c = 0; c < HC / 16; ++c) {
+        float4 tot[4];
+        const float4* src = part_of(first) + size_t(c) * 4 * kBM;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tot[j] = __ldcg(src + j * kBM);
+#pragma unroll 4
+        for (int32_t p = first + 1; p <= last; ++p) {
+          src = part_of(p) + size_t(c) * 4 * kBM;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 x = __ldcg(src + j * kBM);
+            tot[j].x += x.x; tot[j].y += x.y; tot[j].z += x.z; tot[j].w += x.w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[c * 8 + 2 * j] = make_float2(tot[j].x, tot[j].y);
+          acc[c * 8 + 2 * j + 1] = make_float2(tot[j].z, tot[j].w);
+        }
+      }
+    }
+    if (TRANS) {
+      if (mm < args.Mm) {
+        const float bv = bias ? __ldg(bias + mm) : 0.f;
+#pragma unroll
+        for (int j = 0; j < HC; ++j)
+          if (nn0 + j < args.Nm)
+            store_typed(args.C, int64_t(nn0 + j) * args.ldc + mm,
+                        (j & 1 ? acc[j / 2].y : acc[j / 2].x) + bv, args.out_dtype);
+      }
+    } else if (args.out_dtype == GEMM_F32) {
+      f8_store_rows<HC, 4>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
+    } else {
+      f8_store_rows<HC, 2>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
+    }
+  }
+}
+
+// args.work counts 128 x BN tiles and CTAs.
+template <int BN, bool TRANS, bool COLVEC>
+__global__ void __launch_bounds__(kF8Threads, 1)
+    fp8_tc_kernel(const __grid_constant__ Fp8Maps mA, const __grid_constant__ Fp8Maps mB,
+                  const Fp8TcArgs args) {
+  using Cfg = Fp8TcConfig<BN>;
+  constexpr int S = Cfg::kStages, NB = Cfg::kBuffers;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + S * Cfg::kGroup * Cfg::kABytes;
+  float* stage = reinterpret_cast<float*>(sB + S * Cfg::kGroup * Cfg::kBBytes);
+  float* ring = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(stage) + Cfg::kEpiBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ring) +
+                                               Cfg::kScaleBytes);
+  uint64_t* full = bars;                // S: a stage's bytes have landed
+  uint64_t* empty = bars + S;           // S: its MMAs are done
+  uint64_t* acc_full = empty + S;       // NB: a k-block's product is in TMEM
+  uint64_t* acc_empty = acc_full + NB;  // NB: all epilogue warps have read it
+  uint64_t* sc_full = acc_empty + NB;   // kScaleRing: a k-block's scales have landed
+  uint64_t* sc_empty = sc_full + Cfg::kScaleRing;  // kScaleRing: all epilogue warps used them
+  uint64_t* drain = sc_empty + Cfg::kScaleRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
+
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // uniform
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(smem_u32(&acc_full[i]), 1);
+      mbar_init(smem_u32(&acc_empty[i]), kF8EpiWarps);
+    }
+    for (int i = 0; i < Cfg::kScaleRing; ++i) {
+      mbar_init(smem_u32(&sc_full[i]), kF8ScaleThreads);
+      mbar_init(smem_u32(&sc_empty[i]), kF8EpiWarps);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    *last_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&mA.group);
+    tma_prefetch_map(&mB.group);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_launch_dependents();
+  const WaitCtl wc{args.wait_limit_ns, args.status, abort_flag};
+
+  uint32_t filled = 0;
+  if (warp >= kF8RoleWarps) {
+    if (BN >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
+    f8_epilogue<BN, TRANS, COLVEC>(args, smem_u32(acc_full), smem_u32(acc_empty),
+                                   smem_u32(sc_full), smem_u32(sc_empty), wc, tmem_base, stage,
+                                   ring, last_flag);
+  } else {
+    if (BN >= 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RoleRegs));
+    if (warp == 0 && lane == 0) {
+      filled = f8_producer<BN>(mA, mB, args, sA, sB, full, empty, wc);
+    } else if (warp == 1) {
+      pdl_wait_prerequisites();
+      f8_mma<BN>(args, smem_u32(sA), smem_u32(sB), smem_u32(full), smem_u32(empty),
+                 smem_u32(acc_full), smem_u32(acc_empty), smem_u32(drain), wc, tmem_base);
+    } else if (warp >= 2) {
+      f8_scales<BN, COLVEC>(args, smem_u32(ring), sc_full, sc_empty, wc);
+    } else {
+      pdl_wait_prerequisites();
+    }
+  }
+  // after an abort, copies may still be in flight: each stage's last one
+  if (threadIdx.x == 0)
+    for (uint32_t s = 0; s < uint32_t(S) && s < filled; ++s)
+      wait_drain(smem_u32(&full[s]), ((filled - 1 - s) / S) & 1, wc);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  }
+}
+
+}  // namespace dg
