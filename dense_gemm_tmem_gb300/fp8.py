@@ -34,7 +34,8 @@ class Fp8Matrix:
     need).  ``scale`` may have any strides.  The tensors are referenced, not
     copied; replacing them in place is seen by later calls."""
 
-    __slots__ = ("data", "scale", "blocks", "desc", "ref", "device_index", "shape")
+    __slots__ = ("blocks", "desc", "ref", "device_index", "shape", "_data", "_scale", "_buf",
+                 "_layout")
 
     def __init__(self, data: torch.Tensor, scale: torch.Tensor, blocks: str):
         if data.dtype not in _BYTES:
@@ -46,7 +47,7 @@ class Fp8Matrix:
         if len(shape) not in (2, 3):
             raise ValueError("data must be 2-D, or 3-D with one matrix per expert")
         rows, cols = shape[-2:]
-        if data.numel() and cols > 1 and st[-1] != 1:
+        if cols > 1 and st[-1] != 1:
             raise ValueError("rows of data must be contiguous")
         ld = st[-2] if rows > 1 else max(st[-2], cols)
         if ld < cols:
@@ -61,7 +62,7 @@ class Fp8Matrix:
         dev = data.get_device()
         if scale.get_device() != dev:
             raise ValueError("data on %s, scale on %s" % (data.device, scale.device))
-        self.data, self.scale, self.blocks, self.device_index = data, scale, blocks, dev
+        self._data, self._scale, self.blocks, self.device_index = data, scale, blocks, dev
         self.shape = shape
         ss = scale.stride()
         if len(shape) == 3:
@@ -74,19 +75,38 @@ class Fp8Matrix:
 
     @staticmethod
     def empty(rows: int, cols: int, blocks: str, device) -> "Fp8Matrix":
-        """Unwritten storage: rows padded to 16 bytes; the scales of 1 x 128
-        blocks with those of one k-block next to each other (the order the
-        product's threads read them in), others row-major."""
-        ld = -(-cols // 16) * 16
-        data = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)
-        if ld != cols:
-            data = data[:, :cols]
+        """Unwritten storage in one allocation: rows padded to 16 bytes; the
+        scales of 1 x 128 blocks with those of one k-block next to each other
+        (the order the product's threads read them in), others row-major."""
         shape = scale_shape(rows, cols, blocks)
-        if blocks == "row":
-            scale = torch.empty(shape[::-1], dtype=torch.float32, device=device).t()
-        else:
-            scale = torch.empty(shape, dtype=torch.float32, device=device)
-        return Fp8Matrix(data, scale, blocks)
+        ld = (cols + 15) & -16
+        off = (rows * ld + 255) & -256
+        buf = torch.empty(off + 4 * shape[0] * shape[1], dtype=torch.uint8, device=device)
+        strides = (1, shape[0]) if blocks == "row" else (shape[1], 1)
+        m = Fp8Matrix.__new__(Fp8Matrix)
+        m._data = m._scale = None  # made when first asked for
+        m._buf, m._layout = buf, (ld, shape, strides, off)
+        m.blocks, m.device_index, m.shape = blocks, buf.get_device(), torch.Size((rows, cols))
+        ptr = buf.data_ptr()
+        m.desc = B.gemm_fp8_matrix_t(ptr, ld, ptr + off, strides[0], strides[1], BLOCKS[blocks], 0)
+        m.ref = ctypes.byref(m.desc)
+        return m
+
+    @property
+    def data(self) -> torch.Tensor:
+        """The e4m3 values (uint8 if the matrix was made from bytes)."""
+        if self._data is None:
+            self._data = self._buf.view(torch.float8_e4m3fn).as_strided(
+                self.shape, (self._layout[0], 1))
+        return self._data
+
+    @property
+    def scale(self) -> torch.Tensor:
+        """The fp32 scales, one per block."""
+        if self._scale is None:
+            _, shape, strides, off = self._layout
+            self._scale = self._buf.view(torch.float32).as_strided(shape, strides, off // 4)
+        return self._scale
 
     def dequantize(self) -> torch.Tensor:
         """fp32 values, in plain torch (for checks and small matrices)."""

@@ -26,6 +26,8 @@ def problem_dims(A: torch.Tensor, Bm: torch.Tensor, a_major: int, b_major: int):
     return int(M), int(N), int(K)
 
 
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _LAYOUTS = {}  # (a_major, b_major, in, out) -> gemm_layout_t, built once
 
 
@@ -144,6 +146,11 @@ class Gemm:
         return p.as_dict()
 
     # ---- block-scaled 8-bit operators (include/gemm_fp8.h)
+    def _raw_stream(self, stream):
+        """The stream's handle, without building a Stream object for the current
+        one (2 us of a call's 10)."""
+        return stream.cuda_stream if stream is not None else _current_raw(self.device.index)
+
     def fp8_quantize(self, x: torch.Tensor, blocks: str = "row", stream=None):
         """x (rows, cols; float16, bfloat16 or float32, unit stride along its
         rows) as an Fp8Matrix with "row", "col" or "tile" blocks, or, for
@@ -166,7 +173,7 @@ class Gemm:
         out2 = Fp8Matrix.empty(rows, cols, "col", self.device) if both else None
         rc = self._lib.gemm_fp8_quantize(self.handle, rows, cols, x.data_ptr(), max(sr, cols),
                                          code, out.ref, out2.ref if both else None,
-                                         self._stream(stream))
+                                         self._raw_stream(stream))
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_fp8_quantize")
         return (out, out2) if both else out
@@ -203,7 +210,7 @@ class Gemm:
                 raise ValueError("tensor on %s, handle on %s" % (bias.device, self.device))
             bias_ptr = bias.data_ptr()
         rc = self._lib.gemm_fp8_run(self.handle, M, N, K, A.ref, Bm.ref, bias_ptr, C.data_ptr(),
-                                    max(sr, N), a_major, b_major, code, self._stream(stream))
+                                    max(sr, N), a_major, b_major, code, self._raw_stream(stream))
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_fp8_run")
 
@@ -257,7 +264,7 @@ class Gemm:
         rc, n = B.gemm_moe_fp8_workspace(self.handle, L)
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_moe_fp8_workspace")
-        s = self._stream(stream)
+        s = self._raw_stream(stream)
         ws = torch.empty(n, dtype=torch.uint8, device=self.device)
         if stream is not None:
             ws.record_stream(stream)
