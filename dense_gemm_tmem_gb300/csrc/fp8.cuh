@@ -75,8 +75,9 @@ bool fp8_tc_runs(const Fp8Product& p);
 cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream);
 
 // Mixture-of-experts layer (fp8_moe.cu).
-int64_t moe_workspace_bytes(const gemm_moe_fp8_t& L);
-cudaError_t launch_moe(const gemm_moe_fp8_t& L, void* workspace, cudaStream_t stream);
+int64_t moe_workspace_bytes(const gemm_ctx* h, const gemm_moe_fp8_t& L);
+cudaError_t launch_moe(gemm_ctx* h, const gemm_moe_fp8_t& L, void* workspace,
+                       cudaStream_t stream);
 
 // Stores v as element type `dtype`, rounded once.
 __device__ __forceinline__ void store_typed(void* base, int64_t i, float v, int dtype) {

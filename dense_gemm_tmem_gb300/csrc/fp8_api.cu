@@ -110,7 +110,7 @@ int gemm_moe_fp8_workspace(gemm_handle_t h, const gemm_moe_fp8_t* L, int64_t* by
   if (!h) return GEMM_ERR_INVALID_ARG;
   const int rc = dg::check_moe_sizes(L);
   if (rc != GEMM_OK) return rc;
-  *bytes = dg::moe_workspace_bytes(*L);
+  *bytes = dg::moe_workspace_bytes(h, *L);
   return GEMM_OK;
 }
 
@@ -127,10 +127,10 @@ int gemm_moe_fp8(gemm_handle_t h, const gemm_moe_fp8_t* L, void* workspace,
   if ((rc = dg::check_experts(L->up, L->inner, L->hidden, L->experts)) != GEMM_OK) return rc;
   if ((rc = dg::check_experts(L->down, L->hidden, L->inner, L->experts)) != GEMM_OK) return rc;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
-      workspace_bytes < dg::moe_workspace_bytes(*L))
+      workspace_bytes < dg::moe_workspace_bytes(h, *L))
     return GEMM_ERR_INVALID_ARG;
   return dg::on_device(h->device, [&]() -> int {
-    return dg::launch_moe(*L, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return dg::launch_moe(h, *L, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GEMM_OK
                : GEMM_ERR_CUDA;
   });

@@ -1,20 +1,175 @@
-// fp8_moe.cu: the mixture-of-experts layer for a few tokens, on the CUDA cores.
+// fp8_moe.cu: a whole mixture-of-experts layer for a few tokens in one launch.
 //
-// Four launches: router (logits, choice, gates, x quantised), gate and up
-// products with silu, the quantised hidden values, down products with the
-// weighted sum.  One warp per output row; every weight row is read once per
-// token that chose its expert.
-#include "fp8.cuh"
+//   l = x·routerᵀ, top-k and gates;  h = silu(gate_e x̂) * (up_e x̂);
+//   out[t] = sum over the chosen e of gate[t, e] (down_e ĥ)
+//
+// With few tokens the layer is the stream of the chosen experts' weights, each
+// byte used once per token that chose the expert, so the kernel is built around
+// that stream: one persistent CTA per SM (a cooperative launch), and the k-blocks
+// (128 rows x 128 k of one expert's matrix) of all chosen experts, laid end to
+// end, are cut into equal contiguous ranges, first for gate and up, then for
+// down.  The weights are the MMA's 128-row side, the expert's tokens (x̂ or ĥ, 16
+// to 64 rows) its columns; tensor cores because a weight then costs the same
+// for one token or sixteen, and the TMA ring keeps 128 KiB a CTA in flight.
+//
+//   phase A  all workers: router logits, x̂                  -> barrier 1
+//   phase B  every CTA for itself: experts by rank, token lists, work ranges
+//   phase C  gate and up: fp32 partial sums of each range    -> barrier 2
+//   phase D  down: the same, ĥ formed from phase C's partials -> barrier 3
+//   phase E  out from phase D's partials and the gates
+//
+// Roles in C and D: warp 0 streams weights by TMA (it runs ahead into D: weights
+// need no barrier), warp 1 issues MMAs, warp 2 copies the weights' scales, warps
+// 4-7 read each k-block's product from TMEM and add it, scaled, into fp32
+// registers, warps 8-11 build the token operand in shared memory (swizzled as
+// the MMA reads it), one buffer ahead.  A tile cut between CTAs leaves one
+// partial per CTA; whoever reads it adds them in CTA order, so results do not
+// depend on timing.  Every wait is bounded.
+#include <algorithm>
+
+#include "context.h"
+#include "fp8_tc_kernel.cuh"
 
 namespace dg {
 namespace {
 
-constexpr int kMoeThreads = 256;
+constexpr int kMoeThreads = 384;
+constexpr int kMoeStages = 4;                      // of two k-blocks
+constexpr int kMoeStageBytes = 2 * kBM * kFp8Block;
+constexpr int kMoeOperandBytes = 32768;            // one token operand buffer: 256 rows of 128 B
+constexpr int kMoeRows = kMoeOperandBytes / kFp8Block;
+constexpr int kMoeBuffers = 8;                     // TMEM accumulators of 64 columns
+constexpr int kMoeScaleGroup = 8, kMoeScaleRing = 4;
+constexpr int kMoeMinUnits = 2;                    // fewest k-blocks of a CTA's range
 
-__device__ __forceinline__ float load_x(const void* p, int64_t i, int dtype) {
-  return dtype == GEMM_F16 ? __half2float(static_cast<const __half*>(p)[i])
-                           : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
+// Rows of B (tokens) of an MMA, and k-blocks of them that an operand buffer holds.
+__host__ __device__ constexpr int moe_cols(int n) { return (n + 15) & ~15; }
+__host__ __device__ constexpr int moe_cap(int cols) { return (kMoeRows / cols) & ~1; }
+
+struct MoeMaps {
+  CUtensorMap group, one;  // {128, rows, k-block, expert}, {K, rows, expert}
+};
+
+struct MoeArgs {
+  gemm_moe_fp8_t L;
+  int32_t tiles_i, tiles_h, kb_h, kb_i;
+  uint8_t* xq;      // tokens x kb_h * 128
+  float* xs;        // tokens x kb_h
+  float* logits;    // tokens x experts
+  float* part1;     // [segment][gate, up][pick][tiles_i * 128]
+  float* part2;     // [segment][pick][tiles_h * 128]
+  int* counters;    // barriers 1-3 and exits; 0 at launch and again after it
+  int* status;
+  uint64_t wait_limit_ns;
+  int32_t vec;      // x and router rows are 16-byte aligned
+};
+
+// What phase B leaves in shared memory.
+struct MoeRoute {
+  uint64_t mask[GEMM_MOE_MAX_EXPERTS];   // tokens that chose the expert
+  uint16_t off[GEMM_MOE_MAX_EXPERTS];    // first of its picks in `pick`
+  uint16_t index[GEMM_MOE_MAX_EXPERTS];  // its place among the chosen experts
+  uint16_t act[GEMM_MOE_MAX_EXPERTS];    // the chosen experts, ascending
+  uint16_t ids[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];
+  uint16_t pick[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];  // token * top_k + choice
+  int32_t active;
+};
+
+// One phase's work: `units` k-blocks cut into `ctas` equal ranges.
+struct MoeWork {
+  int64_t units;
+  int32_t ctas, kb;
+  __device__ __forceinline__ MoeWork(int64_t tiles, int32_t kb_) {
+    kb = kb_;
+    units = tiles * kb;
+    const int64_t most = units / kMoeMinUnits;
+    ctas = int32_t(most < 1 ? 1 : most < int64_t(gridDim.x) ? most : int64_t(gridDim.x));
+  }
+  __device__ __forceinline__ int64_t begin(int32_t c) const {
+    return c >= ctas ? units : units * c / ctas;
+  }
+  __device__ __forceinline__ int32_t owner(int64_t x) const {
+    const uint64_t num = uint64_t(x + 1) * uint64_t(ctas) - 1;
+    if ((num >> 32) == 0 && (uint64_t(units) >> 32) == 0)
+      return int32_t(uint32_t(num) / uint32_t(units));
+    return int32_t(num / uint64_t(units));
+  }
+  // CTAs that work on a tile.
+  __device__ __forceinline__ int32_t segments(int64_t tile) const {
+    return owner((tile + 1) * kb - 1) - owner(tile * kb) + 1;
+  }
+};
+
+// A CTA's part of one tile.
+struct MoeSeg {
+  int32_t phase;     // 0 gate and up, 1 down
+  int32_t expert, n; // and its tokens
+  int32_t which;     // 0 gate, 1 up, 2 down
+  int32_t tile;      // 128-row tile of the matrix
+  int32_t kb0, kb1, kb;
+  int32_t seg;       // this CTA's place among those that work on the tile
+};
+
+struct MoeIter {
+  const MoeArgs& a;
+  const MoeRoute& r;
+  int64_t x, end;
+  int32_t phase;
+  __device__ __forceinline__ MoeIter(const MoeArgs& a_, const MoeRoute& r_) : a(a_), r(r_) {
+    start(0);
+  }
+  __device__ __forceinline__ MoeWork work(int32_t ph) const {
+    return ph == 0 ? MoeWork(int64_t(r.active) * 2 * a.tiles_i, a.kb_h)
+                   : MoeWork(int64_t(r.active) * a.tiles_h, a.kb_i);
+  }
+  __device__ __forceinline__ void start(int32_t ph) {
+    phase = ph;
+    const MoeWork w = work(ph);
+    x = w.begin(blockIdx.x);
+    end = w.begin(blockIdx.x + 1);
+  }
+  // The next segment of this phase.
+  __device__ __forceinline__ bool next(MoeSeg& s) {
+    if (x >= end) return false;
+    const MoeWork w = work(phase);
+    const int64_t tile = x / w.kb;
+    s.phase = phase;
+    s.kb = w.kb;
+    s.kb0 = int32_t(x - tile * w.kb);
+    const int64_t left = end - x;
+    s.kb1 = left < w.kb - s.kb0 ? int32_t(s.kb0 + left) : w.kb;
+    x += s.kb1 - s.kb0;
+    s.seg = int32_t(blockIdx.x) - w.owner(tile * w.kb);
+    const int32_t per = phase == 0 ? 2 * a.tiles_i : a.tiles_h;
+    const int32_t i = int32_t(tile / per);
+    const int32_t rest = int32_t(tile - int64_t(i) * per);
+    s.expert = r.act[i];
+    s.n = __popcll(r.mask[s.expert]);
+    s.which = phase == 1 ? 2 : rest / a.tiles_i;
+    s.tile = phase == 1 ? rest : rest % a.tiles_i;
+    return true;
+  }
+};
+
+// The token operand's buffers as every role sees them: content is one expert's
+// rows for a range of k-blocks; a whole-K content serves every segment of the
+// same phase and expert that follows.
+struct MoeContent {
+  int32_t phase = -1, expert = -1;
+  bool whole = false;
+  uint32_t count = 0;  // contents so far; buffer (count - 1) & 1
+  // True if the chunk needs a new content.
+  __device__ __forceinline__ bool advance(const MoeSeg& s, bool whole_) {
+    if (whole_ && whole && phase == s.phase && expert == s.expert) return false;
+    phase = s.phase;
+    expert = s.expert;
+    whole = whole_;
+    ++count;
+    return true;
+  }
+  __device__ __forceinline__ uint32_t buf() const { return (count - 1) & 1; }
+  __device__ __forceinline__ uint32_t parity() const { return ((count - 1) >> 1) & 1; }
+};
 
 // Floats in a total order as integers: NaN above +inf, -0 equal to +0.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -23,20 +178,33 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-struct MoeArgs {
-  gemm_moe_fp8_t L;
-  uint8_t* xq;    // tokens x hidden
-  float* xs;      // tokens x ceil(hidden / 128)
-  float* h;       // picks x inner
-  uint8_t* hq;
-  float* hs;
-};
+__device__ __forceinline__ float from16(uint16_t h, int dtype) {
+  if (dtype == GEMM_F16) {
+    __half v;
+    __builtin_memcpy(&v, &h, 2);
+    return __half2float(v);
+  }
+  return __uint_as_float(uint32_t(h) << 16);
+}
 
-// One block of 128 values of a row, quantised by one warp (4 per lane).
-__device__ __forceinline__ void quant_block(const float (&v)[4], int lane, int64_t c0, int64_t cols,
-                                            uint8_t* q, float* s) {
-  float m = 0.f;
-  float w[4];
+// Eight neighbouring 16-bit elements from column c of a row of n, zeros past it.
+__device__ __forceinline__ void load8_16(const uint16_t* row, int64_t c, int64_t n, int vec,
+                                         int dtype, float (&v)[8]) {
+  if (vec && c + 8 <= n) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + c));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = from16(uint16_t(u[j / 2] >> (16 * (j & 1))), dtype);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? from16(row[c + j], dtype) : 0.f;
+  }
+}
+
+// One block of 128 values, 4 per lane, quantised by a warp: this lane's 4 bytes;
+// every lane gets the scale.
+__device__ __forceinline__ uint32_t quant_block(const float (&v)[4], float& scale) {
+  float m = 0.f, w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     w[j] = fabsf(v[j]) == INFINITY ? NAN : v[j];
@@ -45,152 +213,780 @@ __device__ __forceinline__ void quant_block(const float (&v)[4], int lane, int64
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float inv = fp8_inverse(m);
-  const uint32_t pk = pack_e4m3x4(__fmul_rn(w[0], inv), __fmul_rn(w[1], inv),
-                                  __fmul_rn(w[2], inv), __fmul_rn(w[3], inv));
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (c0 + lane * 4 + j < cols) q[c0 + lane * 4 + j] = uint8_t(pk >> (8 * j));
-  if (lane == 0) *s = fp8_scale(m);
+  scale = fp8_scale(m);
+  return pack_e4m3x4(__fmul_rn(w[0], inv), __fmul_rn(w[1], inv), __fmul_rn(w[2], inv),
+                     __fmul_rn(w[3], inv));
 }
 
-__global__ void __launch_bounds__(kMoeThreads) moe_router_kernel(const MoeArgs a) {
-  __shared__ float logit[GEMM_MOE_MAX_EXPERTS];
-  __shared__ uint32_t key[GEMM_MOE_MAX_EXPERTS];
-  __shared__ int chosen[GEMM_MOE_MAX_TOP_K];
-  const int64_t t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t H = a.L.hidden, kbs = (H + 127) / 128;
-  for (int64_t kb = warp; kb < kbs; kb += kMoeThreads / 32) {
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Waits (bounded) until all CTAs have arrived on a barrier's counter.
+__device__ __forceinline__ bool grid_wait(const int* counter, const WaitCtl& wc) {
+  const uint64_t t0 = globaltimer_ns();
+  while (ld_acquire(counter) < int(gridDim.x)) {
+    if (*wc.abort) return false;
+    if (globaltimer_ns() - t0 > wc.limit_ns) {
+      *wc.abort = 1;
+      atomicCAS(wc.status, 0, 1 + kSiteEpilogue);
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ------------------------------------------------------------------- phase A --
+// Router logits: a CTA takes (expert, 8 tokens) tasks, its 8 worker warps an
+// eighth of the hidden axis each.  x̂: a warp per (token, k-block).
+__device__ __forceinline__ void moe_phase_a(const MoeArgs& a, float* red, int tid) {
+  const gemm_moe_fp8_t& L = a.L;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int64_t H = L.hidden;
+  const uint16_t* x = static_cast<const uint16_t*>(L.x);
+  const uint16_t* router = static_cast<const uint16_t*>(L.router);
+  const int32_t T = int32_t(L.tokens), E = int32_t(L.experts);
+  const int32_t groups = (T + 7) / 8;
+  for (int32_t task = blockIdx.x; task < E * groups; task += gridDim.x) {
+    const int32_t e = task / groups, t0 = (task - e * groups) * 8;
+    float s[8] = {};
+    for (int64_t c = (warp * 32 + lane) * 8; c < H; c += 8 * 256) {
+      float w[8];
+      load8_16(router + e * L.ld_router, c, H, a.vec, L.dtype, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (t0 + i >= T) break;
+        float v[8];
+        load8_16(x + (t0 + i) * L.ld_x, c, H, a.vec, L.dtype, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i] = fmaf(v[j], w[j], s[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+    bar_sync(1, 256);  // the previous task's sums have been read
+    if (lane < 8) {
+      float v = s[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) v = lane == i ? s[i] : v;
+      red[warp * 8 + lane] = v;
+    }
+    bar_sync(1, 256);
+    if (tid < 8 && t0 + tid < T) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v += red[w * 8 + tid];
+      a.logits[(t0 + tid) * E + e] = v;
+    }
+  }
+  // from the last CTA backwards, as the logits' tasks go from the first on
+  const int64_t tasks = int64_t(T) * a.kb_h;
+  for (int64_t i = int64_t(gridDim.x - 1 - blockIdx.x) * 8 + warp; i < tasks;
+       i += int64_t(gridDim.x) * 8) {
+    const int64_t t = i / a.kb_h, kb = i - t * a.kb_h;
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t c = kb * 128 + lane * 4 + j;
-      v[j] = c < H ? load_x(a.L.x, t * a.L.ld_x + c, a.L.dtype) : 0.f;
+      const int64_t c = kb * kFp8Block + lane * 4 + j;
+      v[j] = c < H ? from16(x[t * L.ld_x + c], L.dtype) : 0.f;
     }
-    quant_block(v, lane, kb * 128, H, a.xq + t * H, a.xs + t * kbs + kb);
+    float scale;
+    const uint32_t q = quant_block(v, scale);
+    reinterpret_cast<uint32_t*>(a.xq + (t * a.kb_h + kb) * kFp8Block)[lane] = q;
+    if (lane == 0) a.xs[t * a.kb_h + kb] = scale;
   }
-  for (int64_t e = warp; e < a.L.experts; e += kMoeThreads / 32) {
-    float s = 0.f;
-    for (int64_t c = lane; c < H; c += 32)
-      s = fmaf(load_x(a.L.x, t * a.L.ld_x + c, a.L.dtype),
-               load_x(a.L.router, e * a.L.ld_router + c, a.L.dtype), s);
+}
+
+// ------------------------------------------------------------------- phase B --
+// Every thread of the CTA: the experts of each token by rank (how many logits
+// are larger, or equal with a lower index), who chose whom, and the lists.
+__device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r, uint32_t* keys,
+                                            int32_t key_cap) {
+  const gemm_moe_fp8_t& L = a.L;
+  const int32_t T = int32_t(L.tokens), E = int32_t(L.experts), k = L.top_k;
+  const int tid = threadIdx.x;
+  for (int e = tid; e < E; e += kMoeThreads) r.mask[e] = 0;
+  const int32_t chunk = key_cap / E;  // tokens staged at once
+  for (int32_t t0 = 0; t0 < T; t0 += chunk) {
+    const int32_t nt = min(chunk, T - t0);
+    __syncthreads();
+    for (int32_t i = tid; i < nt * E; i += kMoeThreads)
+      keys[i] = order_key(__ldcg(a.logits + int64_t(t0) * E + i));
+    __syncthreads();
+    for (int32_t i = tid; i < nt * E; i += kMoeThreads) {
+      const int32_t t = i / E, e = i - t * E;
+      const uint32_t* row = keys + t * E;
+      const uint32_t key = row[e];
+      int32_t rank = 0;
+#pragma unroll 8
+      for (int32_t j = 0; j < E; ++j) rank += row[j] > key || (row[j] == key && j < e);
+      if (rank < k) {
+        r.ids[(t0 + t) * k + rank] = uint16_t(e);
+        atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[e]), 1ull << (t0 + t));
+      }
+    }
+  }
+  __syncthreads();
+  if (tid < 32) {  // prefix sums over the experts
+    int32_t picks = 0, active = 0;
+    for (int32_t e0 = 0; e0 < E; e0 += 32) {
+      const int32_t e = e0 + tid;
+      const int32_t n = e < E ? __popcll(r.mask[e]) : 0;
+      int32_t sum = n;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0) {
-      logit[e] = s;
-      key[e] = order_key(s);
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (tid >= d) sum += o;
+      }
+      const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+      const int32_t place = active + __popc(some & ((1u << tid) - 1));
+      if (e < E) {
+        r.off[e] = uint16_t(picks + sum - n);
+        r.index[e] = uint16_t(place);
+        if (n > 0) r.act[place] = uint16_t(e);
+      }
+      picks += __shfl_sync(0xffffffffu, sum, 31);
+      active += __popc(some);
+    }
+    if (tid == 0) r.active = active;
+  }
+  __syncthreads();
+  for (int32_t p = tid; p < T * k; p += kMoeThreads) {
+    const int32_t t = p / k, e = r.ids[p];
+    r.pick[r.off[e] + __popcll(r.mask[e] & ((1ull << t) - 1))] = uint16_t(p);
+  }
+  // gates and ids: one warp per token, spread over the CTAs
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int32_t t = int32_t(blockIdx.x) + warp * int32_t(gridDim.x); t < T;
+       t += int32_t(gridDim.x) * (kMoeThreads / 32)) {
+    const float* l = a.logits + int64_t(t) * E;
+    const float top = __ldcg(l + r.ids[t * k]);
+    float sum = 0.f, mine = 0.f;
+    if (lane < k) mine = expf(__ldcg(l + r.ids[t * k + lane]) - top);
+    if (L.renormalize) {
+      sum = mine;
+    } else {
+      for (int32_t e = lane; e < E; e += 32) sum += expf(__ldcg(l + e) - top);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane < k) {
+      L.ids[t * k + lane] = r.ids[t * k + lane];
+      L.gates[t * k + lane] = mine / sum;
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.L.experts; e += kMoeThreads) {
-    int rank = 0;
-    for (int j = 0; j < a.L.experts; ++j) rank += key[j] > key[e] || (key[j] == key[e] && j < e);
-    if (rank < a.L.top_k) chosen[rank] = e;
+}
+
+// --------------------------------------------------------------- phases C, D --
+__device__ __forceinline__ uint32_t moe_producer(const MoeArgs& a, const MoeRoute& r,
+                                                 const MoeMaps* const* maps, uint32_t ring,
+                                                 uint32_t full,
+                                                 uint32_t empty, const WaitCtl& wc) {
+  uint32_t s = 0, ph = 0, filled = 0;
+  MoeIter it(a, r);
+  for (int phase = 0; phase < 2; ++phase) {
+    it.start(phase);
+    MoeSeg g;
+    while (it.next(g)) {
+      const int32_t k_full = int32_t((phase == 0 ? a.L.hidden : a.L.inner) / kFp8Block);
+      const MoeMaps* m = maps[g.which];
+      for (int32_t kb = g.kb0; kb < g.kb1; kb += 2) {
+        if (!wait_bounded(empty + 8 * s, ph ^ 1, wc, kSiteProducer)) return filled;
+        const uint32_t bar = full + 8 * s, dst = ring + s * kMoeStageBytes;
+        mbar_arrive_expect_tx(bar, kMoeStageBytes);
+        if (kb + 2 <= k_full) {
+          tma_load_4d(dst, &m->group, bar, 0, g.tile * kBM, kb, g.expert);
+        } else {
+          for (int j = 0; j < 2; ++j)
+            tma_load_3d(dst + j * kBM * kFp8Block, &m->one, bar, (kb + j) * kFp8Block,
+                        g.tile * kBM, g.expert);
+        }
+        ++filled;
+        if (++s == kMoeStages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
   }
-  __syncthreads();
+  return filled;
+}
+
+// The weights' scales (one per k-block of a tile): 8 at a time, one per lane.
+__device__ __forceinline__ void moe_scales(const MoeArgs& a, const MoeRoute& r, uint32_t ring,
+                                           uint32_t sc_full, uint32_t sc_empty, int lane,
+                                           const WaitCtl& wc) {
+  uint32_t slot = 0, ph = 0;
+  bool ok = true;
+  MoeIter it(a, r);
+  for (int phase = 0; phase < 2 && ok; ++phase) {
+    it.start(phase);
+    MoeSeg g;
+    while (ok && it.next(g)) {
+      const gemm_fp8_experts_t& w = g.which == 0 ? a.L.gate : g.which == 1 ? a.L.up : a.L.down;
+      const float* p = w.scale + g.expert * w.scale_stride_e + g.tile * w.scale_stride_r;
+      for (int32_t kb = g.kb0; kb < g.kb1; kb += kMoeScaleGroup) {
+        ok = __all_sync(0xffffffffu, wait_bounded(sc_empty + 8 * slot, ph ^ 1, wc, kSiteProducer));
+        if (!ok) break;
+        if (lane < kMoeScaleGroup && kb + lane < g.kb1)
+          cp_async4(ring + (slot * kMoeScaleGroup + lane) * 4, p + (kb + lane) * w.scale_stride_c);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sc_full +
+                                                                                 8 * slot)
+                     : "memory");
+        if (++slot == kMoeScaleRing) {
+          slot = 0;
+          ph ^= 1;
+        }
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ void moe_mma(const MoeArgs& a, const MoeRoute& r, uint32_t ring,
+                                        uint32_t operand, uint32_t full, uint32_t empty,
+                                        uint32_t acc_full, uint32_t acc_empty, uint32_t b_full,
+                                        uint32_t b_empty, uint32_t drain, uint32_t tmem_base,
+                                        const WaitCtl& wc) {
+  uint32_t s = 0, ph = 0, b = 0, phases = (1u << kMoeBuffers) - 1;
+  bool ok = true, any = false;
+  const bool leader = f8_elect();
+  const uint64_t adesc0 = make_sdesc_sw128(ring, 16, 1024);
+  const uint64_t bdesc0 = make_sdesc_sw128(operand, 16, 1024);
+  MoeContent content;
+  MoeIter it(a, r);
+  auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+    if (ok && !mbar_test(bar, parity)) ok = wait_bounded(bar, parity, wc, site);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  };
+  for (int phase = 0; phase < 2 && ok; ++phase) {
+    it.start(phase);
+    MoeSeg g;
+    while (ok && it.next(g)) {
+      const int cols = moe_cols(g.n), cap = moe_cap(cols);
+      const bool whole = g.kb <= cap;
+      const uint32_t idesc = make_idesc_f16(kBM, cols, 0, 0);
+      for (int32_t c0 = g.kb0; ok && c0 < g.kb1; c0 += cap) {
+        const int32_t c1 = whole ? g.kb1 : min(c0 + cap, g.kb1);
+        const int32_t base = whole ? 0 : c0;  // the content's first k-block
+        const uint32_t old = content.buf();
+        const bool had = content.count > 0;
+        if (content.advance(g, whole)) {
+          if (had && leader) tc_commit(b_empty + 8 * old);
+          if (!wait(b_full + 8 * content.buf(), content.parity(), kSiteMmaFull)) break;
+          tc_fence_after();
+        }
+        const uint64_t bd = bdesc0 + ((content.buf() * kMoeOperandBytes) >> 4);
+        for (int32_t kb = c0; ok && kb < c1; kb += 2) {
+          if (!wait(full + 8 * s, ph, kSiteMmaFull)) break;
+          for (int j = 0; j < 2 && kb + j < c1; ++j) {
+            if (!wait(acc_empty + 8 * b, (phases >> b) & 1, kSiteMmaAccum)) break;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t ad = adesc0 + ((s * kMoeStageBytes + j * kBM * kFp8Block) >> 4);
+              const uint64_t bj = bd + uint64_t(((kb + j - base) * cols * kFp8Block) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kFp8Block / 32; ++kk)
+                tc_mma_f8(tmem_base + b * 64, ad + 2 * kk, bj + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              if (j == 1 || kb + j + 1 >= c1) tc_commit(empty + 8 * s);
+              tc_commit(acc_full + 8 * b);
+            }
+            __syncwarp();
+            any = true;
+            phases ^= 1u << b;
+            b = (b + 1) & (kMoeBuffers - 1);
+          }
+          if (++s == kMoeStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (whole) break;
+      }
+    }
+  }
+  if (!ok && any && leader) {
+    tc_commit(drain);
+    wait_drain(drain, 0, wc);
+  }
+  __syncwarp();
+}
+
+// Warps 4-7: thread `row` owns one weight row; sums of up to 64 tokens.
+__device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute& r,
+                                               const float* scale_ring, const float* b_scale,
+                                               uint32_t acc_full, uint32_t acc_empty,
+                                               uint32_t b_full, uint32_t b_empty, uint32_t sc_full,
+                                               uint32_t sc_empty, uint32_t tmem_base,
+                                               const WaitCtl& wc) {
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int row = warp * 32 + lane;
+  const uint32_t tlane = tmem_base + (uint32_t(warp * 32) << 16);
+  uint32_t b = 0, phases = 0, slot = 0, sph = 0;
+  bool ok = true;
+  const int32_t picks = int32_t(a.L.tokens) * a.L.top_k;
+  MoeContent content;
+  MoeIter it(a, r);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (ok && !mbar_test(bar, parity)) ok = wait_bounded(bar, parity, wc, kSiteEpilogue);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  };
+  for (int phase = 0; phase < 2; ++phase) {
+    it.start(phase);
+    MoeSeg g;
+    while (ok && it.next(g)) {
+      const int cols = moe_cols(g.n), cap = moe_cap(cols);
+      const bool whole = g.kb <= cap;
+      float acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+      for (int32_t c0 = g.kb0; ok && c0 < g.kb1; c0 += cap) {
+        const int32_t c1 = whole ? g.kb1 : min(c0 + cap, g.kb1);
+        const int32_t base = whole ? 0 : c0;
+        const uint32_t old = content.buf();
+        const bool had = content.count > 0;
+        if (content.advance(g, whole)) {
+          __syncwarp();
+          if (had && lane == 0) mbar_arrive(b_empty + 8 * old);
+          if (!wait(b_full + 8 * content.buf(), content.parity())) break;
+        }
+        const float* bs = b_scale + content.buf() * kMoeRows;
+        for (int32_t kb = c0; ok && kb < c1; ++kb) {
+          const int32_t i = (kb - g.kb0) % kMoeScaleGroup;
+          if (i == 0 && !wait(sc_full + 8 * slot, sph)) break;
+          const float ws = scale_ring[slot * kMoeScaleGroup + i];
+          if (!wait(acc_full + 8 * b, (phases >> b) & 1)) break;
+          tc_fence_after();
+          const float* bk = bs + (kb - base) * cols;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c * 16 < cols) {
+              uint32_t v[16];
+              tmem_issue<16>(tlane + b * 64 + c * 16, v);
+              tmem_wait<16>(v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                acc[c * 16 + j] = fmaf(__uint_as_float(v[j]), ws * bk[c * 16 + j],
+                                       acc[c * 16 + j]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty + 8 * b);
+          phases ^= 1u << b;
+          b = (b + 1) & (kMoeBuffers - 1);
+          if (i == kMoeScaleGroup - 1 || kb + 1 == g.kb1) {
+            if (lane == 0) mbar_arrive(sc_empty + 8 * slot);
+            if (++slot == kMoeScaleRing) {
+              slot = 0;
+              sph ^= 1;
+            }
+          }
+        }
+        if (whole) break;
+      }
+      if (!ok) break;
+      const int64_t ld = int64_t(phase == 0 ? a.tiles_i : a.tiles_h) * kBM;
+      float* out = phase == 0 ? a.part1 + (int64_t(g.seg) * 2 + g.which) * picks * ld
+                              : a.part2 + int64_t(g.seg) * picks * ld;
+      out += g.tile * kBM + row;
+      const uint16_t* pick = r.pick + r.off[g.expert];
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        if (i < g.n) __stcg(out + int64_t(pick[i]) * ld, acc[i]);
+    }
+    // this CTA's partials of the phase are written
+    __threadfence();
+    bar_sync(2, 128);
+    if (threadIdx.x == 128) atomicAdd(a.counters + 1 + phase, 1);
+  }
+}
+
+// Warps 8-11: the token operand.
+__device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, uint8_t* operand,
+                                          float* b_scale, int32_t* seg_counts, uint32_t b_full,
+                                          uint32_t b_empty, int* flag, const WaitCtl& wc) {
+  const int tid = threadIdx.x - 256, warp = tid >> 5, lane = tid & 31;
+  const int32_t k = a.L.top_k, picks = int32_t(a.L.tokens) * k;
+  bool ok = true;
+  MoeContent content;
+  MoeIter it(a, r);
+  for (int phase = 0; phase < 2 && ok; ++phase) {
+    it.start(phase);
+    if (phase == 1) {  // all gate and up partials are written
+      if (tid == 0) *flag = grid_wait(a.counters + 1, wc) ? 1 : 0;
+      bar_sync(3, 128);
+      ok = *flag != 0;
+      __threadfence();
+    }
+    const MoeWork w1 = it.work(0);
+    MoeSeg g;
+    while (ok && it.next(g)) {
+      const int cols = moe_cols(g.n), cap = moe_cap(cols);
+      const bool whole = g.kb <= cap;
+      for (int32_t c0 = g.kb0; ok && c0 < g.kb1; c0 += cap) {
+        const int32_t base = whole ? 0 : c0;
+        const int32_t blocks = whole ? g.kb : min(cap, g.kb1 - c0);
+        if (content.advance(g, whole)) {
+          const uint32_t buf = content.buf();
+          ok = wait_bounded(b_empty + 8 * buf, content.parity() ^ 1, wc, kSiteProducer);
+          if (tid < blocks && phase == 1) {
+            const int64_t tile = int64_t(r.index[g.expert]) * 2 * a.tiles_i + base + tid;
+            seg_counts[2 * tid] = w1.segments(tile);
+            seg_counts[2 * tid + 1] = w1.segments(tile + a.tiles_i);
+          }
+          // the vote of all four warps, and seg_counts, for all
+          if (tid == 0) *flag = 1;
+          bar_sync(3, 128);
+          if (!ok) *flag = 0;
+          bar_sync(3, 128);
+          ok = *flag != 0;
+          if (!ok) break;
+          uint8_t* dst = operand + buf * kMoeOperandBytes;
+          float* bs = b_scale + buf * kMoeRows;
+          const uint16_t* pick = r.pick + r.off[g.expert];
+          if (phase == 0) {
+            const int pieces = blocks * cols * 8;
+#pragma unroll 4
+            for (int i = tid; i < pieces; i += 128) {
+              const int c = i & 7, n = (i >> 3) % cols, kb = (i >> 3) / cols;
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (n < g.n)
+                v = __ldcg(reinterpret_cast<const uint4*>(
+                    a.xq + (int64_t(pick[n] / k) * a.kb_h + base + kb) * kFp8Block + c * 16));
+              *reinterpret_cast<uint4*>(dst + (kb * cols + n) * kFp8Block + ((c ^ (n & 7)) << 4)) =
+                  v;
+            }
+            for (int i = tid; i < blocks * cols; i += 128) {
+              const int n = i % cols, kb = i / cols;
+              bs[i] = n < g.n ? __ldcg(a.xs + int64_t(pick[n] / k) * a.kb_h + base + kb) : 0.f;
+            }
+          } else {
+            const int64_t ld = int64_t(a.tiles_i) * kBM, step = 2 * int64_t(picks) * ld;
+            for (int i = warp; i < blocks * cols; i += 4) {
+              const int kb = i / cols, n = i - kb * cols;
+              uint32_t q = 0;
+              float scale = 0.f;
+              if (n < g.n) {
+                const float* p = a.part1 + int64_t(pick[n]) * ld + (base + kb) * kFp8Block +
+                                 lane * 4;
+                float4 gt = make_float4(0.f, 0.f, 0.f, 0.f), up = gt;
+                const int32_t ng = seg_counts[2 * kb], nu = seg_counts[2 * kb + 1];
+#pragma unroll 2
+                for (int32_t sg = 0; sg < ng; ++sg) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(p + sg * step));
+                  gt.x += v.x; gt.y += v.y; gt.z += v.z; gt.w += v.w;
+                }
+                p += int64_t(picks) * ld;
+#pragma unroll 2
+                for (int32_t sg = 0; sg < nu; ++sg) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(p + sg * step));
+                  up.x += v.x; up.y += v.y; up.z += v.z; up.w += v.w;
+                }
+                const float h[4] = {gt.x / (1.f + expf(-gt.x)) * up.x,
+                                    gt.y / (1.f + expf(-gt.y)) * up.y,
+                                    gt.z / (1.f + expf(-gt.z)) * up.z,
+                                    gt.w / (1.f + expf(-gt.w)) * up.w};
+                q = quant_block(h, scale);
+              }
+              *reinterpret_cast<uint32_t*>(dst + (kb * cols + n) * kFp8Block +
+                                           (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = q;
+              if (lane == 0) bs[kb * cols + n] = scale;
+            }
+          }
+          fence_proxy_async_smem();  // the MMA reads the operand through the async proxy
+          mbar_arrive(b_full + 8 * buf);
+        }
+        if (whole) break;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- phase E --
+__device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r) {
+  const gemm_moe_fp8_t& L = a.L;
+  const int32_t k = L.top_k, picks = int32_t(L.tokens) * k;
+  const int64_t H = L.hidden, ld = int64_t(a.tiles_h) * kBM, step = int64_t(picks) * ld;
+  const MoeWork w(int64_t(r.active) * a.tiles_h, a.kb_i);
+  const int64_t quads = ld / 4, total = L.tokens * quads;
+  for (int64_t i = int64_t(blockIdx.x) * kMoeThreads + threadIdx.x; i < total;
+       i += int64_t(gridDim.x) * kMoeThreads) {
+    const int64_t t = i / quads, h = (i - t * quads) * 4;
+    if (h >= H) continue;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int32_t j = 0; j < k; ++j) {
+      const int32_t p = int32_t(t) * k + j;
+      const float gate = __ldcg(L.gates + p);
+      const int32_t n = w.segments(int64_t(r.index[r.ids[p]]) * a.tiles_h + h / kBM);
+      const float* src = a.part2 + p * ld + h;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int32_t sg = 0; sg < n; ++sg) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + sg * step));
+        y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+      }
+      o.x = fmaf(gate, y.x, o.x);
+      o.y = fmaf(gate, y.y, o.y);
+      o.z = fmaf(gate, y.z, o.z);
+      o.w = fmaf(gate, y.w, o.w);
+    }
+    const float v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (h + j < H) store_typed(L.out, t * L.ld_out + h + j, v[j], L.dtype);
+  }
+}
+
+// Shared memory: weight ring, two operand buffers (phase B's keys before that),
+// routing, scales, barriers.
+struct MoeSmem {
+  static constexpr int ring = 0;
+  static constexpr int operand = ring + kMoeStages * kMoeStageBytes;
+  static constexpr int route = operand + 2 * kMoeOperandBytes;
+  static constexpr int b_scale = route + int((sizeof(MoeRoute) + 15) / 16 * 16);
+  static constexpr int scale_ring = b_scale + 2 * kMoeRows * 4;
+  static constexpr int seg_counts = scale_ring + kMoeScaleRing * kMoeScaleGroup * 4;
+  static constexpr int red = seg_counts + 2 * 16 * 4;
+  static constexpr int bars = red + 64 * 4;
+  static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1;
+  static constexpr int words = bars + kBars * 8;
+  static constexpr int bytes = 1024 + words + 32;
+};
+static_assert(MoeSmem::bytes <= 227 * 1024, "shared memory per CTA");
+static_assert(moe_cap(16) <= 16, "seg_counts");
+
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    moe_kernel(const __grid_constant__ MoeMaps gate, const __grid_constant__ MoeMaps up,
+               const __grid_constant__ MoeMaps down, const __grid_constant__ MoeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  MoeRoute& r = *reinterpret_cast<MoeRoute*>(smem + MoeSmem::route);
+  float* b_scale = reinterpret_cast<float*>(smem + MoeSmem::b_scale);
+  float* scale_ring = reinterpret_cast<float*>(smem + MoeSmem::scale_ring);
+  int32_t* seg_counts = reinterpret_cast<int32_t*>(smem + MoeSmem::seg_counts);
+  const uint32_t full = smem_u32(smem + MoeSmem::bars);
+  const uint32_t empty = full + 8 * kMoeStages;
+  const uint32_t acc_full = empty + 8 * kMoeStages;
+  const uint32_t acc_empty = acc_full + 8 * kMoeBuffers;
+  const uint32_t b_full = acc_empty + 8 * kMoeBuffers;
+  const uint32_t b_empty = b_full + 16;
+  const uint32_t sc_full = b_empty + 16;
+  const uint32_t sc_empty = sc_full + 8 * kMoeScaleRing;
+  const uint32_t drain = sc_empty + 8 * kMoeScaleRing;
+  int* words = reinterpret_cast<int*>(smem + MoeSmem::words);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
+  volatile int* abort_flag = words + 1;
+  const WaitCtl wc{a.wait_limit_ns, a.status, abort_flag};
+
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    const float top = logit[chosen[0]];
-    float sum = 0.f;
-    if (a.L.renormalize)
-      for (int j = 0; j < a.L.top_k; ++j) sum += expf(logit[chosen[j]] - top);
-    else
-      for (int j = 0; j < a.L.experts; ++j) sum += expf(logit[j] - top);
-    for (int j = 0; j < a.L.top_k; ++j) {
-      a.L.ids[t * a.L.top_k + j] = chosen[j];
-      a.L.gates[t * a.L.top_k + j] = expf(logit[chosen[j]] - top) / sum;
+    for (int i = 0; i < kMoeStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kMoeBuffers; ++i) {
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_full + 8 * i, 128);
+      mbar_init(b_empty + 8 * i, 1 + 4);  // the MMA issuer's commit, four reading warps
+    }
+    for (int i = 0; i < kMoeScaleRing; ++i) {
+      mbar_init(sc_full + 8 * i, 32);
+      mbar_init(sc_empty + 8 * i, 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&gate.group);
+    tma_prefetch_map(&up.group);
+    tma_prefetch_map(&down.group);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp >= 4) {
+    moe_phase_a(a, reinterpret_cast<float*>(smem + MoeSmem::red), threadIdx.x - 128);
+    __threadfence();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  if (threadIdx.x == 0) {
+    atomicAdd(a.counters, 1);
+    words[2] = grid_wait(a.counters, wc) ? 1 : 0;
+  }
+  __syncthreads();
+  const bool routed = words[2] != 0;
+  uint32_t filled = 0;
+  if (routed) {
+    __threadfence();
+    moe_phase_b(a, r, reinterpret_cast<uint32_t*>(smem + MoeSmem::operand),
+                2 * kMoeOperandBytes / 4);
+    const uint32_t ring = smem_u32(smem + MoeSmem::ring);
+    if (warp >= 8) {
+      moe_build(a, r, smem + MoeSmem::operand, b_scale, seg_counts, b_full, b_empty, words + 3,
+                wc);
+    } else if (warp >= 4) {
+      moe_accumulate(a, r, scale_ring, b_scale, acc_full, acc_empty, b_full, b_empty, sc_full,
+                     sc_empty, tmem_base, wc);
+    } else if (warp == 2) {
+      moe_scales(a, r, smem_u32(scale_ring), sc_full, sc_empty, lane, wc);
+    } else if (warp == 1) {
+      moe_mma(a, r, ring, smem_u32(smem + MoeSmem::operand), full, empty, acc_full, acc_empty,
+              b_full, b_empty, drain, tmem_base, wc);
+    } else if (warp == 0 && lane == 0) {
+      const MoeMaps* maps[3] = {&gate, &up, &down};
+      filled = moe_producer(a, r, maps, ring, full, empty, wc);
     }
   }
-}
-
-// One weight row times one quantised vector, by a warp.
-__device__ __forceinline__ float row_dot(const gemm_fp8_experts_t& w, int64_t e, int64_t row,
-                                         const uint8_t* q, const float* s, int64_t K, int lane) {
-  const uint8_t* p = static_cast<const uint8_t*>(w.data) + e * w.expert_stride + row * w.ld;
-  const float* ws = w.scale + e * w.scale_stride_e + (row >> 7) * w.scale_stride_r;
-  float acc = 0.f;
-  for (int64_t kb = 0; kb * 128 < K; ++kb) {
-    float part = 0.f;
-    for (int64_t k = kb * 128 + lane; k < min(K, kb * 128 + 128); k += 32)
-      part = fmaf(unpack_e4m3x2(p[k]).x, unpack_e4m3x2(q[k]).x, part);
-    acc = fmaf(part, ws[kb * w.scale_stride_c] * s[kb], acc);
+  // after an abort, copies may still be in flight: each stage's last one
+  if (threadIdx.x == 0)
+    for (uint32_t s = 0; s < uint32_t(kMoeStages) && s < filled; ++s)
+      wait_drain(full + 8 * s, ((filled - 1 - s) / kMoeStages) & 1, wc);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
   }
+  if (!routed || *abort_flag) return;  // gemm_status clears the counters
+  if (threadIdx.x == 0) words[2] = grid_wait(a.counters + 2, wc) ? 1 : 0;
+  __syncthreads();
+  if (words[2] == 0) return;
+  __threadfence();
+  moe_phase_e(a, r);
+  // the last CTA through the last barrier leaves the counters at 0
+  if (threadIdx.x == 0 && atomicAdd(a.counters + 3, 1) == int(gridDim.x) - 1) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-  return acc;
-}
-
-__global__ void __launch_bounds__(kMoeThreads) moe_gate_up_kernel(const MoeArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t i = int64_t(blockIdx.x) * (kMoeThreads / 32) + warp, pick = blockIdx.y;
-  if (i >= a.L.inner) return;
-  const int64_t t = pick / a.L.top_k, e = a.L.ids[pick], H = a.L.hidden;
-  const uint8_t* q = a.xq + t * H;
-  const float* s = a.xs + t * ((H + 127) / 128);
-  const float g = row_dot(a.L.gate, e, i, q, s, H, lane);
-  const float u = row_dot(a.L.up, e, i, q, s, H, lane);
-  if (lane == 0) a.h[pick * a.L.inner + i] = g / (1.f + expf(-g)) * u;
-}
-
-__global__ void __launch_bounds__(kMoeThreads) moe_hidden_kernel(const MoeArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t I = a.L.inner, kbs = (I + 127) / 128, pick = blockIdx.x;
-  for (int64_t kb = warp; kb < kbs; kb += kMoeThreads / 32) {
-    float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t c = kb * 128 + lane * 4 + j;
-      v[j] = c < I ? a.h[pick * I + c] : 0.f;
-    }
-    quant_block(v, lane, kb * 128, I, a.hq + pick * I, a.hs + pick * kbs + kb);
+    for (int i = 0; i < 4; ++i) atomicExch(a.counters + i, 0);
   }
-}
-
-__global__ void __launch_bounds__(kMoeThreads) moe_down_kernel(const MoeArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r = int64_t(blockIdx.x) * (kMoeThreads / 32) + warp, t = blockIdx.y;
-  if (r >= a.L.hidden) return;
-  const int64_t I = a.L.inner;
-  float acc = 0.f;
-  for (int j = 0; j < a.L.top_k; ++j) {
-    const int64_t pick = t * a.L.top_k + j;
-    acc = fmaf(a.L.gates[pick], row_dot(a.L.down, a.L.ids[pick], r, a.hq + pick * I,
-                                        a.hs + pick * ((I + 127) / 128), I, lane), acc);
-  }
-  if (lane == 0) store_typed(a.L.out, t * a.L.ld_out + r, acc, a.L.dtype);
 }
 
 int64_t up256(int64_t b) { return (b + 255) & ~int64_t(255); }
+int64_t ceil128(int64_t n) { return (n + 127) / 128; }
+
+// Most CTAs that can work on one tile of `kb` k-blocks when at least `tiles`
+// tiles are shared out over at most `ctas` CTAs.
+int64_t most_segments(int64_t tiles, int64_t kb, int64_t ctas) {
+  const int64_t least = std::max<int64_t>(kMoeMinUnits, tiles * kb / ctas);
+  return std::min(kb, kb / least + 2);
+}
+
+struct MoeSpace {
+  int64_t xq, xs, logits, part1, part2;
+  MoeSpace(const gemm_moe_fp8_t& L, int64_t ctas) {
+    const int64_t T = L.tokens, P = T * L.top_k, kb_h = ceil128(L.hidden), kb_i = ceil128(L.inner);
+    // a token's choices are different experts, so at least top_k are chosen
+    const int64_t s1 = most_segments(2 * L.top_k * kb_i, kb_h, ctas);
+    const int64_t s2 = most_segments(L.top_k * kb_h, kb_i, ctas);
+    xq = up256(T * kb_h * kFp8Block);
+    xs = up256(T * kb_h * 4);
+    logits = up256(T * L.experts * 4);
+    part1 = up256(s1 * 2 * P * kb_i * kBM * 4);
+    part2 = up256(s2 * P * kb_h * kBM * 4);
+  }
+  int64_t bytes() const { return xq + xs + logits + part1 + part2; }
+};
+
+bool encode_experts(MoeMaps* m, const gemm_fp8_experts_t& w, int64_t rows, int64_t K,
+                    int64_t experts) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t pitch = cuuint64_t(w.ld);
+  const cuuint64_t next = cuuint64_t(experts > 1 ? w.expert_stride : rows * w.ld);
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  auto encode = [&](CUtensorMap* map, cuuint32_t rank, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box) {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(w.data), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t dims3[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(experts)};
+  const cuuint64_t strides3[2] = {pitch, next};
+  const cuuint32_t box3[3] = {kFp8Block, kBM, 1};
+  if (!encode(&m->one, 3, dims3, strides3, box3)) return false;
+  m->group = m->one;
+  if (K < 2 * kFp8Block) return true;  // no whole group: never used
+  const cuuint64_t dims4[4] = {kFp8Block, cuuint64_t(rows), cuuint64_t(K / kFp8Block),
+                               cuuint64_t(experts)};
+  const cuuint64_t strides4[3] = {pitch, kFp8Block, next};
+  const cuuint32_t box4[4] = {kFp8Block, kBM, 2, 1};
+  return encode(&m->group, 4, dims4, strides4, box4);
+}
 
 }  // namespace
 
-int64_t moe_workspace_bytes(const gemm_moe_fp8_t& L) {
-  const int64_t P = L.tokens * L.top_k;
-  return up256(L.tokens * L.hidden) + up256(L.tokens * ((L.hidden + 127) / 128) * 4) +
-         up256(P * L.inner * 4) + up256(P * L.inner) + up256(P * ((L.inner + 127) / 128) * 4);
+int64_t moe_workspace_bytes(const gemm_ctx* h, const gemm_moe_fp8_t& L) {
+  return MoeSpace(L, h->num_sms).bytes();
 }
 
-cudaError_t launch_moe(const gemm_moe_fp8_t& L, void* workspace, cudaStream_t stream) {
+cudaError_t launch_moe(gemm_ctx* h, const gemm_moe_fp8_t& L, void* workspace,
+                       cudaStream_t stream) {
+  const MoeSpace space(L, h->num_sms);
   MoeArgs a{};
   a.L = L;
-  const int64_t P = L.tokens * L.top_k;
+  a.kb_h = int32_t(ceil128(L.hidden));
+  a.kb_i = int32_t(ceil128(L.inner));
+  a.tiles_h = a.kb_h;
+  a.tiles_i = a.kb_i;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.xq = w;
-  w += up256(L.tokens * L.hidden);
-  a.xs = reinterpret_cast<float*>(w);
-  w += up256(L.tokens * ((L.hidden + 127) / 128) * 4);
-  a.h = reinterpret_cast<float*>(w);
-  w += up256(P * L.inner * 4);
-  a.hq = w;
-  w += up256(P * L.inner);
-  a.hs = reinterpret_cast<float*>(w);
-  const unsigned rows = kMoeThreads / 32;
-  moe_router_kernel<<<unsigned(L.tokens), kMoeThreads, 0, stream>>>(a);
-  moe_gate_up_kernel<<<dim3(unsigned((L.inner + rows - 1) / rows), unsigned(P)), kMoeThreads, 0,
-                       stream>>>(a);
-  moe_hidden_kernel<<<unsigned(P), kMoeThreads, 0, stream>>>(a);
-  moe_down_kernel<<<dim3(unsigned((L.hidden + rows - 1) / rows), unsigned(L.tokens)), kMoeThreads,
-                    0, stream>>>(a);
-  return cudaGetLastError();
+  a.xs = reinterpret_cast<float*>(w += space.xq);
+  a.logits = reinterpret_cast<float*>(w += space.xs);
+  a.part1 = reinterpret_cast<float*>(w += space.logits);
+  a.part2 = reinterpret_cast<float*>(w += space.part1);
+  a.counters = h->tickets + kMoeCounters;
+  a.status = h->status;
+  a.wait_limit_ns = h->opt.wait_limit_ns;
+  a.vec = ((reinterpret_cast<uintptr_t>(L.x) | reinterpret_cast<uintptr_t>(L.router)) & 15) == 0 &&
+          L.ld_x % 8 == 0 && L.ld_router % 8 == 0;
+  MoeMaps gate, up, down;
+  if (!encode_experts(&gate, L.gate, L.inner, L.hidden, L.experts) ||
+      !encode_experts(&up, L.up, L.inner, L.hidden, L.experts) ||
+      !encode_experts(&down, L.down, L.hidden, L.inner, L.experts))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(moe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       MoeSmem::bytes);
+  if (e != cudaSuccess) return e;
+  // the CTAs wait for one another: a cooperative launch, all resident at once
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.gridDim = dim3(unsigned(h->num_sms), 1, 1);
+  cfg.blockDim = dim3(kMoeThreads, 1, 1);
+  cfg.dynamicSmemBytes = MoeSmem::bytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_kernel, gate, up, down, a);
 }
 
 }  // namespace dg
