@@ -42,9 +42,11 @@ constexpr int kMoeBuffers = 8;                     // TMEM accumulators of 64 co
 constexpr int kMoeScaleGroup = 8, kMoeScaleRing = 4;
 constexpr int kMoeMinUnits = 2;                    // fewest k-blocks of a CTA's range
 
-// Rows of B (tokens) of an MMA, and k-blocks of them that an operand buffer holds.
-__host__ __device__ constexpr int moe_cols(int n) { return (n + 15) & ~15; }
-__host__ __device__ constexpr int moe_cap(int cols) { return (kMoeRows / cols) & ~1; }
+// Rows of B (tokens) of an MMA, a power of two, and k-blocks of them that an
+// operand buffer holds.  Rows past the expert's tokens hold anything: they only
+// reach columns that nobody reads.
+__host__ __device__ constexpr int moe_shift(int n) { return n <= 16 ? 4 : n <= 32 ? 5 : 6; }
+__host__ __device__ constexpr int moe_cap(int cols) { return kMoeRows / cols; }
 
 struct MoeMaps {
   CUtensorMap group, one;  // {128, rows, k-block, expert}, {K, rows, expert}
@@ -72,6 +74,7 @@ struct MoeRoute {
   uint16_t act[GEMM_MOE_MAX_EXPERTS];    // the chosen experts, ascending
   uint16_t ids[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];
   uint16_t pick[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];  // token * top_k + choice
+  uint8_t token[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];  // and its token
   int32_t active;
 };
 
@@ -370,12 +373,19 @@ __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r, uint3
   __syncthreads();
   for (int32_t p = tid; p < T * k; p += kMoeThreads) {
     const int32_t t = p / k, e = r.ids[p];
-    r.pick[r.off[e] + __popcll(r.mask[e] & ((1ull << t) - 1))] = uint16_t(p);
+    const int32_t at = r.off[e] + __popcll(r.mask[e] & ((1ull << t) - 1));
+    r.pick[at] = uint16_t(p);
+    r.token[at] = uint8_t(t);
   }
-  // gates and ids: one warp per token, spread over the CTAs
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int32_t t = int32_t(blockIdx.x) + warp * int32_t(gridDim.x); t < T;
-       t += int32_t(gridDim.x) * (kMoeThreads / 32)) {
+  __syncthreads();
+}
+
+// Gates and ids: one warp per token, spread over the CTAs (warp 3, beside the
+// streaming).
+__device__ __forceinline__ void moe_gates(const MoeArgs& a, const MoeRoute& r, int lane) {
+  const gemm_moe_fp8_t& L = a.L;
+  const int32_t T = int32_t(L.tokens), E = int32_t(L.experts), k = L.top_k;
+  for (int32_t t = int32_t(blockIdx.x); t < T; t += int32_t(gridDim.x)) {
     const float* l = a.logits + int64_t(t) * E;
     const float top = __ldcg(l + r.ids[t * k]);
     float sum = 0.f, mine = 0.f;
@@ -392,7 +402,6 @@ __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r, uint3
       L.gates[t * k + lane] = mine / sum;
     }
   }
-  __syncthreads();
 }
 
 // --------------------------------------------------------------- phases C, D --
@@ -482,7 +491,7 @@ __device__ __forceinline__ void moe_mma(const MoeArgs& a, const MoeRoute& r, uin
     it.start(phase);
     MoeSeg g;
     while (ok && it.next(g)) {
-      const int cols = moe_cols(g.n), cap = moe_cap(cols);
+      const int cols = 1 << moe_shift(g.n), cap = moe_cap(cols);
       const bool whole = g.kb <= cap;
       const uint32_t idesc = make_idesc_f16(kBM, cols, 0, 0);
       for (int32_t c0 = g.kb0; ok && c0 < g.kb1; c0 += cap) {
@@ -555,7 +564,7 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
     it.start(phase);
     MoeSeg g;
     while (ok && it.next(g)) {
-      const int cols = moe_cols(g.n), cap = moe_cap(cols);
+      const int cols = 1 << moe_shift(g.n), cap = moe_cap(cols);
       const bool whole = g.kb <= cap;
       float acc[64];
 #pragma unroll
@@ -622,6 +631,27 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
   }
 }
 
+// The sum of `n` partials, the first four's loads in flight together.
+__device__ __forceinline__ float4 sum_segments(const float* p, int64_t step, int32_t n) {
+  constexpr int kAhead = 4;
+  float4 v[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) v[i] = __ldcg(reinterpret_cast<const float4*>(p + i * step));
+  }
+  float4 s = v[0];
+#pragma unroll
+  for (int i = 1; i < kAhead; ++i) {
+    s.x += v[i].x; s.y += v[i].y; s.z += v[i].z; s.w += v[i].w;
+  }
+  for (int32_t i = kAhead; i < n; ++i) {
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(p + i * step));
+    s.x += w.x; s.y += w.y; s.z += w.z; s.w += w.w;
+  }
+  return s;
+}
+
 // Warps 8-11: the token operand.
 __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, uint8_t* operand,
                                           float* b_scale, int32_t* seg_counts, uint32_t b_full,
@@ -642,7 +672,7 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, u
     const MoeWork w1 = it.work(0);
     MoeSeg g;
     while (ok && it.next(g)) {
-      const int cols = moe_cols(g.n), cap = moe_cap(cols);
+      const int cols = 1 << moe_shift(g.n), cap = moe_cap(cols);
       const bool whole = g.kb <= cap;
       for (int32_t c0 = g.kb0; ok && c0 < g.kb1; c0 += cap) {
         const int32_t base = whole ? 0 : c0;
@@ -665,50 +695,34 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, u
           uint8_t* dst = operand + buf * kMoeOperandBytes;
           float* bs = b_scale + buf * kMoeRows;
           const uint16_t* pick = r.pick + r.off[g.expert];
+          const uint8_t* token = r.token + r.off[g.expert];
           if (phase == 0) {
-            const int pieces = blocks * cols * 8;
-#pragma unroll 4
-            for (int i = tid; i < pieces; i += 128) {
-              const int c = i & 7, n = (i >> 3) % cols, kb = (i >> 3) / cols;
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (n < g.n)
-                v = __ldcg(reinterpret_cast<const uint4*>(
-                    a.xq + (int64_t(pick[n] / k) * a.kb_h + base + kb) * kFp8Block + c * 16));
+            // 16-byte pieces of the real rows, a thread's own piece of every 16th
+            const int c = tid & 7;
+            for (int i = tid >> 3; i < blocks * g.n; i += 16) {
+              const int kb = i / g.n, n = i - kb * g.n;
+              const int64_t at = int64_t(token[n]) * a.kb_h + base + kb;
+              const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.xq + at * kFp8Block) + c);
               *reinterpret_cast<uint4*>(dst + (kb * cols + n) * kFp8Block + ((c ^ (n & 7)) << 4)) =
                   v;
-            }
-            for (int i = tid; i < blocks * cols; i += 128) {
-              const int n = i % cols, kb = i / cols;
-              bs[i] = n < g.n ? __ldcg(a.xs + int64_t(pick[n] / k) * a.kb_h + base + kb) : 0.f;
+              if (c == 0) bs[kb * cols + n] = __ldcg(a.xs + at);
             }
           } else {
             const int64_t ld = int64_t(a.tiles_i) * kBM, step = 2 * int64_t(picks) * ld;
-            for (int i = warp; i < blocks * cols; i += 4) {
-              const int kb = i / cols, n = i - kb * cols;
-              uint32_t q = 0;
-              float scale = 0.f;
-              if (n < g.n) {
-                const float* p = a.part1 + int64_t(pick[n]) * ld + (base + kb) * kFp8Block +
-                                 lane * 4;
-                float4 gt = make_float4(0.f, 0.f, 0.f, 0.f), up = gt;
-                const int32_t ng = seg_counts[2 * kb], nu = seg_counts[2 * kb + 1];
 #pragma unroll 2
-                for (int32_t sg = 0; sg < ng; ++sg) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(p + sg * step));
-                  gt.x += v.x; gt.y += v.y; gt.z += v.z; gt.w += v.w;
-                }
-                p += int64_t(picks) * ld;
-#pragma unroll 2
-                for (int32_t sg = 0; sg < nu; ++sg) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(p + sg * step));
-                  up.x += v.x; up.y += v.y; up.z += v.z; up.w += v.w;
-                }
-                const float h[4] = {gt.x / (1.f + expf(-gt.x)) * up.x,
-                                    gt.y / (1.f + expf(-gt.y)) * up.y,
-                                    gt.z / (1.f + expf(-gt.z)) * up.z,
-                                    gt.w / (1.f + expf(-gt.w)) * up.w};
-                q = quant_block(h, scale);
-              }
+            for (int i = warp; i < blocks * g.n; i += 4) {
+              const int kb = i / g.n, n = i - kb * g.n;
+              const float* p = a.part1 + int64_t(pick[n]) * ld + (base + kb) * kFp8Block +
+                               lane * 4;
+              const float4 gt = sum_segments(p, step, seg_counts[2 * kb]);
+              const float4 up = sum_segments(p + int64_t(picks) * ld, step,
+                                             seg_counts[2 * kb + 1]);
+              const float h[4] = {gt.x / (1.f + expf(-gt.x)) * up.x,
+                                  gt.y / (1.f + expf(-gt.y)) * up.y,
+                                  gt.z / (1.f + expf(-gt.z)) * up.z,
+                                  gt.w / (1.f + expf(-gt.w)) * up.w};
+              float scale;
+              const uint32_t q = quant_block(h, scale);
               *reinterpret_cast<uint32_t*>(dst + (kb * cols + n) * kFp8Block +
                                            (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = q;
               if (lane == 0) bs[kb * cols + n] = scale;
@@ -730,22 +744,19 @@ __device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r)
   const int64_t H = L.hidden, ld = int64_t(a.tiles_h) * kBM, step = int64_t(picks) * ld;
   const MoeWork w(int64_t(r.active) * a.tiles_h, a.kb_i);
   const int64_t quads = ld / 4, total = L.tokens * quads;
-  for (int64_t i = int64_t(blockIdx.x) * kMoeThreads + threadIdx.x; i < total;
-       i += int64_t(gridDim.x) * kMoeThreads) {
+  // 32 neighbouring quads a warp, warps dealt to the CTAs in turn
+  const int64_t first = (int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 +
+                        (threadIdx.x & 31);
+  for (int64_t i = first; i < total; i += int64_t(gridDim.x) * kMoeThreads) {
     const int64_t t = i / quads, h = (i - t * quads) * 4;
     if (h >= H) continue;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int32_t j = 0; j < k; ++j) {
       const int32_t p = int32_t(t) * k + j;
       const float gate = __ldcg(L.gates + p);
       const int32_t n = w.segments(int64_t(r.index[r.ids[p]]) * a.tiles_h + h / kBM);
-      const float* src = a.part2 + p * ld + h;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-      for (int32_t sg = 0; sg < n; ++sg) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + sg * step));
-        y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-      }
+      const float4 y = sum_segments(a.part2 + p * ld + h, step, n);
       o.x = fmaf(gate, y.x, o.x);
       o.y = fmaf(gate, y.y, o.y);
       o.z = fmaf(gate, y.z, o.z);
@@ -855,6 +866,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     } else if (warp >= 4) {
       moe_accumulate(a, r, scale_ring, b_scale, acc_full, acc_empty, b_full, b_empty, sc_full,
                      sc_empty, tmem_base, wc);
+    } else if (warp == 3) {
+      moe_gates(a, r, lane);
     } else if (warp == 2) {
       moe_scales(a, r, smem_u32(scale_ring), sc_full, sc_empty, lane, wc);
     } else if (warp == 1) {
