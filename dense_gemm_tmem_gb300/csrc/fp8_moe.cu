@@ -13,7 +13,7 @@
 // for one token or sixteen, and the TMA ring keeps 128 KiB a CTA in flight.
 //
 //   phase A  all workers: router logits, x̂                  -> barrier 1
-//   phase B  every CTA for itself: experts by rank, token lists, work ranges
+//   phase B  every CTA for itself: top-k, token lists, work ranges
 //   phase C  gate and up: fp32 partial sums of each range    -> barrier 2
 //   phase D  down: the same, ĥ formed from phase C's partials -> barrier 3
 //   phase E  out from phase D's partials and the gates
@@ -116,11 +116,11 @@ struct MoeSeg {
 struct MoeIter {
   const MoeArgs& a;
   const MoeRoute& r;
-  int64_t x, end;
-  int32_t phase;
-  __device__ __forceinline__ MoeIter(const MoeArgs& a_, const MoeRoute& r_) : a(a_), r(r_) {
-    start(0);
-  }
+  int64_t left;           // k-blocks left of this CTA's range
+  int32_t phase, kb;      // k-blocks of a tile
+  int32_t expert, rest;   // the next segment's: place among the chosen experts, tile within it
+  int32_t per, kb0, seg;  // tiles of an expert; first k-block; place among the tile's CTAs
+  __device__ __forceinline__ MoeIter(const MoeArgs& a_, const MoeRoute& r_) : a(a_), r(r_) {}
   __device__ __forceinline__ MoeWork work(int32_t ph) const {
     return ph == 0 ? MoeWork(int64_t(r.active) * 2 * a.tiles_i, a.kb_h)
                    : MoeWork(int64_t(r.active) * a.tiles_h, a.kb_i);
@@ -128,28 +128,38 @@ struct MoeIter {
   __device__ __forceinline__ void start(int32_t ph) {
     phase = ph;
     const MoeWork w = work(ph);
-    x = w.begin(blockIdx.x);
-    end = w.begin(blockIdx.x + 1);
+    const int64_t x = w.begin(blockIdx.x);
+    left = w.begin(blockIdx.x + 1) - x;
+    kb = w.kb;
+    per = ph == 0 ? 2 * a.tiles_i : a.tiles_h;
+    expert = rest = kb0 = seg = 0;
+    if (left == 0) return;
+    const int64_t tile = x / kb;
+    expert = int32_t(tile / per);
+    rest = int32_t(tile - int64_t(expert) * per);
+    kb0 = int32_t(x - tile * kb);
+    // only a range's first tile can have begun in another CTA's range
+    if (kb0 > 0) seg = int32_t(blockIdx.x) - w.owner(tile * kb);
   }
   // The next segment of this phase.
   __device__ __forceinline__ bool next(MoeSeg& s) {
-    if (x >= end) return false;
-    const MoeWork w = work(phase);
-    const int64_t tile = x / w.kb;
+    if (left == 0) return false;
     s.phase = phase;
-    s.kb = w.kb;
-    s.kb0 = int32_t(x - tile * w.kb);
-    const int64_t left = end - x;
-    s.kb1 = left < w.kb - s.kb0 ? int32_t(s.kb0 + left) : w.kb;
-    x += s.kb1 - s.kb0;
-    s.seg = int32_t(blockIdx.x) - w.owner(tile * w.kb);
-    const int32_t per = phase == 0 ? 2 * a.tiles_i : a.tiles_h;
-    const int32_t i = int32_t(tile / per);
-    const int32_t rest = int32_t(tile - int64_t(i) * per);
-    s.expert = r.act[i];
+    s.kb = kb;
+    s.kb0 = kb0;
+    s.kb1 = left < kb - kb0 ? int32_t(kb0 + left) : kb;
+    s.seg = seg;
+    s.expert = r.act[expert];
     s.n = __popcll(r.mask[s.expert]);
-    s.which = phase == 1 ? 2 : rest / a.tiles_i;
-    s.tile = phase == 1 ? rest : rest % a.tiles_i;
+    const int32_t second = phase == 0 && rest >= a.tiles_i;
+    s.which = phase == 1 ? 2 : second;
+    s.tile = second ? rest - a.tiles_i : rest;
+    left -= s.kb1 - kb0;
+    kb0 = seg = 0;
+    if (++rest == per) {
+      rest = 0;
+      ++expert;
+    }
     return true;
   }
 };
@@ -190,18 +200,10 @@ __device__ __forceinline__ float from16(uint16_t h, int dtype) {
   return __uint_as_float(uint32_t(h) << 16);
 }
 
-// Eight neighbouring 16-bit elements from column c of a row of n, zeros past it.
-__device__ __forceinline__ void load8_16(const uint16_t* row, int64_t c, int64_t n, int vec,
-                                         int dtype, float (&v)[8]) {
-  if (vec && c + 8 <= n) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + c));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void widen8(const uint4& w, int dtype, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = from16(uint16_t(u[j / 2] >> (16 * (j & 1))), dtype);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? from16(row[c + j], dtype) : 0.f;
-  }
+  for (int j = 0; j < 8; ++j) v[j] = from16(uint16_t(u[j / 2] >> (16 * (j & 1))), dtype);
 }
 
 // One block of 128 values, 4 per lane, quantised by a warp: this lane's 4 bytes;
@@ -257,7 +259,7 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 // ------------------------------------------------------------------- phase A --
 // Router logits: a CTA takes (expert, 8 tokens) tasks, its 8 worker warps an
 // eighth of the hidden axis each.  x̂: a warp per (token, k-block).
-__device__ __forceinline__ void moe_phase_a(const MoeArgs& a, float* red, int tid) {
+__device__ __forceinline__ void moe_phase_a(const MoeArgs& a, float* red0, int tid) {
   const gemm_moe_fp8_t& L = a.L;
   const int warp = tid >> 5, lane = tid & 31;
   const int64_t H = L.hidden;
@@ -265,26 +267,43 @@ __device__ __forceinline__ void moe_phase_a(const MoeArgs& a, float* red, int ti
   const uint16_t* router = static_cast<const uint16_t*>(L.router);
   const int32_t T = int32_t(L.tokens), E = int32_t(L.experts);
   const int32_t groups = (T + 7) / 8;
+  float* red = red0;
+  int turn = 0;
   for (int32_t task = blockIdx.x; task < E * groups; task += gridDim.x) {
     const int32_t e = task / groups, t0 = (task - e * groups) * 8;
     float s[8] = {};
     for (int64_t c = (warp * 32 + lane) * 8; c < H; c += 8 * 256) {
-      float w[8];
-      load8_16(router + e * L.ld_router, c, H, a.vec, L.dtype, w);
+      if (a.vec && c + 8 <= H) {  // every load in flight before the first is used
+        uint4 raw[9];
+        raw[8] = __ldg(reinterpret_cast<const uint4*>(router + e * L.ld_router + c));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (t0 + i >= T) break;
-        float v[8];
-        load8_16(x + (t0 + i) * L.ld_x, c, H, a.vec, L.dtype, v);
+        for (int i = 0; i < 8; ++i)  // tokens past the last repeat it
+          if (i == 0 || T > 1)
+            raw[i] = __ldg(reinterpret_cast<const uint4*>(x + min(t0 + i, T - 1) * L.ld_x + c));
+        float w[8];
+        widen8(raw[8], L.dtype, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[i] = fmaf(v[j], w[j], s[i]);
+        for (int i = 0; i < 8; ++i) {
+          if (i > 0 && T == 1) break;
+          float v[8];
+          widen8(raw[i], L.dtype, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[i] = fmaf(v[j], w[j], s[i]);
+        }
+      } else {
+        for (int j = 0; j < 8 && c + j < H; ++j) {
+          const float w = from16(router[e * L.ld_router + c + j], L.dtype);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            s[i] = fmaf(from16(x[min(t0 + i, T - 1) * L.ld_x + c + j], L.dtype), w, s[i]);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-    bar_sync(1, 256);  // the previous task's sums have been read
+    red = red0 + (turn ^= 64);  // the other half: the task before last has been read
     if (lane < 8) {
       float v = s[0];
 #pragma unroll
@@ -318,31 +337,42 @@ __device__ __forceinline__ void moe_phase_a(const MoeArgs& a, float* red, int ti
 }
 
 // ------------------------------------------------------------------- phase B --
-// Every thread of the CTA: the experts of each token by rank (how many logits
-// are larger, or equal with a lower index), who chose whom, and the lists.
-__device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r, uint32_t* keys,
-                                            int32_t key_cap) {
+// Every warp of the CTA: the experts of its tokens, one largest key after the
+// other (of equal ones the lowest index); then who chose whom, and the lists.
+__device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r) {
   const gemm_moe_fp8_t& L = a.L;
   const int32_t T = int32_t(L.tokens), E = int32_t(L.experts), k = L.top_k;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kPer = GEMM_MOE_MAX_EXPERTS / 32;
   for (int e = tid; e < E; e += kMoeThreads) r.mask[e] = 0;
-  const int32_t chunk = key_cap / E;  // tokens staged at once
-  for (int32_t t0 = 0; t0 < T; t0 += chunk) {
-    const int32_t nt = min(chunk, T - t0);
-    __syncthreads();
-    for (int32_t i = tid; i < nt * E; i += kMoeThreads)
-      keys[i] = order_key(__ldcg(a.logits + int64_t(t0) * E + i));
-    __syncthreads();
-    for (int32_t i = tid; i < nt * E; i += kMoeThreads) {
-      const int32_t t = i / E, e = i - t * E;
-      const uint32_t* row = keys + t * E;
-      const uint32_t key = row[e];
-      int32_t rank = 0;
-#pragma unroll 8
-      for (int32_t j = 0; j < E; ++j) rank += row[j] > key || (row[j] == key && j < e);
-      if (rank < k) {
-        r.ids[(t0 + t) * k + rank] = uint16_t(e);
-        atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[e]), 1ull << (t0 + t));
+  __syncthreads();
+  for (int32_t t = warp; t < T; t += kMoeThreads / 32) {
+    uint32_t key[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      key[i] = 0;  // below every logit's
+      if (i * 32 < E && i * 32 + lane < E)
+        key[i] = order_key(__ldcg(a.logits + int64_t(t) * E + i * 32 + lane));
+    }
+    for (int32_t j = 0; j < k; ++j) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (i * 32 >= E) break;
+        most = max(most, key[i]);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      uint32_t e = 0xffffu;
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; --i)
+        if (i * 32 < E && key[i] == most) e = uint32_t(i * 32 + lane);
+      e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (e == uint32_t(i * 32 + lane)) key[i] = 0;
+      if (lane == 0) {
+        r.ids[t * k + j] = uint16_t(e);
+        atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[e]), 1ull << t);
       }
     }
   }
@@ -743,20 +773,27 @@ __device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r)
   const int32_t k = L.top_k, picks = int32_t(L.tokens) * k;
   const int64_t H = L.hidden, ld = int64_t(a.tiles_h) * kBM, step = int64_t(picks) * ld;
   const MoeWork w(int64_t(r.active) * a.tiles_h, a.kb_i);
-  const int64_t quads = ld / 4, total = L.tokens * quads;
-  // 32 neighbouring quads a warp, warps dealt to the CTAs in turn
-  const int64_t first = (int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 +
-                        (threadIdx.x & 31);
-  for (int64_t i = first; i < total; i += int64_t(gridDim.x) * kMoeThreads) {
-    const int64_t t = i / quads, h = (i - t * quads) * 4;
-    if (h >= H) continue;
+  // A warp takes (token, 128 columns): lane j looks up choice j's gate and how
+  // many partials its tile has, then all lanes add 4 columns each.
+  const int lane = threadIdx.x & 31;
+  const int64_t items = L.tokens * a.tiles_h;
+  for (int64_t i = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x; i < items;
+       i += int64_t(gridDim.x) * (kMoeThreads / 32)) {
+    const int32_t t = int32_t(i / a.tiles_h), tile = int32_t(i - int64_t(t) * a.tiles_h);
+    float my_gate = 0.f;
+    int32_t my_n = 0;
+    if (lane < k) {
+      my_gate = __ldcg(L.gates + t * k + lane);
+      my_n = w.segments(int64_t(r.index[r.ids[t * k + lane]]) * a.tiles_h + tile);
+    }
+    const int64_t h = int64_t(tile) * kBM + lane * 4;
+    const float* src = a.part2 + int64_t(t) * k * ld + h;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int32_t j = 0; j < k; ++j) {
-      const int32_t p = int32_t(t) * k + j;
-      const float gate = __ldcg(L.gates + p);
-      const int32_t n = w.segments(int64_t(r.index[r.ids[p]]) * a.tiles_h + h / kBM);
-      const float4 y = sum_segments(a.part2 + p * ld + h, step, n);
+      const float gate = __shfl_sync(0xffffffffu, my_gate, j);
+      const int32_t n = __shfl_sync(0xffffffffu, my_n, j);
+      const float4 y = sum_segments(src + j * ld, step, n);
       o.x = fmaf(gate, y.x, o.x);
       o.y = fmaf(gate, y.y, o.y);
       o.z = fmaf(gate, y.z, o.z);
@@ -769,8 +806,7 @@ __device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r)
   }
 }
 
-// Shared memory: weight ring, two operand buffers (phase B's keys before that),
-// routing, scales, barriers.
+// Shared memory: weight ring, two operand buffers, routing, scales, barriers.
 struct MoeSmem {
   static constexpr int ring = 0;
   static constexpr int operand = ring + kMoeStages * kMoeStageBytes;
@@ -779,7 +815,7 @@ struct MoeSmem {
   static constexpr int scale_ring = b_scale + 2 * kMoeRows * 4;
   static constexpr int seg_counts = scale_ring + kMoeScaleRing * kMoeScaleGroup * 4;
   static constexpr int red = seg_counts + 2 * 16 * 4;
-  static constexpr int bars = red + 64 * 4;
+  static constexpr int bars = red + 2 * 64 * 4;
   static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1;
   static constexpr int words = bars + kBars * 8;
   static constexpr int bytes = 1024 + words + 32;
@@ -857,8 +893,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   uint32_t filled = 0;
   if (routed) {
     __threadfence();
-    moe_phase_b(a, r, reinterpret_cast<uint32_t*>(smem + MoeSmem::operand),
-                2 * kMoeOperandBytes / 4);
+    moe_phase_b(a, r);
     const uint32_t ring = smem_u32(smem + MoeSmem::ring);
     if (warp >= 8) {
       moe_build(a, r, smem + MoeSmem::operand, b_scale, seg_counts, b_full, b_empty, words + 3,
