@@ -76,6 +76,11 @@ struct MoeRoute {
   uint16_t pick[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];  // token * top_k + choice
   uint8_t token[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];  // and its token
   int32_t active;
+  struct Start {            // where this CTA's range of a phase begins
+    int64_t left;           // its k-blocks
+    int32_t expert, rest;   // place among the chosen experts, tile within the expert
+    int32_t kb0, seg;       // first k-block; this CTA's place among the tile's
+  } start[2];
 };
 
 // One phase's work: `units` k-blocks cut into `ctas` equal ranges.
@@ -88,14 +93,16 @@ struct MoeWork {
     const int64_t most = units / kMoeMinUnits;
     ctas = int32_t(most < 1 ? 1 : most < int64_t(gridDim.x) ? most : int64_t(gridDim.x));
   }
+  // A quotient of non-negative numbers, in 32 bits where they fit.
+  static __device__ __forceinline__ int64_t div(int64_t n, int64_t d) {
+    if (((uint64_t(n) | uint64_t(d)) >> 32) == 0) return uint32_t(n) / uint32_t(d);
+    return n / d;
+  }
   __device__ __forceinline__ int64_t begin(int32_t c) const {
-    return c >= ctas ? units : units * c / ctas;
+    return c >= ctas ? units : div(units * c, ctas);
   }
   __device__ __forceinline__ int32_t owner(int64_t x) const {
-    const uint64_t num = uint64_t(x + 1) * uint64_t(ctas) - 1;
-    if ((num >> 32) == 0 && (uint64_t(units) >> 32) == 0)
-      return int32_t(uint32_t(num) / uint32_t(units));
-    return int32_t(num / uint64_t(units));
+    return int32_t(div((x + 1) * ctas - 1, units));
   }
   // CTAs that work on a tile.
   __device__ __forceinline__ int32_t segments(int64_t tile) const {
@@ -121,25 +128,16 @@ struct MoeIter {
   int32_t expert, rest;   // the next segment's: place among the chosen experts, tile within it
   int32_t per, kb0, seg;  // tiles of an expert; first k-block; place among the tile's CTAs
   __device__ __forceinline__ MoeIter(const MoeArgs& a_, const MoeRoute& r_) : a(a_), r(r_) {}
-  __device__ __forceinline__ MoeWork work(int32_t ph) const {
-    return ph == 0 ? MoeWork(int64_t(r.active) * 2 * a.tiles_i, a.kb_h)
-                   : MoeWork(int64_t(r.active) * a.tiles_h, a.kb_i);
-  }
   __device__ __forceinline__ void start(int32_t ph) {
     phase = ph;
-    const MoeWork w = work(ph);
-    const int64_t x = w.begin(blockIdx.x);
-    left = w.begin(blockIdx.x + 1) - x;
-    kb = w.kb;
+    kb = ph == 0 ? a.kb_h : a.kb_i;
     per = ph == 0 ? 2 * a.tiles_i : a.tiles_h;
-    expert = rest = kb0 = seg = 0;
-    if (left == 0) return;
-    const int64_t tile = x / kb;
-    expert = int32_t(tile / per);
-    rest = int32_t(tile - int64_t(expert) * per);
-    kb0 = int32_t(x - tile * kb);
-    // only a range's first tile can have begun in another CTA's range
-    if (kb0 > 0) seg = int32_t(blockIdx.x) - w.owner(tile * kb);
+    const MoeRoute::Start& s = r.start[ph];
+    left = s.left;
+    expert = s.expert;
+    rest = s.rest;
+    kb0 = s.kb0;
+    seg = s.seg;
   }
   // The next segment of this phase.
   __device__ __forceinline__ bool next(MoeSeg& s) {
@@ -163,6 +161,29 @@ struct MoeIter {
     return true;
   }
 };
+
+__device__ __forceinline__ MoeWork moe_work(const MoeArgs& a, const MoeRoute& r, int32_t ph) {
+  return ph == 0 ? MoeWork(int64_t(r.active) * 2 * a.tiles_i, a.kb_h)
+                 : MoeWork(int64_t(r.active) * a.tiles_h, a.kb_i);
+}
+
+// This CTA's start of phase ph (one thread; the divisions of all roles).
+__device__ __noinline__ void moe_start(const MoeArgs& a, MoeRoute& r, int32_t ph) {
+  const MoeWork w = moe_work(a, r, ph);
+  MoeRoute::Start s = {};
+  const int64_t x = w.begin(blockIdx.x);
+  s.left = w.begin(blockIdx.x + 1) - x;
+  if (s.left > 0) {
+    const int32_t per = ph == 0 ? 2 * a.tiles_i : a.tiles_h;
+    const int64_t tile = w.div(x, w.kb);
+    s.expert = int32_t(w.div(tile, per));
+    s.rest = int32_t(tile - int64_t(s.expert) * per);
+    s.kb0 = int32_t(x - tile * w.kb);
+    // only a range's first tile can have begun in another CTA's range
+    if (s.kb0 > 0) s.seg = int32_t(blockIdx.x) - w.owner(tile * w.kb);
+  }
+  r.start[ph] = s;
+}
 
 // The token operand's buffers as every role sees them: content is one expert's
 // rows for a range of k-blocks; a whole-K content serves every segment of the
@@ -337,44 +358,46 @@ __device__ __forceinline__ void moe_phase_a(const MoeArgs& a, float* red0, int t
 }
 
 // ------------------------------------------------------------------- phase B --
-// Every warp of the CTA: the experts of its tokens, one largest key after the
-// other (of equal ones the lowest index); then who chose whom, and the lists.
+// The experts of a token, by one warp: one largest key after the other, of equal
+// ones the lowest index.  PER keys a lane.
+template <int PER>
+__device__ __forceinline__ void moe_choose(const MoeArgs& a, MoeRoute& r, int32_t t, int lane) {
+  const int32_t E = int32_t(a.L.experts), k = a.L.top_k;
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int32_t e = i * 32 + lane;
+    key[i] = e < E ? order_key(__ldcg(a.logits + int64_t(t) * E + e)) : 0;  // 0: below all
+  }
+#pragma unroll 1
+  for (int32_t j = 0; j < k; ++j) {
+    uint32_t most = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) most = max(most, key[i]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    uint32_t e = 0xffffu;
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i) e = key[i] == most ? uint32_t(i * 32 + lane) : e;
+    e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = e == uint32_t(i * 32 + lane) ? 0 : key[i];
+    if (lane == 0) {
+      r.ids[t * k + j] = uint16_t(e);
+      atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[e]), 1ull << t);
+    }
+  }
+}
+
+// Every warp of the CTA: the experts of its tokens; then who chose whom, the
+// lists and the work ranges.
 __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r) {
   const gemm_moe_fp8_t& L = a.L;
   const int32_t T = int32_t(L.tokens), E = int32_t(L.experts), k = L.top_k;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kPer = GEMM_MOE_MAX_EXPERTS / 32;
-  for (int e = tid; e < E; e += kMoeThreads) r.mask[e] = 0;
-  __syncthreads();
   for (int32_t t = warp; t < T; t += kMoeThreads / 32) {
-    uint32_t key[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      key[i] = 0;  // below every logit's
-      if (i * 32 < E && i * 32 + lane < E)
-        key[i] = order_key(__ldcg(a.logits + int64_t(t) * E + i * 32 + lane));
-    }
-    for (int32_t j = 0; j < k; ++j) {
-      uint32_t most = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (i * 32 >= E) break;
-        most = max(most, key[i]);
-      }
-      most = __reduce_max_sync(0xffffffffu, most);
-      uint32_t e = 0xffffu;
-#pragma unroll
-      for (int i = kPer - 1; i >= 0; --i)
-        if (i * 32 < E && key[i] == most) e = uint32_t(i * 32 + lane);
-      e = __reduce_min_sync(0xffffffffu, e);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (e == uint32_t(i * 32 + lane)) key[i] = 0;
-      if (lane == 0) {
-        r.ids[t * k + j] = uint16_t(e);
-        atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[e]), 1ull << t);
-      }
-    }
+    if (E <= 64) moe_choose<2>(a, r, t, lane);
+    else if (E <= 128) moe_choose<4>(a, r, t, lane);
+    else moe_choose<GEMM_MOE_MAX_EXPERTS / 32>(a, r, t, lane);
   }
   __syncthreads();
   if (tid < 32) {  // prefix sums over the experts
@@ -401,6 +424,7 @@ __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r) {
     if (tid == 0) r.active = active;
   }
   __syncthreads();
+  if (warp == 2 && lane < 2) moe_start(a, r, lane);
   for (int32_t p = tid; p < T * k; p += kMoeThreads) {
     const int32_t t = p / k, e = r.ids[p];
     const int32_t at = r.off[e] + __popcll(r.mask[e] & ((1ull << t) - 1));
@@ -693,13 +717,7 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, u
   MoeIter it(a, r);
   for (int phase = 0; phase < 2 && ok; ++phase) {
     it.start(phase);
-    if (phase == 1) {  // all gate and up partials are written
-      if (tid == 0) *flag = grid_wait(a.counters + 1, wc) ? 1 : 0;
-      bar_sync(3, 128);
-      ok = *flag != 0;
-      __threadfence();
-    }
-    const MoeWork w1 = it.work(0);
+    bool written = phase == 0;  // phase D: whether all gate and up partials are
     MoeSeg g;
     while (ok && it.next(g)) {
       const int cols = 1 << moe_shift(g.n), cap = moe_cap(cols);
@@ -711,13 +729,16 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, u
           const uint32_t buf = content.buf();
           ok = wait_bounded(b_empty + 8 * buf, content.parity() ^ 1, wc, kSiteProducer);
           if (tid < blocks && phase == 1) {
+            const MoeWork w1 = moe_work(a, r, 0);
             const int64_t tile = int64_t(r.index[g.expert]) * 2 * a.tiles_i + base + tid;
             seg_counts[2 * tid] = w1.segments(tile);
             seg_counts[2 * tid + 1] = w1.segments(tile + a.tiles_i);
           }
           // the vote of all four warps, and seg_counts, for all
-          if (tid == 0) *flag = 1;
+          if (tid == 0) *flag = written || grid_wait(a.counters + 1, wc) ? 1 : 0;
           bar_sync(3, 128);
+          if (!written) __threadfence();
+          written = true;
           if (!ok) *flag = 0;
           bar_sync(3, 128);
           ok = *flag != 0;
@@ -768,24 +789,28 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, u
 }
 
 // ------------------------------------------------------------------- phase E --
-__device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r) {
+// `arrived` is called once, before the first partial is read.
+template <class F>
+__device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r, F&& arrived) {
   const gemm_moe_fp8_t& L = a.L;
   const int32_t k = L.top_k, picks = int32_t(L.tokens) * k;
   const int64_t H = L.hidden, ld = int64_t(a.tiles_h) * kBM, step = int64_t(picks) * ld;
-  const MoeWork w(int64_t(r.active) * a.tiles_h, a.kb_i);
+  const MoeWork w = moe_work(a, r, 1);
   // A warp takes (token, 128 columns): lane j looks up choice j's gate and how
   // many partials its tile has, then all lanes add 4 columns each.
   const int lane = threadIdx.x & 31;
   const int64_t items = L.tokens * a.tiles_h;
-  for (int64_t i = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x; i < items;
-       i += int64_t(gridDim.x) * (kMoeThreads / 32)) {
-    const int32_t t = int32_t(i / a.tiles_h), tile = int32_t(i - int64_t(t) * a.tiles_h);
-    float my_gate = 0.f;
+  int64_t i = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  bool waiting = true;
+  do {
+    const int32_t t = int32_t(w.div(i, a.tiles_h)), tile = int32_t(i - int64_t(t) * a.tiles_h);
     int32_t my_n = 0;
-    if (lane < k) {
-      my_gate = __ldcg(L.gates + t * k + lane);
+    if (lane < k && i < items)
       my_n = w.segments(int64_t(r.index[r.ids[t * k + lane]]) * a.tiles_h + tile);
-    }
+    if (waiting && !arrived()) return;
+    waiting = false;
+    if (i >= items) return;
+    const float my_gate = lane < k ? __ldcg(L.gates + t * k + lane) : 0.f;
     const int64_t h = int64_t(tile) * kBM + lane * 4;
     const float* src = a.part2 + int64_t(t) * k * ld + h;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -803,7 +828,8 @@ __device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (h + j < H) store_typed(L.out, t * L.ld_out + h + j, v[j], L.dtype);
-  }
+    i += int64_t(gridDim.x) * (kMoeThreads / 32);
+  } while (i < items);
 }
 
 // Shared memory: weight ring, two operand buffers, routing, scales, barriers.
@@ -848,6 +874,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   const WaitCtl wc{a.wait_limit_ns, a.status, abort_flag};
 
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < int(a.L.experts); e += kMoeThreads) r.mask[e] = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMoeStages; ++i) {
       mbar_init(full + 8 * i, 1);
@@ -924,11 +951,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     tmem_dealloc(tmem_base, 512);
   }
   if (!routed || *abort_flag) return;  // gemm_status clears the counters
-  if (threadIdx.x == 0) words[2] = grid_wait(a.counters + 2, wc) ? 1 : 0;
-  __syncthreads();
+  moe_phase_e(a, r, [&]() {
+    if (threadIdx.x == 0) words[2] = grid_wait(a.counters + 2, wc) ? 1 : 0;
+    __syncthreads();
+    __threadfence();
+    return words[2] != 0;
+  });
   if (words[2] == 0) return;
-  __threadfence();
-  moe_phase_e(a, r);
   // the last CTA through the last barrier leaves the counters at 0
   if (threadIdx.x == 0 && atomicAdd(a.counters + 3, 1) == int(gridDim.x) - 1) {
 #pragma unroll
