@@ -38,7 +38,7 @@ constexpr int kMoeStages = 4;                      // of two k-blocks
 constexpr int kMoeStageBytes = 2 * kBM * kFp8Block;
 constexpr int kMoeOperandBytes = 32768;            // one token operand buffer: 256 rows of 128 B
 constexpr int kMoeRows = kMoeOperandBytes / kFp8Block;
-constexpr int kMoeBuffers = 8;                     // TMEM accumulators of 64 columns
+constexpr int kMoeBuffers = 4;                     // TMEM accumulators, two of 64 columns each
 constexpr int kMoeScaleGroup = 8, kMoeScaleRing = 4;
 constexpr int kMoeMinUnits = 2;                    // fewest k-blocks of a CTA's range
 
@@ -264,12 +264,29 @@ __device__ __forceinline__ bool grid_wait(const int* counter, const WaitCtl& wc)
   return true;
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+// Weights are read once: they leave L2 first, and the partials, x and the code stay.
+__device__ __forceinline__ uint64_t policy_evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void load_weights_4d(uint32_t dst, const CUtensorMap* map,
+                                                uint32_t bar, int32_t c0, int32_t c1, int32_t c2,
+                                                int32_t c3, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void load_weights_3d(uint32_t dst, const CUtensorMap* map,
+                                                uint32_t bar, int32_t c0, int32_t c1, int32_t c2,
+                                                uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
 
@@ -320,17 +337,21 @@ __device__ __forceinline__ void moe_phase_a(const MoeArgs& a, float* red0, int t
         }
       }
     }
+    // 8 sums over 32 lanes: halve the sums a lane holds three times, then add
+    // over the 4 lanes left; token i's sum ends in lanes 4 i ... 4 i + 3
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int h = 4; h > 0; h >>= 1) {
+      const bool high = (lane & (h * 4)) != 0;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-    red = red0 + (turn ^= 64);  // the other half: the task before last has been read
-    if (lane < 8) {
-      float v = s[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) v = lane == i ? s[i] : v;
-      red[warp * 8 + lane] = v;
+      for (int i = 0; i < h; ++i) {
+        const float give = high ? s[i] : s[i + h], keep = high ? s[i + h] : s[i];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, h * 4);
+      }
     }
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+    red = red0 + (turn ^= 64);  // the other half: the task before last has been read
+    if ((lane & 3) == 0) red[warp * 8 + (lane >> 2)] = s[0];
     bar_sync(1, 256);
     if (tid < 8 && t0 + tid < T) {
       float v = 0.f;
@@ -363,7 +384,7 @@ __device__ __forceinline__ void moe_phase_a(const MoeArgs& a, float* red0, int t
 template <int PER>
 __device__ __forceinline__ void moe_choose(const MoeArgs& a, MoeRoute& r, int32_t t, int lane) {
   const int32_t E = int32_t(a.L.experts), k = a.L.top_k;
-  uint32_t key[PER];
+  uint32_t key[PER], mine = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int32_t e = i * 32 + lane;
@@ -381,10 +402,11 @@ __device__ __forceinline__ void moe_choose(const MoeArgs& a, MoeRoute& r, int32_
     e = __reduce_min_sync(0xffffffffu, e);
 #pragma unroll
     for (int i = 0; i < PER; ++i) key[i] = e == uint32_t(i * 32 + lane) ? 0 : key[i];
-    if (lane == 0) {
-      r.ids[t * k + j] = uint16_t(e);
-      atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[e]), 1ull << t);
-    }
+    mine = lane == j ? e : mine;
+  }
+  if (lane < k) {
+    r.ids[t * k + lane] = uint16_t(mine);
+    atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[mine]), 1ull << t);
   }
 }
 
@@ -460,27 +482,28 @@ __device__ __forceinline__ void moe_gates(const MoeArgs& a, const MoeRoute& r, i
 
 // --------------------------------------------------------------- phases C, D --
 __device__ __forceinline__ uint32_t moe_producer(const MoeArgs& a, const MoeRoute& r,
-                                                 const MoeMaps* const* maps, uint32_t ring,
-                                                 uint32_t full,
+                                                 const MoeMaps& gate, const MoeMaps& up,
+                                                 const MoeMaps& down, uint32_t ring, uint32_t full,
                                                  uint32_t empty, const WaitCtl& wc) {
   uint32_t s = 0, ph = 0, filled = 0;
+  const uint64_t policy = policy_evict_first();
   MoeIter it(a, r);
   for (int phase = 0; phase < 2; ++phase) {
     it.start(phase);
     MoeSeg g;
     while (it.next(g)) {
       const int32_t k_full = int32_t((phase == 0 ? a.L.hidden : a.L.inner) / kFp8Block);
-      const MoeMaps* m = maps[g.which];
+      const MoeMaps* m = g.which == 0 ? &gate : g.which == 1 ? &up : &down;
       for (int32_t kb = g.kb0; kb < g.kb1; kb += 2) {
         if (!wait_bounded(empty + 8 * s, ph ^ 1, wc, kSiteProducer)) return filled;
         const uint32_t bar = full + 8 * s, dst = ring + s * kMoeStageBytes;
         mbar_arrive_expect_tx(bar, kMoeStageBytes);
         if (kb + 2 <= k_full) {
-          tma_load_4d(dst, &m->group, bar, 0, g.tile * kBM, kb, g.expert);
+          load_weights_4d(dst, &m->group, bar, 0, g.tile * kBM, kb, g.expert, policy);
         } else {
           for (int j = 0; j < 2; ++j)
-            tma_load_3d(dst + j * kBM * kFp8Block, &m->one, bar, (kb + j) * kFp8Block,
-                        g.tile * kBM, g.expert);
+            load_weights_3d(dst + j * kBM * kFp8Block, &m->one, bar, (kb + j) * kFp8Block,
+                            g.tile * kBM, g.expert, policy);
         }
         ++filled;
         if (++s == kMoeStages) {
@@ -561,23 +584,26 @@ __device__ __forceinline__ void moe_mma(const MoeArgs& a, const MoeRoute& r, uin
         const uint64_t bd = bdesc0 + ((content.buf() * kMoeOperandBytes) >> 4);
         for (int32_t kb = c0; ok && kb < c1; kb += 2) {
           if (!wait(full + 8 * s, ph, kSiteMmaFull)) break;
-          for (int j = 0; j < 2 && kb + j < c1; ++j) {
-            if (!wait(acc_empty + 8 * b, (phases >> b) & 1, kSiteMmaAccum)) break;
-            tc_fence_after();
-            if (leader) {
+          if (!wait(acc_empty + 8 * b, (phases >> b) & 1, kSiteMmaAccum)) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (kb + j >= c1) break;
               const uint64_t ad = adesc0 + ((s * kMoeStageBytes + j * kBM * kFp8Block) >> 4);
               const uint64_t bj = bd + uint64_t(((kb + j - base) * cols * kFp8Block) >> 4);
 #pragma unroll
               for (int kk = 0; kk < kFp8Block / 32; ++kk)
-                tc_mma_f8(tmem_base + b * 64, ad + 2 * kk, bj + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-              if (j == 1 || kb + j + 1 >= c1) tc_commit(empty + 8 * s);
-              tc_commit(acc_full + 8 * b);
+                tc_mma_f8(tmem_base + b * 128 + j * 64, ad + 2 * kk, bj + 2 * kk, idesc,
+                          kk > 0 ? 1u : 0u);
             }
-            __syncwarp();
-            any = true;
-            phases ^= 1u << b;
-            b = (b + 1) & (kMoeBuffers - 1);
+            tc_commit(empty + 8 * s);
+            tc_commit(acc_full + 8 * b);
           }
+          __syncwarp();
+          any = true;
+          phases ^= 1u << b;
+          b = (b + 1) & (kMoeBuffers - 1);
           if (++s == kMoeStages) {
             s = 0;
             ph ^= 1;
@@ -634,23 +660,32 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
           if (!wait(b_full + 8 * content.buf(), content.parity())) break;
         }
         const float* bs = b_scale + content.buf() * kMoeRows;
-        for (int32_t kb = c0; ok && kb < c1; ++kb) {
+        for (int32_t kb = c0; ok && kb < c1; kb += 2) {
           const int32_t i = (kb - g.kb0) % kMoeScaleGroup;
           if (i == 0 && !wait(sc_full + 8 * slot, sph)) break;
-          const float ws = scale_ring[slot * kMoeScaleGroup + i];
+          const bool two = kb + 1 < c1;
+          const float w0 = scale_ring[slot * kMoeScaleGroup + i];
+          const float w1 = two ? scale_ring[slot * kMoeScaleGroup + i + 1] : 0.f;
           if (!wait(acc_full + 8 * b, (phases >> b) & 1)) break;
           tc_fence_after();
           const float* bk = bs + (kb - base) * cols;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (c * 16 < cols) {
-              uint32_t v[16];
-              tmem_issue<16>(tlane + b * 64 + c * 16, v);
-              tmem_wait<16>(v);
+            if (c * 16 >= cols) break;
+            uint32_t v0[16], v1[16];
+            tmem_issue<16>(tlane + b * 128 + c * 16, v0);
+            if (two) tmem_issue<16>(tlane + b * 128 + 64 + c * 16, v1);
+            tmem_wait<16>(v0);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[c * 16 + j] =
+                  fmaf(__uint_as_float(v0[j]), w0 * bk[c * 16 + j], acc[c * 16 + j]);
+            if (two) {
+              tmem_wait<16>(v1);
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                acc[c * 16 + j] = fmaf(__uint_as_float(v[j]), ws * bk[c * 16 + j],
-                                       acc[c * 16 + j]);
+                acc[c * 16 + j] =
+                    fmaf(__uint_as_float(v1[j]), w1 * bk[cols + c * 16 + j], acc[c * 16 + j]);
             }
           }
           tc_fence_before();
@@ -658,7 +693,7 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
           if (lane == 0) mbar_arrive(acc_empty + 8 * b);
           phases ^= 1u << b;
           b = (b + 1) & (kMoeBuffers - 1);
-          if (i == kMoeScaleGroup - 1 || kb + 1 == g.kb1) {
+          if (i + 2 >= kMoeScaleGroup || kb + 2 >= g.kb1) {
             if (lane == 0) mbar_arrive(sc_empty + 8 * slot);
             if (++slot == kMoeScaleRing) {
               slot = 0;
@@ -675,8 +710,12 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
       out += g.tile * kBM + row;
       const uint16_t* pick = r.pick + r.off[g.expert];
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (i < g.n) __stcg(out + int64_t(pick[i]) * ld, acc[i]);
+      for (int c = 0; c < 4; ++c) {
+        if (c * 16 >= g.n) break;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c * 16 + i < g.n) __stcg(out + int64_t(pick[c * 16 + i]) * ld, acc[c * 16 + i]);
+      }
     }
     // this CTA's partials of the phase are written
     __threadfence();
@@ -936,8 +975,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       moe_mma(a, r, ring, smem_u32(smem + MoeSmem::operand), full, empty, acc_full, acc_empty,
               b_full, b_empty, drain, tmem_base, wc);
     } else if (warp == 0 && lane == 0) {
-      const MoeMaps* maps[3] = {&gate, &up, &down};
-      filled = moe_producer(a, r, maps, ring, full, empty, wc);
+      filled = moe_producer(a, r, gate, up, down, ring, full, empty, wc);
     }
   }
   // after an abort, copies may still be in flight: each stage's last one
