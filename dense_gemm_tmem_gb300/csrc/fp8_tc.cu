@@ -55,23 +55,34 @@ bool encode_fp8(Fp8Maps* m, const Fp8Operand& o, int64_t mn, int64_t K, int box_
   return encode(&m->group, 3, dims3, strides3, box3);
 }
 
-template <int BN, bool TRANS, bool COLVEC>
+template <int BN, bool TRANS, bool COLVEC, bool OUT32>
 cudaError_t launch_inst(const Fp8Maps& mA, const Fp8Maps& mB, const Fp8TcArgs& args, bool pdl,
                         cudaStream_t stream) {
-  auto kern = fp8_tc_kernel<BN, TRANS, COLVEC>;
+  auto kern = fp8_tc_kernel<BN, TRANS, COLVEC, OUT32>;
   constexpr int smem = Fp8TcConfig<BN>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  if (args.work.csplit > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = unsigned(args.work.csplit);
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
   cfg.gridDim = dim3(unsigned(args.work.grid), 1, 1);
   cfg.blockDim = dim3(kF8Threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1u : 0u;
+  cfg.numAttrs = unsigned(n);
   return cudaLaunchKernelEx(&cfg, kern, mA, mB, args);
 }
 
@@ -100,26 +111,37 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
     bn = Nm > 128 && tiles_m * ceil_div(Nm, 256) >= sms / 2 ? 256 : 128;
   const int64_t tiles_n = ceil_div(Nm, bn), T = tiles_m * tiles_n;
   if (T > INT32_MAX / 2) return cudaErrorInvalidValue;
-  // Fewer tiles than half the SMs: every tile's k-blocks split evenly over the
-  // SMs, at least kMinSplit k-blocks each.
-  constexpr int64_t kMinSplit = 4;
-  int64_t grid = std::min(sms, T), sk = 0;
-  if (2 * T < sms) {
-    const int64_t g = std::min(sms, std::max(T, T * I / kMinSplit));
-    if (g > T) {
-      grid = g;
-      sk = T;
+  // Fewer tiles than half the SMs: each tile's k-blocks over a cluster, the
+  // largest whose clusters are all resident at once, if that takes more than
+  // kSplitGain k-blocks off each CTA: adding the partials costs about as long as
+  // 8 k-blocks (2 us of 0.28 at 32 columns, 3 of 0.35 at 64, 4.3 of 0.51 at 128).
+  // Measured (graph replay, cold inputs, us, split / whole): 1 x 4096 x 4096 7.5
+  // / 12.0, 64 x 4096 x 4096 9.4 / 14.6, 128 x 1024 x 8192 11.3 / 36.5, 512 x 512
+  // x 2048 8.9 / 9.4; not taken: 515 x 1000 x 2056 12.2 / 10.8, 1024^3 10.4 / 7.1,
+  // 32 x 2048 x 1024 5.4 / 5.1.
+  constexpr int64_t kSplitGain = 8;
+  int64_t grid = std::min(sms, T), split = 1;
+  const int forced = h->opt.csplit;  // GEMM_OPT_CLUSTER_SPLIT
+  if (bn <= 128 && (forced >= 2 || (forced < 0 && 2 * T < sms))) {
+    for (int s : {8, 4, 2}) {
+      const int64_t cap = h->opt.csplit_clusters[s];
+      if (forced >= 2 ? s == forced && I >= s && T * s <= INT32_MAX
+                      : T <= cap && T * s <= sms && I - ceil_div(I, s) > kSplitGain) {
+        split = s;
+        grid = T * s;
+        break;
+      }
     }
   }
   Fp8TcArgs a{};
   a.work.tiles_m = int32_t(tiles_m);
   a.work.tiles_n = int32_t(tiles_n);
   a.work.k_iters = int32_t(I);
-  a.work.dp_tiles = int32_t(T - sk);
-  a.work.sk_tiles = int32_t(sk);
+  a.work.dp_tiles = int32_t(split > 1 ? 0 : T);
+  a.work.sk_tiles = int32_t(split > 1 ? T : 0);
   a.work.grid = int32_t(grid);
   a.work.group_m = 16;
-  a.work.csplit = 0;
+  a.work.csplit = int32_t(split);
   a.Mm = int32_t(Mm);
   a.Nm = int32_t(Nm);
   a.row = Fp8Scales{opA.scale, opA.c_mn, opA.c_kb, opA.mn_shift};
@@ -133,8 +155,6 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
   a.a_mn = opA.s_k != 1;
   a.b_mn = opB.s_k != 1;
   a.k_full = int32_t(p.K / kFp8Block);
-  a.workspace = h->workspace;
-  a.tickets = h->tickets;
   a.status = h->status;
   a.wait_limit_ns = h->opt.wait_limit_ns;
   // e4m3 is type code 0 of kind::f8f6f4, as fp16 is of kind::f16
@@ -145,16 +165,25 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
     return cudaErrorInvalidValue;
   const bool pdl = h->opt.pdl != 0;
   const bool colvec = trans || opB.mn_shift == 0;
+  const bool out32 = p.out_dtype == GEMM_F32;
+  auto launch = [&](auto inst) { return inst(mA, mB, a, pdl, stream); };
   if (trans) {
-    if (bn == 32) return launch_inst<32, true, true>(mA, mB, a, pdl, stream);
-    if (bn == 64) return launch_inst<64, true, true>(mA, mB, a, pdl, stream);
-    return launch_inst<128, true, true>(mA, mB, a, pdl, stream);
+    if (bn == 32) return launch(launch_inst<32, true, true, false>);
+    if (bn == 64) return launch(launch_inst<64, true, true, false>);
+    return launch(launch_inst<128, true, true, false>);
   }
-  if (bn == 256)
-    return colvec ? launch_inst<256, false, true>(mA, mB, a, pdl, stream)
-                  : launch_inst<256, false, false>(mA, mB, a, pdl, stream);
-  return colvec ? launch_inst<128, false, true>(mA, mB, a, pdl, stream)
-                : launch_inst<128, false, false>(mA, mB, a, pdl, stream);
+  if (bn == 256) {
+    if (colvec)
+      return out32 ? launch(launch_inst<256, false, true, true>)
+                   : launch(launch_inst<256, false, true, false>);
+    return out32 ? launch(launch_inst<256, false, false, true>)
+                 : launch(launch_inst<256, false, false, false>);
+  }
+  if (colvec)
+    return out32 ? launch(launch_inst<128, false, true, true>)
+                 : launch(launch_inst<128, false, true, false>);
+  return out32 ? launch(launch_inst<128, false, false, true>)
+               : launch(launch_inst<128, false, false, false>);
 }
 
 }  // namespace dg

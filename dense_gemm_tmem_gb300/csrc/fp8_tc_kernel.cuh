@@ -30,10 +30,13 @@
 // and the same epilogue without the scale ring took 727 us against 656.
 // For skinny problems (TRANS: operands swapped, C stored transposed) the bound
 // is the stream of the weights.
-// Small problems split the k-blocks of all tiles evenly over the CTAs; the last
-// CTA to finish a tile adds the fp32 partials in ascending k order, so the sum
-// does not depend on who is last and no CTA waits for another.
+// Small problems split each tile's k-blocks over a cluster of 2, 4 or 8 CTAs,
+// which park their fp32 partial tiles in shared memory and add them through
+// distributed shared memory in rank order (a split through global memory with a
+// ticket took 16.1 us for 1 x 4096 x 4096, clusters of 4 take 7.5).
 #pragma once
+
+#include <type_traits>
 
 #include "fp8.cuh"
 #include "tc_kernel.cuh"
@@ -61,7 +64,8 @@ struct Fp8TcConfig {
   static constexpr int kBuffers = BN == 256 ? 2 : 4;      // TMEM accumulators
   static constexpr int kTmemCols = BN * kBuffers;         // a power of two >= 32
   static constexpr int kHalf = BN / 2;                    // columns per warpgroup
-  static constexpr int kChunk = kHalf < 32 ? kHalf : 32;  // columns per TMEM load
+  // columns per TMEM load (two loads' registers beside 128 sums leave room for 16)
+  static constexpr int kChunk = BN == 256 || kHalf < 32 ? 16 : 32;
   static constexpr int kStoreLd = 16 + 4;                 // staged store: 64 bytes a row, in floats
   static constexpr int kEpiBytes = kF8EpiWarps * 32 * kStoreLd * 4;
   // scales of one k-block: the tile's rows, then its columns
@@ -72,6 +76,10 @@ struct Fp8TcConfig {
   static constexpr int kBarBytes = 384;
   static constexpr int kSmemBytes =
       1024 + kStages * kStageBytes + kEpiBytes + kScaleBytes + kBarBytes;
+  // a parked partial tile (BN <= 128): rows (or, transposed, columns) padded by 4 floats
+  static constexpr int kParkRow = BN + 4, kParkCol = kBM + 4;
+  static_assert(kBM * kParkRow * 4 <= kStages * kStageBytes &&
+                BN * kParkCol * 4 <= kStages * kStageBytes, "the ring holds it");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   static_assert((2 * kStages + 2 * kBuffers + 1 + 2 * kScaleRing) * 8 + 16 <= kBarBytes, "barrier area");
 };
@@ -95,8 +103,6 @@ struct Fp8TcArgs {
   int32_t c_vec;       // 1: C's base is 16-byte aligned, its pitch a multiple of 16 bytes
   int32_t a_mn, b_mn;  // 1: the operand is MN-major (b_mn: BN a multiple of 128)
   int32_t k_full;      // whole k-blocks of K
-  float* workspace;
-  int* tickets;
   int* status;
   uint64_t wait_limit_ns;
   uint32_t idesc;
@@ -137,19 +143,20 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
-// Barrier among the 256 epilogue threads.
-__device__ __forceinline__ void f8_epi_sync() {
-  asm volatile("bar.sync 1, 256;" ::: "memory");
-}
-
 // d += a * b, two lanes; as two scalar FMAs: the packed form needs register
 // pairs that the TMEM loads do not give (8192^3: 590 us packed, 571 scalar).
 __device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
   d.x = fmaf(a.x, b.x, d.x);
   d.y = fmaf(a.y, b.y, d.y);
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  return make_float2(a.x * b.x, a.y * b.y);
+// Four floats of shared memory, read here and not earlier: loads that the
+// compiler moves up cost the registers of the sums.
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
 }
 
 // An operand's two tensor maps: `group` brings kGroup whole k-blocks in one
@@ -240,21 +247,19 @@ __device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, uint32_t ring, 
   while (ok && it.next(W, u)) {
     int32_t tm, tn;
     tile_coords(W, u.tile, tm, tn);
-    const float* src[2 + kCols];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    // addresses are worked out for every copy: registers are short here
+    auto row_at = [&](int i, int32_t kb) {
       const int32_t r = min(tm * kBM + t + i * kF8ScaleThreads, args.Mm - 1);
-      src[i] = args.row.p + int64_t(r >> args.row.shift) * args.row.stride +
-               u.kb0 * args.row.kb_stride;
-    }
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) {
+      return args.row.p + int64_t(r >> args.row.shift) * args.row.stride +
+             kb * args.row.kb_stride;
+    };
+    auto col_at = [&](int i, int32_t kb) {
       // uniform columns: threads 0 and 1 fetch the two warpgroups' scales
       const int32_t c = COLVEC ? t + i * kF8ScaleThreads : (t & 1) * Cfg::kHalf;
       const int32_t n = min(tn * BN + c, args.Nm - 1);
-      src[2 + i] = args.col.p + int64_t(n >> args.col.shift) * args.col.stride +
-                   u.kb0 * args.col.kb_stride;
-    }
+      return args.col.p + int64_t(n >> args.col.shift) * args.col.stride +
+             kb * args.col.kb_stride;
+    };
     for (int32_t kb = u.kb0; kb < u.kb1; kb += Cfg::kScaleGroup) {
       if (!wait_bounded(smem_u32(&sc_empty[slot]), ph ^ 1, wc, kSiteProducer)) {
         ok = false;
@@ -265,14 +270,12 @@ __device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, uint32_t ring, 
       for (int j = 0; j < Cfg::kScaleGroup && kb + j < u.kb1; ++j) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          cp_async4(dst + (t + i * kF8ScaleThreads) * 4, src[i]);
-          src[i] += args.row.kb_stride;
+          cp_async4(dst + (t + i * kF8ScaleThreads) * 4, row_at(i, kb + j));
         }
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
           const int c = t + i * kF8ScaleThreads;
-          if (c < (COLVEC ? BN : 2)) cp_async4(dst + (kBM + c) * 4, src[2 + i]);
-          src[2 + i] += args.col.kb_stride;
+          if (c < (COLVEC ? BN : 2)) cp_async4(dst + (kBM + c) * 4, col_at(i, kb + j));
         }
         dst += Cfg::kScaleFloats * 4;
       }
@@ -404,35 +407,33 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float2 (
     for (int j = 0; j < 4; ++j)
       own[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     __syncwarp();
-    uint4 x[4];
+    const int32_t cols = min(HC - c, PER);     // of this pass
+    if (a.c_vec && nn0 + c + cols <= a.Nm) {
+      uint4 x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      x[i] = *reinterpret_cast<const uint4*>(stage_w + (i * 8 + rs) * LD + 4 * piece);
-    const int32_t n = nn0 + c + piece * VEC;
-    int32_t valid = a.Nm - n;                  // columns of this lane's 16 bytes inside C
-    if (HC - c < PER && HC - c - piece * VEC < valid) valid = HC - c - piece * VEC;
-    if (valid <= 0) continue;
-    const int32_t r0 = mrow0 + rs;
-    uint8_t* p = static_cast<uint8_t*>(a.C) + (int64_t(r0) * a.ldc + n) * SIZE;
-    const int64_t step = a.ldc * (8 * SIZE);
-    if (valid >= VEC && a.c_vec) {
+      for (int i = 0; i < 4; ++i)
+        x[i] = *reinterpret_cast<const uint4*>(stage_w + (i * 8 + rs) * LD + 4 * piece);
+      if (piece * VEC >= cols) continue;
+      const int32_t r0 = mrow0 + rs;
+      uint8_t* p = static_cast<uint8_t*>(a.C) +
+                   (int64_t(r0) * a.ldc + nn0 + c + piece * VEC) * SIZE;
+      const int64_t step = a.ldc * (8 * SIZE);
 #pragma unroll
       for (int i = 0; i < 4; ++i, p += step)
         if (r0 + 8 * i < a.Mm) *reinterpret_cast<uint4*>(p) = x[i];
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i, p += step) {
-        if (r0 + 8 * i >= a.Mm) break;
-        const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if (j >= valid) break;
-          if constexpr (SIZE == 4)
-            reinterpret_cast<uint32_t*>(p)[j] = xw[j];
-          else
-            reinterpret_cast<uint16_t*>(p)[j] = uint16_t(xw[j / 2] >> (16 * (j & 1)));
-        }
-      }
+      // unaligned rows or the matrix's edge: element by element, neighbouring
+      // lanes still on neighbouring columns (16-byte pieces taken apart by one
+      // lane each cost 1001 x 2050 x 4100 9 of its 26 us)
+      using E = typename std::conditional<SIZE == 4, uint32_t, uint16_t>::type;
+      const int col = lane % PER, r0 = lane / PER;
+      const E* from = reinterpret_cast<const E*>(stage_w + r0 * LD) + col;
+      const bool in = col < cols && nn0 + c + col < a.Nm;
+      E* p = static_cast<E*>(a.C) + int64_t(mrow0 + r0) * a.ldc + nn0 + c + col;
+      constexpr int kStep = 32 / PER;          // rows an instruction
+#pragma unroll 4
+      for (int i = 0; i < 32; i += kStep)
+        if (in && mrow0 + r0 + i < a.Mm) p[int64_t(i) * a.ldc] = from[i * (LD * 4 / SIZE)];
     }
   }
 }
@@ -467,12 +468,12 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[CW]) {
   }
 }
 
-template <int BN, bool TRANS, bool COLVEC>
+template <int BN, bool TRANS, bool COLVEC, bool OUT32>
 __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_full,
                                             uint32_t acc_empty, uint32_t sc_full,
                                             uint32_t sc_empty, const WaitCtl& wc,
                                             uint32_t tmem_base, float* stage, const float* ring,
-                                            volatile int* last_flag) {
+                                            float* park) {
   using Cfg = Fp8TcConfig<BN>;
   constexpr int HC = Cfg::kHalf, CW = Cfg::kChunk;
   const WorkSpec& W = args.work;
@@ -490,8 +491,6 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
   uint32_t phases = 0, slot = 0, sph = 0;
   bool ok = true;
   const uint32_t tlane = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(wg * HC);
-  // After a wait gave up the units run on without waiting or storing, so that
-  // every warp still meets every barrier of the split tiles below.
   while (it.next(W, u)) {
     int32_t tm, tn;
     tile_coords(W, u.tile, tm, tn);
@@ -523,6 +522,7 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
       ok = __all_sync(0xffffffffu, wait_bounded(sc_full + 8 * slot, sph, wc, kSiteEpilogue));
       if (!ok) break;
       const float* sc = ring + slot * (SG * Cfg::kScaleFloats);
+      const uint32_t sc_at = smem_u32(sc + wg * HC);
       float rs[SG];
 #pragma unroll
       for (int j = 0; j < SG; ++j) {
@@ -534,7 +534,6 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
         if (!ok || kb + j >= u.kb1) break;
         const int i = j % NB, next = (j + 1) % NB;
         const bool more = kb + j + 1 < u.kb1;
-        const float2 rs2 = make_float2(rs[j], rs[j]);
         phases ^= 1u << i;
         bool ready = false;
         tmem_wait<CW>(v[0]);
@@ -555,17 +554,24 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
               }
             }
           }
+          if constexpr (COLVEC) {
+            const uint32_t cs = sc_at + uint32_t(j * Cfg::kScaleFloats + kBM + c * CW) * 4;
 #pragma unroll
-          for (int e = 0; e < CW / 2; ++e) {
-            const float2 p2 = make_float2(__uint_as_float(v[c & 1][2 * e]),
-                                          __uint_as_float(v[c & 1][2 * e + 1]));
-            if constexpr (COLVEC) {
-              const float2 cs = *reinterpret_cast<const float2*>(
-                  sc + j * Cfg::kScaleFloats + kBM + wg * HC + c * CW + 2 * e);
-              fma2(acc[c * (CW / 2) + e], mul2(cs, rs2), p2);
-            } else {
-              fma2(acc[c * (CW / 2) + e], rs2, p2);
+            for (int e = 0; e < CW / 4; ++e) {
+              const float4 s4 = lds4(cs + e * 16);
+              float2* d = acc + c * (CW / 2) + 2 * e;
+              const uint32_t* x = v[c & 1] + 4 * e;
+              fma2(d[0], make_float2(s4.x * rs[j], s4.y * rs[j]),
+                   make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])));
+              fma2(d[1], make_float2(s4.z * rs[j], s4.w * rs[j]),
+                   make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])));
             }
+          } else {
+#pragma unroll
+            for (int e = 0; e < CW / 2; ++e)
+              fma2(acc[c * (CW / 2) + e], make_float2(rs[j], rs[j]),
+                   make_float2(__uint_as_float(v[c & 1][2 * e]),
+                               __uint_as_float(v[c & 1][2 * e + 1])));
           }
           if (c + 1 < NC) tmem_wait<CW>(v[(c + 1) & 1]);
         }
@@ -579,60 +585,27 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
       }
     }
 
-    // Split tile: this CTA's fp32 partial goes to the workspace (128 rows x BN,
-    // float4 j of row r at j * 128 + r); the last CTA to arrive adds them all.
-    bool mine = true;
-    int32_t first = cta, last = cta;
-    const int32_t st = u.tile - W.dp_tiles;
-    const bool partial = unit_is_partial(W, u);
-    auto part_of = [&](int32_t p) {
-      return reinterpret_cast<float4*>(args.workspace) +
-             size_t(split_slot(W, p, st)) * (size_t(kBM) * BN / 4) + size_t(wg) * (HC / 4) * kBM +
-             row;
-    };
-    if (partial) {
-      float4* dst = part_of(cta);
-#pragma unroll
-      for (int j = 0; j < HC / 4; ++j)
-        __stcg(dst + j * kBM, make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x,
-                                          acc[2 * j + 1].y));
-      __threadfence();
-      f8_epi_sync();
-      split_contributors(W, st, first, last);
-      if (threadIdx.x == 32 * kF8RoleWarps) {
-        const int old = atomicAdd(args.tickets + st, 1);
-        *last_flag = (old == last - first) ? 1 : 0;
-        if (old == last - first) atomicExch(args.tickets + st, 0);  // for the next launch
-      }
-      f8_epi_sync();
-      mine = *last_flag != 0;
-      if (mine) __threadfence();
-    }
-    if (!mine || !ok) continue;
+    if (!ok) return;
     const float* bias = args.bias;
-    if (partial) {
-      // the sum of all partials replaces this CTA's own
+    if (BN <= 128 && W.csplit > 1) {
+      // The CTA's only unit: its MMAs have read the ring and every copy into it
+      // has landed, so the partial tile may take its place.  Columns are kept
+      // together for the transposed store, rows otherwise.
+      fence_proxy_async_smem();
 #pragma unroll
-      for (int c = 0; c < HC / 16; ++c) {
-        float4 tot[4];
-        const float4* src = part_of(first) + size_t(c) * 4 * kBM;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tot[j] = __ldcg(src + j * kBM);
-#pragma unroll 4
-        for (int32_t p = first + 1; p <= last; ++p) {
-          src = part_of(p) + size_t(c) * 4 * kBM;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 x = __ldcg(src + j * kBM);
-            tot[j].x += x.x; tot[j].y += x.y; tot[j].z += x.z; tot[j].w += x.w;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[c * 8 + 2 * j] = make_float2(tot[j].x, tot[j].y);
-          acc[c * 8 + 2 * j + 1] = make_float2(tot[j].z, tot[j].w);
+      for (int j = 0; j < HC / 4; ++j) {
+        const float4 x = make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+        const int c = wg * HC + 4 * j;
+        if constexpr (TRANS) {
+          park[(c + 0) * Cfg::kParkCol + row] = x.x;
+          park[(c + 1) * Cfg::kParkCol + row] = x.y;
+          park[(c + 2) * Cfg::kParkCol + row] = x.z;
+          park[(c + 3) * Cfg::kParkCol + row] = x.w;
+        } else {
+          *reinterpret_cast<float4*>(park + row * Cfg::kParkRow + c) = x;
         }
       }
+      return;
     }
     if (TRANS) {
       if (mm < args.Mm) {
@@ -643,16 +616,97 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
             store_typed(args.C, int64_t(nn0 + j) * args.ldc + mm,
                         (j & 1 ? acc[j / 2].y : acc[j / 2].x) + bv, args.out_dtype);
       }
-    } else if (args.out_dtype == GEMM_F32) {
-      f8_store_rows<HC, 4>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
     } else {
-      f8_store_rows<HC, 2>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
+      f8_store_rows<HC, OUT32 ? 4 : 2>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
     }
   }
 }
 
-// args.work counts 128 x BN tiles and CTAs.
-template <int BN, bool TRANS, bool COLVEC>
+// Four neighbouring outputs of a row of C, `valid` of them inside the matrix.
+__device__ __forceinline__ void f8_store4(const Fp8TcArgs& a, int64_t off, const float (&v)[4],
+                                          int valid) {
+  if (valid >= 4 && a.c_vec) {
+    if (a.out_dtype == GEMM_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.C) + off) =
+          make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint2 pk;
+      if (a.out_dtype == GEMM_F16) {
+        const __half2 x = __floats2half2_rn(v[0], v[1]), y = __floats2half2_rn(v[2], v[3]);
+        __builtin_memcpy(&pk.x, &x, 4);
+        __builtin_memcpy(&pk.y, &y, 4);
+      } else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(v[2], v[3]);
+        __builtin_memcpy(&pk.x, &x, 4);
+        __builtin_memcpy(&pk.y, &y, 4);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.C) + off) = pk;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < valid) store_typed(a.C, off + j, v[j], a.out_dtype);
+}
+
+// Cluster split, after every CTA of the cluster has parked its partial: the
+// tile's valid outputs, four neighbours at a time, are dealt to the cluster's
+// threads; each adds the partials in rank order and stores.  8 remote loads a
+// thread are in flight (one quad at a time cost 6 us of a 128 x 128 tile split
+// in two).
+template <int BN, bool TRANS, int SPLIT>
+__device__ __forceinline__ void f8_cluster_reduce(const Fp8TcArgs& a, uint32_t park) {
+  using Cfg = Fp8TcConfig<BN>;
+  constexpr int kThreads = 32 * kF8EpiWarps, U = 8 / SPLIT;
+  const int32_t tile = int32_t(blockIdx.x) / SPLIT;
+  const int rank = int(blockIdx.x) % SPLIT;
+  int32_t tm, tn;
+  tile_coords(a.work, tile, tm, tn);
+  const int rows = min(kBM, a.Mm - tm * kBM), cols = min(BN, a.Nm - tn * BN);
+  // quads run along C's rows: the tile's columns, or its rows when transposed
+  const int per = TRANS ? (rows + 3) / 4 : (cols + 3) / 4;
+  const int total = per * (TRANS ? cols : rows);
+  uint32_t peer[SPLIT];
+#pragma unroll
+  for (int r = 0; r < SPLIT; ++r) peer[r] = map_to_rank(park, uint32_t(r));
+  for (int i0 = rank * kThreads + int(threadIdx.x) - 32 * kF8RoleWarps; i0 < total;
+       i0 += U * SPLIT * kThreads) {
+    float4 x[U][SPLIT];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = min(i0 + k * SPLIT * kThreads, total - 1);
+      const int line = i / per, q = (i - line * per) * 4;
+      const uint32_t at = uint32_t(line * (TRANS ? Cfg::kParkCol : Cfg::kParkRow) + q) * 4;
+#pragma unroll
+      for (int r = 0; r < SPLIT; ++r) x[k][r] = ld_dsmem_f32x4(peer[r] + at);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * SPLIT * kThreads;
+      if (i >= total) break;
+      const int line = i / per, q = (i - line * per) * 4;
+      float v[4] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w};
+#pragma unroll
+      for (int r = 1; r < SPLIT; ++r) {
+        v[0] += x[k][r].x; v[1] += x[k][r].y; v[2] += x[k][r].z; v[3] += x[k][r].w;
+      }
+      // C row and first column in the problem's view
+      const int64_t crow = TRANS ? tn * BN + line : tm * kBM + line;
+      const int32_t c0 = TRANS ? tm * kBM + q : tn * BN + q;
+      const int valid = (TRANS ? a.Mm : a.Nm) - c0;
+      if (a.bias)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < valid) v[j] += __ldg(a.bias + c0 + j);
+      f8_store4(a, crow * a.ldc + c0, v, valid);
+    }
+  }
+}
+
+// args.work counts 128 x BN tiles and CTAs.  COLVEC: a scale per column, not per
+// 128; OUT32: fp32 output (the transposed store takes any type).
+template <int BN, bool TRANS, bool COLVEC, bool OUT32>
 __global__ void __launch_bounds__(kF8Threads, 1)
     fp8_tc_kernel(const __grid_constant__ Fp8Maps mA, const __grid_constant__ Fp8Maps mB,
                   const Fp8TcArgs args) {
@@ -676,7 +730,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint64_t* drain = sc_empty + Cfg::kScaleRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
 
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
@@ -695,7 +748,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
-    *last_flag = 0;
     fence_barrier_init();
     tma_prefetch_map(&mA.group);
     tma_prefetch_map(&mB.group);
@@ -714,9 +766,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint32_t filled = 0;
   if (warp >= kF8RoleWarps) {
     if (BN >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
-    f8_epilogue<BN, TRANS, COLVEC>(args, smem_u32(acc_full), smem_u32(acc_empty),
+    f8_epilogue<BN, TRANS, COLVEC, OUT32>(args, smem_u32(acc_full), smem_u32(acc_empty),
                                    smem_u32(sc_full), smem_u32(sc_empty), wc, tmem_base, stage,
-                                   ring, last_flag);
+                                   ring, reinterpret_cast<float*>(smem));
   } else {
     if (BN >= 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RoleRegs));
     if (warp == 0 && lane == 0) {
@@ -740,6 +792,16 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  }
+  if (BN <= 128 && args.work.csplit > 1) {
+    cluster_sync_all();  // every partial of the cluster is parked
+    if (warp >= kF8RoleWarps) {
+      const uint32_t park = smem_u32(smem);
+      if (args.work.csplit == 2) f8_cluster_reduce<BN, TRANS, 2>(args, park);
+      else if (args.work.csplit == 4) f8_cluster_reduce<BN, TRANS, 4>(args, park);
+      else f8_cluster_reduce<BN, TRANS, 8>(args, park);
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its partial
   }
 }
 
