@@ -675,17 +675,13 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
             uint32_t v0[16], v1[16];
             tmem_issue<16>(tlane + b * 128 + c * 16, v0);
             if (two) tmem_issue<16>(tlane + b * 128 + 64 + c * 16, v1);
-            tmem_wait<16>(v0);
+            tmem_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[c * 16 + j] =
-                  fmaf(__uint_as_float(v0[j]), w0 * bk[c * 16 + j], acc[c * 16 + j]);
+            for (int j = 0; j < 16; ++j) fma_tmem(acc[c * 16 + j], w0 * bk[c * 16 + j], v0[j]);
             if (two) {
-              tmem_wait<16>(v1);
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                acc[c * 16 + j] =
-                    fmaf(__uint_as_float(v1[j]), w1 * bk[cols + c * 16 + j], acc[c * 16 + j]);
+                fma_tmem(acc[c * 16 + j], w1 * bk[cols + c * 16 + j], v1[j]);
             }
           }
           tc_fence_before();

@@ -22,12 +22,13 @@
 //   warps 4-11         epilogue, two warpgroups of BN / 2 columns: TMEM ->
 //                      registers, acc += (sa sb) * P, and the buffer goes back.
 //                      A 128 x 256 tile keeps 128 fp32 sums a thread.
-// What bounds it: a buffer's round trip (512 cycles of MMA for 128 x 256 x 128,
-// its commit, 128 KB of TMEM reads and 32768 FMAs, the hand-back) against two
-// buffers of 256 columns, all the TMEM there is: 8192^3 takes 567 us (1939
-// TFLOP/s), 397 without the FMAs.  That round trip is why the tile belongs to
-// one SM: on CTA pairs (cta_group::2, 256 x 256) each hand-over crosses SMs,
-// and the same epilogue without the scale ring took 727 us against 656.
+// What bounds it: the epilogue.  A k-block of a 128 x 256 tile takes the tensor
+// pipe 512 cycles, its loads (48 KiB) about 750, and the epilogue's 256 issue
+// slots of FMAs a scheduler come on top of the hand-overs, as two buffers of 256
+// columns are all the TMEM there is: 8192^3 takes 484 us (2271 TFLOP/s), 394 with
+// an eighth of the FMAs, 452 without the stores.  The tile belongs to one SM
+// because on CTA pairs (cta_group::2, 256 x 256) each hand-over crosses SMs (727
+// against 656 us with the same, slower epilogue).
 // For skinny problems (TRANS: operands swapped, C stored transposed) the bound
 // is the stream of the weights.
 // Small problems split each tile's k-blocks over a cluster of 2, 4 or 8 CTAs,
@@ -143,12 +144,12 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
-// d += a * b, two lanes; as two scalar FMAs: the packed form needs register
-// pairs that the TMEM loads do not give (8192^3: 590 us packed, 571 scalar).
-__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
-  d.x = fmaf(a.x, b.x, d.x);
-  d.y = fmaf(a.y, b.y, d.y);
+// d += a * b with b straight from a TMEM load.  Volatile, so that it stays
+// behind the (volatile) wait for that load, which need not name the registers.
+__device__ __forceinline__ void fma_tmem(float& d, float a, uint32_t b) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "f"(a), "f"(__uint_as_float(b)));
 }
+
 // Four floats of shared memory, read here and not earlier: loads that the
 // compiler moves up cost the registers of the sums.
 __device__ __forceinline__ float4 lds4(uint32_t addr) {
@@ -364,7 +365,7 @@ __device__ __forceinline__ void f8_mma(const Fp8TcArgs& args, uint32_t sA, uint3
 // store a row's 64 bytes and an instruction 8 rows.  SIZE: bytes an element.
 // The bias is added in fp32 before the one rounding.
 template <int HC, int SIZE>
-__device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float2 (&acc)[HC / 2],
+__device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float (&acc)[HC],
                                               float* stage_w, int32_t mrow0, int lane,
                                               int32_t nn0) {
   constexpr int PER = 64 / SIZE;               // columns a pass
@@ -380,13 +381,12 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float2 (
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       if constexpr (SIZE == 4) {
-        const float2 x = acc[(c + j) / 2];
         const float b = a.bias && nn0 + c + j < a.Nm ? __ldg(a.bias + nn0 + c + j) : 0.f;
-        w[j] = __float_as_uint((j & 1 ? x.y : x.x) + b);
+        w[j] = __float_as_uint(acc[c + j] + b);
       } else {
         w[j] = 0;
         if (c + 2 * j < HC) {
-          float2 x = acc[(c + 2 * j) / 2];
+          float2 x = make_float2(acc[c + 2 * j], acc[c + 2 * j + 1]);
           if (a.bias) {
             const int32_t n = nn0 + c + 2 * j;
             if (n < a.Nm) x.x += __ldg(a.bias + n);
@@ -439,7 +439,7 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float2 (
 }
 
 // CW consecutive fp32 columns of this thread's TMEM lane; the registers may be
-// read after tmem_wait.
+// read, by volatile statements, after tmem_wait.
 template <int CW>
 __device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&r)[CW]) {
   if constexpr (CW == 32) {
@@ -456,16 +456,8 @@ __device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&r)[CW]) {
         : "memory");
   }
 }
-template <int CW>
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[CW]) {
-  if constexpr (CW == 32) {
-    tmem_wait_ld32(r);
-  } else {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-  }
+__device__ __forceinline__ void tmem_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 template <int BN, bool TRANS, bool COLVEC, bool OUT32>
@@ -497,30 +489,27 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
     const int32_t mrow0 = tm * kBM;
     const int32_t mm = mrow0 + row;
     const int32_t nn0 = tn * BN + wg * HC;
-    float2 acc[HC / 2];
+    float acc[HC];
 #pragma unroll
-    for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+    for (int j = 0; j < HC; ++j) acc[j] = 0.f;
     // kScaleGroup k-blocks a turn, unrolled, so that buffers and chunks are
-    // constants.  Chunk c + 1 of a buffer is loaded while chunk c is added, and
-    // so is chunk 0 of the next buffer if its product is there by then (asked
-    // for a chunk ahead, so the answer costs no wait).
+    // constants.  Chunk c + 1 of a buffer is loaded while chunk c is added.
+    // (Asking for the next buffer a chunk ahead, to load its first chunk early,
+    // was slower: 561 against 520 us at 8192^3, all else equal.)  After a wait gave up the loop
+    // runs on to its end on whatever it reads, each further wait returning at
+    // once; the tile is then not stored.
     constexpr int NC = HC / CW, NB = Cfg::kBuffers, SG = Cfg::kScaleGroup;
     static_assert(SG % NB == 0 && (NC == 1 || NC % 2 == 0), "constant buffers and chunks");
     uint32_t v[2][CW];
-    // true once buffer i's product is there; its first chunk is then on its way
+    // waits for buffer i's product and sends its first chunk on its way
     auto begin = [&](int i) {
-      if (!mbar_test(acc_full + 8 * i, (phases >> i) & 1))
-        ok = wait_bounded(acc_full + 8 * i, (phases >> i) & 1, wc, kSiteEpilogue);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        tc_fence_after();
-        tmem_issue<CW>(tlane + uint32_t(i * BN), v[0]);
-      }
+      ok &= wait_bounded(acc_full + 8 * i, (phases >> i) & 1, wc, kSiteEpilogue);
+      tc_fence_after();
+      tmem_issue<CW>(tlane + uint32_t(i * BN), v[0]);
     };
     begin(0);
-    for (int32_t kb = u.kb0; ok && kb < u.kb1; kb += SG) {
-      ok = __all_sync(0xffffffffu, wait_bounded(sc_full + 8 * slot, sph, wc, kSiteEpilogue));
-      if (!ok) break;
+    for (int32_t kb = u.kb0; kb < u.kb1; kb += SG) {
+      ok &= wait_bounded(sc_full + 8 * slot, sph, wc, kSiteEpilogue);
       const float* sc = ring + slot * (SG * Cfg::kScaleFloats);
       const uint32_t sc_at = smem_u32(sc + wg * HC);
       float rs[SG];
@@ -531,51 +520,38 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
       }
 #pragma unroll
       for (int j = 0; j < SG; ++j) {
-        if (!ok || kb + j >= u.kb1) break;
+        if (kb + j >= u.kb1) break;
         const int i = j % NB, next = (j + 1) % NB;
-        const bool more = kb + j + 1 < u.kb1;
         phases ^= 1u << i;
-        bool ready = false;
-        tmem_wait<CW>(v[0]);
+        tmem_wait();
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           if (c + 1 < NC) {
             tmem_issue<CW>(tlane + uint32_t(i * BN + (c + 1) * CW), v[(c + 1) & 1]);
-            if (c + 2 == NC && more) ready = mbar_test(acc_full + 8 * next, (phases >> next) & 1);
           } else {  // the buffer's last read is done: back to the MMA issuer
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty + 8 * i);
-            if (NC > 1 && more) {
-              ready = __all_sync(0xffffffffu, ready);
-              if (ready) {
-                tc_fence_after();
-                tmem_issue<CW>(tlane + uint32_t(next * BN), v[0]);
-              }
-            }
           }
+          float* d = acc + c * CW;
+          const uint32_t* x = v[c & 1];
           if constexpr (COLVEC) {
             const uint32_t cs = sc_at + uint32_t(j * Cfg::kScaleFloats + kBM + c * CW) * 4;
 #pragma unroll
-            for (int e = 0; e < CW / 4; ++e) {
-              const float4 s4 = lds4(cs + e * 16);
-              float2* d = acc + c * (CW / 2) + 2 * e;
-              const uint32_t* x = v[c & 1] + 4 * e;
-              fma2(d[0], make_float2(s4.x * rs[j], s4.y * rs[j]),
-                   make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])));
-              fma2(d[1], make_float2(s4.z * rs[j], s4.w * rs[j]),
-                   make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])));
+            for (int e = 0; e < CW; e += 4) {
+              const float4 s4 = lds4(cs + e * 4);
+              fma_tmem(d[e], s4.x * rs[j], x[e]);
+              fma_tmem(d[e + 1], s4.y * rs[j], x[e + 1]);
+              fma_tmem(d[e + 2], s4.z * rs[j], x[e + 2]);
+              fma_tmem(d[e + 3], s4.w * rs[j], x[e + 3]);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < CW / 2; ++e)
-              fma2(acc[c * (CW / 2) + e], make_float2(rs[j], rs[j]),
-                   make_float2(__uint_as_float(v[c & 1][2 * e]),
-                               __uint_as_float(v[c & 1][2 * e + 1])));
+            for (int e = 0; e < CW; ++e) fma_tmem(d[e], rs[j], x[e]);
           }
-          if (c + 1 < NC) tmem_wait<CW>(v[(c + 1) & 1]);
+          if (c + 1 < NC) tmem_wait();
         }
-        if (more && !ready) begin(next);
+        if (kb + j + 1 < u.kb1) begin(next);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(sc_empty + 8 * slot);
@@ -585,6 +561,7 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
       }
     }
 
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) return;
     const float* bias = args.bias;
     if (BN <= 128 && W.csplit > 1) {
@@ -594,7 +571,7 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
       fence_proxy_async_smem();
 #pragma unroll
       for (int j = 0; j < HC / 4; ++j) {
-        const float4 x = make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+        const float4 x = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
         const int c = wg * HC + 4 * j;
         if constexpr (TRANS) {
           park[(c + 0) * Cfg::kParkCol + row] = x.x;
@@ -614,7 +591,7 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
         for (int j = 0; j < HC; ++j)
           if (nn0 + j < args.Nm)
             store_typed(args.C, int64_t(nn0 + j) * args.ldc + mm,
-                        (j & 1 ? acc[j / 2].y : acc[j / 2].x) + bv, args.out_dtype);
+                        acc[j] + bv, args.out_dtype);
       }
     } else {
       f8_store_rows<HC, OUT32 ? 4 : 2>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
