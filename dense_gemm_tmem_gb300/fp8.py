@@ -17,14 +17,18 @@ from . import binding as B
 BLOCK = 128
 BLOCKS = {"row": B.GEMM_FP8_ROW, "col": B.GEMM_FP8_COL, "tile": B.GEMM_FP8_TILE}
 _BYTES = (torch.float8_e4m3fn, torch.uint8)
+_byref, _new = ctypes.byref, object.__new__
 
 
 def scale_shape(rows: int, cols: int, blocks: str):
     """Scales of a rows x cols matrix: one per block, the last ones ragged."""
-    if blocks not in BLOCKS:
-        raise ValueError("blocks must be 'row', 'col' or 'tile', got %r" % (blocks,))
-    rb, cb = -(-rows // BLOCK), -(-cols // BLOCK)
-    return {"row": (rows, cb), "col": (rb, cols), "tile": (rb, cb)}[blocks]
+    if blocks == "row":
+        return rows, (cols + 127) >> 7
+    if blocks == "tile":
+        return (rows + 127) >> 7, (cols + 127) >> 7
+    if blocks == "col":
+        return (rows + 127) >> 7, cols
+    raise ValueError("blocks must be 'row', 'col' or 'tile', got %r" % (blocks,))
 
 
 class Fp8Matrix:
@@ -71,41 +75,54 @@ class Fp8Matrix:
         else:
             self.desc = B.gemm_fp8_matrix_t(data.data_ptr(), ld, scale.data_ptr(), ss[0], ss[1],
                                             BLOCKS[blocks], 0)
-            self.ref = ctypes.byref(self.desc)
+            self.ref = _byref(self.desc)
 
     @staticmethod
     def empty(rows: int, cols: int, blocks: str, device) -> "Fp8Matrix":
         """Unwritten storage in one allocation: rows padded to 16 bytes; the
         scales of 1 x 128 blocks with those of one k-block next to each other
         (the order the product's threads read them in), others row-major."""
-        shape = scale_shape(rows, cols, blocks)
+        return Fp8Matrix._carve(rows, cols, (blocks,), device)[0]
+
+    @staticmethod
+    def _carve(rows, cols, kinds, device):
+        """One unwritten matrix per block shape, all in one allocation."""
         ld = (cols + 15) & -16
-        off = (rows * ld + 255) & -256
-        buf = torch.empty(off + 4 * shape[0] * shape[1], dtype=torch.uint8, device=device)
-        strides = (1, shape[0]) if blocks == "row" else (shape[1], 1)
-        m = Fp8Matrix.__new__(Fp8Matrix)
-        m._data = m._scale = None  # made when first asked for
-        m._buf, m._layout = buf, (ld, shape, strides, off)
-        m.blocks, m.device_index, m.shape = blocks, buf.get_device(), torch.Size((rows, cols))
-        ptr = buf.data_ptr()
-        m.desc = B.gemm_fp8_matrix_t(ptr, ld, ptr + off, strides[0], strides[1], BLOCKS[blocks], 0)
-        m.ref = ctypes.byref(m.desc)
-        return m
+        values = (rows * ld + 255) & -256
+        parts, total = [], 0
+        for blocks in kinds:
+            shape = scale_shape(rows, cols, blocks)
+            parts.append((blocks, shape, total))
+            total += values + ((4 * shape[0] * shape[1] + 255) & -256)
+        buf = torch.empty(total, dtype=torch.uint8, device=device)
+        ptr, index = buf.data_ptr(), buf.get_device()
+        out = []
+        for blocks, shape, at in parts:
+            m = _new(Fp8Matrix)
+            m._data = m._scale = None  # made when first asked for
+            strides = (1, shape[0]) if blocks == "row" else (shape[1], 1)
+            m._buf, m._layout = buf, (ld, shape, strides, at, at + values)
+            m.blocks, m.device_index, m.shape = blocks, index, (rows, cols)
+            m.desc = B.gemm_fp8_matrix_t(ptr + at, ld, ptr + at + values, strides[0], strides[1],
+                                         BLOCKS[blocks], 0)
+            m.ref = _byref(m.desc)
+            out.append(m)
+        return out
 
     @property
     def data(self) -> torch.Tensor:
         """The e4m3 values (uint8 if the matrix was made from bytes)."""
         if self._data is None:
-            self._data = self._buf.view(torch.float8_e4m3fn).as_strided(
-                self.shape, (self._layout[0], 1))
+            ld, _, _, at, _ = self._layout
+            self._data = self._buf.view(torch.float8_e4m3fn).as_strided(self.shape, (ld, 1), at)
         return self._data
 
     @property
     def scale(self) -> torch.Tensor:
         """The fp32 scales, one per block."""
         if self._scale is None:
-            _, shape, strides, off = self._layout
-            self._scale = self._buf.view(torch.float32).as_strided(shape, strides, off // 4)
+            _, shape, strides, _, at = self._layout
+            self._scale = self._buf.view(torch.float32).as_strided(shape, strides, at // 4)
         return self._scale
 
     def dequantize(self) -> torch.Tensor:

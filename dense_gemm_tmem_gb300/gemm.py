@@ -26,6 +26,7 @@ def problem_dims(A: torch.Tensor, Bm: torch.Tensor, a_major: int, b_major: int):
     return int(M), int(N), int(K)
 
 
+_BOTH = ("row", "col")
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _LAYOUTS = {}  # (a_major, b_major, in, out) -> gemm_layout_t, built once
@@ -168,15 +169,15 @@ class Gemm:
             raise ValueError("rows of x must be contiguous")
         if rows > 1 and sr < cols:
             raise ValueError("rows of x overlap")
-        both = blocks == "row+col"
-        out = Fp8Matrix.empty(rows, cols, "row" if both else blocks, self.device)
-        out2 = Fp8Matrix.empty(rows, cols, "col", self.device) if both else None
-        rc = self._lib.gemm_fp8_quantize(self.handle, rows, cols, x.data_ptr(), max(sr, cols),
-                                         code, out.ref, out2.ref if both else None,
+        kinds = _BOTH if blocks == "row+col" else (blocks,)
+        m = Fp8Matrix._carve(rows, cols, kinds, self.device)
+        rc = self._lib.gemm_fp8_quantize(self.handle, rows, cols, x.data_ptr(),
+                                         sr if sr > cols else cols, code, m[0].ref,
+                                         m[1].ref if len(m) == 2 else None,
                                          self._raw_stream(stream))
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_fp8_quantize")
-        return (out, out2) if both else out
+        return tuple(m) if len(m) == 2 else m[0]
 
     def fp8_run(self, A: Fp8Matrix, Bm: Fp8Matrix, C: torch.Tensor, bias=None, a_major=ROW,
                 b_major=ROW, stream=None) -> None:
@@ -184,15 +185,9 @@ class Gemm:
         float16, bfloat16 or float32, unit stride along its rows).  A is stored
         (M, K) row-major or (K, M) column-major, B (K, N) or (N, K); the blocks
         of each must run along K."""
-        if len(A.shape) != 2 or len(Bm.shape) != 2:
-            raise ValueError("A and B must be 2-D")
-        M, K = A.shape if a_major == ROW else A.shape[::-1]
-        Kb, N = Bm.shape if b_major == ROW else Bm.shape[::-1]
-        if K != Kb:
-            raise ValueError("inner dimensions differ: %d vs %d" % (K, Kb))
-        idx = self.device.index
-        if A.device_index != idx or Bm.device_index != idx or C.get_device() != idx:
-            raise ValueError("operands must be on the handle's device, %s" % self.device)
+        M, N, K = self._fp8_dims(A, Bm, a_major, b_major)
+        if C.get_device() != self.device.index:
+            raise ValueError("tensor on %s, handle on %s" % (C.device, self.device))
         code = _DT8.get(C.dtype)
         if code is None:
             raise TypeError("C must be float16, bfloat16 or float32, got %s" % C.dtype)
@@ -201,26 +196,45 @@ class Gemm:
         sr, sc = C.stride()
         if (N > 1 and sc != 1) or (M > 1 and sr < N):
             raise ValueError("rows of C must be contiguous and not overlap")
+        self._fp8_launch(M, N, K, A, Bm, bias, C, max(sr, N), a_major, b_major, code, stream)
+
+    def _fp8_dims(self, A, Bm, a_major, b_major):
+        """(M, N, K) of a product of two Fp8Matrix on this handle's device."""
+        sa, sb = A.shape, Bm.shape
+        if len(sa) != 2 or len(sb) != 2:
+            raise ValueError("A and B must be 2-D")
+        M, K = sa if a_major == ROW else (sa[1], sa[0])
+        Kb, N = sb if b_major == ROW else (sb[1], sb[0])
+        if K != Kb:
+            raise ValueError("inner dimensions differ: %d vs %d" % (K, Kb))
+        idx = self.device.index
+        if A.device_index != idx or Bm.device_index != idx:
+            raise ValueError("operands must be on the handle's device, %s" % self.device)
+        return M, N, K
+
+    def _fp8_launch(self, M, N, K, A, Bm, bias, C, ldc, a_major, b_major, code, stream):
         bias_ptr = None
         if bias is not None:
             if (bias.dtype != torch.float32 or tuple(bias.shape) != (N,)
                     or not bias.is_contiguous()):
                 raise ValueError("bias must be contiguous float32 of shape (N,)")
-            if bias.get_device() != idx:
+            if bias.get_device() != self.device.index:
                 raise ValueError("tensor on %s, handle on %s" % (bias.device, self.device))
             bias_ptr = bias.data_ptr()
         rc = self._lib.gemm_fp8_run(self.handle, M, N, K, A.ref, Bm.ref, bias_ptr, C.data_ptr(),
-                                    max(sr, N), a_major, b_major, code, self._raw_stream(stream))
+                                    ldc, a_major, b_major, code, self._raw_stream(stream))
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_fp8_run")
 
     def fp8_matmul(self, A: Fp8Matrix, Bm: Fp8Matrix, bias=None, a_major=ROW, b_major=ROW,
                    out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """A·B (+bias) as a new tensor (see fp8_run)."""
-        M = A.shape[0] if a_major == ROW else A.shape[1]
-        N = Bm.shape[1] if b_major == ROW else Bm.shape[0]
+        M, N, K = self._fp8_dims(A, Bm, a_major, b_major)
+        code = _DT8.get(out_dtype)
+        if code is None:
+            raise TypeError("out_dtype must be float16, bfloat16 or float32, got %s" % out_dtype)
         C = torch.empty((M, N), dtype=out_dtype, device=self.device)
-        self.fp8_run(A, Bm, C, bias, a_major, b_major, stream)
+        self._fp8_launch(M, N, K, A, Bm, bias, C, N, a_major, b_major, code, stream)
         return C
 
     def moe_fp8(self, x: torch.Tensor, router: torch.Tensor, gate: Fp8Matrix, up: Fp8Matrix,
