@@ -6,6 +6,7 @@ module raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 from . import build as _build
@@ -137,6 +138,23 @@ def load(build_if_missing: bool = True):
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+_native = None
+
+
+def native():
+    """The extension module (csrc/native.cpp), pointed at the loaded library."""
+    global _native
+    if _native is None:
+        lib = load()
+        spec = importlib.util.spec_from_file_location("_dgemm_native", _build.NATIVE)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.init(*(ctypes.cast(getattr(lib, f), c_void_p).value for f in (
+            "gemm_fp8_quantize", "gemm_fp8_run", "gemm_moe_fp8_workspace", "gemm_moe_fp8")))
+        _native = mod
+    return _native
 
 
 def layout(a_major=0, b_major=0, in_dtype=GEMM_F16, out_dtype=GEMM_F32) -> gemm_layout_t:

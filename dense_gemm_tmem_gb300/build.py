@@ -3,11 +3,15 @@
 Each translation unit is compiled for sm_103a only, in parallel, then linked
 with nvcc (static CUDA runtime; the driver is reached at run time through the
 runtime's entry-point query, so the library loads on a machine without a GPU).
+Beside it, _build/_dgemm_native.so: the tensor-facing calls (csrc/native.cpp)
+as a Python extension against the installed torch.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdgemm_gb300.so")
+NATIVE = os.path.join(OUT_DIR, "_dgemm_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "native.cpp")
 SOURCES = ["api.cu", "simt.cu", "simt_f16.cu", "selftest.cu", "noalloc.cu", "tc2.cu",
            "tc_n256.cu", "tc_n128.cu", "tc_small.cu", "tc_narrow.cu", "tc64.cu",
            "fp8_api.cu", "fp8_quant.cu", "fp8_simt.cu", "fp8_moe.cu", "fp8_tc.cu"]
@@ -39,11 +45,31 @@ def _inputs():
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target, files) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in files)
+
+
+def up_to_date() -> bool:
+    return (_newer(LIB, _inputs())
+            and _newer(NATIVE, _inputs()[-2:] + [NATIVE_SOURCE]))
+
+
+def _build_native():
+    """Compiles the Python extension with the host compiler."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    tmp = NATIVE + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], NATIVE_SOURCE, "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (cmd[0], r.stdout, r.stderr))
+    os.replace(tmp, NATIVE)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -63,8 +89,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        native = ex.submit(_build_native)
         objs = list(ex.map(compile_one, SOURCES))
+        native.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

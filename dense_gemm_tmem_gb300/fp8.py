@@ -8,8 +8,6 @@ and ``linear_backward`` are the three products of a linear layer on them, and
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import binding as B
@@ -17,7 +15,7 @@ from . import binding as B
 BLOCK = 128
 BLOCKS = {"row": B.GEMM_FP8_ROW, "col": B.GEMM_FP8_COL, "tile": B.GEMM_FP8_TILE}
 _BYTES = (torch.float8_e4m3fn, torch.uint8)
-_byref, _new = ctypes.byref, object.__new__
+_new = object.__new__
 
 
 def scale_shape(rows: int, cols: int, blocks: str):
@@ -38,8 +36,7 @@ class Fp8Matrix:
     need).  ``scale`` may have any strides.  The tensors are referenced, not
     copied; replacing them in place is seen by later calls."""
 
-    __slots__ = ("blocks", "desc", "ref", "device_index", "shape", "_data", "_scale", "_buf",
-                 "_layout")
+    __slots__ = ("data", "scale", "blocks", "kind")
 
     def __init__(self, data: torch.Tensor, scale: torch.Tensor, blocks: str):
         if data.dtype not in _BYTES:
@@ -47,83 +44,55 @@ class Fp8Matrix:
                             % data.dtype)
         if scale.dtype != torch.float32:
             raise TypeError("scale must be float32, got %s" % scale.dtype)
-        shape, st = data.shape, data.stride()
+        shape = data.shape
         if len(shape) not in (2, 3):
             raise ValueError("data must be 2-D, or 3-D with one matrix per expert")
         rows, cols = shape[-2:]
-        if cols > 1 and st[-1] != 1:
-            raise ValueError("rows of data must be contiguous")
-        ld = st[-2] if rows > 1 else max(st[-2], cols)
-        if ld < cols:
-            raise ValueError("rows of data overlap")
+        st = data.stride()
+        if (cols > 1 and st[-1] != 1) or (rows > 1 and st[-2] < cols):
+            raise ValueError("rows of data must be contiguous and not overlap")
         want = scale_shape(rows, cols, blocks)
         if len(shape) == 3:
             if blocks != "tile":
                 raise ValueError("expert weights have tile blocks")
             want = (shape[0],) + want
-        if tuple(scale.shape) != want:
+        if scale.shape != want:
             raise ValueError("scale has shape %s, expected %s" % (tuple(scale.shape), want))
-        dev = data.get_device()
-        if scale.get_device() != dev:
+        if scale.get_device() != data.get_device():
             raise ValueError("data on %s, scale on %s" % (data.device, scale.device))
-        self._data, self._scale, self.blocks, self.device_index = data, scale, blocks, dev
-        self.shape = shape
-        ss = scale.stride()
-        if len(shape) == 3:
-            self.desc = B.gemm_fp8_experts_t(data.data_ptr(), ld, st[0], scale.data_ptr(), *ss)
-            self.ref = None
-        else:
-            self.desc = B.gemm_fp8_matrix_t(data.data_ptr(), ld, scale.data_ptr(), ss[0], ss[1],
-                                            BLOCKS[blocks], 0)
-            self.ref = _byref(self.desc)
+        self.data, self.scale, self.blocks, self.kind = data, scale, blocks, BLOCKS[blocks]
 
     @staticmethod
     def empty(rows: int, cols: int, blocks: str, device) -> "Fp8Matrix":
-        """Unwritten storage in one allocation: rows padded to 16 bytes; the
-        scales of 1 x 128 blocks with those of one k-block next to each other
-        (the order the product's threads read them in), others row-major."""
-        return Fp8Matrix._carve(rows, cols, (blocks,), device)[0]
+        """Unwritten storage as fp8_quantize lays it: rows padded to 16 bytes;
+        the scales of 1 x 128 blocks with those of one k-block next to each
+        other (the order the product's threads read them in), others row-major."""
+        data = torch.empty((rows, (cols + 15) & -16), dtype=torch.float8_e4m3fn, device=device)
+        shape = scale_shape(rows, cols, blocks)
+        if blocks == "row":
+            scale = torch.empty(shape[::-1], dtype=torch.float32, device=device).t()
+        else:
+            scale = torch.empty(shape, dtype=torch.float32, device=device)
+        return Fp8Matrix(data[:, :cols], scale, blocks)
 
     @staticmethod
-    def _carve(rows, cols, kinds, device):
-        """One unwritten matrix per block shape, all in one allocation."""
-        ld = (cols + 15) & -16
-        values = (rows * ld + 255) & -256
-        parts, total = [], 0
-        for blocks in kinds:
-            shape = scale_shape(rows, cols, blocks)
-            parts.append((blocks, shape, total))
-            total += values + ((4 * shape[0] * shape[1] + 255) & -256)
-        buf = torch.empty(total, dtype=torch.uint8, device=device)
-        ptr, index = buf.data_ptr(), buf.get_device()
-        out = []
-        for blocks, shape, at in parts:
-            m = _new(Fp8Matrix)
-            m._data = m._scale = None  # made when first asked for
-            strides = (1, shape[0]) if blocks == "row" else (shape[1], 1)
-            m._buf, m._layout = buf, (ld, shape, strides, at, at + values)
-            m.blocks, m.device_index, m.shape = blocks, index, (rows, cols)
-            m.desc = B.gemm_fp8_matrix_t(ptr + at, ld, ptr + at + values, strides[0], strides[1],
-                                         BLOCKS[blocks], 0)
-            m.ref = _byref(m.desc)
-            out.append(m)
-        return out
+    def _wrap(data, scale, blocks):
+        """What the quantiser made, without checks."""
+        m = _new(Fp8Matrix)
+        m.data, m.scale, m.blocks, m.kind = data, scale, blocks, BLOCKS[blocks]
+        return m
 
     @property
-    def data(self) -> torch.Tensor:
-        """The e4m3 values (uint8 if the matrix was made from bytes)."""
-        if self._data is None:
-            ld, _, _, at, _ = self._layout
-            self._data = self._buf.view(torch.float8_e4m3fn).as_strided(self.shape, (ld, 1), at)
-        return self._data
+    def shape(self):
+        return self.data.shape
 
-    @property
-    def scale(self) -> torch.Tensor:
-        """The fp32 scales, one per block."""
-        if self._scale is None:
-            _, shape, strides, _, at = self._layout
-            self._scale = self._buf.view(torch.float32).as_strided(shape, strides, at // 4)
-        return self._scale
+    def desc(self) -> "B.gemm_fp8_matrix_t":
+        """The C-ABI's description of a 2-D matrix."""
+        rows, cols = self.data.shape
+        sr, sc = self.scale.stride()
+        ld = self.data.stride(0)
+        return B.gemm_fp8_matrix_t(self.data.data_ptr(), ld if rows > 1 else max(ld, cols),
+                                   self.scale.data_ptr(), sr, sc, self.kind, 0)
 
     def dequantize(self) -> torch.Tensor:
         """fp32 values, in plain torch (for checks and small matrices)."""

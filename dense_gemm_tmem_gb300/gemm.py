@@ -2,8 +2,6 @@
 the current CUDA stream.  PyTorch supplies device memory and streams only."""
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import binding as B
@@ -26,7 +24,8 @@ def problem_dims(A: torch.Tensor, Bm: torch.Tensor, a_major: int, b_major: int):
     return int(M), int(N), int(K)
 
 
-_BOTH = ("row", "col")
+_KINDS = {"row": (B.GEMM_FP8_ROW, -1), "col": (B.GEMM_FP8_COL, -1),
+          "tile": (B.GEMM_FP8_TILE, -1), "row+col": (B.GEMM_FP8_ROW, B.GEMM_FP8_COL)}
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _LAYOUTS = {}  # (a_major, b_major, in, out) -> gemm_layout_t, built once
@@ -49,8 +48,8 @@ class Gemm:
             dev = torch.device("cuda", 0)
         self.device = dev
         self.handle = B.gemm_create(dev.index)
-        self._lib = B.load()
-        self._run = self._lib.gemm_run  # argument types set once by the binding
+        self._native = B.native()
+        self._run = B.load().gemm_run  # argument types set once by the binding
 
     def close(self):
         if getattr(self, "handle", None):
@@ -156,28 +155,17 @@ class Gemm:
         """x (rows, cols; float16, bfloat16 or float32, unit stride along its
         rows) as an Fp8Matrix with "row", "col" or "tile" blocks, or, for
         "row+col", a pair of them from one pass over x."""
-        code = _DT8.get(x.dtype)
-        if code is None:
-            raise TypeError("x must be float16, bfloat16 or float32, got %s" % x.dtype)
-        if x.dim() != 2:
-            raise ValueError("x must be 2-D")
-        if x.get_device() != self.device.index:
-            raise ValueError("tensor on %s, handle on %s" % (x.device, self.device))
-        rows, cols = x.shape
-        sr, sc = x.stride()
-        if cols > 1 and sc != 1:
-            raise ValueError("rows of x must be contiguous")
-        if rows > 1 and sr < cols:
-            raise ValueError("rows of x overlap")
-        kinds = _BOTH if blocks == "row+col" else (blocks,)
-        m = Fp8Matrix._carve(rows, cols, kinds, self.device)
-        rc = self._lib.gemm_fp8_quantize(self.handle, rows, cols, x.data_ptr(),
-                                         sr if sr > cols else cols, code, m[0].ref,
-                                         m[1].ref if len(m) == 2 else None,
-                                         self._raw_stream(stream))
-        if rc != B.GEMM_OK:
-            raise B.GemmError(rc, "gemm_fp8_quantize")
-        return tuple(m) if len(m) == 2 else m[0]
+        kinds = _KINDS.get(blocks)
+        if kinds is None:
+            raise ValueError("blocks must be 'row', 'col', 'tile' or 'row+col', got %r"
+                             % (blocks,))
+        r = self._native.quantize(self.handle, self.device.index, x, kinds[0], kinds[1],
+                                  self._raw_stream(stream))
+        if r.__class__ is int:
+            raise B.GemmError(r, "gemm_fp8_quantize")
+        if len(r) == 4:
+            return Fp8Matrix._wrap(r[0], r[1], "row"), Fp8Matrix._wrap(r[2], r[3], "col")
+        return Fp8Matrix._wrap(r[0], r[1], blocks)
 
     def fp8_run(self, A: Fp8Matrix, Bm: Fp8Matrix, C: torch.Tensor, bias=None, a_major=ROW,
                 b_major=ROW, stream=None) -> None:
@@ -185,9 +173,16 @@ class Gemm:
         float16, bfloat16 or float32, unit stride along its rows).  A is stored
         (M, K) row-major or (K, M) column-major, B (K, N) or (N, K); the blocks
         of each must run along K."""
-        M, N, K = self._fp8_dims(A, Bm, a_major, b_major)
-        if C.get_device() != self.device.index:
-            raise ValueError("tensor on %s, handle on %s" % (C.device, self.device))
+        if len(A.shape) != 2 or len(Bm.shape) != 2:
+            raise ValueError("A and B must be 2-D")
+        M, K = A.shape if a_major == ROW else A.shape[::-1]
+        Kb, N = Bm.shape if b_major == ROW else Bm.shape[::-1]
+        if K != Kb:
+            raise ValueError("inner dimensions differ: %d vs %d" % (K, Kb))
+        idx = self.device.index
+        for t in (A.data, Bm.data, C) + ((bias,) if bias is not None else ()):
+            if t.get_device() != idx:
+                raise ValueError("tensor on %s, handle on %s" % (t.device, self.device))
         code = _DT8.get(C.dtype)
         if code is None:
             raise TypeError("C must be float16, bfloat16 or float32, got %s" % C.dtype)
@@ -196,45 +191,26 @@ class Gemm:
         sr, sc = C.stride()
         if (N > 1 and sc != 1) or (M > 1 and sr < N):
             raise ValueError("rows of C must be contiguous and not overlap")
-        self._fp8_launch(M, N, K, A, Bm, bias, C, max(sr, N), a_major, b_major, code, stream)
-
-    def _fp8_dims(self, A, Bm, a_major, b_major):
-        """(M, N, K) of a product of two Fp8Matrix on this handle's device."""
-        sa, sb = A.shape, Bm.shape
-        if len(sa) != 2 or len(sb) != 2:
-            raise ValueError("A and B must be 2-D")
-        M, K = sa if a_major == ROW else (sa[1], sa[0])
-        Kb, N = sb if b_major == ROW else (sb[1], sb[0])
-        if K != Kb:
-            raise ValueError("inner dimensions differ: %d vs %d" % (K, Kb))
-        idx = self.device.index
-        if A.device_index != idx or Bm.device_index != idx:
-            raise ValueError("operands must be on the handle's device, %s" % self.device)
-        return M, N, K
-
-    def _fp8_launch(self, M, N, K, A, Bm, bias, C, ldc, a_major, b_major, code, stream):
-        bias_ptr = None
-        if bias is not None:
-            if (bias.dtype != torch.float32 or tuple(bias.shape) != (N,)
-                    or not bias.is_contiguous()):
-                raise ValueError("bias must be contiguous float32 of shape (N,)")
-            if bias.get_device() != self.device.index:
-                raise ValueError("tensor on %s, handle on %s" % (bias.device, self.device))
-            bias_ptr = bias.data_ptr()
-        rc = self._lib.gemm_fp8_run(self.handle, M, N, K, A.ref, Bm.ref, bias_ptr, C.data_ptr(),
-                                    ldc, a_major, b_major, code, self._raw_stream(stream))
+        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,)
+                                 or not bias.is_contiguous()):
+            raise ValueError("bias must be contiguous float32 of shape (N,)")
+        rc = B.gemm_fp8_run(self.handle, M, N, K, A.desc(), Bm.desc(),
+                            bias.data_ptr() if bias is not None else None, C.data_ptr(),
+                            max(sr, N), a_major, b_major, code, self._raw_stream(stream))
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_fp8_run")
 
     def fp8_matmul(self, A: Fp8Matrix, Bm: Fp8Matrix, bias=None, a_major=ROW, b_major=ROW,
                    out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """A·B (+bias) as a new tensor (see fp8_run)."""
-        M, N, K = self._fp8_dims(A, Bm, a_major, b_major)
         code = _DT8.get(out_dtype)
         if code is None:
             raise TypeError("out_dtype must be float16, bfloat16 or float32, got %s" % out_dtype)
-        C = torch.empty((M, N), dtype=out_dtype, device=self.device)
-        self._fp8_launch(M, N, K, A, Bm, bias, C, N, a_major, b_major, code, stream)
+        C = self._native.matmul(self.handle, self.device.index, A.data, A.scale, A.kind, Bm.data,
+                                Bm.scale, Bm.kind, bias, a_major, b_major, code,
+                                self._raw_stream(stream))
+        if C.__class__ is int:
+            raise B.GemmError(C, "gemm_fp8_run")
         return C
 
     def moe_fp8(self, x: torch.Tensor, router: torch.Tensor, gate: Fp8Matrix, up: Fp8Matrix,
@@ -244,45 +220,11 @@ class Gemm:
         (experts, inner, hidden), down (experts, hidden, inner).  Returns out
         (tokens, hidden), ids (tokens, top_k) int32 and gates (tokens, top_k)
         float32; the arithmetic is that of gemm_moe_fp8."""
-        if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
-            raise ValueError("x must be (tokens, hidden), router (experts, hidden)")
-        T, H = x.shape
-        E = router.shape[0]
-        if len(gate.shape) != 3 or len(up.shape) != 3 or len(down.shape) != 3:
-            raise ValueError("gate, up and down must be (experts, rows, cols)")
-        I = gate.shape[1]
-        if (tuple(gate.shape) != (E, I, H) or tuple(up.shape) != (E, I, H)
-                or tuple(down.shape) != (E, H, I)):
-            raise ValueError("weights have shapes %s, %s and %s, expected gate and up (%d, inner, "
-                             "%d), down (%d, %d, inner)" % (tuple(gate.shape), tuple(up.shape),
-                                                            tuple(down.shape), E, H, E, H))
-        if x.dtype != router.dtype or x.dtype not in (torch.float16, torch.bfloat16):
-            raise TypeError("x and router: both float16 or both bfloat16")
-        if not 1 <= top_k <= E:
-            raise ValueError("top_k must be 1 ... %d, got %d" % (E, top_k))
-        idx = self.device.index
-        for d in (x.get_device(), router.get_device(), gate.device_index, up.device_index,
-                  down.device_index):
-            if d != idx:
-                raise ValueError("operands must be on the handle's device, %s" % self.device)
-        for t in (x, router):
-            if (H > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < H):
-                raise ValueError("rows of x and router must be contiguous")
-        out = torch.empty((T, H), dtype=x.dtype, device=self.device)
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=self.device)
-        gates = torch.empty((T, top_k), dtype=torch.float32, device=self.device)
-        L = B.gemm_moe_fp8_t(T, H, I, E, top_k, 1 if renormalize else 0, _DT8[x.dtype], 0,
-                             x.data_ptr(), max(x.stride(0), H), router.data_ptr(),
-                             max(router.stride(0), H), gate.desc, up.desc, down.desc,
-                             out.data_ptr(), H, ids.data_ptr(), gates.data_ptr())
-        rc, n = B.gemm_moe_fp8_workspace(self.handle, L)
-        if rc != B.GEMM_OK:
-            raise B.GemmError(rc, "gemm_moe_fp8_workspace")
-        s = self._raw_stream(stream)
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        r = self._native.moe(self.handle, self.device.index, x, router, gate.data, gate.scale,
+                             up.data, up.scale, down.data, down.scale, top_k,
+                             1 if renormalize else 0, self._raw_stream(stream))
+        if r.__class__ is int:
+            raise B.GemmError(r, "gemm_moe_fp8")
         if stream is not None:
-            ws.record_stream(stream)
-        rc = self._lib.gemm_moe_fp8(self.handle, ctypes.byref(L), ws.data_ptr(), n, s)
-        if rc != B.GEMM_OK:
-            raise B.GemmError(rc, "gemm_moe_fp8")
-        return out, ids, gates
+            r[3].record_stream(stream)  # the scratch, freed here in the current stream's order
+        return r[:3]

@@ -95,7 +95,7 @@ def test_quantize_leaves_padding_alone(g):
     x = torch.ones(5, 21, dtype=F32, device="cuda")
     data = torch.full((5, 32), 0x5a, dtype=torch.uint8, device="cuda")
     m = Fp8Matrix(data[:, :21], torch.empty(5, 1, device="cuda"), "row")
-    rc = B.gemm_fp8_quantize(g.handle, 5, 21, x.data_ptr(), 21, B.GEMM_F32, m.desc, None,
+    rc = B.gemm_fp8_quantize(g.handle, 5, 21, x.data_ptr(), 21, B.GEMM_F32, m.desc(), None,
                              torch.cuda.current_stream().cuda_stream)
     assert rc == B.GEMM_OK
     assert bool((data[:, 21:] == 0x5a).all()) and bool((data[:, :21] == 0x7e).all())
