@@ -250,7 +250,15 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
   return v;
 }
 
-// Waits (bounded) until all CTAs have arrived on a barrier's counter.
+// One thread arrives on a barrier's counter for its CTA, after a barrier among
+// the threads whose writes the arrival is to publish: the fence covers theirs too.
+__device__ __forceinline__ void grid_arrive(int* counter) {
+  __threadfence();
+  atomicAdd(counter, 1);
+}
+
+// Waits (bounded) until all CTAs have arrived on a barrier's counter.  A barrier
+// among the CTA's threads then hands what was acquired on to them.
 __device__ __forceinline__ bool grid_wait(const int* counter, const WaitCtl& wc) {
   const uint64_t t0 = globaltimer_ns();
   while (ld_acquire(counter) < int(gridDim.x)) {
@@ -414,7 +422,7 @@ __device__ __forceinline__ void moe_choose(const MoeArgs& a, MoeRoute& r, int32_
 // lists and the work ranges.
 __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r) {
   const gemm_moe_fp8_t& L = a.L;
-  const int32_t T = int32_t(L.tokens), E = int32_t(L.experts), k = L.top_k;
+  const int32_t T = int32_t(L.tokens), E = int32_t(L.experts);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int32_t t = warp; t < T; t += kMoeThreads / 32) {
     if (E <= 64) moe_choose<2>(a, r, t, lane);
@@ -447,35 +455,48 @@ __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r) {
   }
   __syncthreads();
   if (warp == 2 && lane < 2) moe_start(a, r, lane);
-  for (int32_t p = tid; p < T * k; p += kMoeThreads) {
+  __syncthreads();
+}
+
+// Who of an expert's tokens picked it as what: its readers' own (warps 4-11).
+__device__ __forceinline__ void moe_picks(const MoeArgs& a, MoeRoute& r) {
+  const int32_t T = int32_t(a.L.tokens), k = a.L.top_k;
+  for (int32_t p = int32_t(threadIdx.x) - 128; p < T * k; p += 256) {
     const int32_t t = p / k, e = r.ids[p];
     const int32_t at = r.off[e] + __popcll(r.mask[e] & ((1ull << t) - 1));
     r.pick[at] = uint16_t(p);
     r.token[at] = uint8_t(t);
   }
-  __syncthreads();
+  bar_sync(1, 256);
 }
 
-// Gates and ids: one warp per token, spread over the CTAs (warp 3, beside the
-// streaming).
-__device__ __forceinline__ void moe_gates(const MoeArgs& a, const MoeRoute& r, int lane) {
-  const gemm_moe_fp8_t& L = a.L;
-  const int32_t T = int32_t(L.tokens), E = int32_t(L.experts), k = L.top_k;
-  for (int32_t t = int32_t(blockIdx.x); t < T; t += int32_t(gridDim.x)) {
-    const float* l = a.logits + int64_t(t) * E;
-    const float top = __ldcg(l + r.ids[t * k]);
-    float sum = 0.f, mine = 0.f;
-    if (lane < k) mine = expf(__ldcg(l + r.ids[t * k + lane]) - top);
-    if (L.renormalize) {
-      sum = mine;
-    } else {
-      for (int32_t e = lane; e < E; e += 32) sum += expf(__ldcg(l + e) - top);
-    }
+// Token t's gates, choice j's in lane j (one warp): the exponentials of the chosen
+// logits over the sum of theirs, or of all.
+__device__ __forceinline__ float moe_gate(const MoeArgs& a, const MoeRoute& r, int32_t t,
+                                          int lane) {
+  const int32_t E = int32_t(a.L.experts), k = a.L.top_k;
+  const float* l = a.logits + int64_t(t) * E;
+  const float top = __ldcg(l + r.ids[t * k]);
+  const float mine = lane < k ? expf(__ldcg(l + r.ids[t * k + lane]) - top) : 0.f;
+  float sum = mine;
+  if (!a.L.renormalize) {
+    sum = 0.f;
+    for (int32_t e = lane; e < E; e += 32) sum += expf(__ldcg(l + e) - top);
+  }
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return mine / sum;
+}
+
+// Gates and ids, as the layer returns them: one warp per token, spread over the
+// CTAs (warp 3, beside the streaming).
+__device__ __forceinline__ void moe_gates(const MoeArgs& a, const MoeRoute& r, int lane) {
+  const int32_t k = a.L.top_k;
+  for (int32_t t = int32_t(blockIdx.x); t < int32_t(a.L.tokens); t += int32_t(gridDim.x)) {
+    const float gate = moe_gate(a, r, t, lane);
     if (lane < k) {
-      L.ids[t * k + lane] = r.ids[t * k + lane];
-      L.gates[t * k + lane] = mine / sum;
+      a.L.ids[t * k + lane] = r.ids[t * k + lane];
+      a.L.gates[t * k + lane] = gate;
     }
   }
 }
@@ -714,9 +735,8 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
       }
     }
     // this CTA's partials of the phase are written
-    __threadfence();
     bar_sync(2, 128);
-    if (threadIdx.x == 128) atomicAdd(a.counters + 1 + phase, 1);
+    if (threadIdx.x == 128) grid_arrive(a.counters + 1 + phase);
   }
 }
 
@@ -762,21 +782,22 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, u
         const int32_t blocks = whole ? g.kb : min(cap, g.kb1 - c0);
         if (content.advance(g, whole)) {
           const uint32_t buf = content.buf();
-          ok = wait_bounded(b_empty + 8 * buf, content.parity() ^ 1, wc, kSiteProducer);
           if (tid < blocks && phase == 1) {
             const MoeWork w1 = moe_work(a, r, 0);
             const int64_t tile = int64_t(r.index[g.expert]) * 2 * a.tiles_i + base + tid;
-            seg_counts[2 * tid] = w1.segments(tile);
-            seg_counts[2 * tid + 1] = w1.segments(tile + a.tiles_i);
+            int32_t* sc = seg_counts + (content.count & 1) * 32;
+            sc[2 * tid] = w1.segments(tile);
+            sc[2 * tid + 1] = w1.segments(tile + a.tiles_i);
           }
-          // the vote of all four warps, and seg_counts, for all
-          if (tid == 0) *flag = written || grid_wait(a.counters + 1, wc) ? 1 : 0;
+          // one thread waits for all: for the buffer and, once, for phase C; the
+          // flag alternates, as a slow thread may still read the last one
+          int* say = flag + (content.count & 1);
+          if (tid == 0)
+            *say = wait_bounded(b_empty + 8 * buf, content.parity() ^ 1, wc, kSiteProducer) &&
+                   (written || grid_wait(a.counters + 1, wc));
           bar_sync(3, 128);
-          if (!written) __threadfence();
           written = true;
-          if (!ok) *flag = 0;
-          bar_sync(3, 128);
-          ok = *flag != 0;
+          ok = *say != 0;
           if (!ok) break;
           uint8_t* dst = operand + buf * kMoeOperandBytes;
           float* bs = b_scale + buf * kMoeRows;
@@ -795,14 +816,15 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, u
             }
           } else {
             const int64_t ld = int64_t(a.tiles_i) * kBM, step = 2 * int64_t(picks) * ld;
+            const int32_t* sc = seg_counts + (content.count & 1) * 32;
 #pragma unroll 2
             for (int i = warp; i < blocks * g.n; i += 4) {
               const int kb = i / g.n, n = i - kb * g.n;
               const float* p = a.part1 + int64_t(pick[n]) * ld + (base + kb) * kFp8Block +
                                lane * 4;
-              const float4 gt = sum_segments(p, step, seg_counts[2 * kb]);
+              const float4 gt = sum_segments(p, step, sc[2 * kb]);
               const float4 up = sum_segments(p + int64_t(picks) * ld, step,
-                                             seg_counts[2 * kb + 1]);
+                                             sc[2 * kb + 1]);
               const float h[4] = {gt.x / (1.f + expf(-gt.x)) * up.x,
                                   gt.y / (1.f + expf(-gt.y)) * up.y,
                                   gt.z / (1.f + expf(-gt.z)) * up.z,
@@ -831,8 +853,9 @@ __device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r,
   const int32_t k = L.top_k, picks = int32_t(L.tokens) * k;
   const int64_t H = L.hidden, ld = int64_t(a.tiles_h) * kBM, step = int64_t(picks) * ld;
   const MoeWork w = moe_work(a, r, 1);
-  // A warp takes (token, 128 columns): lane j looks up choice j's gate and how
-  // many partials its tile has, then all lanes add 4 columns each.
+  // A warp takes (token, 128 columns): lane j works out choice j's gate and how
+  // many partials its tile has (the first item's before the barrier), then all
+  // lanes add 4 columns each.
   const int lane = threadIdx.x & 31;
   const int64_t items = L.tokens * a.tiles_h;
   int64_t i = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
@@ -842,10 +865,10 @@ __device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r,
     int32_t my_n = 0;
     if (lane < k && i < items)
       my_n = w.segments(int64_t(r.index[r.ids[t * k + lane]]) * a.tiles_h + tile);
+    const float my_gate = i < items ? moe_gate(a, r, t, lane) : 0.f;
     if (waiting && !arrived()) return;
     waiting = false;
     if (i >= items) return;
-    const float my_gate = lane < k ? __ldcg(L.gates + t * k + lane) : 0.f;
     const int64_t h = int64_t(tile) * kBM + lane * 4;
     const float* src = a.part2 + int64_t(t) * k * ld + h;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -875,11 +898,11 @@ struct MoeSmem {
   static constexpr int b_scale = route + int((sizeof(MoeRoute) + 15) / 16 * 16);
   static constexpr int scale_ring = b_scale + 2 * kMoeRows * 4;
   static constexpr int seg_counts = scale_ring + kMoeScaleRing * kMoeScaleGroup * 4;
-  static constexpr int red = seg_counts + 2 * 16 * 4;
+  static constexpr int red = seg_counts + 2 * 2 * 16 * 4;
   static constexpr int bars = red + 2 * 64 * 4;
   static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1;
   static constexpr int words = bars + kBars * 8;
-  static constexpr int bytes = 1024 + words + 32;
+  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier, builder's two
 };
 static_assert(MoeSmem::bytes <= 227 * 1024, "shared memory per CTA");
 static_assert(moe_cap(16) <= 16, "seg_counts");
@@ -940,23 +963,22 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   }
   if (warp >= 4) {
     moe_phase_a(a, reinterpret_cast<float*>(smem + MoeSmem::red), threadIdx.x - 128);
-    __threadfence();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   if (threadIdx.x == 0) {
-    atomicAdd(a.counters, 1);
+    grid_arrive(a.counters);
     words[2] = grid_wait(a.counters, wc) ? 1 : 0;
   }
   __syncthreads();
   const bool routed = words[2] != 0;
   uint32_t filled = 0;
   if (routed) {
-    __threadfence();
     moe_phase_b(a, r);
     const uint32_t ring = smem_u32(smem + MoeSmem::ring);
+    if (warp >= 4) moe_picks(a, r);
     if (warp >= 8) {
       moe_build(a, r, smem + MoeSmem::operand, b_scale, seg_counts, b_full, b_empty, words + 3,
                 wc);
@@ -988,7 +1010,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   moe_phase_e(a, r, [&]() {
     if (threadIdx.x == 0) words[2] = grid_wait(a.counters + 2, wc) ? 1 : 0;
     __syncthreads();
-    __threadfence();
     return words[2] != 0;
   });
   if (words[2] == 0) return;
