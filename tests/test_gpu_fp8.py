@@ -442,3 +442,103 @@ def test_refusals(g):
         g.moe_fp8(torch.zeros(65, H, dtype=F16, device="cuda"), router, W1, W3, W2, 1)
     assert e.value.code == B.GEMM_ERR_UNSUPPORTED
     g.status()
+
+
+# ------------------------------------------------- splits, chunks and time-outs --
+@pytest.mark.parametrize("split", [0, 2, 4, 8])
+@pytest.mark.parametrize("M,N,K", [(1, 130, 1100), (20, 300, 1024), (50, 257, 1300),
+                                   (100, 200, 2000), (150, 130, 1025)])
+def test_product_forced_cluster_splits(g, M, N, K, split):
+    """Every cluster size (and none) on ragged tiles, transposed and not."""
+    g.set_option(B.GEMM_OPT_CLUSTER_SPLIT, split)
+    try:
+        check_product(g, M, N, K, bias=True)
+        check_product(g, M, N, K, COL, ROW, b_tile=False, out=F16, ldc_pad=1)
+    finally:
+        g.set_option(B.GEMM_OPT_CLUSTER_SPLIT, -1)
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(2, 2304, 2200, 3, 2), (40, 1300, 700, 2, 1),
+                                       (64, 1100, 900, 1, 1), (50, 1200, 130, 2, 2),
+                                       (3, 256, 4500, 2, 1)])
+def test_moe_long_axes_in_pieces(g, T, H, I, E, k):
+    """More k-blocks than an operand buffer holds, at each of its widths."""
+    check_moe(g, T, H, I, E, k)
+
+
+def test_moe_scale_strides_and_unaligned_activations(g):
+    """Weight scales stored in another order, rows of x and the router that no
+    16-byte load can read."""
+    rng = np.random.default_rng(8)
+    T, H, I, E, k = 4, 300, 260, 6, 3
+    ws, vals = [], []
+    for s in ((I, H), (I, H), (H, I)):
+        m, v = expert_weights(rng, E, *s)
+        ws.append(Fp8Matrix(m.data, m.scale.permute(2, 1, 0).contiguous().permute(2, 1, 0), "tile"))
+        vals.append(v)
+    flat = normal(rng, T * (H + 1) + 1).to(BF16).cuda()
+    x = torch.as_strided(flat, (T, H), (H + 1, 1), 1)
+    rflat = (normal(rng, E * (H + 3) + 1) * H ** -0.5).to(BF16).cuda()
+    router = torch.as_strided(rflat, (E, H), (H + 3, 1), 1)
+    out, ids, gates = g.moe_fp8(x, router, *ws, k)
+    g.status()
+    ids = ids.cpu().numpy().astype(np.int64)
+    R.check_choice(R.host(x), R.host(router), ids)
+    want, slack, gv, e_g = R.moe(R.host(x), R.host(router), *vals, ids, True)
+    assert (np.abs(R.host(gates) - gv) <= e_g).all()
+    bound = slack + R.OUT_U[BF16] * (np.abs(want) + slack) + R.OUT_TINY[BF16]
+    assert (np.abs(R.host(out) - want) <= bound).all()
+
+
+def test_moe_other_stream(g):
+    rng = np.random.default_rng(6)
+    T, H, I, E, k = 6, 256, 128, 8, 2
+    (W1, _), (W3, _), (W2, _) = (expert_weights(rng, E, *s) for s in ((I, H), (I, H), (H, I)))
+    x, router = normal(rng, T, H).half().cuda(), normal(rng, E, H).half().cuda()
+    want = g.moe_fp8(x, router, W1, W3, W2, k)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = g.moe_fp8(x, router, W1, W3, W2, k, stream=s)
+    s.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_wait_limit_is_reported_and_the_handle_recovers():
+    """With a limit of a nanosecond the expert layer's grid barriers give up: the
+    launch ends, gemm_status says so, and the handle works again.  A product
+    either finishes right or is reported."""
+    h = Gemm(torch.device("cuda", 0))
+    rng = np.random.default_rng(12)
+    T, H, I, E, k = 16, 1024, 512, 16, 4
+    (W1, _), (W3, _), (W2, _) = (expert_weights(rng, E, *s) for s in ((I, H), (I, H), (H, I)))
+    x, router = normal(rng, T, H).half().cuda(), normal(rng, E, H).half().cuda()
+    want = h.moe_fp8(x, router, W1, W3, W2, k)
+    h.status()
+    s = torch.cuda.current_stream().cuda_stream
+    h.set_option(B.GEMM_OPT_WAIT_LIMIT_NS, 1)
+    h.moe_fp8(x, router, W1, W3, W2, k)
+    assert B.gemm_status(h.handle, s) == B.GEMM_ERR_DEVICE_TIMEOUT
+    A = h.fp8_quantize(normal(rng, 300, 2048).half().cuda(), "row")
+    W = h.fp8_quantize(normal(rng, 700, 2048).half().cuda(), "tile")
+    C = h.fp8_matmul(A, W, b_major=COL, out_dtype=F32)
+    rc = B.gemm_status(h.handle, s)
+    assert rc in (B.GEMM_OK, B.GEMM_ERR_DEVICE_TIMEOUT)
+    h.set_option(B.GEMM_OPT_WAIT_LIMIT_NS, -1)
+    again = h.fp8_matmul(A, W, b_major=COL, out_dtype=F32)
+    if rc == B.GEMM_OK:
+        assert torch.equal(C, again)
+    for a, b in zip(want, h.moe_fp8(x, router, W1, W3, W2, k)):
+        assert torch.equal(a, b)
+    h.status()
+    h.close()
+
+
+def test_example_trains_and_serves(capsys):
+    import os
+    import runpy
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "fp8_layers.py")
+    losses, off, drift = runpy.run_path(path)["main"](["--hidden", "256", "--steps", "12"])
+    # 8 bits keep about 4 % of an operand's elements' size as noise
+    assert losses[-1] < 0.1 * losses[0] and off < 0.3 and drift < 0.02
