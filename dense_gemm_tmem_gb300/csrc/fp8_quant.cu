@@ -11,8 +11,10 @@
 // from them.  What is left to keep short is the instruction count: 16-bit
 // elements stay packed and their maxima are taken two at a time as integers
 // (magnitudes order like their bits), and the divisions of a thread's 8 rows
-// are shared out among the 16 threads that need them.  8192 x 8192 bf16 both
-// ways: 53 us, 5.1 TB/s of the 6.8 a copy reaches here.
+// are shared out among the 16 threads that need them.  Four CTAs an SM for
+// 16-bit sources (8192 x 8192 bf16 both ways: 53 us with three, 48 with four,
+// 5.7 TB/s of the 6.8 a copy reaches here); for fp32 ones the tile's registers
+// allow two.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -134,7 +136,8 @@ struct QuantArgs {
 enum : int { kRow = 1, kCol = 2, kTile = 4 };
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 1 : 4)
+    quantize_kernel(const QuantArgs a) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int warp = threadIdx.x >> 5;
   const int32_t bi = int32_t(blockIdx.x / uint32_t(a.tiles_c));
