@@ -10,9 +10,9 @@ namespace dg {
 constexpr int kMaxTileN = 256;
 constexpr int kTicketCap = 16384;     // split tiles one launch may have
 // after the tickets: the two-SM kernel's tile counter and finished-pair count
-// and the expert layer's three barriers and its exits
+// and the expert layer's four barriers, its exits and its two piece counters
 constexpr int kMoeCounters = kTicketCap + 2;
-constexpr int kCounterInts = kMoeCounters + 4;
+constexpr int kCounterInts = kMoeCounters + 7;
 constexpr int kTmapCacheSize = 32;
 constexpr int64_t kMaxCoord = (int64_t(1) << 31) - 1024;  // TMA coordinates are int32
 

@@ -6,25 +6,35 @@
 // With few tokens the layer is the stream of the chosen experts' weights, each
 // byte used once per token that chose the expert, so the kernel is built around
 // that stream: one persistent CTA per SM (a cooperative launch), and the k-blocks
-// (128 rows x 128 k of one expert's matrix) of all chosen experts, laid end to
-// end, are cut into equal contiguous ranges, first for gate and up, then for
-// down.  The weights are the MMA's 128-row side, the expert's tokens (x̂ or ĥ, 16
-// to 64 rows) its columns; tensor cores because a weight then costs the same
-// for one token or sixteen, and the TMA ring keeps 128 KiB a CTA in flight.
+// (128 rows x 128 k of one expert's matrix) of all chosen experts are shared out
+// over the CTAs, first for gate and up, then for down: laid end to end and cut
+// into equal ranges when they are few, handed out in fixed pieces at run time when
+// they are many.  The weights are the MMA's 128-row side, the expert's tokens (x̂
+// or ĥ, 16 to 64 rows) its columns; tensor cores because a weight then costs the
+// same for one token or sixteen, and the TMA ring keeps 128 KiB a CTA in flight.
 //
 //   phase A  all workers: router logits, x̂                  -> barrier 1
-//   phase B  every CTA for itself: top-k, token lists, work ranges
-//   phase C  gate and up: fp32 partial sums of each range    -> barrier 2
-//   phase D  down: the same, ĥ formed from phase C's partials -> barrier 3
+//   phase B  every CTA for itself: top-k, token lists
+//   phase C  gate and up: fp32 partial sums of each part     -> barrier 2
+//            ĥ from those, each row once                     -> barrier 3
+//   phase D  down: as C                                      -> barrier 4
 //   phase E  out from phase D's partials and the gates
 //
 // Roles in C and D: warp 0 streams weights by TMA (it runs ahead into D: weights
 // need no barrier), warp 1 issues MMAs, warp 2 copies the weights' scales, warps
 // 4-7 read each k-block's product from TMEM and add it, scaled, into fp32
-// registers, warps 8-11 build the token operand in shared memory (swizzled as
-// the MMA reads it), one buffer ahead.  A tile cut between CTAs leaves one
-// partial per CTA; whoever reads it adds them in CTA order, so results do not
-// depend on timing.  Every wait is bounded.
+// registers, warps 8-11 copy the token operand into shared memory (swizzled as
+// the MMA reads it), one buffer ahead.  The producer draws the work up and hands
+// it to the other roles through a small ring.  A tile cut between CTAs leaves one
+// partial per part; whoever reads it adds them in their order along K, so results
+// do not depend on timing.  Every wait is bounded.
+//
+// Measured, weights from HBM: 32 tokens, 8 of 128 experts of 4096 x 1024: 235 us,
+// 6.0 TB/s, 88 % of a copy's rate, so HBM bounds it; one token, 8 of 64 of 2048 x
+// 1024: 28.7 us, of which 50 MB take 7.5: the rest is four grid barriers, code
+// fetched cold and each phase's first loads.  ĥ formed by every CTA for its own
+// tiles instead of once spares a barrier (28.5 us for the one token) but takes
+// 173 instead of 92 us for 64 tokens, 2 of 16 experts of 4096 x 2048.
 #include <algorithm>
 
 #include "context.h"
@@ -40,7 +50,21 @@ constexpr int kMoeOperandBytes = 32768;            // one token operand buffer: 
 constexpr int kMoeRows = kMoeOperandBytes / kFp8Block;
 constexpr int kMoeBuffers = 4;                     // TMEM accumulators, two of 64 columns each
 constexpr int kMoeScaleGroup = 8, kMoeScaleRing = 4;
-constexpr int kMoeMinUnits = 2;                    // fewest k-blocks of a CTA's range
+// A phase's k-blocks are cut into equal ranges of at least kMoeMinUnits (2 to 8
+// time alike, 16 cost 8 us at 512 k-blocks), unless there are kMoeDynamicPieces
+// pieces a CTA to hand out at run time: SMs get unequal shares of HBM, and whole
+// tiles leave one partial each.  Measured, pieces against ranges: 238 and 246 us
+// (32 tokens, 114 of 128 experts of 4096 x 1024), 86 and 92 (32 tokens, 63 of 64
+// of 2048 x 1024); with 2 or 3 pieces a CTA 63 and 58 (8 tokens, 10 of 16 of 4096
+// x 2048), 80 and 78 (4 tokens, 29 of 128 of 4096 x 1024).
+constexpr int kMoeMinUnits = 4;
+constexpr int kMoeDynamicPieces = 4;
+// A piece is a part of one tile or several tiles, of about as many k-blocks as
+// this (gate and up; down), and several only while kMoeRunPieces a CTA remain.
+// Parts of 16 instead of 32: 4 us of 250 more; pieces of 64 and 32 for down alike.
+constexpr int kMoePieceC = 32, kMoePieceD = 64;
+constexpr int kMoeRunC = 16, kMoeRunD = 32;
+constexpr int kMoeRunPieces = 6;
 
 // Rows of B (tokens) of an MMA, a power of two, and k-blocks of them that an
 // operand buffer holds.  Rows past the expert's tokens hold anything: they only
@@ -52,18 +76,28 @@ struct MoeMaps {
   CUtensorMap group, one;  // {128, rows, k-block, expert}, {K, rows, expert}
 };
 
+// How a phase's tiles are cut when they are handed out at run time: `chunks`
+// pieces of `chunk` k-blocks a tile, or up to `run` tiles of one expert a piece.
+struct MoePieces {
+  int32_t run, chunks, chunk;
+};
+
 struct MoeArgs {
   gemm_moe_fp8_t L;
   int32_t tiles_i, tiles_h, kb_h, kb_i;
   uint8_t* xq;      // tokens x kb_h * 128
   float* xs;        // tokens x kb_h
   float* logits;    // tokens x experts
+  uint8_t* hq;      // picks x kb_i * 128
+  float* hs;        // picks x kb_i
   float* part1;     // [segment][gate, up][pick][tiles_i * 128]
   float* part2;     // [segment][pick][tiles_h * 128]
-  int* counters;    // barriers 1-3 and exits; 0 at launch and again after it
+  int* counters;    // barriers 1-4, exits, C's and D's pieces; 0 at launch and after
   int* status;
   uint64_t wait_limit_ns;
   int32_t vec;      // x and router rows are 16-byte aligned
+  MoePieces pieces[2];
+  int32_t dynamic;  // 1: pieces are handed out at run time whatever their number
 };
 
 // What phase B leaves in shared memory.
@@ -76,36 +110,50 @@ struct MoeRoute {
   uint16_t pick[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];  // token * top_k + choice
   uint8_t token[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K];  // and its token
   int32_t active;
-  struct Start {            // where this CTA's range of a phase begins
-    int64_t left;           // its k-blocks
-    int32_t expert, rest;   // place among the chosen experts, tile within the expert
-    int32_t kb0, seg;       // first k-block; this CTA's place among the tile's
-  } start[2];
 };
 
-// One phase's work: `units` k-blocks cut into `ctas` equal ranges.
+// A quotient of non-negative numbers, in 32 bits where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if (((uint64_t(n) | uint64_t(d)) >> 32) == 0) return uint32_t(n) / uint32_t(d);
+  return n / d;
+}
+
+// One phase's work: k-blocks laid end to end in `ctas` equal ranges, or (dynamic)
+// pieces handed out by a counter.
 struct MoeWork {
-  int64_t units;
-  int32_t ctas, kb;
-  __device__ __forceinline__ MoeWork(int64_t tiles, int32_t kb_) {
-    kb = kb_;
-    units = tiles * kb;
-    const int64_t most = units / kMoeMinUnits;
+  int64_t blocks;   // k-blocks
+  int64_t total;    // pieces
+  int32_t per, kb;  // tiles of an expert, k-blocks of a tile
+  int32_t ctas;
+  const MoePieces& p;
+  bool dynamic;
+  int32_t run;      // tiles a piece
+  int32_t pieces;   // of an expert
+  __device__ __forceinline__ MoeWork(const MoeArgs& a, const MoeRoute& r, int32_t ph)
+      : p(a.pieces[ph]) {
+    kb = ph == 0 ? a.kb_h : a.kb_i;
+    per = ph == 0 ? 2 * a.tiles_i : a.tiles_h;
+    blocks = int64_t(r.active) * per * kb;
+    const int64_t most = blocks / kMoeMinUnits;
     ctas = int32_t(most < 1 ? 1 : most < int64_t(gridDim.x) ? most : int64_t(gridDim.x));
-  }
-  // A quotient of non-negative numbers, in 32 bits where they fit.
-  static __device__ __forceinline__ int64_t div(int64_t n, int64_t d) {
-    if (((uint64_t(n) | uint64_t(d)) >> 32) == 0) return uint32_t(n) / uint32_t(d);
-    return n / d;
+    const int64_t tiles = int64_t(r.active) * per;
+    dynamic = a.dynamic || tiles * p.chunks >= kMoeDynamicPieces * int64_t(gridDim.x);
+    run = 1;
+    if (p.run > 1)
+      run = int32_t(max(int64_t(1), min(int64_t(p.run),
+                                        quotient(tiles, kMoeRunPieces * gridDim.x))));
+    pieces = p.chunks > 1 ? per * p.chunks : (per + run - 1) / run;
+    total = int64_t(r.active) * pieces;
   }
   __device__ __forceinline__ int64_t begin(int32_t c) const {
-    return c >= ctas ? units : div(units * c, ctas);
+    return c >= ctas ? blocks : quotient(blocks * c, ctas);
   }
   __device__ __forceinline__ int32_t owner(int64_t x) const {
-    return int32_t(div((x + 1) * ctas - 1, units));
+    return int32_t(quotient((x + 1) * ctas - 1, blocks));
   }
-  // CTAs that work on a tile.
+  // Partials that a tile leaves.
   __device__ __forceinline__ int32_t segments(int64_t tile) const {
+    if (dynamic) return p.chunks;
     return owner((tile + 1) * kb - 1) - owner(tile * kb) + 1;
   }
 };
@@ -113,48 +161,76 @@ struct MoeWork {
 // A CTA's part of one tile.
 struct MoeSeg {
   int32_t phase;     // 0 gate and up, 1 down
-  int32_t expert, n; // and its tokens
+  int32_t expert, n; // and its tokens; n == 0: the phase is over
   int32_t which;     // 0 gate, 1 up, 2 down
   int32_t tile;      // 128-row tile of the matrix
   int32_t kb0, kb1, kb;
-  int32_t seg;       // this CTA's place among those that work on the tile
+  int32_t seg;       // which of the tile's partials
 };
 
-struct MoeIter {
+// A CTA's segments of a phase, one after the other (the producer's; the other
+// roles read them from its ring).
+struct MoeSource {
   const MoeArgs& a;
   const MoeRoute& r;
-  int64_t left;           // k-blocks left of this CTA's range
-  int32_t phase, kb;      // k-blocks of a tile
-  int32_t expert, rest;   // the next segment's: place among the chosen experts, tile within it
-  int32_t per, kb0, seg;  // tiles of an expert; first k-block; place among the tile's CTAs
-  __device__ __forceinline__ MoeIter(const MoeArgs& a_, const MoeRoute& r_) : a(a_), r(r_) {}
-  __device__ __forceinline__ void start(int32_t ph) {
-    phase = ph;
-    kb = ph == 0 ? a.kb_h : a.kb_i;
-    per = ph == 0 ? 2 * a.tiles_i : a.tiles_h;
-    const MoeRoute::Start& s = r.start[ph];
-    left = s.left;
-    expert = s.expert;
-    rest = s.rest;
-    kb0 = s.kb0;
-    seg = s.seg;
+  const MoeWork w;
+  const int32_t phase;
+  int64_t left = 0;           // static: k-blocks left of this CTA's range; dynamic: tiles
+                              // left of the piece
+  int32_t expert = 0, rest = 0, kb0 = 0, kb1 = 0, seg = 0;
+  int32_t ahead = 0;          // dynamic: the piece after this one
+  __device__ __forceinline__ MoeSource(const MoeArgs& a_, const MoeRoute& r_, int32_t ph)
+      : a(a_), r(r_), w(a_, r_, ph), phase(ph) {
+    if (w.dynamic) {
+      ahead = int32_t(blockIdx.x);  // the counter hands out the rest
+      return;
+    }
+    const int64_t x = w.begin(blockIdx.x);
+    left = w.begin(blockIdx.x + 1) - x;
+    if (left == 0) return;
+    const int64_t tile = quotient(x, w.kb);
+    expert = int32_t(quotient(tile, w.per));
+    rest = int32_t(tile - int64_t(expert) * w.per);
+    kb0 = int32_t(x - tile * w.kb);
+    // only a range's first tile can have begun in another CTA's range
+    if (kb0 > 0) seg = int32_t(blockIdx.x) - w.owner(tile * w.kb);
   }
-  // The next segment of this phase.
   __device__ __forceinline__ bool next(MoeSeg& s) {
+    if (w.dynamic && left == 0) {
+      const int64_t piece = ahead;
+      if (piece >= w.total) return false;
+      // asked for one piece early: the answer takes about a microsecond
+      ahead = int32_t(gridDim.x) + atomicAdd(a.counters + 5 + phase, 1);
+      expert = int32_t(quotient(piece, w.pieces));
+      const int32_t i = int32_t(piece - int64_t(expert) * w.pieces);
+      if (w.p.chunks > 1) {
+        rest = i / w.p.chunks;
+        seg = i - rest * w.p.chunks;
+        kb0 = seg * w.p.chunk;
+        kb1 = min(kb0 + w.p.chunk, w.kb);
+        left = 1;
+      } else {
+        rest = i * w.run;
+        seg = kb0 = 0;
+        kb1 = w.kb;
+        left = min(w.run, w.per - rest);
+      }
+    }
     if (left == 0) return false;
+    if (!w.dynamic) kb1 = left < w.kb - kb0 ? int32_t(kb0 + left) : w.kb;
     s.phase = phase;
-    s.kb = kb;
+    s.kb = w.kb;
     s.kb0 = kb0;
-    s.kb1 = left < kb - kb0 ? int32_t(kb0 + left) : kb;
+    s.kb1 = kb1;
     s.seg = seg;
     s.expert = r.act[expert];
     s.n = __popcll(r.mask[s.expert]);
     const int32_t second = phase == 0 && rest >= a.tiles_i;
     s.which = phase == 1 ? 2 : second;
     s.tile = second ? rest - a.tiles_i : rest;
-    left -= s.kb1 - kb0;
-    kb0 = seg = 0;
-    if (++rest == per) {
+    left -= w.dynamic ? 1 : kb1 - kb0;
+    if (!w.dynamic) kb0 = seg = 0;
+    if (++rest == w.per && !w.dynamic) {
       rest = 0;
       ++expert;
     }
@@ -162,28 +238,28 @@ struct MoeIter {
   }
 };
 
-__device__ __forceinline__ MoeWork moe_work(const MoeArgs& a, const MoeRoute& r, int32_t ph) {
-  return ph == 0 ? MoeWork(int64_t(r.active) * 2 * a.tiles_i, a.kb_h)
-                 : MoeWork(int64_t(r.active) * a.tiles_h, a.kb_i);
-}
-
-// This CTA's start of phase ph (one thread; the divisions of all roles).
-__device__ __noinline__ void moe_start(const MoeArgs& a, MoeRoute& r, int32_t ph) {
-  const MoeWork w = moe_work(a, r, ph);
-  MoeRoute::Start s = {};
-  const int64_t x = w.begin(blockIdx.x);
-  s.left = w.begin(blockIdx.x + 1) - x;
-  if (s.left > 0) {
-    const int32_t per = ph == 0 ? 2 * a.tiles_i : a.tiles_h;
-    const int64_t tile = w.div(x, w.kb);
-    s.expert = int32_t(w.div(tile, per));
-    s.rest = int32_t(tile - int64_t(s.expert) * per);
-    s.kb0 = int32_t(x - tile * w.kb);
-    // only a range's first tile can have begun in another CTA's range
-    if (s.kb0 > 0) s.seg = int32_t(blockIdx.x) - w.owner(tile * w.kb);
+// The ring of segments, from the producer to the warps of the other roles.
+constexpr int kMoeSegs = 4;
+constexpr int kMoeSegReaders = 1 + 1 + 4 + 4;  // warps: MMA, scales, accumulators, builders
+struct MoeRing {
+  const MoeSeg* slot;
+  uint32_t full, empty;
+  uint32_t d = 0, ph = 0;
+  // The next segment; false at the end of a phase, or (ok cleared) when the wait
+  // gave up.
+  __device__ __forceinline__ bool next(MoeSeg& s, const WaitCtl& wc, bool& ok) {
+    ok = __all_sync(0xffffffffu, ok && wait_bounded(full + 8 * d, ph, wc, kSiteEpilogue));
+    if (!ok) return false;
+    s = slot[d];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * d);
+    if (++d == kMoeSegs) {
+      d = 0;
+      ph ^= 1;
+    }
+    return s.n > 0;
   }
-  r.start[ph] = s;
-}
+};
 
 // The token operand's buffers as every role sees them: content is one expert's
 // rows for a range of k-blocks; a whole-K content serves every segment of the
@@ -454,7 +530,6 @@ __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r) {
     if (tid == 0) r.active = active;
   }
   __syncthreads();
-  if (warp == 2 && lane < 2) moe_start(a, r, lane);
   __syncthreads();
 }
 
@@ -504,16 +579,29 @@ __device__ __forceinline__ void moe_gates(const MoeArgs& a, const MoeRoute& r, i
 // --------------------------------------------------------------- phases C, D --
 __device__ __forceinline__ uint32_t moe_producer(const MoeArgs& a, const MoeRoute& r,
                                                  const MoeMaps& gate, const MoeMaps& up,
-                                                 const MoeMaps& down, uint32_t ring, uint32_t full,
+                                                 const MoeMaps& down, MoeSeg* segs,
+                                                 uint32_t seg_full, uint32_t seg_empty,
+                                                 uint32_t ring, uint32_t full,
                                                  uint32_t empty, const WaitCtl& wc) {
   uint32_t s = 0, ph = 0, filled = 0;
   const uint64_t policy = policy_evict_first();
-  MoeIter it(a, r);
+  uint32_t d = 0, dph = 0;
+  auto publish = [&](const MoeSeg& g) {
+    if (!wait_bounded(seg_empty + 8 * d, dph ^ 1, wc, kSiteProducer)) return false;
+    segs[d] = g;
+    mbar_arrive(seg_full + 8 * d);
+    if (++d == kMoeSegs) {
+      d = 0;
+      dph ^= 1;
+    }
+    return true;
+  };
   for (int phase = 0; phase < 2; ++phase) {
-    it.start(phase);
+    MoeSource source(a, r, phase);
+    const int32_t k_full = int32_t((phase == 0 ? a.L.hidden : a.L.inner) / kFp8Block);
     MoeSeg g;
-    while (it.next(g)) {
-      const int32_t k_full = int32_t((phase == 0 ? a.L.hidden : a.L.inner) / kFp8Block);
+    while (source.next(g)) {
+      if (!publish(g)) return filled;
       const MoeMaps* m = g.which == 0 ? &gate : g.which == 1 ? &up : &down;
       for (int32_t kb = g.kb0; kb < g.kb1; kb += 2) {
         if (!wait_bounded(empty + 8 * s, ph ^ 1, wc, kSiteProducer)) return filled;
@@ -533,21 +621,21 @@ __device__ __forceinline__ uint32_t moe_producer(const MoeArgs& a, const MoeRout
         }
       }
     }
+    g.n = 0;
+    if (!publish(g)) return filled;
   }
   return filled;
 }
 
 // The weights' scales (one per k-block of a tile): 8 at a time, one per lane.
-__device__ __forceinline__ void moe_scales(const MoeArgs& a, const MoeRoute& r, uint32_t ring,
+__device__ __forceinline__ void moe_scales(const MoeArgs& a, MoeRing segs, uint32_t ring,
                                            uint32_t sc_full, uint32_t sc_empty, int lane,
                                            const WaitCtl& wc) {
   uint32_t slot = 0, ph = 0;
   bool ok = true;
-  MoeIter it(a, r);
   for (int phase = 0; phase < 2 && ok; ++phase) {
-    it.start(phase);
     MoeSeg g;
-    while (ok && it.next(g)) {
+    while (segs.next(g, wc, ok)) {
       const gemm_fp8_experts_t& w = g.which == 0 ? a.L.gate : g.which == 1 ? a.L.up : a.L.down;
       const float* p = w.scale + g.expert * w.scale_stride_e + g.tile * w.scale_stride_r;
       for (int32_t kb = g.kb0; kb < g.kb1; kb += kMoeScaleGroup) {
@@ -568,7 +656,7 @@ __device__ __forceinline__ void moe_scales(const MoeArgs& a, const MoeRoute& r, 
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-__device__ __forceinline__ void moe_mma(const MoeArgs& a, const MoeRoute& r, uint32_t ring,
+__device__ __forceinline__ void moe_mma(MoeRing segs, uint32_t ring,
                                         uint32_t operand, uint32_t full, uint32_t empty,
                                         uint32_t acc_full, uint32_t acc_empty, uint32_t b_full,
                                         uint32_t b_empty, uint32_t drain, uint32_t tmem_base,
@@ -579,16 +667,14 @@ __device__ __forceinline__ void moe_mma(const MoeArgs& a, const MoeRoute& r, uin
   const uint64_t adesc0 = make_sdesc_sw128(ring, 16, 1024);
   const uint64_t bdesc0 = make_sdesc_sw128(operand, 16, 1024);
   MoeContent content;
-  MoeIter it(a, r);
   auto wait = [&](uint32_t bar, uint32_t parity, int site) {
     if (ok && !mbar_test(bar, parity)) ok = wait_bounded(bar, parity, wc, site);
     ok = __all_sync(0xffffffffu, ok);
     return ok;
   };
   for (int phase = 0; phase < 2 && ok; ++phase) {
-    it.start(phase);
     MoeSeg g;
-    while (ok && it.next(g)) {
+    while (segs.next(g, wc, ok)) {
       const int cols = 1 << moe_shift(g.n), cap = moe_cap(cols);
       const bool whole = g.kb <= cap;
       const uint32_t idesc = make_idesc_f16(kBM, cols, 0, 0);
@@ -642,7 +728,7 @@ __device__ __forceinline__ void moe_mma(const MoeArgs& a, const MoeRoute& r, uin
 }
 
 // Warps 4-7: thread `row` owns one weight row; sums of up to 64 tokens.
-__device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute& r,
+__device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute& r, MoeRing segs,
                                                const float* scale_ring, const float* b_scale,
                                                uint32_t acc_full, uint32_t acc_empty,
                                                uint32_t b_full, uint32_t b_empty, uint32_t sc_full,
@@ -655,16 +741,14 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
   bool ok = true;
   const int32_t picks = int32_t(a.L.tokens) * a.L.top_k;
   MoeContent content;
-  MoeIter it(a, r);
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (ok && !mbar_test(bar, parity)) ok = wait_bounded(bar, parity, wc, kSiteEpilogue);
     ok = __all_sync(0xffffffffu, ok);
     return ok;
   };
   for (int phase = 0; phase < 2; ++phase) {
-    it.start(phase);
     MoeSeg g;
-    while (ok && it.next(g)) {
+    while (segs.next(g, wc, ok)) {
       const int cols = 1 << moe_shift(g.n), cap = moe_cap(cols);
       const bool whole = g.kb <= cap;
       float acc[64];
@@ -736,7 +820,7 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
     }
     // this CTA's partials of the phase are written
     bar_sync(2, 128);
-    if (threadIdx.x == 128) grid_arrive(a.counters + 1 + phase);
+    if (threadIdx.x == 128) grid_arrive(a.counters + 1 + 2 * phase);
   }
 }
 
@@ -761,20 +845,73 @@ __device__ __forceinline__ float4 sum_segments(const float* p, int64_t step, int
   return s;
 }
 
-// Warps 8-11: the token operand.
-__device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, uint8_t* operand,
-                                          float* b_scale, int32_t* seg_counts, uint32_t b_full,
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// ĥ from phase C's partials, quantised, shared out over all CTAs: a warp takes a
+// row of 128 values (a pick's k-block), two at a time (warps 8-11).
+__device__ __forceinline__ void moe_rows(const MoeArgs& a, const MoeRoute& r, int warp, int lane) {
+  constexpr int kRows = 2;
+  const MoeWork w(a, r, 0);
+  const int64_t picks = a.L.tokens * a.L.top_k, rows = picks * a.kb_i;
+  const int64_t ld = int64_t(a.tiles_i) * kBM, to_up = picks * ld;
+  const int64_t step = 4 * int64_t(gridDim.x);
+  for (int64_t i0 = blockIdx.x + int64_t(warp) * gridDim.x; i0 < rows; i0 += step * kRows) {
+    float4 gt[kRows], up[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int64_t i = i0 + step * j;
+      if (i >= rows) break;
+      const int32_t pick = int32_t(quotient(i, a.kb_i)), kb = int32_t(i - int64_t(pick) * a.kb_i);
+      const float* p = a.part1 + pick * ld + kb * kFp8Block + lane * 4;
+      const int64_t tile = int64_t(r.index[r.ids[pick]]) * 2 * a.tiles_i + kb;
+      const int32_t n = w.segments(tile + (lane & 1) * a.tiles_i);
+      gt[j] = sum_segments(p, 2 * to_up, __shfl_sync(0xffffffffu, n, 0));
+      up[j] = sum_segments(p + to_up, 2 * to_up, __shfl_sync(0xffffffffu, n, 1));
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int64_t i = i0 + step * j;
+      if (i >= rows) break;
+      const float h[4] = {gt[j].x / (1.f + expf(-gt[j].x)) * up[j].x,
+                          gt[j].y / (1.f + expf(-gt[j].y)) * up[j].y,
+                          gt[j].z / (1.f + expf(-gt[j].z)) * up[j].z,
+                          gt[j].w / (1.f + expf(-gt[j].w)) * up[j].w};
+      float scale;
+      const uint32_t q = quant_block(h, scale);
+      __stcg(reinterpret_cast<uint32_t*>(a.hq + i * kFp8Block) + lane, q);
+      if (lane == 0) __stcg(a.hs + i, scale);
+    }
+  }
+}
+
+// Warps 8-11: ĥ between the phases, and the token operand.
+__device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, MoeRing segs,
+                                          uint8_t* operand, float* b_scale, uint32_t b_full,
                                           uint32_t b_empty, int* flag, const WaitCtl& wc) {
   const int tid = threadIdx.x - 256, warp = tid >> 5, lane = tid & 31;
-  const int32_t k = a.L.top_k, picks = int32_t(a.L.tokens) * k;
   bool ok = true;
   MoeContent content;
-  MoeIter it(a, r);
   for (int phase = 0; phase < 2 && ok; ++phase) {
-    it.start(phase);
-    bool written = phase == 0;  // phase D: whether all gate and up partials are
+    if (phase == 1) {  // also in a CTA without work in phase D
+      if (tid == 0) *flag = grid_wait(a.counters + 1, wc);
+      bar_sync(3, 128);
+      ok = *flag != 0;
+      if (!ok) break;
+      moe_rows(a, r, warp, lane);
+      bar_sync(3, 128);
+      if (tid == 0) {
+        grid_arrive(a.counters + 2);
+        *flag = grid_wait(a.counters + 2, wc);
+      }
+      bar_sync(3, 128);
+      ok = *flag != 0;
+    }
+    const uint8_t* rows_q = phase == 0 ? a.xq : a.hq;
+    const float* rows_s = phase == 0 ? a.xs : a.hs;
     MoeSeg g;
-    while (ok && it.next(g)) {
+    while (segs.next(g, wc, ok)) {
       const int cols = 1 << moe_shift(g.n), cap = moe_cap(cols);
       const bool whole = g.kb <= cap;
       for (int32_t c0 = g.kb0; ok && c0 < g.kb1; c0 += cap) {
@@ -782,60 +919,31 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, u
         const int32_t blocks = whole ? g.kb : min(cap, g.kb1 - c0);
         if (content.advance(g, whole)) {
           const uint32_t buf = content.buf();
-          if (tid < blocks && phase == 1) {
-            const MoeWork w1 = moe_work(a, r, 0);
-            const int64_t tile = int64_t(r.index[g.expert]) * 2 * a.tiles_i + base + tid;
-            int32_t* sc = seg_counts + (content.count & 1) * 32;
-            sc[2 * tid] = w1.segments(tile);
-            sc[2 * tid + 1] = w1.segments(tile + a.tiles_i);
-          }
-          // one thread waits for all: for the buffer and, once, for phase C; the
-          // flag alternates, as a slow thread may still read the last one
-          int* say = flag + (content.count & 1);
-          if (tid == 0)
-            *say = wait_bounded(b_empty + 8 * buf, content.parity() ^ 1, wc, kSiteProducer) &&
-                   (written || grid_wait(a.counters + 1, wc));
-          bar_sync(3, 128);
-          written = true;
-          ok = *say != 0;
+          ok = __all_sync(0xffffffffu, wait_bounded(b_empty + 8 * buf, content.parity() ^ 1, wc,
+                                                    kSiteProducer));
           if (!ok) break;
           uint8_t* dst = operand + buf * kMoeOperandBytes;
           float* bs = b_scale + buf * kMoeRows;
           const uint16_t* pick = r.pick + r.off[g.expert];
           const uint8_t* token = r.token + r.off[g.expert];
-          if (phase == 0) {
-            // 16-byte pieces of the real rows, a thread's own piece of every 16th
-            const int c = tid & 7;
-            for (int i = tid >> 3; i < blocks * g.n; i += 16) {
-              const int kb = i / g.n, n = i - kb * g.n;
-              const int64_t at = int64_t(token[n]) * a.kb_h + base + kb;
-              const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.xq + at * kFp8Block) + c);
-              *reinterpret_cast<uint4*>(dst + (kb * cols + n) * kFp8Block + ((c ^ (n & 7)) << 4)) =
-                  v;
-              if (c == 0) bs[kb * cols + n] = __ldcg(a.xs + at);
-            }
-          } else {
-            const int64_t ld = int64_t(a.tiles_i) * kBM, step = 2 * int64_t(picks) * ld;
-            const int32_t* sc = seg_counts + (content.count & 1) * 32;
-#pragma unroll 2
-            for (int i = warp; i < blocks * g.n; i += 4) {
-              const int kb = i / g.n, n = i - kb * g.n;
-              const float* p = a.part1 + int64_t(pick[n]) * ld + (base + kb) * kFp8Block +
-                               lane * 4;
-              const float4 gt = sum_segments(p, step, sc[2 * kb]);
-              const float4 up = sum_segments(p + int64_t(picks) * ld, step,
-                                             sc[2 * kb + 1]);
-              const float h[4] = {gt.x / (1.f + expf(-gt.x)) * up.x,
-                                  gt.y / (1.f + expf(-gt.y)) * up.y,
-                                  gt.z / (1.f + expf(-gt.z)) * up.z,
-                                  gt.w / (1.f + expf(-gt.w)) * up.w};
-              float scale;
-              const uint32_t q = quant_block(h, scale);
-              *reinterpret_cast<uint32_t*>(dst + (kb * cols + n) * kFp8Block +
-                                           (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = q;
-              if (lane == 0) bs[kb * cols + n] = scale;
-            }
+          const int32_t rows = blocks * g.n;
+          auto at = [&](int32_t i, int32_t& row) {  // row i of the content: its block in memory
+            const int32_t kb = i / g.n, n = i - kb * g.n;
+            row = kb * cols + n;
+            return int64_t(phase == 0 ? token[n] : pick[n]) * g.kb + base + kb;
+          };
+          // the real rows' 16-byte pieces, all in flight together
+          const int c = tid & 7;
+          int32_t row;
+          for (int32_t i = tid >> 3; i < rows; i += 16) {
+            const uint8_t* src = rows_q + at(i, row) * kFp8Block + c * 16;
+            cp_async16(smem_u32(dst + row * kFp8Block + ((c ^ (row & 7)) << 4)), src);
           }
+          for (int32_t i = tid; i < rows; i += 128) {
+            const float s = __ldcg(rows_s + at(i, row));
+            bs[row] = s;
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();  // the MMA reads the operand through the async proxy
           mbar_arrive(b_full + 8 * buf);
         }
@@ -852,7 +960,7 @@ __device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r,
   const gemm_moe_fp8_t& L = a.L;
   const int32_t k = L.top_k, picks = int32_t(L.tokens) * k;
   const int64_t H = L.hidden, ld = int64_t(a.tiles_h) * kBM, step = int64_t(picks) * ld;
-  const MoeWork w = moe_work(a, r, 1);
+  const MoeWork w(a, r, 1);
   // A warp takes (token, 128 columns): lane j works out choice j's gate and how
   // many partials its tile has (the first item's before the barrier), then all
   // lanes add 4 columns each.
@@ -861,7 +969,7 @@ __device__ __forceinline__ void moe_phase_e(const MoeArgs& a, const MoeRoute& r,
   int64_t i = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
   bool waiting = true;
   do {
-    const int32_t t = int32_t(w.div(i, a.tiles_h)), tile = int32_t(i - int64_t(t) * a.tiles_h);
+    const int32_t t = int32_t(quotient(i, a.tiles_h)), tile = int32_t(i - int64_t(t) * a.tiles_h);
     int32_t my_n = 0;
     if (lane < k && i < items)
       my_n = w.segments(int64_t(r.index[r.ids[t * k + lane]]) * a.tiles_h + tile);
@@ -897,15 +1005,15 @@ struct MoeSmem {
   static constexpr int route = operand + 2 * kMoeOperandBytes;
   static constexpr int b_scale = route + int((sizeof(MoeRoute) + 15) / 16 * 16);
   static constexpr int scale_ring = b_scale + 2 * kMoeRows * 4;
-  static constexpr int seg_counts = scale_ring + kMoeScaleRing * kMoeScaleGroup * 4;
-  static constexpr int red = seg_counts + 2 * 2 * 16 * 4;
-  static constexpr int bars = red + 2 * 64 * 4;
-  static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1;
+  static constexpr int red = scale_ring + kMoeScaleRing * kMoeScaleGroup * 4;
+  static constexpr int segs = red + 2 * 64 * 4;
+  static constexpr int bars = segs + int(sizeof(MoeSeg)) * kMoeSegs;
+  static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1 +
+                               2 * kMoeSegs;
   static constexpr int words = bars + kBars * 8;
-  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier, builder's two
+  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier, builder
 };
 static_assert(MoeSmem::bytes <= 227 * 1024, "shared memory per CTA");
-static_assert(moe_cap(16) <= 16, "seg_counts");
 
 __global__ void __launch_bounds__(kMoeThreads, 1)
     moe_kernel(const __grid_constant__ MoeMaps gate, const __grid_constant__ MoeMaps up,
@@ -916,7 +1024,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   MoeRoute& r = *reinterpret_cast<MoeRoute*>(smem + MoeSmem::route);
   float* b_scale = reinterpret_cast<float*>(smem + MoeSmem::b_scale);
   float* scale_ring = reinterpret_cast<float*>(smem + MoeSmem::scale_ring);
-  int32_t* seg_counts = reinterpret_cast<int32_t*>(smem + MoeSmem::seg_counts);
   const uint32_t full = smem_u32(smem + MoeSmem::bars);
   const uint32_t empty = full + 8 * kMoeStages;
   const uint32_t acc_full = empty + 8 * kMoeStages;
@@ -925,7 +1032,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   const uint32_t b_empty = b_full + 16;
   const uint32_t sc_full = b_empty + 16;
   const uint32_t sc_empty = sc_full + 8 * kMoeScaleRing;
-  const uint32_t drain = sc_empty + 8 * kMoeScaleRing;
+  const uint32_t seg_full = sc_empty + 8 * kMoeScaleRing;
+  const uint32_t seg_empty = seg_full + 8 * kMoeSegs;
+  const uint32_t drain = seg_empty + 8 * kMoeSegs;
+  MoeSeg* seg_slot = reinterpret_cast<MoeSeg*>(smem + MoeSmem::segs);
+  const MoeRing segs{seg_slot, seg_full, seg_empty};
   int* words = reinterpret_cast<int*>(smem + MoeSmem::words);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   volatile int* abort_flag = words + 1;
@@ -949,6 +1060,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     for (int i = 0; i < kMoeScaleRing; ++i) {
       mbar_init(sc_full + 8 * i, 32);
       mbar_init(sc_empty + 8 * i, 4);
+    }
+    for (int i = 0; i < kMoeSegs; ++i) {
+      mbar_init(seg_full + 8 * i, 1);
+      mbar_init(seg_empty + 8 * i, kMoeSegReaders);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -980,20 +1095,20 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const uint32_t ring = smem_u32(smem + MoeSmem::ring);
     if (warp >= 4) moe_picks(a, r);
     if (warp >= 8) {
-      moe_build(a, r, smem + MoeSmem::operand, b_scale, seg_counts, b_full, b_empty, words + 3,
-                wc);
+      moe_build(a, r, segs, smem + MoeSmem::operand, b_scale, b_full, b_empty, words + 3, wc);
     } else if (warp >= 4) {
-      moe_accumulate(a, r, scale_ring, b_scale, acc_full, acc_empty, b_full, b_empty, sc_full,
+      moe_accumulate(a, r, segs, scale_ring, b_scale, acc_full, acc_empty, b_full, b_empty, sc_full,
                      sc_empty, tmem_base, wc);
     } else if (warp == 3) {
       moe_gates(a, r, lane);
     } else if (warp == 2) {
-      moe_scales(a, r, smem_u32(scale_ring), sc_full, sc_empty, lane, wc);
+      moe_scales(a, segs, smem_u32(scale_ring), sc_full, sc_empty, lane, wc);
     } else if (warp == 1) {
-      moe_mma(a, r, ring, smem_u32(smem + MoeSmem::operand), full, empty, acc_full, acc_empty,
+      moe_mma(segs, ring, smem_u32(smem + MoeSmem::operand), full, empty, acc_full, acc_empty,
               b_full, b_empty, drain, tmem_base, wc);
     } else if (warp == 0 && lane == 0) {
-      filled = moe_producer(a, r, gate, up, down, ring, full, empty, wc);
+      filled = moe_producer(a, r, gate, up, down, seg_slot, seg_full, seg_empty, ring, full, empty,
+                            wc);
     }
   }
   // after an abort, copies may still be in flight: each stage's last one
@@ -1008,42 +1123,54 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   }
   if (!routed || *abort_flag) return;  // gemm_status clears the counters
   moe_phase_e(a, r, [&]() {
-    if (threadIdx.x == 0) words[2] = grid_wait(a.counters + 2, wc) ? 1 : 0;
+    if (threadIdx.x == 0) words[2] = grid_wait(a.counters + 3, wc) ? 1 : 0;
     __syncthreads();
     return words[2] != 0;
   });
   if (words[2] == 0) return;
   // the last CTA through the last barrier leaves the counters at 0
-  if (threadIdx.x == 0 && atomicAdd(a.counters + 3, 1) == int(gridDim.x) - 1) {
+  if (threadIdx.x == 0 && atomicAdd(a.counters + 4, 1) == int(gridDim.x) - 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) atomicExch(a.counters + i, 0);
+    for (int i = 0; i < 7; ++i) atomicExch(a.counters + i, 0);
   }
 }
 
 int64_t up256(int64_t b) { return (b + 255) & ~int64_t(255); }
 int64_t ceil128(int64_t n) { return (n + 127) / 128; }
 
-// Most CTAs that can work on one tile of `kb` k-blocks when at least `tiles`
-// tiles are shared out over at most `ctas` CTAs.
-int64_t most_segments(int64_t tiles, int64_t kb, int64_t ctas) {
+// Most partials that one tile of `kb` k-blocks can leave: in equal ranges, when at
+// least `tiles` tiles are shared out over at most `ctas` CTAs, or in pieces.
+int64_t most_segments(int64_t tiles, int64_t kb, int64_t ctas, int64_t piece) {
   const int64_t least = std::max<int64_t>(kMoeMinUnits, tiles * kb / ctas);
-  return std::min(kb, kb / least + 2);
+  const int64_t pieces = (kb + piece - 1) / piece;
+  return std::max(pieces, std::min(kb, kb / least + 2));
+}
+
+MoePieces pieces_of(int64_t kb, int64_t budget, int64_t run) {
+  MoePieces p{};
+  p.run = int32_t(kb < run ? run / kb : 1);
+  const int64_t chunks = (kb + budget - 1) / budget;
+  p.chunk = int32_t(((kb + chunks - 1) / chunks + 1) & ~int64_t(1));  // weights come in pairs
+  p.chunks = int32_t((kb + p.chunk - 1) / p.chunk);
+  return p;
 }
 
 struct MoeSpace {
-  int64_t xq, xs, logits, part1, part2;
+  int64_t xq, xs, logits, hq, hs, part1, part2;
   MoeSpace(const gemm_moe_fp8_t& L, int64_t ctas) {
     const int64_t T = L.tokens, P = T * L.top_k, kb_h = ceil128(L.hidden), kb_i = ceil128(L.inner);
     // a token's choices are different experts, so at least top_k are chosen
-    const int64_t s1 = most_segments(2 * L.top_k * kb_i, kb_h, ctas);
-    const int64_t s2 = most_segments(L.top_k * kb_h, kb_i, ctas);
+    const int64_t s1 = most_segments(2 * L.top_k * kb_i, kb_h, ctas, kMoePieceC);
+    const int64_t s2 = most_segments(L.top_k * kb_h, kb_i, ctas, kMoePieceD);
     xq = up256(T * kb_h * kFp8Block);
     xs = up256(T * kb_h * 4);
     logits = up256(T * L.experts * 4);
+    hq = up256(P * kb_i * kFp8Block);
+    hs = up256(P * kb_i * 4);
     part1 = up256(s1 * 2 * P * kb_i * kBM * 4);
     part2 = up256(s2 * P * kb_h * kBM * 4);
   }
-  int64_t bytes() const { return xq + xs + logits + part1 + part2; }
+  int64_t bytes() const { return xq + xs + logits + hq + hs + part1 + part2; }
 };
 
 bool encode_experts(MoeMaps* m, const gemm_fp8_experts_t& w, int64_t rows, int64_t K,
@@ -1092,13 +1219,18 @@ cudaError_t launch_moe(gemm_ctx* h, const gemm_moe_fp8_t& L, void* workspace,
   a.xq = w;
   a.xs = reinterpret_cast<float*>(w += space.xq);
   a.logits = reinterpret_cast<float*>(w += space.xs);
-  a.part1 = reinterpret_cast<float*>(w += space.logits);
+  a.hq = w += space.logits;
+  a.hs = reinterpret_cast<float*>(w += space.hq);
+  a.part1 = reinterpret_cast<float*>(w += space.hs);
   a.part2 = reinterpret_cast<float*>(w += space.part1);
   a.counters = h->tickets + kMoeCounters;
   a.status = h->status;
   a.wait_limit_ns = h->opt.wait_limit_ns;
   a.vec = ((reinterpret_cast<uintptr_t>(L.x) | reinterpret_cast<uintptr_t>(L.router)) & 15) == 0 &&
           L.ld_x % 8 == 0 && L.ld_router % 8 == 0;
+  a.pieces[0] = pieces_of(a.kb_h, kMoePieceC, kMoeRunC);
+  a.pieces[1] = pieces_of(a.kb_i, kMoePieceD, kMoeRunD);
+  a.dynamic = h->opt.dyn_sched > 0;
   MoeMaps gate, up, down;
   if (!encode_experts(&gate, L.gate, L.inner, L.hidden, L.experts) ||
       !encode_experts(&up, L.up, L.inner, L.hidden, L.experts) ||

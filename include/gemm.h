@@ -147,7 +147,8 @@ enum {
                                     pairs, ...), measured faster with raster groups of 16
                                     once operands come in two-k-block copies.  The split
                                     tail and the bias seeding always use the static
-                                    schedule. */
+                                    schedule.  The expert layer hands its work out at run
+                                    time by itself when there is much of it; 1: always. */
   GEMM_OPT_STAGES = 14,          /* one-SM tensor-core kernel: shared-memory ring stages.
                                     -1 (default) the picker's: all the ring holds, or, for a
                                     cluster split over more than half the SMs, as many as

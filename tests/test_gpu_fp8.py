@@ -466,6 +466,27 @@ def test_moe_long_axes_in_pieces(g, T, H, I, E, k):
     check_moe(g, T, H, I, E, k)
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 16, 16, 1, 1), (3, 1000, 700, 10, 3), (2, 2304, 2200, 3, 2),
+                                       (5, 8400, 130, 4, 2), (3, 256, 8500, 2, 1),
+                                       (64, 1100, 900, 3, 2), (64, 130, 100, 130, 16)])
+def test_moe_pieces_handed_out_at_run_time(g, T, H, I, E, k):
+    """Tiles cut into pieces and pieces of several tiles, forced on work that would
+    be cut into equal ranges; the same bits every time."""
+    g.set_option(B.GEMM_OPT_DYNAMIC_TILES, 1)
+    try:
+        first = check_moe(g, T, H, I, E, k)
+        for _ in range(3):
+            assert torch.equal(first, check_moe(g, T, H, I, E, k))
+    finally:
+        g.set_option(B.GEMM_OPT_DYNAMIC_TILES, -1)
+
+
+def test_moe_many_pieces(g):
+    """Enough work that pieces are handed out at run time in both phases."""
+    first = check_moe(g, 60, 1700, 1300, 64, 2)
+    assert torch.equal(first, check_moe(g, 60, 1700, 1300, 64, 2))
+
+
 def test_moe_scale_strides_and_unaligned_activations(g):
     """Weight scales stored in another order, rows of x and the router that no
     16-byte load can read."""
