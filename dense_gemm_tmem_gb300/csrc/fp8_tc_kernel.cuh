@@ -150,6 +150,20 @@ __device__ __forceinline__ void fma_tmem(float& d, float a, uint32_t b) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "f"(a), "f"(__uint_as_float(b)));
 }
 
+// (x a, y a), one instruction.  (A scale per column is a product per element on
+// top of the FMA: 106 us instead of 78 at 4096^3; 108 with scalar products.)
+__device__ __forceinline__ float2 mul2(float x, float y, float a) {
+  float2 r;
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%2, %3};\n\t"
+      "mov.b64 q, {%4, %4};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x), "f"(y), "f"(a));
+  return r;
+}
+
 // Four floats of shared memory, read here and not earlier: loads that the
 // compiler moves up cost the registers of the sums.
 __device__ __forceinline__ float4 lds4(uint32_t addr) {
@@ -540,10 +554,11 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
 #pragma unroll
             for (int e = 0; e < CW; e += 4) {
               const float4 s4 = lds4(cs + e * 4);
-              fma_tmem(d[e], s4.x * rs[j], x[e]);
-              fma_tmem(d[e + 1], s4.y * rs[j], x[e + 1]);
-              fma_tmem(d[e + 2], s4.z * rs[j], x[e + 2]);
-              fma_tmem(d[e + 3], s4.w * rs[j], x[e + 3]);
+              const float2 lo = mul2(s4.x, s4.y, rs[j]), hi = mul2(s4.z, s4.w, rs[j]);
+              fma_tmem(d[e], lo.x, x[e]);
+              fma_tmem(d[e + 1], lo.y, x[e + 1]);
+              fma_tmem(d[e + 2], hi.x, x[e + 2]);
+              fma_tmem(d[e + 3], hi.y, x[e + 3]);
             }
           } else {
 #pragma unroll
