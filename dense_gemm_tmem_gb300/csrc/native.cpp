@@ -8,6 +8,7 @@
 #include <ATen/ATen.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/gemm_fp8.h"
@@ -230,8 +231,8 @@ gemm_fp8_experts_t experts(PyObject* data, PyObject* scale, int64_t device, int6
 
 // moe(handle, device, x, router, gate data, scale, up data, scale, down data,
 // scale, top_k, renormalize, stream) -> (out, ids, gates) or a gemm_status_t.
-// The scratch is freed on return in the caching allocator's order, the current
-// stream's: `stream` is that stream, or the caller keeps the result until it ran.
+// `stream` is the current stream: the scratch is freed on return, in that stream's
+// order.
 PyObject* moe(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n != 13) fail(PyExc_TypeError, "moe takes 13 arguments");
@@ -251,11 +252,12 @@ PyObject* moe(PyObject*, PyObject* const* args, Py_ssize_t n) {
     L.experts = router.size(0);
     const at::Tensor& g = tensor(args[4], "gate must be a tensor");
     L.inner = g.dim() == 3 ? g.size(1) : 0;
-    L.top_k = int32_t(integer(args[10]));
+    const int64_t top_k = integer(args[10]);
+    if (top_k < 1 || top_k > L.experts)
+      fail(PyExc_ValueError, "top_k must be between 1 and the number of experts");
+    L.top_k = int32_t(std::min<int64_t>(top_k, INT32_MAX));
     L.renormalize = int32_t(integer(args[11]));
     L.dtype = code_of(x.scalar_type());
-    if (L.top_k < 1 || L.top_k > L.experts)
-      fail(PyExc_ValueError, "top_k must be between 1 and the number of experts");
     L.gate = experts(args[4], args[5], device, L.experts, L.inner, L.hidden);
     L.up = experts(args[6], args[7], device, L.experts, L.inner, L.hidden);
     L.down = experts(args[8], args[9], device, L.experts, L.hidden, L.inner);
@@ -278,12 +280,11 @@ PyObject* moe(PyObject*, PyObject* const* args, Py_ssize_t n) {
     L.gates = static_cast<float*>(gates.data_ptr());
     rc = moe_fn(h, &L, space.data_ptr(), bytes, address<void>(args[12]));
     if (rc != GEMM_OK) return PyLong_FromLong(rc);
-    PyObject* r = PyTuple_New(4);
+    PyObject* r = PyTuple_New(3);
     if (!r) throw Raised{};
     PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(out)));
     PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(ids)));
     PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(gates)));
-    PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(std::move(space)));
     return r;
   });
 }

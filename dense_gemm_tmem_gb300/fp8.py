@@ -9,6 +9,7 @@ and ``linear_backward`` are the three products of a linear layer on them, and
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -137,6 +138,7 @@ class _Linear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         dy = dy.contiguous()
         dx, dw = linear_backward(ctx.g, dy, ctx.saved)

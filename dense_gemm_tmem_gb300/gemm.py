@@ -154,13 +154,18 @@ class Gemm:
     def fp8_quantize(self, x: torch.Tensor, blocks: str = "row", stream=None):
         """x (rows, cols; float16, bfloat16 or float32, unit stride along its
         rows) as an Fp8Matrix with "row", "col" or "tile" blocks, or, for
-        "row+col", a pair of them from one pass over x."""
+        "row+col", a pair of them from one pass over x.  With a stream, here and
+        in fp8_matmul and moe_fp8, the tensors that the call makes are
+        allocated on it; order it after what wrote the inputs."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.fp8_quantize(x, blocks)
         kinds = _KINDS.get(blocks)
         if kinds is None:
             raise ValueError("blocks must be 'row', 'col', 'tile' or 'row+col', got %r"
                              % (blocks,))
         r = self._native.quantize(self.handle, self.device.index, x, kinds[0], kinds[1],
-                                  self._raw_stream(stream))
+                                  _current_raw(self.device.index))
         if r.__class__ is int:
             raise B.GemmError(r, "gemm_fp8_quantize")
         if len(r) == 4:
@@ -203,12 +208,15 @@ class Gemm:
     def fp8_matmul(self, A: Fp8Matrix, Bm: Fp8Matrix, bias=None, a_major=ROW, b_major=ROW,
                    out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """A·B (+bias) as a new tensor (see fp8_run)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.fp8_matmul(A, Bm, bias, a_major, b_major, out_dtype)
         code = _DT8.get(out_dtype)
         if code is None:
             raise TypeError("out_dtype must be float16, bfloat16 or float32, got %s" % out_dtype)
         C = self._native.matmul(self.handle, self.device.index, A.data, A.scale, A.kind, Bm.data,
                                 Bm.scale, Bm.kind, bias, a_major, b_major, code,
-                                self._raw_stream(stream))
+                                _current_raw(self.device.index))
         if C.__class__ is int:
             raise B.GemmError(C, "gemm_fp8_run")
         return C
@@ -220,11 +228,12 @@ class Gemm:
         (experts, inner, hidden), down (experts, hidden, inner).  Returns out
         (tokens, hidden), ids (tokens, top_k) int32 and gates (tokens, top_k)
         float32; the arithmetic is that of gemm_moe_fp8."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.moe_fp8(x, router, gate, up, down, top_k, renormalize)
         r = self._native.moe(self.handle, self.device.index, x, router, gate.data, gate.scale,
                              up.data, up.scale, down.data, down.scale, top_k,
-                             1 if renormalize else 0, self._raw_stream(stream))
+                             1 if renormalize else 0, _current_raw(self.device.index))
         if r.__class__ is int:
             raise B.GemmError(r, "gemm_moe_fp8")
-        if stream is not None:
-            r[3].record_stream(stream)  # the scratch, freed here in the current stream's order
-        return r[:3]
+        return r

@@ -525,6 +525,27 @@ def test_moe_other_stream(g):
         assert torch.equal(a, b)
 
 
+def test_temporaries_belong_to_the_call_s_stream(g):
+    """linear_backward on a busy stream: the quantised dy that it drops must not
+    be handed to the current stream's next tensors while that stream is behind."""
+    rng = np.random.default_rng(17)
+    x, w, dy = (normal(rng, *s).to(BF16).cuda() for s in ((256, 512), (384, 512), (256, 384)))
+    y, saved = fp8.linear_forward(g, x, w)
+    dx, dw = fp8.linear_backward(g, dy, saved)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = fp8.linear_backward(g, dy, saved, stream=s)
+        junk = [torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda")
+                for n in (256 * 384, 256 * 384 * 2, 4 * 256 * 3, 4 * 2 * 384) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+        del junk
+    g.status()
+
+
 def test_wait_limit_is_reported_and_the_handle_recovers():
     """With a limit of a nanosecond the expert layer's grid barriers give up: the
     launch ends, gemm_status says so, and the handle works again.  A product
