@@ -108,7 +108,9 @@ typedef struct {
  *     out[t] = sum_j gates[t][j] * (down_e · ĥ), ĥ = h quantised with ROW blocks,
  * products and sums in fp32, out rounded once to `dtype`.  gate and up are
  * inner x hidden, down is hidden x inner.
- * ids (tokens x top_k int32) and gates (tokens x top_k fp32) are outputs too. */
+ * ids (tokens x top_k int32) and gates (tokens x top_k fp32) are outputs too.
+ * The same call gives the same bits every time; with other tokens beside it a
+ * token's sums may be cut differently, which moves their last bits. */
 typedef struct {
   int64_t tokens, hidden, inner, experts;
   int32_t top_k;
