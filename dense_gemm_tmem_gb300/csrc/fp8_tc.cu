@@ -55,9 +55,25 @@ bool encode_fp8(Fp8Maps* m, const Fp8Operand& o, int64_t mn, int64_t K, int box_
   return encode(&m->group, 3, dims3, strides3, box3);
 }
 
+// Row-major C for the epilogue's TMA stores: boxes of 32 rows of 128 bytes,
+// 128-byte swizzle.  Only rows of whole 16-byte pieces: a store cut off by the
+// matrix's edge inside a piece writes the rest of it (seen: zeros past N).
+bool encode_c(CUtensorMap* map, const Fp8Product& p) {
+  EncodeTiledFn fn = encode_fn();
+  const int size = p.out_dtype == GEMM_F32 ? 4 : 2;
+  const cuuint64_t dims[2] = {cuuint64_t(p.N), cuuint64_t(p.M)};
+  const cuuint64_t pitch = cuuint64_t(p.ldc) * size;
+  const cuuint32_t box[2] = {cuuint32_t(128 / size), 32}, estr[2] = {1, 1};
+  if (!fn || pitch >= (cuuint64_t(1) << 40) || p.N * size % 16 != 0) return false;
+  return fn(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+            p.C, dims, &pitch, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN, bool TRANS, bool COLVEC, bool OUT32>
-cudaError_t launch_inst(const Fp8Maps& mA, const Fp8Maps& mB, const Fp8TcArgs& args, bool pdl,
-                        cudaStream_t stream) {
+cudaError_t launch_inst(const Fp8Maps& mA, const Fp8Maps& mB, const CUtensorMap& mC,
+                        const Fp8TcArgs& args, bool pdl, cudaStream_t stream) {
   auto kern = fp8_tc_kernel<BN, TRANS, COLVEC, OUT32>;
   constexpr int smem = Fp8TcConfig<BN>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -83,7 +99,7 @@ cudaError_t launch_inst(const Fp8Maps& mA, const Fp8Maps& mB, const Fp8TcArgs& a
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = unsigned(n);
-  return cudaLaunchKernelEx(&cfg, kern, mA, mB, args);
+  return cudaLaunchKernelEx(&cfg, kern, mA, mB, mC, args);
 }
 
 }  // namespace
@@ -163,10 +179,12 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
   const int group = bn == 256 ? Fp8TcConfig<256>::kGroup : Fp8TcConfig<128>::kGroup;
   if (!encode_fp8(&mA, opA, Mm, p.K, kBM, group) || !encode_fp8(&mB, opB, Nm, p.K, bn, group))
     return cudaErrorInvalidValue;
+  CUtensorMap mC{};
+  a.c_tma = bn == 256 && a.c_vec && encode_c(&mC, p);
   const bool pdl = h->opt.pdl != 0;
   const bool colvec = trans || opB.mn_shift == 0;
   const bool out32 = p.out_dtype == GEMM_F32;
-  auto launch = [&](auto inst) { return inst(mA, mB, a, pdl, stream); };
+  auto launch = [&](auto inst) { return inst(mA, mB, mC, a, pdl, stream); };
   if (trans) {
     if (bn == 32) return launch(launch_inst<32, true, true, false>);
     if (bn == 64) return launch(launch_inst<64, true, true, false>);

@@ -22,13 +22,17 @@
 //   warps 4-11         epilogue, two warpgroups of BN / 2 columns: TMEM ->
 //                      registers, acc += (sa sb) * P, and the buffer goes back.
 //                      A 128 x 256 tile keeps 128 fp32 sums a thread.
-// What bounds it: the epilogue.  A k-block of a 128 x 256 tile takes the tensor
-// pipe 512 cycles, its loads (48 KiB) about 750, and the epilogue's 256 issue
-// slots of FMAs a scheduler come on top of the hand-overs, as two buffers of 256
-// columns are all the TMEM there is: 8192^3 takes 484 us (2271 TFLOP/s), 394 with
-// an eighth of the FMAs, 452 without the stores.  The tile belongs to one SM
-// because on CTA pairs (cta_group::2, 256 x 256) each hand-over crosses SMs (727
-// against 656 us with the same, slower epilogue).
+//                      (C of 256-wide tiles leaves by TMA from staged boxes, so
+//                      that the next tile is summed meanwhile.)
+// What bounds it: nothing alone.  A k-block of a 128 x 256 tile takes the tensor
+// pipe 512 cycles, the epilogue 256 issue slots of FMAs a scheduler and as many
+// cycles of TMEM reads, and two buffers of 256 columns are all the TMEM there is
+// to overlap them: 1020 cycles a k-block, 8192^3 in 473 us (2322 TFLOP/s).  With
+// an eighth of the FMAs 396, a quarter of the MMAs 417, one TMEM read of eight
+// 451, a third of the loads 478 of the 487 it then was.  The tile belongs to one
+// SM because on CTA pairs (cta_group::2, 256 x 256) each hand-over crosses SMs
+// (727 against 656 us with the same, slower epilogue), and the loads that a pair
+// would save are not the bound.
 // For skinny problems (TRANS: operands swapped, C stored transposed) the bound
 // is the stream of the weights.
 // Small problems split each tile's k-blocks over a cluster of 2, 4 or 8 CTAs,
@@ -61,14 +65,17 @@ struct Fp8TcConfig {
   static constexpr int kABytes = kBM * kFp8Block;  // per k-block
   static constexpr int kBBytes = BN * kFp8Block;
   static constexpr int kStageBytes = kGroup * (kABytes + kBBytes);
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
+  // (a fourth stage of 256-wide tiles would take the room of the stores' boxes)
+  static constexpr int kStages = BN == 256 ? 3 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
   static constexpr int kBuffers = BN == 256 ? 2 : 4;      // TMEM accumulators
   static constexpr int kTmemCols = BN * kBuffers;         // a power of two >= 32
   static constexpr int kHalf = BN / 2;                    // columns per warpgroup
   // columns per TMEM load (two loads' registers beside 128 sums leave room for 16)
   static constexpr int kChunk = BN == 256 || kHalf < 32 ? 16 : 32;
   static constexpr int kStoreLd = 16 + 4;                 // staged store: 64 bytes a row, in floats
-  static constexpr int kEpiBytes = kF8EpiWarps * 32 * kStoreLd * 4;
+  // a warp's staging: rows of kStoreLd, or two boxes of 32 rows of 128 bytes
+  static constexpr int kWarpStage = BN == 256 ? 8192 : 32 * kStoreLd * 4;
+  static constexpr int kEpiBytes = kF8EpiWarps * kWarpStage;
   // scales of one k-block: the tile's rows, then its columns
   static constexpr int kScaleGroup = 4;  // k-blocks per ring slot
   static constexpr int kScaleRing = 2;
@@ -102,6 +109,7 @@ struct Fp8TcArgs {
   const float* bias;   // NULL or one per column of C
   int32_t out_dtype;
   int32_t c_vec;       // 1: C's base is 16-byte aligned, its pitch a multiple of 16 bytes
+  int32_t c_tma;       // 1: C leaves by TMA (256-wide tiles)
   int32_t a_mn, b_mn;  // 1: the operand is MN-major (b_mn: BN a multiple of 128)
   int32_t k_full;      // whole k-blocks of K
   int* status;
@@ -151,7 +159,8 @@ __device__ __forceinline__ void fma_tmem(float& d, float a, uint32_t b) {
 }
 
 // (x a, y a), one instruction.  (A scale per column is a product per element on
-// top of the FMA: 106 us instead of 78 at 4096^3; 108 with scalar products.)
+// top of the FMA: 105 us instead of 73 at 4096^3.  With scalar products 1 x 4096 x
+// 4096 takes 7.53 us instead of 7.41, a linear step of 4096^3 312 instead of 310.)
 __device__ __forceinline__ float2 mul2(float x, float y, float a) {
   float2 r;
   asm("{\n\t.reg .b64 p, q;\n\t"
@@ -452,6 +461,59 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float (&
   }
 }
 
+// The same by TMA, 128 bytes of the 32 rows (a swizzled box) at a time through two
+// boxes a warp: the stores drain while the next tile is summed (4096^3 73.2 against
+// 76.7 us with f8_store_rows, a linear step of three such products 317 against 327).
+// Outside the matrix nothing is stored.
+template <int HC, int SIZE>
+__device__ __forceinline__ void f8_store_tma(const Fp8TcArgs& a, const CUtensorMap* map,
+                                             const float (&acc)[HC], uint32_t stage,
+                                             int32_t mrow0, int lane, int32_t nn0) {
+  constexpr int PER = 128 / SIZE;              // columns a box
+  const bool f16 = a.out_dtype == GEMM_F16;
+#pragma unroll
+  for (int c = 0; c < HC; c += PER) {
+    if (mrow0 >= a.Mm || nn0 + c >= a.Nm) break;
+    if (lane == 0) {                           // the box's last store has been read
+      if (c == 0) bulk_wait_read_all();
+      else if (c >= 2 * PER) bulk_wait_read_1();
+    }
+    __syncwarp();
+    const uint32_t box = stage + uint32_t((c / PER) & 1) * 4096u, row = box + uint32_t(lane) * 128u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        constexpr int E = 4 / SIZE;            // elements a word
+        const int at = c + (4 * k + j) * E;
+        float x[2] = {acc[at], E == 2 ? acc[at + E - 1] : 0.f};
+        if (a.bias) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (nn0 + at + e < a.Nm) x[e] += __ldg(a.bias + nn0 + at + e);
+        }
+        if constexpr (SIZE == 4) {
+          w[j] = __float_as_uint(x[0]);
+        } else if (f16) {
+          const __half2 h = __floats2half2_rn(x[0], x[1]);
+          __builtin_memcpy(&w[j], &h, 4);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[0], x[1]);
+          __builtin_memcpy(&w[j], &h, 4);
+        }
+      }
+      st_shared_v4(row + uint32_t((k ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, box, nn0 + c, mrow0);
+      bulk_commit_group();
+    }
+  }
+}
+
 // CW consecutive fp32 columns of this thread's TMEM lane; the registers may be
 // read, by volatile statements, after tmem_wait.
 template <int CW>
@@ -475,7 +537,8 @@ __device__ __forceinline__ void tmem_wait() {
 }
 
 template <int BN, bool TRANS, bool COLVEC, bool OUT32>
-__device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_full,
+__device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, const CUtensorMap* tmC,
+                                            uint32_t acc_full,
                                             uint32_t acc_empty, uint32_t sc_full,
                                             uint32_t sc_empty, const WaitCtl& wc,
                                             uint32_t tmem_base, float* stage, const float* ring,
@@ -487,7 +550,7 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
   const int q = warp & 3;               // TMEM lane quarter this warp may access
   const int wg = (warp - kF8RoleWarps) >> 2;       // which half of the columns
   const int row = q * 32 + lane;
-  float* stage_w = stage + (warp - kF8RoleWarps) * 32 * Cfg::kStoreLd;
+  float* stage_w = stage + (warp - kF8RoleWarps) * (Cfg::kWarpStage / 4);
   WorkIter it;
   const int32_t cta = int32_t(blockIdx.x);
   it.init(W, cta);
@@ -507,19 +570,22 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
 #pragma unroll
     for (int j = 0; j < HC; ++j) acc[j] = 0.f;
     // kScaleGroup k-blocks a turn, unrolled, so that buffers and chunks are
-    // constants.  Chunk c + 1 of a buffer is loaded while chunk c is added.
+    // constants.  Chunk c + 1 of a buffer is loaded while chunk c is added (NV = 2),
+    // but not where 128 sums and one scale for all columns leave it to the other
+    // warp to fill the wait (8192^3 476 against 484 us).
     // (Asking for the next buffer a chunk ahead, to load its first chunk early,
     // was slower: 561 against 520 us at 8192^3, all else equal.)  After a wait gave up the loop
     // runs on to its end on whatever it reads, each further wait returning at
     // once; the tile is then not stored.
+    constexpr int NV = BN == 256 && !COLVEC ? 1 : 2;
     constexpr int NC = HC / CW, NB = Cfg::kBuffers, SG = Cfg::kScaleGroup;
     static_assert(SG % NB == 0 && (NC == 1 || NC % 2 == 0), "constant buffers and chunks");
-    uint32_t v[2][CW];
+    uint32_t v[NV][CW];
     // waits for buffer i's product and sends its first chunk on its way
     auto begin = [&](int i) {
       ok &= wait_bounded(acc_full + 8 * i, (phases >> i) & 1, wc, kSiteEpilogue);
       tc_fence_after();
-      tmem_issue<CW>(tlane + uint32_t(i * BN), v[0]);
+      if (NV == 2) tmem_issue<CW>(tlane + uint32_t(i * BN), v[0]);
     };
     begin(0);
     for (int32_t kb = u.kb0; kb < u.kb1; kb += SG) {
@@ -537,18 +603,22 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
         if (kb + j >= u.kb1) break;
         const int i = j % NB, next = (j + 1) % NB;
         phases ^= 1u << i;
-        tmem_wait();
+        if (NV == 2) tmem_wait();
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          if (c + 1 < NC) {
-            tmem_issue<CW>(tlane + uint32_t(i * BN + (c + 1) * CW), v[(c + 1) & 1]);
-          } else {  // the buffer's last read is done: back to the MMA issuer
+          if (NV == 1) {
+            tmem_issue<CW>(tlane + uint32_t(i * BN + c * CW), v[0]);
+            tmem_wait();
+          }
+          if (NV == 2 && c + 1 < NC) {
+            tmem_issue<CW>(tlane + uint32_t(i * BN + (c + 1) * CW), v[(c + 1) & (NV - 1)]);
+          } else if (c + 1 == NC) {  // the buffer's last read is done: back to the MMA issuer
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty + 8 * i);
           }
           float* d = acc + c * CW;
-          const uint32_t* x = v[c & 1];
+          const uint32_t* x = v[c & (NV - 1)];
           if constexpr (COLVEC) {
             const uint32_t cs = sc_at + uint32_t(j * Cfg::kScaleFloats + kBM + c * CW) * 4;
 #pragma unroll
@@ -564,7 +634,7 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
 #pragma unroll
             for (int e = 0; e < CW; ++e) fma_tmem(d[e], rs[j], x[e]);
           }
-          if (c + 1 < NC) tmem_wait();
+          if (NV == 2 && c + 1 < NC) tmem_wait();
         }
         if (kb + j + 1 < u.kb1) begin(next);
       }
@@ -577,7 +647,7 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
     }
 
     ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return;
+    if (!ok) break;
     const float* bias = args.bias;
     if (BN <= 128 && W.csplit > 1) {
       // The CTA's only unit: its MMAs have read the ring and every copy into it
@@ -608,10 +678,15 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, uint32_t acc_
             store_typed(args.C, int64_t(nn0 + j) * args.ldc + mm,
                         acc[j] + bv, args.out_dtype);
       }
+    } else if (BN == 256 && args.c_tma) {
+      f8_store_tma<HC, OUT32 ? 4 : 2>(args, tmC, acc, smem_u32(stage_w), mrow0 + q * 32, lane,
+                                      nn0);
     } else {
       f8_store_rows<HC, OUT32 ? 4 : 2>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
     }
   }
+  // every store this warp issued has landed before the CTA moves on
+  if (BN == 256 && lane == 0) bulk_wait_all();
 }
 
 // Four neighbouring outputs of a row of C, `valid` of them inside the matrix.
@@ -701,7 +776,7 @@ __device__ __forceinline__ void f8_cluster_reduce(const Fp8TcArgs& a, uint32_t p
 template <int BN, bool TRANS, bool COLVEC, bool OUT32>
 __global__ void __launch_bounds__(kF8Threads, 1)
     fp8_tc_kernel(const __grid_constant__ Fp8Maps mA, const __grid_constant__ Fp8Maps mB,
-                  const Fp8TcArgs args) {
+                  const __grid_constant__ CUtensorMap tmC, const Fp8TcArgs args) {
   using Cfg = Fp8TcConfig<BN>;
   constexpr int S = Cfg::kStages, NB = Cfg::kBuffers;
   extern __shared__ uint8_t smem_raw[];
@@ -758,7 +833,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint32_t filled = 0;
   if (warp >= kF8RoleWarps) {
     if (BN >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
-    f8_epilogue<BN, TRANS, COLVEC, OUT32>(args, smem_u32(acc_full), smem_u32(acc_empty),
+    f8_epilogue<BN, TRANS, COLVEC, OUT32>(args, &tmC, smem_u32(acc_full), smem_u32(acc_empty),
                                    smem_u32(sc_full), smem_u32(sc_empty), wc, tmem_base, stage,
                                    ring, reinterpret_cast<float*>(smem));
   } else {

@@ -458,6 +458,15 @@ def test_product_forced_cluster_splits(g, M, N, K, split):
         g.set_option(B.GEMM_OPT_CLUSTER_SPLIT, -1)
 
 
+@pytest.mark.parametrize("out,pad", [(F16, 0), (BF16, 4), (F32, 0), (F32, 4), (F16, 3), (F32, 1)])
+@pytest.mark.parametrize("am,bm,b_tile", [(ROW, COL, True), (COL, ROW, False)])
+@pytest.mark.parametrize("M,N,K", [(2600, 2100, 300), (1281, 5000, 516), (2500, 2136, 257)])
+def test_product_wide_tiles(g, M, N, K, am, bm, b_tile, out, pad):
+    """More 256-wide tiles than SMs, ragged on both edges, with C whose rows the
+    TMA can store and C whose rows it cannot; bytes past N stay."""
+    check_product(g, M, N, K, am, bm, b_tile=b_tile, out=out, bias=pad > 0, ldc_pad=pad)
+
+
 @pytest.mark.parametrize("T,H,I,E,k", [(2, 2304, 2200, 3, 2), (40, 1300, 700, 2, 1),
                                        (64, 1100, 900, 1, 1), (50, 1200, 130, 2, 2),
                                        (3, 256, 4500, 2, 1)])
