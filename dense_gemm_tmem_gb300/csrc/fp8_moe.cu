@@ -29,8 +29,8 @@
 // partial per part; whoever reads it adds them in their order along K, so results
 // do not depend on timing.  Every wait is bounded.
 //
-// Measured, weights from HBM: 32 tokens, 8 of 128 experts of 4096 x 1024: 235 us,
-// 6.0 TB/s, 88 % of a copy's rate, so HBM bounds it; one token, 8 of 64 of 2048 x
+// Measured, weights from HBM: 32 tokens, 8 of 128 experts of 4096 x 1024: 231 to
+// 235 us, 6.0 TB/s, 88 % of a copy's rate, so HBM bounds it; one token, 8 of 64 of 2048 x
 // 1024: 28.7 us, of which 50 MB take 7.5: the rest is four grid barriers, code
 // fetched cold and each phase's first loads.  ĥ formed by every CTA for its own
 // tiles instead of once spares a barrier (28.5 us for the one token) but takes
