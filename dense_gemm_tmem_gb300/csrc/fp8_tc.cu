@@ -120,35 +120,45 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
   const int64_t Mm = trans ? p.N : p.M, Nm = trans ? p.M : p.N;
   const int64_t sms = h->num_sms;
   const int64_t tiles_m = ceil_div(Mm, kBM), I = ceil_div(p.K, kFp8Block);
-  int bn;
-  if (trans)
-    bn = Nm <= 32 ? 32 : Nm <= 64 ? 64 : 128;
-  else
-    bn = Nm > 128 && tiles_m * ceil_div(Nm, 256) >= sms / 2 ? 256 : 128;
-  const int64_t tiles_n = ceil_div(Nm, bn), T = tiles_m * tiles_n;
-  if (T > INT32_MAX / 2) return cudaErrorInvalidValue;
   // Fewer tiles than half the SMs: each tile's k-blocks over a cluster, the
   // largest whose clusters are all resident at once, if that takes more than
   // kSplitGain k-blocks off each CTA: adding the partials costs about as long as
   // 8 k-blocks (2 us of 0.28 at 32 columns, 3 of 0.35 at 64, 4.3 of 0.51 at 128).
   // Measured (graph replay, cold inputs, us, split / whole): 1 x 4096 x 4096 7.5
   // / 12.0, 64 x 4096 x 4096 9.4 / 14.6, 128 x 1024 x 8192 11.3 / 36.5, 512 x 512
-  // x 2048 8.9 / 9.4; not taken: 515 x 1000 x 2056 12.2 / 10.8, 1024^3 10.4 / 7.1,
-  // 32 x 2048 x 1024 5.4 / 5.1.
+  // x 2048 7.3 / 7.9; not taken: 515 x 1000 x 2056 12.2 / 10.8, 1024^3 10.4 / 7.1
+  // (both 128 wide), 32 x 2048 x 1024 5.4 / 5.1.
   constexpr int64_t kSplitGain = 8;
-  int64_t grid = std::min(sms, T), split = 1;
   const int forced = h->opt.csplit;  // GEMM_OPT_CLUSTER_SPLIT
-  if (bn <= 128 && (forced >= 2 || (forced < 0 && 2 * T < sms))) {
+  auto split_of = [&](int64_t T) -> int64_t {
+    if (forced < 2 && (forced >= 0 || 2 * T >= sms)) return 1;
     for (int s : {8, 4, 2}) {
-      const int64_t cap = h->opt.csplit_clusters[s];
       if (forced >= 2 ? s == forced && I >= s && T * s <= INT32_MAX
-                      : T <= cap && T * s <= sms && I - ceil_div(I, s) > kSplitGain) {
-        split = s;
-        grid = T * s;
-        break;
-      }
+                      : T <= h->opt.csplit_clusters[s] && T * s <= sms &&
+                            I - ceil_div(I, s) > kSplitGain)
+        return s;
     }
+    return 1;
+  };
+  // Tiles of 64 columns instead of 128 where both leave SMs idle (B K-major, whose
+  // boxes may have 64 rows): 515 x 1000 x 2056 9.3 us instead of 10.9, 1024^3 6.1
+  // instead of 7.2, 256 x 1024 x 4096 8.7 instead of 10.6; but over a deep K, where
+  // the wider tiles can be split further, 512 x 1024 x 8192 15.4 instead of 14.4.
+  constexpr int64_t kDeepK = 48;  // k-blocks
+  int bn;
+  if (trans) {
+    bn = Nm <= 32 ? 32 : Nm <= 64 ? 64 : 128;
+  } else if (Nm > 128 && tiles_m * ceil_div(Nm, 256) >= sms / 2) {
+    bn = 256;
+  } else {
+    const int64_t wide = tiles_m * ceil_div(Nm, 128), narrow = tiles_m * ceil_div(Nm, 64);
+    bn = opB.s_k == 1 && 2 * wide <= sms && (I < kDeepK || split_of(wide) == split_of(narrow))
+             ? 64 : 128;
   }
+  const int64_t tiles_n = ceil_div(Nm, bn), T = tiles_m * tiles_n;
+  if (T > INT32_MAX / 2) return cudaErrorInvalidValue;
+  const int64_t split = bn <= 128 ? split_of(T) : 1;
+  const int64_t grid = split > 1 ? T * split : std::min(sms, T);
   Fp8TcArgs a{};
   a.work.tiles_m = int32_t(tiles_m);
   a.work.tiles_n = int32_t(tiles_n);
@@ -196,6 +206,13 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
                    : launch(launch_inst<256, false, true, false>);
     return out32 ? launch(launch_inst<256, false, false, true>)
                  : launch(launch_inst<256, false, false, false>);
+  }
+  if (bn == 64) {
+    if (colvec)
+      return out32 ? launch(launch_inst<64, false, true, true>)
+                   : launch(launch_inst<64, false, true, false>);
+    return out32 ? launch(launch_inst<64, false, false, true>)
+                 : launch(launch_inst<64, false, false, false>);
   }
   if (colvec)
     return out32 ? launch(launch_inst<128, false, true, true>)
