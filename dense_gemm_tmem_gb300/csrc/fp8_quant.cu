@@ -13,8 +13,10 @@
 // (magnitudes order like their bits), and the divisions of a thread's 8 rows
 // are shared out among the 16 threads that need them.  Four CTAs an SM for
 // 16-bit sources (8192 x 8192 bf16 both ways: 53 us with three, 48 with four,
-// 5.7 TB/s of the 6.8 a copy reaches here); for fp32 ones the tile's registers
-// allow two.
+// 5.7 TB/s of the 6.8 a copy reaches here).  For fp32 ones the tile alone takes 64
+// registers: three CTAs for 128 x 128 and 128 x 1 blocks (2050 x 5000 tiles 10.6 us
+// with two, 9.6 with three), two where rows are kept as well (8192 x 8192 both ways
+// 69.6 us, 79.6 with three, which spill).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -135,8 +137,13 @@ struct QuantArgs {
 
 enum : int { kRow = 1, kCol = 2, kTile = 4 };
 
+// CTAs an SM that the registers are cut for.
+constexpr int quant_ctas(size_t size, int mode) {
+  return size == 2 ? 4 : mode == kTile || mode == kCol ? 3 : 1;
+}
+
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 1 : 4)
+__global__ void __launch_bounds__(kQuantThreads, quant_ctas(sizeof(T), MODE))
     quantize_kernel(const QuantArgs a) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int warp = threadIdx.x >> 5;
