@@ -1,6 +1,7 @@
 // context.h: the handle behind gemm_handle_t and what the API files share.
 #pragma once
 
+#include <atomic>
 #include <mutex>
 
 #include "internal.h"
@@ -32,6 +33,21 @@ struct TmapEntry {
   TmapKey key;
   CUtensorMap map;
   bool valid = false;
+};
+
+// A kernel's dynamic shared memory limit, raised once per device (on every launch it
+// cost 0.5 us of a product's 4.4 of host time).
+struct SharedMemoryOnce {
+  std::atomic<uint64_t> devices{0};  // those that have it; past 63, none is noted
+  template <class Kernel>
+  cudaError_t allow(Kernel kern, int bytes, int device) {
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
 };
 
 // Runs `f` with the handle's device current, restoring the caller's.

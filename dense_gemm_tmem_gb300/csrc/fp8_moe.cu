@@ -1236,8 +1236,8 @@ cudaError_t launch_moe(gemm_ctx* h, const gemm_moe_fp8_t& L, void* workspace,
       !encode_experts(&up, L.up, L.inner, L.hidden, L.experts) ||
       !encode_experts(&down, L.down, L.hidden, L.inner, L.experts))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(moe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       MoeSmem::bytes);
+  static SharedMemoryOnce once;
+  cudaError_t e = once.allow(moe_kernel, MoeSmem::bytes, h->device);
   if (e != cudaSuccess) return e;
   // the CTAs wait for one another: a cooperative launch, all resident at once
   cudaLaunchConfig_t cfg = {};

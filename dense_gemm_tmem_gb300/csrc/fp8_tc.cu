@@ -73,10 +73,11 @@ bool encode_c(CUtensorMap* map, const Fp8Product& p) {
 
 template <int BN, bool TRANS, bool COLVEC, bool OUT32>
 cudaError_t launch_inst(const Fp8Maps& mA, const Fp8Maps& mB, const CUtensorMap& mC,
-                        const Fp8TcArgs& args, bool pdl, cudaStream_t stream) {
+                        const Fp8TcArgs& args, int device, bool pdl, cudaStream_t stream) {
   auto kern = fp8_tc_kernel<BN, TRANS, COLVEC, OUT32>;
   constexpr int smem = Fp8TcConfig<BN>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SharedMemoryOnce once;
+  cudaError_t e = once.allow(kern, smem, device);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -194,7 +195,7 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
   const bool pdl = h->opt.pdl != 0;
   const bool colvec = trans || opB.mn_shift == 0;
   const bool out32 = p.out_dtype == GEMM_F32;
-  auto launch = [&](auto inst) { return inst(mA, mB, mC, a, pdl, stream); };
+  auto launch = [&](auto inst) { return inst(mA, mB, mC, a, h->device, pdl, stream); };
   if (trans) {
     if (bn == 32) return launch(launch_inst<32, true, true, false>);
     if (bn == 64) return launch(launch_inst<64, true, true, false>);
