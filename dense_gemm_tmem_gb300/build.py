@@ -26,7 +26,7 @@ SOURCES = ["api.cu", "simt.cu", "simt_f16.cu", "selftest.cu", "noalloc.cu", "tc2
            "fp8_api.cu", "fp8_quant.cu", "fp8_simt.cu", "fp8_moe.cu", "fp8_tc.cu"]
 HEADERS = ["ptx.cuh", "work.cuh", "tc_kernel.cuh", "tc2_kernel.cuh", "tc64_kernel.cuh",
            "tc_launch.cuh", "simt_kernel.cuh", "internal.h", "context.h", "fp8.cuh",
-           "fp8_tc_kernel.cuh"]
+           "fp8_tc_kernel.cuh", "moe_order.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-I", os.path.join(ROOT, "include")]

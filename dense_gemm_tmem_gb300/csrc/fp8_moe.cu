@@ -39,6 +39,7 @@
 
 #include "context.h"
 #include "fp8_tc_kernel.cuh"
+#include "moe_order.h"
 
 namespace dg {
 namespace {
@@ -376,6 +377,19 @@ __device__ __forceinline__ void load_weights_3d(uint32_t dst, const CUtensorMap*
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The same, and whether all of the threads are ok.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(ok)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
 }
 
 // ------------------------------------------------------------------- phase A --
@@ -886,28 +900,40 @@ __device__ __forceinline__ void moe_rows(const MoeArgs& a, const MoeRoute& r, in
   }
 }
 
-// Warps 8-11: ĥ between the phases, and the token operand.
-__device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, MoeRing segs,
-                                          uint8_t* operand, float* b_scale, uint32_t b_full,
-                                          uint32_t b_empty, int* flag, const WaitCtl& wc) {
-  const int tid = threadIdx.x - 256, warp = tid >> 5, lane = tid & 31;
-  bool ok = true;
+// Warps 8-11: ĥ between the phases, and the token operand.  The order is
+// builder_run's.
+struct MoeBuilder {
+  const MoeArgs& a;
+  const MoeRoute& r;
+  MoeRing segs;
+  uint8_t* operand;
+  float* b_scale;
+  uint32_t b_full, b_empty;
+  const WaitCtl& wc;
   MoeContent content;
-  for (int phase = 0; phase < 2 && ok; ++phase) {
-    if (phase == 1) {  // also in a CTA without work in phase D
-      if (tid == 0) *flag = grid_wait(a.counters + 1, wc);
-      bar_sync(3, 128);
-      ok = *flag != 0;
-      if (!ok) break;
-      moe_rows(a, r, warp, lane);
-      bar_sync(3, 128);
-      if (tid == 0) {
-        grid_arrive(a.counters + 2);
-        *flag = grid_wait(a.counters + 2, wc);
-      }
-      bar_sync(3, 128);
-      ok = *flag != 0;
+
+  // Every CTA's partials of phase C, also in a CTA without work in phase D.
+  __device__ __forceinline__ bool partials(bool ok) {
+    if (threadIdx.x == 256) ok = ok && grid_wait(a.counters + 1, wc);
+    __syncwarp();
+    return bar_all(3, 128, ok);
+  }
+  __device__ __forceinline__ void rows() {
+    moe_rows(a, r, int(threadIdx.x - 256) >> 5, threadIdx.x & 31);
+  }
+  __device__ __forceinline__ bool rows_done() {
+    bar_sync(3, 128);
+    bool ok = true;
+    if (threadIdx.x == 256) {
+      grid_arrive(a.counters + 2);
+      ok = grid_wait(a.counters + 2, wc);
     }
+    __syncwarp();
+    return bar_all(3, 128, ok);
+  }
+  __device__ __forceinline__ bool contents(int phase) {
+    const int tid = threadIdx.x - 256;
+    bool ok = true;
     const uint8_t* rows_q = phase == 0 ? a.xq : a.hq;
     const float* rows_s = phase == 0 ? a.xs : a.hs;
     MoeSeg g;
@@ -950,8 +976,9 @@ __device__ __forceinline__ void moe_build(const MoeArgs& a, const MoeRoute& r, M
         if (whole) break;
       }
     }
+    return ok;
   }
-}
+};
 
 // ------------------------------------------------------------------- phase E --
 // `arrived` is called once, before the first partial is read.
@@ -1011,7 +1038,7 @@ struct MoeSmem {
   static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1 +
                                2 * kMoeSegs;
   static constexpr int words = bars + kBars * 8;
-  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier, builder
+  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier
 };
 static_assert(MoeSmem::bytes <= 227 * 1024, "shared memory per CTA");
 
@@ -1095,7 +1122,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const uint32_t ring = smem_u32(smem + MoeSmem::ring);
     if (warp >= 4) moe_picks(a, r);
     if (warp >= 8) {
-      moe_build(a, r, segs, smem + MoeSmem::operand, b_scale, b_full, b_empty, words + 3, wc);
+      MoeBuilder builder{a, r, segs, smem + MoeSmem::operand, b_scale, b_full, b_empty, wc, {}};
+      builder_run(builder);
     } else if (warp >= 4) {
       moe_accumulate(a, r, segs, scale_ring, b_scale, acc_full, acc_empty, b_full, b_empty, sc_full,
                      sc_empty, tmem_base, wc);
