@@ -1038,7 +1038,7 @@ struct MoeSmem {
   static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1 +
                                2 * kMoeSegs;
   static constexpr int words = bars + kBars * 8;
-  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier
+  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier, abort in phase E
 };
 static_assert(MoeSmem::bytes <= 227 * 1024, "shared memory per CTA");
 
@@ -1094,6 +1094,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    words[3] = 0;
     fence_barrier_init();
     tma_prefetch_map(&gate.group);
     tma_prefetch_map(&up.group);
@@ -1149,9 +1150,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
+  // All warps or none: a wait of phase E that runs out has a flag of its own, as a
+  // slower warp may have this one still to read.
   if (!routed || *abort_flag) return;  // gemm_status clears the counters
+  const WaitCtl last{a.wait_limit_ns, a.status, words + 3};
   moe_phase_e(a, r, [&]() {
-    if (threadIdx.x == 0) words[2] = grid_wait(a.counters + 3, wc) ? 1 : 0;
+    if (threadIdx.x == 0) words[2] = grid_wait(a.counters + 3, last) ? 1 : 0;
     __syncthreads();
     return words[2] != 0;
   });
