@@ -378,19 +378,6 @@ __device__ __forceinline__ void load_weights_3d(uint32_t dst, const CUtensorMap*
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// The same, and whether all of the threads are ok.
-__device__ __forceinline__ bool bar_all(int id, int threads, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(uint32_t(ok)), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
-}
 
 // ------------------------------------------------------------------- phase A --
 // Router logits: a CTA takes (expert, 8 tokens) tasks, its 8 worker warps an
@@ -909,27 +896,30 @@ struct MoeBuilder {
   uint8_t* operand;
   float* b_scale;
   uint32_t b_full, b_empty;
+  volatile int* flag;     // whether the grid's barrier came
+  volatile int* gave_up;  // 1: a warp's wait in phase C ran out
   const WaitCtl& wc;
   MoeContent content;
 
-  // Every CTA's partials of phase C, also in a CTA without work in phase D.
+  // Every CTA's partials of phase C, also in a CTA without work in phase D.  (A
+  // barrier that votes, bar.red, cost the one-token layer 0.35 of 29 us.)
   __device__ __forceinline__ bool partials(bool ok) {
-    if (threadIdx.x == 256) ok = ok && grid_wait(a.counters + 1, wc);
-    __syncwarp();
-    return bar_all(3, 128, ok);
+    if (!ok) *gave_up = 1;
+    if (threadIdx.x == 256) *flag = ok && grid_wait(a.counters + 1, wc);
+    bar_sync(3, 128);
+    return *flag != 0 && *gave_up == 0;
   }
   __device__ __forceinline__ void rows() {
     moe_rows(a, r, int(threadIdx.x - 256) >> 5, threadIdx.x & 31);
   }
   __device__ __forceinline__ bool rows_done() {
     bar_sync(3, 128);
-    bool ok = true;
     if (threadIdx.x == 256) {
       grid_arrive(a.counters + 2);
-      ok = grid_wait(a.counters + 2, wc);
+      *flag = grid_wait(a.counters + 2, wc);
     }
-    __syncwarp();
-    return bar_all(3, 128, ok);
+    bar_sync(3, 128);
+    return *flag != 0;
   }
   __device__ __forceinline__ bool contents(int phase) {
     const int tid = threadIdx.x - 256;
@@ -1038,7 +1028,7 @@ struct MoeSmem {
   static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1 +
                                2 * kMoeSegs;
   static constexpr int words = bars + kBars * 8;
-  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier, abort in phase E
+  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier, abort in phase E, builders (2)
 };
 static_assert(MoeSmem::bytes <= 227 * 1024, "shared memory per CTA");
 
@@ -1094,7 +1084,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    words[3] = 0;
+    words[3] = words[5] = 0;
     fence_barrier_init();
     tma_prefetch_map(&gate.group);
     tma_prefetch_map(&up.group);
@@ -1123,7 +1113,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const uint32_t ring = smem_u32(smem + MoeSmem::ring);
     if (warp >= 4) moe_picks(a, r);
     if (warp >= 8) {
-      MoeBuilder builder{a, r, segs, smem + MoeSmem::operand, b_scale, b_full, b_empty, wc, {}};
+      MoeBuilder builder{a,       r,         segs,      smem + MoeSmem::operand, b_scale, b_full,
+                         b_empty, words + 4, words + 5, wc,                      {}};
       builder_run(builder);
     } else if (warp >= 4) {
       moe_accumulate(a, r, segs, scale_ring, b_scale, acc_full, acc_empty, b_full, b_empty, sc_full,
