@@ -657,11 +657,11 @@ __device__ __forceinline__ void moe_scales(const MoeArgs& a, MoeRing segs, uint3
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-__device__ __forceinline__ void moe_mma(MoeRing segs, uint32_t ring,
-                                        uint32_t operand, uint32_t full, uint32_t empty,
-                                        uint32_t acc_full, uint32_t acc_empty, uint32_t b_full,
-                                        uint32_t b_empty, uint32_t drain, uint32_t tmem_base,
-                                        const WaitCtl& wc) {
+// Whether it issued anything.
+__device__ __forceinline__ bool moe_mma(MoeRing segs, uint32_t ring, uint32_t operand,
+                                        uint32_t full, uint32_t empty, uint32_t acc_full,
+                                        uint32_t acc_empty, uint32_t b_full, uint32_t b_empty,
+                                        uint32_t tmem_base, const WaitCtl& wc) {
   uint32_t s = 0, ph = 0, b = 0, phases = (1u << kMoeBuffers) - 1;
   bool ok = true, any = false;
   const bool leader = f8_elect();
@@ -721,11 +721,7 @@ __device__ __forceinline__ void moe_mma(MoeRing segs, uint32_t ring,
       }
     }
   }
-  if (!ok && any && leader) {
-    tc_commit(drain);
-    wait_drain(drain, 0, wc);
-  }
-  __syncwarp();
+  return any;
 }
 
 // Warps 4-7: thread `row` owns one weight row; sums of up to 64 tokens.
@@ -1108,6 +1104,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   __syncthreads();
   const bool routed = words[2] != 0;
   uint32_t filled = 0;
+  bool issued = false;
   if (routed) {
     moe_phase_b(a, r);
     const uint32_t ring = smem_u32(smem + MoeSmem::ring);
@@ -1124,8 +1121,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     } else if (warp == 2) {
       moe_scales(a, segs, smem_u32(scale_ring), sc_full, sc_empty, lane, wc);
     } else if (warp == 1) {
-      moe_mma(segs, ring, smem_u32(smem + MoeSmem::operand), full, empty, acc_full, acc_empty,
-              b_full, b_empty, drain, tmem_base, wc);
+      issued = moe_mma(segs, ring, smem_u32(smem + MoeSmem::operand), full, empty, acc_full,
+                       acc_empty, b_full, b_empty, tmem_base, wc);
     } else if (warp == 0 && lane == 0) {
       filled = moe_producer(a, r, gate, up, down, seg_slot, seg_full, seg_empty, ring, full, empty,
                             wc);
@@ -1138,6 +1135,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    if (issued) f8_drain(drain, wc);
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }

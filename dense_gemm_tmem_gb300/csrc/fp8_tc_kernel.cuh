@@ -315,13 +315,25 @@ __device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, uint32_t ring, 
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// After an abort the MMAs in flight must finish before their TMEM is freed.  Called
+// by the issuing warp when every role has ended: the wait that gave up may have been
+// a reader's, after the issuer's own last one.
+__device__ __forceinline__ void f8_drain(uint32_t drain, const WaitCtl& wc) {
+  if (*wc.abort == 0) return;
+  if (f8_elect()) {
+    tc_commit(drain);
+    wait_drain(drain, 0, wc);
+  }
+  __syncwarp();
+}
+
 // MMA issuer: the whole warp runs the loop, so that addresses and descriptors
 // stay in uniform registers; one lane issues.  Buffer j of a unit's k-block j
-// modulo kBuffers; `phases` holds each buffer's parity.
+// modulo kBuffers; `phases` holds each buffer's parity.  Whether it issued anything.
 template <int BN>
-__device__ __forceinline__ void f8_mma(const Fp8TcArgs& args, uint32_t sA, uint32_t sB,
+__device__ __forceinline__ bool f8_mma(const Fp8TcArgs& args, uint32_t sA, uint32_t sB,
                                        uint32_t full, uint32_t empty, uint32_t acc_full,
-                                       uint32_t acc_empty, uint32_t drain, const WaitCtl& wc,
+                                       uint32_t acc_empty, const WaitCtl& wc,
                                        uint32_t tmem_base) {
   using Cfg = Fp8TcConfig<BN>;
   constexpr int G = Cfg::kGroup, NB = Cfg::kBuffers;
@@ -376,11 +388,7 @@ __device__ __forceinline__ void f8_mma(const Fp8TcArgs& args, uint32_t sA, uint3
       }
     }
   }
-  if (!ok && any && leader) {  // every MMA issued so far must finish before TMEM is freed
-    tc_commit(drain);
-    wait_drain(drain, 0, wc);
-  }
-  __syncwarp();
+  return any;
 }
 
 // Row-major store of a warp's 32 rows x HC columns (lane i holds row mrow0 + i),
@@ -831,6 +839,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const WaitCtl wc{args.wait_limit_ns, args.status, abort_flag};
 
   uint32_t filled = 0;
+  bool issued = false;
   if (warp >= kF8RoleWarps) {
     if (BN >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
     f8_epilogue<BN, TRANS, COLVEC, OUT32>(args, &tmC, smem_u32(acc_full), smem_u32(acc_empty),
@@ -842,8 +851,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       filled = f8_producer<BN>(mA, mB, args, sA, sB, full, empty, wc);
     } else if (warp == 1) {
       pdl_wait_prerequisites();
-      f8_mma<BN>(args, smem_u32(sA), smem_u32(sB), smem_u32(full), smem_u32(empty),
-                 smem_u32(acc_full), smem_u32(acc_empty), smem_u32(drain), wc, tmem_base);
+      issued = f8_mma<BN>(args, smem_u32(sA), smem_u32(sB), smem_u32(full), smem_u32(empty),
+                          smem_u32(acc_full), smem_u32(acc_empty), wc, tmem_base);
     } else if (warp >= 2) {
       f8_scales<BN, COLVEC>(args, smem_u32(ring), sc_full, sc_empty, wc);
     } else {
@@ -857,6 +866,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    if (issued) f8_drain(smem_u32(drain), wc);
     tc_fence_after();
     tmem_dealloc(tmem_base, Cfg::kTmemCols);
   }

@@ -56,3 +56,12 @@ def test_expert_layer_under_short_limits(h, tokens, hidden, inner, count, top_k)
     x = torch.randn(tokens, hidden, device="cuda").bfloat16()
     router = torch.randn(count, hidden, device="cuda").bfloat16()
     limited(h, lambda: h.moe_fp8(x, router, *w, top_k), [1, 300, 1000, 3000, 10000, 30000])
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (300, 700, 2048), (2048, 2048, 2048)])
+def test_product_under_short_limits(h, M, N, K):
+    """Split over clusters, whole tiles of one wave, and several tiles a CTA."""
+    torch.manual_seed(M)
+    a = h.fp8_quantize(torch.randn(M, K, device="cuda").half(), "row")
+    b = h.fp8_quantize(torch.randn(N, K, device="cuda").half(), "tile")
+    limited(h, lambda: [h.fp8_matmul(a, b, b_major=B.GEMM_COL_MAJOR)], [1, 300, 1000, 3000, 10000])
