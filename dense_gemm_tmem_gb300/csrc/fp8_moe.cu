@@ -724,7 +724,8 @@ __device__ __forceinline__ bool moe_mma(MoeRing segs, uint32_t ring, uint32_t op
   return any;
 }
 
-// Warps 4-7: thread `row` owns one weight row; sums of up to 64 tokens.
+// Warps 4-7: thread `row` owns one weight row; sums of up to 64 tokens.  A block's sum
+// meets the weight's scale, then the token's, whose product might not fit fp32.
 __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute& r, MoeRing segs,
                                                const float* scale_ring, const float* b_scale,
                                                uint32_t acc_full, uint32_t acc_empty,
@@ -779,11 +780,11 @@ __device__ __forceinline__ void moe_accumulate(const MoeArgs& a, const MoeRoute&
             if (two) tmem_issue<16>(tlane + b * 128 + 64 + c * 16, v1);
             tmem_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma_tmem(acc[c * 16 + j], w0 * bk[c * 16 + j], v0[j]);
+            for (int j = 0; j < 16; ++j) fma_tmem2(acc[c * 16 + j], w0, bk[c * 16 + j], v0[j]);
             if (two) {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                fma_tmem(acc[c * 16 + j], w1 * bk[cols + c * 16 + j], v1[j]);
+                fma_tmem2(acc[c * 16 + j], w1, bk[cols + c * 16 + j], v1[j]);
             }
           }
           tc_fence_before();

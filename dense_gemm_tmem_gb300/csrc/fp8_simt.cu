@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(256) fp8_simt_kernel(const Fp8Product p, int32
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(part[i][j], sa[i] * sb[j], acc[i][j]);
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = add_scaled(acc[i][j], part[i][j], sa[i], sb[j]);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -80,7 +80,9 @@ struct Fp8TcConfig {
   static constexpr int kScaleGroup = 4;  // k-blocks per ring slot
   static constexpr int kScaleRing = 2;
   static constexpr int kScaleFloats = kBM + BN;
-  static constexpr int kScaleBytes = kScaleRing * kScaleGroup * kScaleFloats * 4;
+  // a slot: its k-blocks' scales, then a factor for each warpgroup's rows (f8_scales)
+  static constexpr int kSlotFloats = kScaleGroup * kScaleFloats + 4;
+  static constexpr int kScaleBytes = kScaleRing * kSlotFloats * 4;
   static constexpr int kBarBytes = 384;
   static constexpr int kSmemBytes =
       1024 + kStages * kStageBytes + kEpiBytes + kScaleBytes + kBarBytes;
@@ -158,18 +160,28 @@ __device__ __forceinline__ void fma_tmem(float& d, float a, uint32_t b) {
   asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "f"(a), "f"(__uint_as_float(b)));
 }
 
-// (x a, y a), one instruction.  (A scale per column is a product per element on
-// top of the FMA: 105 us instead of 73 at 4096^3.  With scalar products 1 x 4096 x
-// 4096 takes 7.53 us instead of 7.41, a linear step of 4096^3 312 instead of 310.)
-__device__ __forceinline__ float2 mul2(float x, float y, float a) {
+// d += (b lo) hi, likewise (scale_order).
+__device__ __forceinline__ void fma_tmem2(float& d, float lo, float hi, uint32_t b) {
+  asm volatile(
+      "{\n\t.reg .f32 t;\n\t"
+      "mul.rn.f32 t, %3, %1;\n\t"
+      "fma.rn.f32 %0, t, %2, %0;\n\t}"
+      : "+f"(d)
+      : "f"(lo), "f"(hi), "f"(__uint_as_float(b)));
+}
+
+// (x a, y b) with a and b likewise, one instruction.  (A scale per column is a
+// product per element on top of the FMA: 105 us instead of 73 at 4096^3.)
+__device__ __forceinline__ float2 mul2_tmem(float x, float y, uint32_t a, uint32_t b) {
   float2 r;
-  asm("{\n\t.reg .b64 p, q;\n\t"
+  asm volatile(
+      "{\n\t.reg .b64 p, q;\n\t"
       "mov.b64 p, {%2, %3};\n\t"
-      "mov.b64 q, {%4, %4};\n\t"
+      "mov.b64 q, {%4, %5};\n\t"
       "mul.rn.f32x2 p, p, q;\n\t"
       "mov.b64 {%0, %1}, p;\n\t}"
       : "=f"(r.x), "=f"(r.y)
-      : "f"(x), "f"(y), "f"(a));
+      : "f"(x), "f"(y), "r"(a), "r"(b));
   return r;
 }
 
@@ -251,16 +263,24 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Scale loaders (64 threads): rows t and t + 64 of the tile and columns t, t +
-// 64, ..., rows and columns past the matrix clamped to its last.  A thread
-// arrives on a ring slot's barrier when its copies into it have landed.  Where
-// 128 columns share a scale only the first of each is needed.
+// Scale loaders (64 threads): rows t and t + 64 of the tile and, a warp for each
+// warpgroup of the epilogue, its half's columns; rows and columns past the matrix
+// clamped to its last, and k-blocks past the unit to its last, so that a slot is
+// always whole.  Where 128 columns share a scale only one a warp is needed, and the
+// copies' landing arrives on the ring slot's barrier.
+// With a scale per column a warp looks its columns over first.  The epilogue
+// multiplies a block's sum (up to 2^25) by the column's scale before the row's, so
+// columns above 2^103 are taken down by 2^25 and the warpgroup told to take its rows
+// up by as much.  (Row times column, whose range takes a look at every pair, cost a
+// linear step of 4096^3 326 us instead of 315, 64 x 4096 x 4096 9.0 instead of 8.85.)
+constexpr float kColumnMost = 0x1p103f, kColumnDown = 0x1p-25f, kRowUp = 0x1p25f;
+
 template <int BN, bool COLVEC>
-__device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, uint32_t ring, uint64_t* sc_full,
+__device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, float* ring, uint64_t* sc_full,
                                           uint64_t* sc_empty, const WaitCtl& wc) {
   using Cfg = Fp8TcConfig<BN>;
-  constexpr int kCols = COLVEC ? (BN + kF8ScaleThreads - 1) / kF8ScaleThreads : 1;
-  const int t = int(threadIdx.x) - 64;
+  constexpr int HC = Cfg::kHalf, kCols = COLVEC ? (HC + 31) / 32 : 1;
+  const int t = int(threadIdx.x) - 64, w = t >> 5, lane = t & 31;
   const WorkSpec& W = args.work;
   WorkIter it;
   it.init(W, int32_t(blockIdx.x));
@@ -268,6 +288,10 @@ __device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, uint32_t ring, 
   uint32_t slot = 0, ph = 0;
   bool ok = true;
   pdl_wait_prerequisites();
+  // this thread's column i of the tile and its place behind the rows
+  auto column = [&](int i) { return w * HC + (COLVEC ? lane + i * 32 : 0); };
+  auto place = [&](int i) { return kBM + (COLVEC ? column(i) : w); };
+  auto mine = [&](int i) { return COLVEC ? lane + i * 32 < HC : lane == 0; };
   while (ok && it.next(W, u)) {
     int32_t tm, tn;
     tile_coords(W, u.tile, tm, tn);
@@ -278,34 +302,51 @@ __device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, uint32_t ring, 
              kb * args.row.kb_stride;
     };
     auto col_at = [&](int i, int32_t kb) {
-      // uniform columns: threads 0 and 1 fetch the two warpgroups' scales
-      const int32_t c = COLVEC ? t + i * kF8ScaleThreads : (t & 1) * Cfg::kHalf;
-      const int32_t n = min(tn * BN + c, args.Nm - 1);
+      const int32_t n = min(tn * BN + column(i), args.Nm - 1);
       return args.col.p + int64_t(n >> args.col.shift) * args.col.stride +
              kb * args.col.kb_stride;
     };
     for (int32_t kb = u.kb0; kb < u.kb1; kb += Cfg::kScaleGroup) {
-      if (!wait_bounded(smem_u32(&sc_empty[slot]), ph ^ 1, wc, kSiteProducer)) {
-        ok = false;
-        break;
-      }
-      uint32_t dst = ring + slot * (Cfg::kScaleGroup * Cfg::kScaleFloats * 4);
+      // the warp's lanes together: they look the slot over together
+      ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(&sc_empty[slot]), ph ^ 1, wc,
+                                                kSiteProducer));
+      if (!ok) break;
+            float* to = ring + slot * Cfg::kSlotFloats;
+      uint32_t dst = smem_u32(to);
 #pragma unroll 1
-      for (int j = 0; j < Cfg::kScaleGroup && kb + j < u.kb1; ++j) {
+      for (int j = 0; j < Cfg::kScaleGroup; ++j) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          cp_async4(dst + (t + i * kF8ScaleThreads) * 4, row_at(i, kb + j));
+          cp_async4(dst + (t + i * kF8ScaleThreads) * 4, row_at(i, min(kb + j, u.kb1 - 1)));
         }
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const int c = t + i * kF8ScaleThreads;
-          if (c < (COLVEC ? BN : 2)) cp_async4(dst + (kBM + c) * 4, col_at(i, kb + j));
-        }
+        for (int i = 0; i < kCols; ++i)
+          if (mine(i)) cp_async4(dst + place(i) * 4, col_at(i, min(kb + j, u.kb1 - 1)));
         dst += Cfg::kScaleFloats * 4;
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                       smem_u32(&sc_full[slot]))
-                   : "memory");
+      if constexpr (COLVEC) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        bool big = false;
+#pragma unroll 1
+        for (int j = 0; j < Cfg::kScaleGroup; ++j)
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)
+            if (mine(i)) big |= fabsf(to[j * Cfg::kScaleFloats + place(i)]) > kColumnMost;
+        big = __any_sync(0xffffffffu, big);
+        if (big) {
+#pragma unroll 1
+          for (int j = 0; j < Cfg::kScaleGroup; ++j)
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+              if (mine(i)) to[j * Cfg::kScaleFloats + place(i)] *= kColumnDown;
+        }
+        if (lane == 0) to[Cfg::kScaleGroup * Cfg::kScaleFloats + w] = big ? kRowUp : 1.f;
+        mbar_arrive(smem_u32(&sc_full[slot]));
+      } else {
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_u32(&sc_full[slot]))
+                     : "memory");
+      }
       if (++slot == uint32_t(Cfg::kScaleRing)) {
         slot = 0;
         ph ^= 1;
@@ -596,15 +637,30 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, const CUtenso
       if (NV == 2) tmem_issue<CW>(tlane + uint32_t(i * BN), v[0]);
     };
     begin(0);
-    for (int32_t kb = u.kb0; kb < u.kb1; kb += SG) {
+    int32_t kb = u.kb0;
+    bool odd = false;
+    for (; kb < u.kb1; kb += SG) {
       ok &= wait_bounded(sc_full + 8 * slot, sph, wc, kSiteEpilogue);
-      const float* sc = ring + slot * (SG * Cfg::kScaleFloats);
+      const float* sc = ring + slot * Cfg::kSlotFloats;
       const uint32_t sc_at = smem_u32(sc + wg * HC);
       float rs[SG];
+      const float up = COLVEC ? sc[SG * Cfg::kScaleFloats + wg] : 1.f;
 #pragma unroll
       for (int j = 0; j < SG; ++j) {
         rs[j] = sc[j * Cfg::kScaleFloats + row];
-        if (!COLVEC) rs[j] *= sc[j * Cfg::kScaleFloats + kBM + wg];
+        if (COLVEC) {
+          rs[j] *= up;
+        } else {
+          rs[j] *= sc[j * Cfg::kScaleFloats + kBM + wg];
+        }
+      }
+      if constexpr (!COLVEC) {
+        static_assert(SG == 4, "the four of a slot");
+        const float a0 = fabsf(rs[0]), a1 = fabsf(rs[1]), a2 = fabsf(rs[2]), a3 = fabsf(rs[3]);
+        const float most = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
+        const float least = fminf(fminf(a0, a1), fminf(a2, a3));
+        odd = __any_sync(0xffffffffu, !(scale_fits(most) && scale_fits(least)));
+        if (__builtin_expect(odd, 0)) break;
       }
 #pragma unroll
       for (int j = 0; j < SG; ++j) {
@@ -632,11 +688,12 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, const CUtenso
 #pragma unroll
             for (int e = 0; e < CW; e += 4) {
               const float4 s4 = lds4(cs + e * 4);
-              const float2 lo = mul2(s4.x, s4.y, rs[j]), hi = mul2(s4.z, s4.w, rs[j]);
-              fma_tmem(d[e], lo.x, x[e]);
-              fma_tmem(d[e + 1], lo.y, x[e + 1]);
-              fma_tmem(d[e + 2], hi.x, x[e + 2]);
-              fma_tmem(d[e + 3], hi.y, x[e + 3]);
+              const float2 lo = mul2_tmem(s4.x, s4.y, x[e], x[e + 1]);
+              const float2 hi = mul2_tmem(s4.z, s4.w, x[e + 2], x[e + 3]);
+              d[e] = fmaf(lo.x, rs[j], d[e]);
+              d[e + 1] = fmaf(lo.y, rs[j], d[e + 1]);
+              d[e + 2] = fmaf(hi.x, rs[j], d[e + 2]);
+              d[e + 3] = fmaf(hi.y, rs[j], d[e + 3]);
             }
           } else {
 #pragma unroll
@@ -651,6 +708,45 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, const CUtenso
       if (++slot == uint32_t(Cfg::kScaleRing)) {
         slot = 0;
         sph ^= 1;
+      }
+    }
+    if constexpr (!COLVEC) {
+      if (__builtin_expect(odd, 0)) {
+        // From a slot on with scale products that fp32 cannot hold: the scale of smaller
+        // magnitude first.  (A loop of its own: a branch in the one above cost it 30 of
+        // 470 us.)
+        if (NV == 2) tmem_wait();  // the chunk under way is read again
+        const int32_t odd0 = kb;
+#pragma unroll 1
+        for (; kb < u.kb1; ++kb) {
+          const int j = (kb - odd0) % SG, i = j % NB;
+          if (kb > odd0) {
+            if (j == 0) ok &= wait_bounded(sc_full + 8 * slot, sph, wc, kSiteEpilogue);
+            ok &= wait_bounded(acc_full + 8 * i, (phases >> i) & 1, wc, kSiteEpilogue);
+            tc_fence_after();
+          }
+          phases ^= 1u << i;
+          const float* s = ring + slot * Cfg::kSlotFloats + j * Cfg::kScaleFloats;
+          float lo, hi;
+          scale_order(s[row], s[kBM + wg], lo, hi);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            tmem_issue<CW>(tlane + uint32_t(i * BN + c * CW), v[0]);
+            tmem_wait();
+#pragma unroll
+            for (int e = 0; e < CW; ++e) fma_tmem2(acc[c * CW + e], lo, hi, v[0][e]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty + 8 * i);
+          if (j == SG - 1 || kb + 1 == u.kb1) {
+            if (lane == 0) mbar_arrive(sc_empty + 8 * slot);
+            if (++slot == uint32_t(Cfg::kScaleRing)) {
+              slot = 0;
+              sph ^= 1;
+            }
+          }
+        }
       }
     }
 
@@ -854,7 +950,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       issued = f8_mma<BN>(args, smem_u32(sA), smem_u32(sB), smem_u32(full), smem_u32(empty),
                           smem_u32(acc_full), smem_u32(acc_empty), wc, tmem_base);
     } else if (warp >= 2) {
-      f8_scales<BN, COLVEC>(args, smem_u32(ring), sc_full, sc_empty, wc);
+      f8_scales<BN, COLVEC>(args, ring, sc_full, sc_empty, wc);
     } else {
       pdl_wait_prerequisites();
     }

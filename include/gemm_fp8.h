@@ -71,6 +71,10 @@ int gemm_fp8_quantize(gemm_handle_t h, int64_t rows, int64_t cols, const void *s
  * GEMM_COL_MAJOR: stored N x K.  Scales must be constant along 128 elements of
  * K: an operand stored with K along its rows has ROW or TILE blocks, one stored
  * with K down its columns COL or TILE blocks.
+ * The sum of 128 of K is multiplied by its two scales in an order that keeps it
+ * within fp32's range wherever the result is, for scales down to 2^-109 (the least
+ * that quantising makes), unless both operands have scales above 2^103 (block maxima
+ * above 4.5e33) within 512 of K.
  * bias: NULL or N fp32 values added in fp32 before the rounding.  C is
  * row-major with ldc >= N elements from row to row.
  * The three products of a linear layer: forward y = x·Wᵀ (x ROW row-major, W
@@ -107,7 +111,8 @@ typedef struct {
  *     h = silu(gate_e · x̂) * (up_e · x̂),   x̂ = x quantised with ROW blocks,
  *     out[t] = sum_j gates[t][j] * (down_e · ĥ), ĥ = h quantised with ROW blocks,
  * products and sums in fp32, out rounded once to `dtype`.  gate and up are
- * inner x hidden, down is hidden x inner.
+ * inner x hidden, down is hidden x inner.  Weight scales lie between 2^-109 and
+ * 2^103, x̂'s and ĥ's may be any.
  * ids (tokens x top_k int32) and gates (tokens x top_k fp32) are outputs too.
  * The same call gives the same bits every time; with other tokens beside it a
  * token's sums may be cut differently, which moves their last bits. */
