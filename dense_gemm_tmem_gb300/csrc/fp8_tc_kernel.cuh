@@ -311,7 +311,7 @@ __device__ __forceinline__ void f8_scales(const Fp8TcArgs& args, float* ring, ui
       ok = __all_sync(0xffffffffu, wait_bounded(smem_u32(&sc_empty[slot]), ph ^ 1, wc,
                                                 kSiteProducer));
       if (!ok) break;
-            float* to = ring + slot * Cfg::kSlotFloats;
+      float* to = ring + slot * Cfg::kSlotFloats;
       uint32_t dst = smem_u32(to);
 #pragma unroll 1
       for (int j = 0; j < Cfg::kScaleGroup; ++j) {

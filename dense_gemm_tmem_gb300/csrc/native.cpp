@@ -125,25 +125,23 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int64_t rows = x.size(0), cols = x.size(1), ld = (cols + 15) & ~int64_t(15);
     const int64_t values = (rows * ld + 255) & ~int64_t(255);
     const int count = kinds[1] >= 0 ? 2 : 1;
-    int64_t sr[2], sc[2], at[2], total = 0;
-    for (int i = 0; i < count; ++i) {
-      sr[i] = kinds[i] == GEMM_FP8_ROW ? rows : blocks_of(rows);
-      sc[i] = kinds[i] == GEMM_FP8_COL ? cols : blocks_of(cols);
-      at[i] = total;
-      total += values + ((sr[i] * sc[i] * 4 + 255) & ~int64_t(255));
-    }
-    const at::Tensor buf = at::empty({total}, x.options().dtype(at::kByte).requires_grad(false));
-    uint8_t* base = static_cast<uint8_t*>(buf.data_ptr());
+    const auto opt = x.options().dtype(at::kByte).requires_grad(false);
     gemm_fp8_matrix_t m[2];
     at::Tensor out[4];
     for (int i = 0; i < count; ++i) {
-      // row blocks: the scales of one k-block next to each other
+      // values and scales in one allocation, each matrix in its own: a program that
+      // keeps one of the two does not hold the other's bytes
       const bool row = kinds[i] == GEMM_FP8_ROW;
-      const int64_t s_r = row ? 1 : sc[i], s_c = row ? sr[i] : 1;
-      m[i] = gemm_fp8_matrix_t{base + at[i], ld, reinterpret_cast<float*>(base + at[i] + values),
-                               s_r, s_c, int32_t(kinds[i]), 0};
-      out[2 * i] = carve(buf, at::kFloat8_e4m3fn, at[i], rows, cols, ld, 1);
-      out[2 * i + 1] = carve(buf, at::kFloat, at[i] + values, sr[i], sc[i], s_r, s_c);
+      const int64_t sr = row ? rows : blocks_of(rows);
+      const int64_t sc = kinds[i] == GEMM_FP8_COL ? cols : blocks_of(cols);
+      const at::Tensor buf = at::empty({values + sr * sc * 4}, opt);
+      uint8_t* base = static_cast<uint8_t*>(buf.data_ptr());
+      // row blocks: the scales of one k-block next to each other
+      const int64_t s_r = row ? 1 : sc, s_c = row ? sr : 1;
+      m[i] = gemm_fp8_matrix_t{base, ld, reinterpret_cast<float*>(base + values),
+                               s_r,  s_c, int32_t(kinds[i]), 0};
+      out[2 * i] = carve(buf, at::kFloat8_e4m3fn, 0, rows, cols, ld, 1);
+      out[2 * i + 1] = carve(buf, at::kFloat, values, sr, sc, s_r, s_c);
     }
     const int rc = quantize_fn(address<gemm_ctx>(args[0]), rows, cols, x.data_ptr(), ld_x, code,
                                &m[0], count == 2 ? &m[1] : nullptr, address<void>(args[5]));
