@@ -133,7 +133,8 @@ def linear_backward(g, dy: torch.Tensor, saved, stream=None):
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, g, x, w, bias):
-        y, ctx.saved = linear_forward(g, x, w, bias)
+        y, (x_col, wq) = linear_forward(g, x, w, bias)
+        ctx.save_for_backward(x_col.data, x_col.scale, wq.data, wq.scale)
         ctx.g, ctx.w_dtype, ctx.has_bias = g, w.dtype, bias is not None
         return y
 
@@ -141,7 +142,9 @@ class _Linear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         dy = dy.contiguous()
-        dx, dw = linear_backward(ctx.g, dy, ctx.saved)
+        x_data, x_scale, w_data, w_scale = ctx.saved_tensors
+        saved = Fp8Matrix._wrap(x_data, x_scale, "col"), Fp8Matrix._wrap(w_data, w_scale, "tile")
+        dx, dw = linear_backward(ctx.g, dy, saved)
         return None, dx, dw.to(ctx.w_dtype), dy.float().sum(0) if ctx.has_bias else None
 
 

@@ -1,0 +1,76 @@
+"""The differentiable linear layer's bookkeeping, on the host: what it keeps for the
+backward pass and which of its quantisations and products it asks for, seen by a
+stand-in for the library handle that computes them in plain torch."""
+import gc
+import itertools
+import weakref
+
+import pytest
+import torch
+
+import fp8_reference as R
+from dense_gemm_tmem_gb300 import fp8
+from dense_gemm_tmem_gb300.fp8 import Fp8Matrix
+from dense_gemm_tmem_gb300.gemm import COL, ROW
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+class Plain:
+    """fp8_quantize and fp8_matmul of a Gemm, noting each call."""
+
+    def __init__(self):
+        self.calls, self.made = [], []
+
+    def fp8_quantize(self, x, blocks="row", stream=None):
+        self.calls.append(blocks)
+        out = []
+        for kind in blocks.split("+"):
+            q, s = R.quantize(R.host(x), kind)
+            out.append(Fp8Matrix(torch.from_numpy(q).float().to(torch.float8_e4m3fn),
+                                 torch.from_numpy(s), kind))
+            self.made.append((kind, weakref.ref(out[-1].data)))
+        return tuple(out) if len(out) == 2 else out[0]
+
+    def fp8_matmul(self, A, Bm, bias=None, a_major=ROW, b_major=ROW, out_dtype=BF16, stream=None):
+        self.calls.append((tuple(A.shape), tuple(Bm.shape), out_dtype))
+        a, b = A.dequantize().double(), Bm.dequantize().double()
+        c = (a if a_major == ROW else a.t()) @ (b if b_major == ROW else b.t())
+        return (c if bias is None else c + bias.double()).to(out_dtype)
+
+    def products(self):
+        return [c for c in self.calls if isinstance(c, tuple)]
+
+
+T, N, K = 5, 6, 7
+
+
+def leaves(need_x=True, need_w=True, need_b=True, dtype=F32):
+    torch.manual_seed(0)
+    return (torch.randn(T, K).to(dtype).requires_grad_(need_x),
+            torch.randn(N, K).to(dtype).requires_grad_(need_w),
+            torch.randn(N).requires_grad_(need_b))
+
+
+def alive(g, kind):
+    gc.collect()
+    return [i for i, (k, r) in enumerate(g.made) if k == kind and r() is not None]
+
+
+def test_nothing_is_kept_after_the_backward_pass():
+    g = Plain()
+    x, w, bias = leaves()
+    y = fp8.linear(g, x, w, bias)
+    assert alive(g, "col") and alive(g, "tile")
+    assert not alive(g, "row")  # the forward product's own copy
+    y.sum().backward()
+    assert not alive(g, "col") and not alive(g, "tile")  # y is alive still
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+    y2 = fp8.linear(g, x, w, bias)
+    y2.sum().backward(retain_graph=True)
+    x.grad = None
+    y2.sum().backward(retain_graph=True)
+    first, x.grad = x.grad, None
+    y2.sum().backward()
+    assert torch.equal(x.grad, first)
