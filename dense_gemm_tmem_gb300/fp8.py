@@ -106,11 +106,16 @@ class Fp8Matrix:
         return self.data.view(torch.float8_e4m3fn).float() * s
 
 
-def linear_forward(g, x: torch.Tensor, w, bias: torch.Tensor | None = None, stream=None):
+def linear_forward(g, x: torch.Tensor, w, bias: torch.Tensor | None = None, stream=None,
+                   need_dw: bool = True):
     """y = x·Wᵀ (+bias) in 8 bits, and what linear_backward needs: x (tokens,
-    inputs) is quantised along both axes in one pass, w is (outputs, inputs) or
-    an Fp8Matrix of it with tile blocks.  y has x's type."""
-    x_row, x_col = g.fp8_quantize(x, "row+col", stream=stream)
+    inputs) is quantised along both axes in one pass (along its rows only when
+    no dW is needed), w is (outputs, inputs) or an Fp8Matrix of it with tile
+    blocks.  y has x's type."""
+    if need_dw:
+        x_row, x_col = g.fp8_quantize(x, "row+col", stream=stream)
+    else:
+        x_row, x_col = g.fp8_quantize(x, "row", stream=stream), None
     if not isinstance(w, Fp8Matrix):
         w = g.fp8_quantize(w, "tile", stream=stream)
     y = g.fp8_matmul(x_row, w, bias, a_major=B.GEMM_ROW_MAJOR, b_major=B.GEMM_COL_MAJOR,
@@ -118,38 +123,60 @@ def linear_forward(g, x: torch.Tensor, w, bias: torch.Tensor | None = None, stre
     return y, (x_col, w)
 
 
-def linear_backward(g, dy: torch.Tensor, saved, stream=None):
+def linear_backward(g, dy: torch.Tensor, saved, stream=None, need_dx: bool = True,
+                    need_dw: bool = True):
     """(dx, dW) of linear_forward for the gradient dy of y: dx = dy·W in dy's
-    type, dW = dyᵀ·x in fp32, dy quantised along both axes in one pass."""
+    type, dW = dyᵀ·x in fp32, dy quantised along both axes in one pass.  One
+    that is not needed is None and costs nothing."""
     x_col, w = saved
-    dy_row, dy_col = g.fp8_quantize(dy, "row+col", stream=stream)
-    dx = g.fp8_matmul(dy_row, w, a_major=B.GEMM_ROW_MAJOR, b_major=B.GEMM_ROW_MAJOR,
-                      out_dtype=dy.dtype, stream=stream)
-    dw = g.fp8_matmul(dy_col, x_col, a_major=B.GEMM_COL_MAJOR, b_major=B.GEMM_ROW_MAJOR,
-                      out_dtype=torch.float32, stream=stream)
+    if need_dw and x_col is None:
+        raise ValueError("linear_forward was told that no dW is needed")
+    dx = dw = dy_row = dy_col = None
+    if need_dx and need_dw:
+        dy_row, dy_col = g.fp8_quantize(dy, "row+col", stream=stream)
+    elif need_dx:
+        dy_row = g.fp8_quantize(dy, "row", stream=stream)
+    elif need_dw:
+        dy_col = g.fp8_quantize(dy, "col", stream=stream)
+    if need_dx:
+        dx = g.fp8_matmul(dy_row, w, a_major=B.GEMM_ROW_MAJOR, b_major=B.GEMM_ROW_MAJOR,
+                          out_dtype=dy.dtype, stream=stream)
+    if need_dw:
+        dw = g.fp8_matmul(dy_col, x_col, a_major=B.GEMM_COL_MAJOR, b_major=B.GEMM_ROW_MAJOR,
+                          out_dtype=torch.float32, stream=stream)
     return dx, dw
 
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, g, x, w, bias):
-        y, (x_col, wq) = linear_forward(g, x, w, bias)
-        ctx.save_for_backward(x_col.data, x_col.scale, wq.data, wq.scale)
-        ctx.g, ctx.w_dtype, ctx.has_bias = g, w.dtype, bias is not None
+    def forward(ctx, g, x, w, bias, need_dx, need_dw):
+        y, (x_col, wq) = linear_forward(g, x, w, bias, need_dw=need_dw)
+        ctx.save_for_backward(*((x_col.data, x_col.scale) if need_dw else (None, None)),
+                              *((wq.data, wq.scale) if need_dx else (None, None)))
+        ctx.g, ctx.w_dtype, ctx.need = g, w.dtype, (need_dx, need_dw)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        dy = dy.contiguous()
+        need_dx, need_dw = ctx.need
         x_data, x_scale, w_data, w_scale = ctx.saved_tensors
-        saved = Fp8Matrix._wrap(x_data, x_scale, "col"), Fp8Matrix._wrap(w_data, w_scale, "tile")
-        dx, dw = linear_backward(ctx.g, dy, saved)
-        return None, dx, dw.to(ctx.w_dtype), dy.float().sum(0) if ctx.has_bias else None
+        dx = dw = None
+        if need_dx or need_dw:
+            dy = dy.contiguous()
+            saved = (Fp8Matrix._wrap(x_data, x_scale, "col") if need_dw else None,
+                     Fp8Matrix._wrap(w_data, w_scale, "tile") if need_dx else None)
+            dx, dw = linear_backward(ctx.g, dy, saved, need_dx=need_dx, need_dw=need_dw)
+        if dw is not None:
+            dw = dw.to(ctx.w_dtype)
+        dbias = dy.float().sum(0) if ctx.needs_input_grad[3] else None
+        return None, dx, dw, dbias, None, None
 
 
 def linear(g, x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None):
     """Differentiable x·wᵀ (+bias) on handle ``g``: products in 8 bits, gradients
     passed straight through the quantisation; x (tokens, inputs) float16,
-    bfloat16 or float32, w (outputs, inputs), bias float32 (outputs,)."""
-    return _Linear.apply(g, x, w, bias)
+    bfloat16 or float32, w (outputs, inputs), bias float32 (outputs,).  What
+    needs no gradient is neither kept nor computed."""
+    grad = torch.is_grad_enabled()
+    return _Linear.apply(g, x, w, bias, grad and x.requires_grad, grad and w.requires_grad)

@@ -74,3 +74,50 @@ def test_nothing_is_kept_after_the_backward_pass():
     first, x.grad = x.grad, None
     y2.sum().backward()
     assert torch.equal(x.grad, first)
+
+
+@pytest.mark.parametrize("need", list(itertools.product([False, True], repeat=3)))
+def test_only_what_is_needed_is_computed_and_kept(need):
+    """Each combination of x, w and bias that require a gradient: the same values as
+    with all of them, and no quantisation, product or kept copy beside."""
+    need_x, need_w, need_b = need
+    whole = leaves()
+    fp8.linear(Plain(), *whole).square().sum().backward()
+    g = Plain()
+    some = leaves(*need)
+    y = fp8.linear(g, *some)
+    assert g.calls == ["row+col" if need_w else "row", "tile", ((T, K), (N, K), F32)]
+    assert bool(alive(g, "col")) == need_w and bool(alive(g, "tile")) == need_x
+    assert not alive(g, "row")
+    if not any(need):
+        assert not y.requires_grad
+        return
+    g.calls.clear()
+    y.square().sum().backward()
+    want = {(True, True): ["row+col"], (True, False): ["row"], (False, True): ["col"],
+            (False, False): []}[need_x, need_w]
+    assert [c for c in g.calls if isinstance(c, str)] == want
+    assert len(g.products()) == need_x + need_w
+    for a, b, n in zip(some, whole, need):
+        assert (a.grad is not None) == n
+        if n:
+            assert torch.equal(a.grad, b.grad)
+
+
+def test_without_a_graph_nothing_is_kept():
+    g = Plain()
+    with torch.no_grad():
+        y = fp8.linear(g, *leaves())
+    assert not y.requires_grad and g.calls[0] == "row"
+    assert not alive(g, "tile")
+
+
+def test_backward_refuses_what_forward_was_told_to_drop():
+    g = Plain()
+    x, w, _ = (t.detach() for t in leaves())
+    y, saved = fp8.linear_forward(g, x, w, need_dw=False)
+    assert saved[0] is None
+    dx, dw = fp8.linear_backward(g, y, saved, need_dw=False)
+    assert dw is None and dx.shape == x.shape
+    with pytest.raises(ValueError):
+        fp8.linear_backward(g, y, saved)
