@@ -124,10 +124,11 @@ def linear_forward(g, x: torch.Tensor, w, bias: torch.Tensor | None = None, stre
 
 
 def linear_backward(g, dy: torch.Tensor, saved, stream=None, need_dx: bool = True,
-                    need_dw: bool = True):
+                    need_dw: bool = True, dw_dtype=torch.float32):
     """(dx, dW) of linear_forward for the gradient dy of y: dx = dy·W in dy's
-    type, dW = dyᵀ·x in fp32, dy quantised along both axes in one pass.  One
-    that is not needed is None and costs nothing."""
+    type, dW = dyᵀ·x summed in fp32 and rounded once to dw_dtype, dy quantised
+    along both axes in one pass.  One that is not needed is None and costs
+    nothing."""
     x_col, w = saved
     if need_dw and x_col is None:
         raise ValueError("linear_forward was told that no dW is needed")
@@ -143,7 +144,7 @@ def linear_backward(g, dy: torch.Tensor, saved, stream=None, need_dx: bool = Tru
                           out_dtype=dy.dtype, stream=stream)
     if need_dw:
         dw = g.fp8_matmul(dy_col, x_col, a_major=B.GEMM_COL_MAJOR, b_major=B.GEMM_ROW_MAJOR,
-                          out_dtype=torch.float32, stream=stream)
+                          out_dtype=dw_dtype, stream=stream)
     return dx, dw
 
 
@@ -166,10 +167,9 @@ class _Linear(torch.autograd.Function):
             dy = dy.contiguous()
             saved = (Fp8Matrix._wrap(x_data, x_scale, "col") if need_dw else None,
                      Fp8Matrix._wrap(w_data, w_scale, "tile") if need_dx else None)
-            dx, dw = linear_backward(ctx.g, dy, saved, need_dx=need_dx, need_dw=need_dw)
-        if dw is not None:
-            dw = dw.to(ctx.w_dtype)
-        dbias = dy.float().sum(0) if ctx.needs_input_grad[3] else None
+            dx, dw = linear_backward(ctx.g, dy, saved, need_dx=need_dx, need_dw=need_dw,
+                                     dw_dtype=ctx.w_dtype)
+        dbias = dy.sum(0, dtype=torch.float32) if ctx.needs_input_grad[3] else None
         return None, dx, dw, dbias, None, None
 
 

@@ -7,6 +7,7 @@ import weakref
 
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 import fp8_reference as R
 from dense_gemm_tmem_gb300 import fp8
@@ -121,3 +122,40 @@ def test_backward_refuses_what_forward_was_told_to_drop():
     assert dw is None and dx.shape == x.shape
     with pytest.raises(ValueError):
         fp8.linear_backward(g, y, saved)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, BF16, F32])
+def test_the_weight_gradient_is_asked_for_in_the_weight_s_type(dtype):
+    """One rounding of the fp32 sums, not a product in fp32 and a pass that casts it."""
+    g = Plain()
+    x, w, bias = leaves(dtype=dtype)
+    y = fp8.linear(g, x, w, bias)
+    g.calls.clear()
+    y.sum().backward()
+    assert [c[2] for c in g.products()] == [dtype, dtype]
+    assert w.grad.dtype == dtype and bias.grad.dtype == F32
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, BF16])
+def test_the_bias_gradient_makes_no_copy_of_dy(dtype):
+    x, w, bias = leaves(False, False, True, dtype)
+    y = fp8.linear(Plain(), x, w, bias)
+    dy, seen = torch.randn(T, N).to(dtype), []
+    with Seen(seen):
+        y.backward(dy)
+    assert not any(shape == (T, N) and t == F32 for _, shape, t in seen)
+    assert torch.equal(bias.grad, dy.float().sum(0))
+
+
+class Seen(TorchDispatchMode):
+    """Notes what runs and what it makes."""
+
+    def __init__(self, out):
+        super().__init__()
+        self.out = out
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        r = func(*args, **(kwargs or {}))
+        if isinstance(r, torch.Tensor):
+            self.out.append((func._schema.name, tuple(r.shape), r.dtype))
+        return r
