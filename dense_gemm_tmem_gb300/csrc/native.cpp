@@ -153,38 +153,64 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-gemm_fp8_matrix_t matrix(PyObject* data, PyObject* scale, PyObject* kind, int64_t device) {
+// Types of a block-scaled matrix's tensors, and the shape of its scales.  They are
+// looked at on every call: a program may replace the tensors of an Fp8Matrix.
+void check_types(const at::Tensor& q, const at::Tensor& s) {
+  if (q.scalar_type() != at::kFloat8_e4m3fn && q.scalar_type() != at::kByte)
+    fail(PyExc_TypeError, "data must be float8_e4m3fn (or its bytes as uint8)");
+  if (s.scalar_type() != at::kFloat) fail(PyExc_TypeError, "scale must be float32");
+}
+void check_scales(const at::Tensor& s, int64_t rows, int64_t cols) {
+  const int64_t d = s.dim();
+  if (s.size(d - 2) != rows || s.size(d - 1) != cols) {
+    PyErr_Format(PyExc_ValueError, "scale has shape (%lld, %lld), expected (%lld, %lld)",
+                 (long long)s.size(d - 2), (long long)s.size(d - 1), (long long)rows,
+                 (long long)cols);
+    throw Raised{};
+  }
+}
+
+gemm_fp8_matrix_t matrix(PyObject* data, PyObject* scale, PyObject* blocks) {
   const at::Tensor& q = tensor(data, "data must be a tensor");
   const at::Tensor& s = tensor(scale, "scale must be a tensor");
   if (q.dim() != 2 || s.dim() != 2) fail(PyExc_ValueError, "A and B must be 2-D");
-  on_device(q, device);
-  on_device(s, device);
+  check_types(q, s);
+  const int64_t kind = integer(blocks);
+  if (kind < GEMM_FP8_ROW || kind > GEMM_FP8_TILE) fail(PyExc_ValueError, "unknown blocks");
+  check_scales(s, kind == GEMM_FP8_ROW ? q.size(0) : blocks_of(q.size(0)),
+               kind == GEMM_FP8_COL ? q.size(1) : blocks_of(q.size(1)));
   return gemm_fp8_matrix_t{q.data_ptr(), pitch_of(q, "rows of data must be contiguous"),
                            static_cast<float*>(s.data_ptr()), s.stride(0), s.stride(1),
-                           int32_t(integer(kind)), 0};
+                           int32_t(kind), 0};
 }
 
-// matmul(handle, device, A data, A scale, A kind, B data, B scale, B kind, bias or
-// None, a_major, b_major, output type as a tensor's code, stream) -> C or a gemm_status_t
-PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    if (n != 13) fail(PyExc_TypeError, "matmul takes 13 arguments");
-    const int64_t device = integer(args[1]);
-    const gemm_fp8_matrix_t a = matrix(args[2], args[3], args[4], device);
-    const gemm_fp8_matrix_t b = matrix(args[5], args[6], args[7], device);
-    const int64_t a_major = integer(args[9]), b_major = integer(args[10]);
-    const int64_t code = integer(args[11]);
+// The arguments that both product calls take: handle, device, A data, A scale, A kind,
+// B data, B scale, B kind, bias or None, a_major, b_major.
+struct Product {
+  gemm_ctx* h;
+  int64_t device;
+  gemm_fp8_matrix_t a, b;
+  int64_t a_major, b_major, M, N, K;
+  const float* bias = nullptr;
+  explicit Product(PyObject* const* args)
+      : h(address<gemm_ctx>(args[0])),
+        device(integer(args[1])),
+        a(matrix(args[2], args[3], args[4])),
+        b(matrix(args[5], args[6], args[7])),
+        a_major(integer(args[9])),
+        b_major(integer(args[10])) {
+    for (int i : {2, 3, 5, 6}) on_device(THPVariable_Unpack(args[i]), device);
     const at::Tensor& qa = THPVariable_Unpack(args[2]);
     const at::Tensor& qb = THPVariable_Unpack(args[5]);
     const bool ar = a_major == GEMM_ROW_MAJOR, br = b_major == GEMM_ROW_MAJOR;
-    const int64_t M = qa.size(ar ? 0 : 1), K = qa.size(ar ? 1 : 0);
-    const int64_t N = qb.size(br ? 1 : 0);
+    M = qa.size(ar ? 0 : 1);
+    K = qa.size(ar ? 1 : 0);
+    N = qb.size(br ? 1 : 0);
     if (qb.size(br ? 0 : 1) != K) {
       PyErr_Format(PyExc_ValueError, "inner dimensions differ: %lld vs %lld", (long long)K,
                    (long long)qb.size(br ? 0 : 1));
       throw Raised{};
     }
-    const float* bias = nullptr;
     if (args[8] != Py_None) {
       const at::Tensor& t = tensor(args[8], "bias must be a tensor");
       if (t.scalar_type() != at::kFloat || t.dim() != 1 || t.size(0) != N || !t.is_contiguous())
@@ -192,18 +218,50 @@ PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
       on_device(t, device);
       bias = static_cast<const float*>(t.data_ptr());
     }
+  }
+  int run(void* C, int64_t ldc, int code, PyObject* stream) const {
+    return run_fn(h, M, N, K, &a, &b, bias, C, ldc, int(a_major), int(b_major), code,
+                  address<void>(stream));
+  }
+};
+
+// matmul(the product's arguments, output type's code, stream) -> C or a gemm_status_t
+PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 13) fail(PyExc_TypeError, "matmul takes 13 arguments");
+    const Product p(args);
+    const int64_t code = integer(args[11]);
     const at::ScalarType type = code == GEMM_F16    ? at::kHalf
                                 : code == GEMM_BF16 ? at::kBFloat16
                                                     : at::kFloat;
-    at::Tensor C = at::empty({M, N}, qa.options().dtype(type).requires_grad(false));
-    const int rc = run_fn(address<gemm_ctx>(args[0]), M, N, K, &a, &b, bias, C.data_ptr(), N,
-                          int(a_major), int(b_major), int(code), address<void>(args[12]));
+    at::Tensor C = at::empty({p.M, p.N},
+                             THPVariable_Unpack(args[2]).options().dtype(type).requires_grad(false));
+    const int rc = p.run(C.data_ptr(), p.N, int(code), args[12]);
     if (rc != GEMM_OK) return PyLong_FromLong(rc);
     return THPVariable_Wrap(std::move(C));
   });
 }
 
-gemm_fp8_experts_t experts(PyObject* data, PyObject* scale, int64_t device, int64_t E, int64_t rows,
+// run(the product's arguments, C, stream) -> a gemm_status_t
+PyObject* run(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 13) fail(PyExc_TypeError, "run takes 13 arguments");
+    const Product p(args);
+    const at::Tensor& C = tensor(args[11], "C must be a tensor");
+    const int code = code_of(C.scalar_type());
+    if (code < 0) fail(PyExc_TypeError, "C must be float16, bfloat16 or float32");
+    if (C.dim() != 2 || C.size(0) != p.M || C.size(1) != p.N) {
+      PyErr_Format(PyExc_ValueError, "C must have shape (%lld, %lld)", (long long)p.M,
+                   (long long)p.N);
+      throw Raised{};
+    }
+    on_device(C, p.device);
+    const int64_t ldc = pitch_of(C, "rows of C must be contiguous and not overlap");
+    return PyLong_FromLong(p.run(C.data_ptr(), ldc, code, args[12]));
+  });
+}
+
+gemm_fp8_experts_t experts(PyObject* data, PyObject* scale, int64_t E, int64_t rows,
                            int64_t cols) {
   const at::Tensor& q = tensor(data, "data must be a tensor");
   const at::Tensor& s = tensor(scale, "scale must be a tensor");
@@ -216,8 +274,10 @@ gemm_fp8_experts_t experts(PyObject* data, PyObject* scale, int64_t device, int6
                  (long long)rows, (long long)cols);
     throw Raised{};
   }
-  on_device(q, device);
-  on_device(s, device);
+  check_types(q, s);
+  if (s.size(0) != E) fail(PyExc_ValueError, "scale must have one matrix per expert");
+  check_scales(s, blocks_of(rows), blocks_of(cols));
+  if (cols > 1 && q.stride(2) != 1) fail(PyExc_ValueError, "rows of data must be contiguous");
   return gemm_fp8_experts_t{q.data_ptr(),
                             rows > 1 ? q.stride(1) : std::max(q.stride(1), cols),
                             q.stride(0),
@@ -242,8 +302,6 @@ PyObject* moe(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (x.scalar_type() != router.scalar_type() ||
         (x.scalar_type() != at::kHalf && x.scalar_type() != at::kBFloat16))
       fail(PyExc_TypeError, "x and router: both float16 or both bfloat16");
-    on_device(x, device);
-    on_device(router, device);
     gemm_moe_fp8_t L = {};
     L.tokens = x.size(0);
     L.hidden = x.size(1);
@@ -256,9 +314,10 @@ PyObject* moe(PyObject*, PyObject* const* args, Py_ssize_t n) {
     L.top_k = int32_t(std::min<int64_t>(top_k, INT32_MAX));
     L.renormalize = int32_t(integer(args[11]));
     L.dtype = code_of(x.scalar_type());
-    L.gate = experts(args[4], args[5], device, L.experts, L.inner, L.hidden);
-    L.up = experts(args[6], args[7], device, L.experts, L.inner, L.hidden);
-    L.down = experts(args[8], args[9], device, L.experts, L.hidden, L.inner);
+    L.gate = experts(args[4], args[5], L.experts, L.inner, L.hidden);
+    L.up = experts(args[6], args[7], L.experts, L.inner, L.hidden);
+    L.down = experts(args[8], args[9], L.experts, L.hidden, L.inner);
+    for (int i = 2; i < 10; ++i) on_device(THPVariable_Unpack(args[i]), device);
     L.x = x.data_ptr();
     L.ld_x = pitch_of(x, "rows of x must be contiguous and not overlap");
     L.router = router.data_ptr();
@@ -291,6 +350,7 @@ PyMethodDef methods[] = {
     {"init", reinterpret_cast<PyCFunction>(init), METH_FASTCALL, nullptr},
     {"quantize", reinterpret_cast<PyCFunction>(quantize), METH_FASTCALL, nullptr},
     {"matmul", reinterpret_cast<PyCFunction>(matmul), METH_FASTCALL, nullptr},
+    {"run", reinterpret_cast<PyCFunction>(run), METH_FASTCALL, nullptr},
     {"moe", reinterpret_cast<PyCFunction>(moe), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

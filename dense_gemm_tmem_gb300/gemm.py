@@ -178,30 +178,9 @@ class Gemm:
         float16, bfloat16 or float32, unit stride along its rows).  A is stored
         (M, K) row-major or (K, M) column-major, B (K, N) or (N, K); the blocks
         of each must run along K."""
-        if len(A.shape) != 2 or len(Bm.shape) != 2:
-            raise ValueError("A and B must be 2-D")
-        M, K = A.shape if a_major == ROW else A.shape[::-1]
-        Kb, N = Bm.shape if b_major == ROW else Bm.shape[::-1]
-        if K != Kb:
-            raise ValueError("inner dimensions differ: %d vs %d" % (K, Kb))
-        idx = self.device.index
-        for t in (A.data, Bm.data, C) + ((bias,) if bias is not None else ()):
-            if t.get_device() != idx:
-                raise ValueError("tensor on %s, handle on %s" % (t.device, self.device))
-        code = _DT8.get(C.dtype)
-        if code is None:
-            raise TypeError("C must be float16, bfloat16 or float32, got %s" % C.dtype)
-        if C.dim() != 2 or C.shape[0] != M or C.shape[1] != N:
-            raise ValueError("C has shape %s, expected (%d, %d)" % (tuple(C.shape), M, N))
-        sr, sc = C.stride()
-        if (N > 1 and sc != 1) or (M > 1 and sr < N):
-            raise ValueError("rows of C must be contiguous and not overlap")
-        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,)
-                                 or not bias.is_contiguous()):
-            raise ValueError("bias must be contiguous float32 of shape (N,)")
-        rc = B.gemm_fp8_run(self.handle, M, N, K, A.desc(), Bm.desc(),
-                            bias.data_ptr() if bias is not None else None, C.data_ptr(),
-                            max(sr, N), a_major, b_major, code, self._raw_stream(stream))
+        rc = self._native.run(self.handle, self.device.index, A.data, A.scale, A.kind, Bm.data,
+                              Bm.scale, Bm.kind, bias, a_major, b_major, C,
+                              self._raw_stream(stream))
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_fp8_run")
 
