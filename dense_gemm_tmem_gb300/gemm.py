@@ -28,6 +28,16 @@ _KINDS = {"row": (B.GEMM_FP8_ROW, -1), "col": (B.GEMM_FP8_COL, -1),
           "tile": (B.GEMM_FP8_TILE, -1), "row+col": (B.GEMM_FP8_ROW, B.GEMM_FP8_COL)}
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _in_use(stream, *tensors):
+    """The allocator keeps the tensors' memory until the stream has passed this point,
+    though they are another stream's and may be dropped meanwhile."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 _LAYOUTS = {}  # (a_major, b_major, in, out) -> gemm_layout_t, built once
 
 
@@ -155,11 +165,14 @@ class Gemm:
         """x (rows, cols; float16, bfloat16 or float32, unit stride along its
         rows) as an Fp8Matrix with "row", "col" or "tile" blocks, or, for
         "row+col", a pair of them from one pass over x.  With a stream, here and
-        in fp8_matmul and moe_fp8, the tensors that the call makes are
-        allocated on it; order it after what wrote the inputs."""
+        in fp8_run, fp8_matmul and moe_fp8, the tensors that the call makes are
+        allocated on it, and those that it is given may be dropped at once;
+        order it after what wrote the inputs."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.fp8_quantize(x, blocks)
+                r = self.fp8_quantize(x, blocks)
+            _in_use(stream, x)
+            return r
         kinds = _KINDS.get(blocks)
         if kinds is None:
             raise ValueError("blocks must be 'row', 'col', 'tile' or 'row+col', got %r"
@@ -183,13 +196,17 @@ class Gemm:
                               self._raw_stream(stream))
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_fp8_run")
+        if stream is not None:
+            _in_use(stream, A.data, A.scale, Bm.data, Bm.scale, bias, C)
 
     def fp8_matmul(self, A: Fp8Matrix, Bm: Fp8Matrix, bias=None, a_major=ROW, b_major=ROW,
                    out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """A·B (+bias) as a new tensor (see fp8_run)."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.fp8_matmul(A, Bm, bias, a_major, b_major, out_dtype)
+                C = self.fp8_matmul(A, Bm, bias, a_major, b_major, out_dtype)
+            _in_use(stream, A.data, A.scale, Bm.data, Bm.scale, bias)
+            return C
         code = _DT8.get(out_dtype)
         if code is None:
             raise TypeError("out_dtype must be float16, bfloat16 or float32, got %s" % out_dtype)
@@ -209,7 +226,9 @@ class Gemm:
         float32; the arithmetic is that of gemm_moe_fp8."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.moe_fp8(x, router, gate, up, down, top_k, renormalize)
+                r = self.moe_fp8(x, router, gate, up, down, top_k, renormalize)
+            _in_use(stream, x, router, *(t for w in (gate, up, down) for t in (w.data, w.scale)))
+            return r
         r = self._native.moe(self.handle, self.device.index, x, router, gate.data, gate.scale,
                              up.data, up.scale, down.data, down.scale, top_k,
                              1 if renormalize else 0, _current_raw(self.device.index))
