@@ -144,10 +144,13 @@ _native = None
 
 
 def native():
-    """The extension module (csrc/native.cpp), pointed at the loaded library."""
+    """The extension module (csrc/native.cpp), pointed at the loaded library; built
+    for the installed Python and torch if there is none."""
     global _native
     if _native is None:
         lib = load()
+        if not _build.native_up_to_date():
+            _build.build_native()
         spec = importlib.util.spec_from_file_location("_dgemm_native", _build.NATIVE)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)

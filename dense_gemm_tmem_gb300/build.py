@@ -3,15 +3,20 @@
 Each translation unit is compiled for sm_103a only, in parallel, then linked
 with nvcc (static CUDA runtime; the driver is reached at run time through the
 runtime's entry-point query, so the library loads on a machine without a GPU).
-Beside it, _build/_dgemm_native.so: the tensor-facing calls (csrc/native.cpp)
-as a Python extension against the installed torch.
+Beside it, _build/_dgemm_native-*.so: the 8-bit operators' tensor-facing calls
+(csrc/native.cpp) as a Python extension against the installed torch.  Only those
+calls need it: where it cannot be built (no host compiler, Python or torch
+headers), the library is there all the same and they say why.
 """
 from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import subprocess
+import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,7 +24,19 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdgemm_gb300.so")
-NATIVE = os.path.join(OUT_DIR, "_dgemm_native.so")
+def _torch_version() -> str:
+    """torch.__version__, without importing it where its file says it plainly."""
+    try:
+        where = importlib.util.find_spec("torch").submodule_search_locations[0]
+        with open(os.path.join(where, "version.py")) as f:
+            return re.search(r"^__version__ = ['\"]([^'\"]+)['\"]", f.read(), re.M).group(1)
+    except (AttributeError, OSError):
+        return "none"
+
+
+# the extension links against torch's C++ and Python's C interface: one for each pair
+NATIVE = os.path.join(OUT_DIR, "_dgemm_native-%s-torch%s.so"
+                      % (sys.implementation.cache_tag, _torch_version()))
 NATIVE_SOURCE = os.path.join(CSRC, "native.cpp")
 SOURCES = ["api.cu", "simt.cu", "simt_f16.cu", "selftest.cu", "noalloc.cu", "tc2.cu",
            "tc_n256.cu", "tc_n128.cu", "tc_small.cu", "tc_narrow.cu", "tc64.cu",
@@ -53,12 +70,16 @@ def _newer(target, files) -> bool:
 
 
 def up_to_date() -> bool:
-    return (_newer(LIB, _inputs())
-            and _newer(NATIVE, _inputs()[-2:] + [NATIVE_SOURCE]))
+    return _newer(LIB, _inputs())
 
 
-def _build_native():
+def native_up_to_date() -> bool:
+    return _newer(NATIVE, _inputs()[-2:] + [NATIVE_SOURCE])
+
+
+def build_native() -> str:
     """Compiles the Python extension with the host compiler."""
+    os.makedirs(OUT_DIR, exist_ok=True)
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     tmp = NATIVE + ".tmp%d" % os.getpid()
@@ -70,11 +91,23 @@ def _build_native():
     if r.returncode != 0:
         raise RuntimeError("%s failed:\n%s\n%s" % (cmd[0], r.stdout, r.stderr))
     os.replace(tmp, NATIVE)
+    return NATIVE
+
+
+def _native_if_possible():
+    try:
+        build_native()
+    except (OSError, RuntimeError, AttributeError) as e:
+        warnings.warn("the 8-bit operators' Python calls are not available: %s" % e)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles and links the library unless it is newer than every source."""
+    """Compiles and links the library unless it is newer than every source, and the
+    extension likewise, whose failure is a warning."""
+    native = force or not native_up_to_date()
     if not force and up_to_date():
+        if native:
+            _native_if_possible()
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -90,9 +123,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        native = ex.submit(_build_native)
+        extension = ex.submit(_native_if_possible) if native else None
         objs = list(ex.map(compile_one, SOURCES))
-        native.result()
+        if extension:
+            extension.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -2,6 +2,8 @@
 the current CUDA stream.  PyTorch supplies device memory and streams only."""
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import binding as B
@@ -58,7 +60,6 @@ class Gemm:
             dev = torch.device("cuda", 0)
         self.device = dev
         self.handle = B.gemm_create(dev.index)
-        self._native = B.native()
         self._run = B.load().gemm_run  # argument types set once by the binding
 
     def close(self):
@@ -156,6 +157,11 @@ class Gemm:
         return p.as_dict()
 
     # ---- block-scaled 8-bit operators (include/gemm_fp8.h)
+    @functools.cached_property
+    def _native(self):
+        """The extension, which only these calls need: loaded at the first of them."""
+        return B.native()
+
     def _raw_stream(self, stream):
         """The stream's handle, without building a Stream object for the current
         one (2 us of a call's 10)."""
