@@ -401,7 +401,7 @@ __device__ __forceinline__ void tc2_mma(const TcArgs& args, uint8_t* sA, uint8_t
       aph ^= 1;
     }
   }
-  if (!ok && any) {  // every MMA issued so far must finish before TMEM is freed
+  if (any) {  // every MMA finishes before TMEM is freed, also when the epilogue gave up
     tc_commit_pair_self(smem_u32(drain));
     wait_drain(smem_u32(drain), 0, wc);
   }

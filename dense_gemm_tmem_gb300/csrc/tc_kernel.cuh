@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           aph ^= 1;
         }
       }
-      if (!ok && any) {  // every MMA issued so far must finish before TMEM is freed
+      if (any) {  // every MMA finishes before TMEM is freed, also when the epilogue gave up
         tc_commit(smem_u32(drain));
         wait_drain(smem_u32(drain), 0, wc);
       }
