@@ -495,8 +495,8 @@ __device__ __forceinline__ void moe_choose(const MoeArgs& a, MoeRoute& r, int32_
   }
 }
 
-// Every warp of the CTA: the experts of its tokens; then who chose whom, the
-// lists and the work ranges.
+// Every warp of the CTA: the experts of its tokens; then, by one, who was chosen and
+// where each expert's picks begin.
 __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r) {
   const gemm_moe_fp8_t& L = a.L;
   const int32_t T = int32_t(L.tokens), E = int32_t(L.experts);
@@ -530,7 +530,6 @@ __device__ __forceinline__ void moe_phase_b(const MoeArgs& a, MoeRoute& r) {
     }
     if (tid == 0) r.active = active;
   }
-  __syncthreads();
   __syncthreads();
 }
 

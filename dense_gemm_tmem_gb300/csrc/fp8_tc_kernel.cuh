@@ -91,7 +91,8 @@ struct Fp8TcConfig {
   static_assert(kBM * kParkRow * 4 <= kStages * kStageBytes &&
                 BN * kParkCol * 4 <= kStages * kStageBytes, "the ring holds it");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
-  static_assert((2 * kStages + 2 * kBuffers + 1 + 2 * kScaleRing) * 8 + 16 <= kBarBytes, "barrier area");
+  static_assert((2 * kStages + 2 * kBuffers + 1 + 2 * kScaleRing) * 8 + 16 <= kBarBytes,
+                "barrier area");
 };
 
 // One operand's scales in the MMA view: row (or column) r of k-block kb at
@@ -443,7 +444,7 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float (&
   constexpr int PER = 64 / SIZE;               // columns a pass
   constexpr int VEC = 16 / SIZE;               // columns a lane stores
   constexpr int LD = 20;                       // floats a staged row
-  static_assert(HC % 16 == 0, "whole passes, or half of one");
+  static_assert(HC % PER == 0, "whole passes");
   const bool f16 = a.out_dtype == GEMM_F16;
   const int piece = lane & 3, rs = lane >> 2;
 #pragma unroll
@@ -456,21 +457,18 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float (&
         const float b = a.bias && nn0 + c + j < a.Nm ? __ldg(a.bias + nn0 + c + j) : 0.f;
         w[j] = __float_as_uint(acc[c + j] + b);
       } else {
-        w[j] = 0;
-        if (c + 2 * j < HC) {
-          float2 x = make_float2(acc[c + 2 * j], acc[c + 2 * j + 1]);
-          if (a.bias) {
-            const int32_t n = nn0 + c + 2 * j;
-            if (n < a.Nm) x.x += __ldg(a.bias + n);
-            if (n + 1 < a.Nm) x.y += __ldg(a.bias + n + 1);
-          }
-          if (f16) {
-            const __half2 h = __floats2half2_rn(x.x, x.y);
-            __builtin_memcpy(&w[j], &h, 4);
-          } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-            __builtin_memcpy(&w[j], &h, 4);
-          }
+        float2 x = make_float2(acc[c + 2 * j], acc[c + 2 * j + 1]);
+        if (a.bias) {
+          const int32_t n = nn0 + c + 2 * j;
+          if (n < a.Nm) x.x += __ldg(a.bias + n);
+          if (n + 1 < a.Nm) x.y += __ldg(a.bias + n + 1);
+        }
+        if (f16) {
+          const __half2 h = __floats2half2_rn(x.x, x.y);
+          __builtin_memcpy(&w[j], &h, 4);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+          __builtin_memcpy(&w[j], &h, 4);
         }
       }
     }
@@ -479,13 +477,11 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float (&
     for (int j = 0; j < 4; ++j)
       own[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     __syncwarp();
-    const int32_t cols = min(HC - c, PER);     // of this pass
-    if (a.c_vec && nn0 + c + cols <= a.Nm) {
+    if (a.c_vec && nn0 + c + PER <= a.Nm) {
       uint4 x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         x[i] = *reinterpret_cast<const uint4*>(stage_w + (i * 8 + rs) * LD + 4 * piece);
-      if (piece * VEC >= cols) continue;
       const int32_t r0 = mrow0 + rs;
       uint8_t* p = static_cast<uint8_t*>(a.C) +
                    (int64_t(r0) * a.ldc + nn0 + c + piece * VEC) * SIZE;
@@ -500,7 +496,7 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float (&
       using E = typename std::conditional<SIZE == 4, uint32_t, uint16_t>::type;
       const int col = lane % PER, r0 = lane / PER;
       const E* from = reinterpret_cast<const E*>(stage_w + r0 * LD) + col;
-      const bool in = col < cols && nn0 + c + col < a.Nm;
+      const bool in = nn0 + c + col < a.Nm;
       E* p = static_cast<E*>(a.C) + int64_t(mrow0 + r0) * a.ldc + nn0 + c + col;
       constexpr int kStep = 32 / PER;          // rows an instruction
 #pragma unroll 4
@@ -773,7 +769,7 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, const CUtenso
       }
       return;
     }
-    if (TRANS) {
+    if constexpr (TRANS) {
       if (mm < args.Mm) {
         const float bv = bias ? __ldg(bias + mm) : 0.f;
 #pragma unroll
@@ -782,11 +778,12 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, const CUtenso
             store_typed(args.C, int64_t(nn0 + j) * args.ldc + mm,
                         acc[j] + bv, args.out_dtype);
       }
-    } else if (BN == 256 && args.c_tma) {
-      f8_store_tma<HC, OUT32 ? 4 : 2>(args, tmC, acc, smem_u32(stage_w), mrow0 + q * 32, lane,
-                                      nn0);
     } else {
-      f8_store_rows<HC, OUT32 ? 4 : 2>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
+      constexpr int SIZE = OUT32 ? 4 : 2;
+      if (BN == 256 && args.c_tma)
+        f8_store_tma<HC, SIZE>(args, tmC, acc, smem_u32(stage_w), mrow0 + q * 32, lane, nn0);
+      else
+        f8_store_rows<HC, SIZE>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
     }
   }
   // every store this warp issued has landed before the CTA moves on
