@@ -52,10 +52,17 @@ constexpr int kF8EpiWarps = 8;
 constexpr int kF8RoleWarps = 4;  // producer, MMA issuer, two scale loaders: one warpgroup
 constexpr int kF8ScaleThreads = 64;
 constexpr int kF8Threads = 32 * (kF8RoleWarps + kF8EpiWarps);
-// Registers a thread: 3 warpgroups launch with 168 each (504 in all); for a
-// 256-wide tile, whose epilogue threads keep 128 sums, the role warpgroup gives
-// up all but 40 and the epilogue's two take 232 each (40 + 2 * 232 = 504).
+// Registers a thread: 3 warpgroups launch with 168 each (504 in all).  Where the
+// epilogue needs more, the role warpgroup gives up all but 40 (its scale loaders then
+// spill some 100 bytes, beside the main loop) and the epilogue's two take 232 each (40
+// + 2 * 232 = 504): for 256-wide tiles, 128 sums a thread, and for 128-wide ones with a
+// scale per column.  Measured, with / without, us: 128-wide with columns' scales, dW of
+// 1024^3 8.8 / 11.7, of 1000 x 2000 x 4096 23.2 / 33.7, transposed 128 x 1024 x 8192
+// 11.0 / 11.2 but 100 x 4096 x 4096 12.2 / 11.7; with tile scales, which take no part,
+// 1001 x 2050 x 4100 18.9 / 18.5, 700 x 2048 x 2048 10.3 / 9.9.
 constexpr int kF8RoleRegs = 40, kF8EpiRegs = 232;
+template <int BN, bool COLVEC>
+constexpr bool kF8SplitRegs = BN == 256 || (BN == 128 && COLVEC);
 
 template <int BN>
 struct Fp8TcConfig {
@@ -934,12 +941,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint32_t filled = 0;
   bool issued = false;
   if (warp >= kF8RoleWarps) {
-    if (BN >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
+    if constexpr (kF8SplitRegs<BN, COLVEC>)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8EpiRegs));
     f8_epilogue<BN, TRANS, COLVEC, OUT32>(args, &tmC, smem_u32(acc_full), smem_u32(acc_empty),
                                    smem_u32(sc_full), smem_u32(sc_empty), wc, tmem_base, stage,
                                    ring, reinterpret_cast<float*>(smem));
   } else {
-    if (BN >= 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RoleRegs));
+    if constexpr (kF8SplitRegs<BN, COLVEC>)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RoleRegs));
     if (warp == 0 && lane == 0) {
       filled = f8_producer<BN>(mA, mB, args, sA, sB, full, empty, wc);
     } else if (warp == 1) {
