@@ -48,10 +48,10 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t w) {
 // A k-block's term of a product is P a b: its sum P and the two operands' scales.  |P|
 // is 0 or at least 2^-18, and at most 2^25, but a b may pass fp32's range, or lose
 // bits below 2^-126, where the term is an ordinary number (a block whose maximum is
-// 1e30 against one of 1e14 where the other operand is zero: inf * 0).  So either a b
-// is formed only where it is a normal number, and otherwise P meets the scale of
-// smaller magnitude first, or P meets one of them first whatever they are, which is
-// right for scales between 2^-109 and 2^103.
+// 1e30 against one of 1e14 where the other operand is zero: inf * 0).  So a b is
+// formed only where it is a normal number; otherwise P meets the scale of smaller
+// magnitude first, or one of the two whatever they are, which is right for scales
+// between 2^-109 and 2^103.
 __device__ __forceinline__ bool scale_fits(float ab) {
   return fabsf(ab) <= 0x1.fffffep127f && fabsf(ab) >= 0x1p-126f;  // NaN does not
 }
@@ -61,8 +61,6 @@ __device__ __forceinline__ void scale_order(float a, float b, float& lo, float& 
   hi = less ? b : a;
 }
 __device__ __forceinline__ float add_scaled(float acc, float P, float a, float b) {
-  const float ab = a * b;
-  if (scale_fits(ab)) return fmaf(P, ab, acc);
   float lo, hi;
   scale_order(a, b, lo, hi);
   return fmaf(__fmul_rn(P, lo), hi, acc);
