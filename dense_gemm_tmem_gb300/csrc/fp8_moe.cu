@@ -31,7 +31,7 @@
 //
 // Measured, weights from HBM: 32 tokens, 8 of 128 experts of 4096 x 1024: 231 to
 // 235 us, 6.0 TB/s, 88 % of a copy's rate, so HBM bounds it; one token, 8 of 64 of 2048 x
-// 1024: 28.7 us, of which 50 MB take 7.5: the rest is four grid barriers, code
+// 1024: 29.1 us, of which 50 MB take 7.5: the rest is four grid barriers, code
 // fetched cold and each phase's first loads.  ĥ formed by every CTA for its own
 // tiles instead of once spares a barrier (28.5 us for the one token) but takes
 // 173 instead of 92 us for 64 tokens, 2 of 16 experts of 4096 x 2048.
@@ -1024,7 +1024,8 @@ struct MoeSmem {
   static constexpr int kBars = 2 * kMoeStages + 2 * kMoeBuffers + 2 * 2 + 2 * kMoeScaleRing + 1 +
                                2 * kMoeSegs;
   static constexpr int words = bars + kBars * 8;
-  static constexpr int bytes = 1024 + words + 32;  // TMEM, abort, barrier, abort in phase E, builders (2)
+  // TMEM, abort, barrier, abort in phase E, builders (2)
+  static constexpr int bytes = 1024 + words + 32;
 };
 static_assert(MoeSmem::bytes <= 227 * 1024, "shared memory per CTA");
 

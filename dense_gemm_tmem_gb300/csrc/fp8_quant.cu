@@ -15,8 +15,13 @@
 // 16-bit sources (8192 x 8192 bf16 both ways: 53 us with three, 48 with four,
 // 5.7 TB/s of the 6.8 a copy reaches here).  For fp32 ones the tile alone takes 64
 // registers: three CTAs for 128 x 128 and 128 x 1 blocks (2050 x 5000 tiles 10.6 us
-// with two, 9.6 with three), two where rows are kept as well (8192 x 8192 both ways
-// 69.6 us, 79.6 with three, which spill).
+// with two, 9.6 with three; 8192 x 8192 columns 53.3 and 51.3, though they spill 60
+// bytes: 2050 x 5000 11.8 and 12.0, 2048 x 4101, which 16-byte loads cannot read, 13.7
+// and 16.1), two where rows are kept as well (8192 x 8192 both ways 69.6 us, 79.6 with
+// three, which spill; 4096 x 4096 rows 18.1 and 19.3).
+// Rows that 16-byte loads cannot read (an odd pitch, an unaligned base) are read element
+// by element: 8192 x 8191 bf16 rows 70 us, 8192 x 8192 36; 2048 x 4101 11.7, 2048 x 4096
+// 8.2.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -125,10 +125,10 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
   // largest whose clusters are all resident at once, if that takes more than
   // kSplitGain k-blocks off each CTA: adding the partials costs about as long as
   // 8 k-blocks (2 us of 0.28 at 32 columns, 3 of 0.35 at 64, 4.3 of 0.51 at 128).
-  // Measured (graph replay, cold inputs, us, split / whole): 1 x 4096 x 4096 7.5
-  // / 12.0, 64 x 4096 x 4096 9.4 / 14.6, 128 x 1024 x 8192 11.3 / 36.5, 512 x 512
-  // x 2048 7.3 / 7.9; not taken: 515 x 1000 x 2056 12.2 / 10.8, 1024^3 10.4 / 7.1
-  // (both 128 wide), 32 x 2048 x 1024 5.4 / 5.1.
+  // Measured (graph replay, cold inputs, us, split / whole): 1 x 4096 x 4096 8.4
+  // / 12.4, 64 x 4096 x 4096 9.9 / 14.2, 128 x 1024 x 8192 11.0 / 31.9, 512 x 512
+  // x 2048 7.4 / 7.8; not taken: 515 x 1000 x 2056 15.7 / 9.2, 1024^3 14.0 / 6.0,
+  // 32 x 2048 x 1024 5.3 / 5.2.
   constexpr int64_t kSplitGain = 8;
   const int forced = h->opt.csplit;  // GEMM_OPT_CLUSTER_SPLIT
   auto split_of = [&](int64_t T) -> int64_t {
@@ -142,9 +142,9 @@ cudaError_t launch_fp8_tc(gemm_ctx* h, const Fp8Product& p, cudaStream_t stream)
     return 1;
   };
   // Tiles of 64 columns instead of 128 where both leave SMs idle (B K-major, whose
-  // boxes may have 64 rows): 515 x 1000 x 2056 9.3 us instead of 10.9, 1024^3 6.1
-  // instead of 7.2, 256 x 1024 x 4096 8.7 instead of 10.6; but over a deep K, where
-  // the wider tiles can be split further, 512 x 1024 x 8192 15.4 instead of 14.4.
+  // boxes may have 64 rows): 515 x 1000 x 2056 9.2 us instead of 10.8, 1024^3 6.0
+  // instead of 7.0, 256 x 1024 x 4096 8.7 instead of 9.4; but over a deep K, where
+  // the wider tiles can be split further, 512 x 1024 x 8192 15.2 instead of 13.0.
   constexpr int64_t kDeepK = 48;  // k-blocks
   int bn;
   if (trans) {

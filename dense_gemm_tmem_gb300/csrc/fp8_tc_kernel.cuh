@@ -20,15 +20,16 @@
 //                      by the epilogue, two k-blocks ahead, their latency cost 180
 //                      of 656 us at 8192^3.
 //   warps 4-11         epilogue, two warpgroups of BN / 2 columns: TMEM ->
-//                      registers, acc += (sa sb) * P, and the buffer goes back.
-//                      A 128 x 256 tile keeps 128 fp32 sums a thread.
+//                      registers, acc += (sa sb) P, or, with a scale per column,
+//                      (P sb) sa, and the buffer goes back (fp8.cuh says why in
+//                      this order).  A 128 x 256 tile keeps 128 fp32 sums a thread.
 //                      (C of 256-wide tiles leaves by TMA from staged boxes, so
 //                      that the next tile is summed meanwhile.)
 // What bounds it: nothing alone.  A k-block of a 128 x 256 tile takes the tensor
 // pipe 512 cycles, the epilogue 256 issue slots of FMAs a scheduler and as many
 // cycles of TMEM reads, and two buffers of 256 columns are all the TMEM there is
-// to overlap them: 1020 cycles a k-block, 8192^3 in 473 us (2322 TFLOP/s).  With
-// an eighth of the FMAs 396, a quarter of the MMAs 417, one TMEM read of eight
+// to overlap them: 1015 cycles a k-block, 8192^3 in 471 us (2334 TFLOP/s).  With
+// a sixteenth of the FMAs 396, a quarter of the MMAs 417, one TMEM read of eight
 // 451, a third of the loads 478 of the 487 it then was.  The tile belongs to one
 // SM because on CTA pairs (cta_group::2, 256 x 256) each hand-over crosses SMs
 // (727 against 656 us with the same, slower epilogue), and the loads that a pair
@@ -179,7 +180,7 @@ __device__ __forceinline__ void fma_tmem2(float& d, float lo, float hi, uint32_t
 }
 
 // (x a, y b) with a and b likewise, one instruction.  (A scale per column is a
-// product per element on top of the FMA: 105 us instead of 73 at 4096^3.)
+// product per element on top of the FMA: 104 us instead of 74 at 4096^3.)
 __device__ __forceinline__ float2 mul2_tmem(float x, float y, uint32_t a, uint32_t b) {
   float2 r;
   asm volatile(

@@ -234,8 +234,8 @@ PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::ScalarType type = code == GEMM_F16    ? at::kHalf
                                 : code == GEMM_BF16 ? at::kBFloat16
                                                     : at::kFloat;
-    at::Tensor C = at::empty({p.M, p.N},
-                             THPVariable_Unpack(args[2]).options().dtype(type).requires_grad(false));
+    const auto opt = THPVariable_Unpack(args[2]).options().dtype(type).requires_grad(false);
+    at::Tensor C = at::empty({p.M, p.N}, opt);
     const int rc = p.run(C.data_ptr(), p.N, int(code), args[12]);
     if (rc != GEMM_OK) return PyLong_FromLong(rc);
     return THPVariable_Wrap(std::move(C));

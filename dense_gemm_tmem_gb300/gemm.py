@@ -173,7 +173,9 @@ class Gemm:
         "row+col", a pair of them from one pass over x.  With a stream, here and
         in fp8_run, fp8_matmul and moe_fp8, the tensors that the call makes are
         allocated on it, and those that it is given may be dropped at once;
-        order it after what wrote the inputs."""
+        order it after what wrote the inputs.  None of them is differentiable:
+        their results carry no gradient, whatever the inputs require
+        (fp8.linear differentiates)."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 r = self.fp8_quantize(x, blocks)
@@ -207,7 +209,7 @@ class Gemm:
 
     def fp8_matmul(self, A: Fp8Matrix, Bm: Fp8Matrix, bias=None, a_major=ROW, b_major=ROW,
                    out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
-        """A·B (+bias) as a new tensor (see fp8_run)."""
+        """A·B (+bias) as a new tensor (see fp8_run), which carries no gradient."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 C = self.fp8_matmul(A, Bm, bias, a_major, b_major, out_dtype)
@@ -229,7 +231,7 @@ class Gemm:
         router (experts, hidden) float16 or bfloat16, gate and up Fp8Matrix
         (experts, inner, hidden), down (experts, hidden, inner).  Returns out
         (tokens, hidden), ids (tokens, top_k) int32 and gates (tokens, top_k)
-        float32; the arithmetic is that of gemm_moe_fp8."""
+        float32, without gradients; the arithmetic is that of gemm_moe_fp8."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 r = self.moe_fp8(x, router, gate, up, down, top_k, renormalize)

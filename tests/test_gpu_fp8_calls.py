@@ -285,3 +285,23 @@ def test_calls_in_a_row_on_a_busy_stream(g):
             s.synchronize()
             assert all(torch.equal(y, want) for y in got)
     g.status()
+
+
+def test_a_given_stream_in_a_capture(g):
+    """The calls with stream= inside a graph's capture on that stream, inputs from another."""
+    torch.manual_seed(9)
+    x, w = torch.randn(50, 384, device="cuda").half(), torch.randn(200, 384, device="cuda").half()
+    wq = g.fp8_quantize(w, "tile")
+    want = g.fp8_matmul(g.fp8_quantize(x, "row"), wq, b_major=COL)
+    C = torch.empty_like(want)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        xq = g.fp8_quantize(x, "row", stream=s)
+        y = g.fp8_matmul(xq, wq, b_major=COL, stream=s)
+        g.fp8_run(xq, wq, C, b_major=COL, stream=s)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(C, want)
+    g.status()
