@@ -2,8 +2,6 @@
 the current CUDA stream.  PyTorch supplies device memory and streams only."""
 from __future__ import annotations
 
-import functools
-
 import torch
 
 from . import binding as B
@@ -60,6 +58,7 @@ class Gemm:
             dev = torch.device("cuda", 0)
         self.device = dev
         self.handle = B.gemm_create(dev.index)
+        self._native = None  # the extension, once an 8-bit call has been made
         self._run = B.load().gemm_run  # argument types set once by the binding
 
     def close(self):
@@ -157,10 +156,10 @@ class Gemm:
         return p.as_dict()
 
     # ---- block-scaled 8-bit operators (include/gemm_fp8.h)
-    @functools.cached_property
-    def _native(self):
+    def _extension(self):
         """The extension, which only these calls need: loaded at the first of them."""
-        return B.native()
+        self._native = B.native()
+        return self._native
 
     def _raw_stream(self, stream):
         """The stream's handle, without building a Stream object for the current
@@ -185,8 +184,9 @@ class Gemm:
         if kinds is None:
             raise ValueError("blocks must be 'row', 'col', 'tile' or 'row+col', got %r"
                              % (blocks,))
-        r = self._native.quantize(self.handle, self.device.index, x, kinds[0], kinds[1],
-                                  _current_raw(self.device.index))
+        native = self._native or self._extension()
+        r = native.quantize(self.handle, self.device.index, x, kinds[0], kinds[1],
+                            _current_raw(self.device.index))
         if r.__class__ is int:
             raise B.GemmError(r, "gemm_fp8_quantize")
         if len(r) == 4:
@@ -199,9 +199,9 @@ class Gemm:
         float16, bfloat16 or float32, unit stride along its rows).  A is stored
         (M, K) row-major or (K, M) column-major, B (K, N) or (N, K); the blocks
         of each must run along K."""
-        rc = self._native.run(self.handle, self.device.index, A.data, A.scale, A.kind, Bm.data,
-                              Bm.scale, Bm.kind, bias, a_major, b_major, C,
-                              self._raw_stream(stream))
+        native = self._native or self._extension()
+        rc = native.run(self.handle, self.device.index, A.data, A.scale, A.kind, Bm.data,
+                        Bm.scale, Bm.kind, bias, a_major, b_major, C, self._raw_stream(stream))
         if rc != B.GEMM_OK:
             raise B.GemmError(rc, "gemm_fp8_run")
         if stream is not None:
@@ -218,9 +218,10 @@ class Gemm:
         code = _DT8.get(out_dtype)
         if code is None:
             raise TypeError("out_dtype must be float16, bfloat16 or float32, got %s" % out_dtype)
-        C = self._native.matmul(self.handle, self.device.index, A.data, A.scale, A.kind, Bm.data,
-                                Bm.scale, Bm.kind, bias, a_major, b_major, code,
-                                _current_raw(self.device.index))
+        native = self._native or self._extension()
+        C = native.matmul(self.handle, self.device.index, A.data, A.scale, A.kind, Bm.data,
+                          Bm.scale, Bm.kind, bias, a_major, b_major, code,
+                          _current_raw(self.device.index))
         if C.__class__ is int:
             raise B.GemmError(C, "gemm_fp8_run")
         return C
@@ -237,9 +238,10 @@ class Gemm:
                 r = self.moe_fp8(x, router, gate, up, down, top_k, renormalize)
             _in_use(stream, x, router, *(t for w in (gate, up, down) for t in (w.data, w.scale)))
             return r
-        r = self._native.moe(self.handle, self.device.index, x, router, gate.data, gate.scale,
-                             up.data, up.scale, down.data, down.scale, top_k,
-                             1 if renormalize else 0, _current_raw(self.device.index))
+        native = self._native or self._extension()
+        r = native.moe(self.handle, self.device.index, x, router, gate.data, gate.scale, up.data,
+                       up.scale, down.data, down.scale, top_k, 1 if renormalize else 0,
+                       _current_raw(self.device.index))
         if r.__class__ is int:
             raise B.GemmError(r, "gemm_moe_fp8")
         return r
