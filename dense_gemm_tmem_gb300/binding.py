@@ -1,4 +1,5 @@
-"""ctypes binding of include/gemm.h and gemm_fp8.h: the same names, argument marshalling only.
+"""ctypes binding of include/gemm.h, gemm_fp8.h, gemm_fp4.h and gemm_ortho.h: the same names,
+argument marshalling only.
 
 Every computation happens in the CUDA library; if the library is missing this
 module raises instead of falling back to anything else.
@@ -75,6 +76,24 @@ class gemm_moe_fp8_t(ctypes.Structure):
                 ("ld_out", c_int64), ("ids", c_void_p), ("gates", c_void_p)]
 
 
+# ---- include/gemm_fp4.h and gemm_ortho.h
+GEMM_MXFP4, GEMM_NVFP4 = range(2)
+GEMM_ORTHO_MAX_STEPS = 64
+
+
+class gemm_fp4_matrix_t(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("ld", c_int64), ("scale", c_void_p),
+                ("row_scale", c_void_p), ("row_scale_stride", c_int64), ("format", c_int32),
+                ("reserved", c_int32)]
+
+
+class gemm_orthogonalize_t(ctypes.Structure):
+    _fields_ = [("batch", c_int64), ("rows", c_int64), ("cols", c_int64), ("steps", c_int32),
+                ("dtype", c_int32), ("coefficients", c_void_p), ("eps", ctypes.c_double),
+                ("g", c_void_p), ("ld_g", c_int64), ("stride_g", c_int64), ("out", c_void_p),
+                ("ld_out", c_int64), ("stride_out", c_int64)]
+
+
 class GemmError(RuntimeError):
     def __init__(self, code, what=""):
         self.code = code
@@ -131,6 +150,17 @@ def load(build_if_missing: bool = True):
                                  c_int, c_void_p]),
         "gemm_moe_fp8_workspace": (c_int, [c_void_p, P(gemm_moe_fp8_t), P(c_int64)]),
         "gemm_moe_fp8": (c_int, [c_void_p, P(gemm_moe_fp8_t), c_void_p, c_int64, c_void_p]),
+        "gemm_fp4_scale_bytes": (c_int64, [c_int64, c_int64, c_int]),
+        "gemm_fp4_quantize": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int,
+                                      P(gemm_fp4_matrix_t), c_void_p]),
+        "gemm_fp4_dequantize": (c_int, [c_void_p, c_int64, c_int64, P(gemm_fp4_matrix_t),
+                                        c_void_p, c_int64, c_int, c_void_p]),
+        "gemm_fp4_run": (c_int, [c_void_p, c_int64, c_int64, c_int64, P(gemm_fp4_matrix_t),
+                                 P(gemm_fp4_matrix_t), c_void_p, c_void_p, c_int64, c_int,
+                                 c_void_p]),
+        "gemm_orthogonalize_workspace": (c_int, [c_void_p, P(gemm_orthogonalize_t), P(c_int64)]),
+        "gemm_orthogonalize": (c_int, [c_void_p, P(gemm_orthogonalize_t), c_void_p, c_int64,
+                                       c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -155,7 +185,9 @@ def native():
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         mod.init(*(ctypes.cast(getattr(lib, f), c_void_p).value for f in (
-            "gemm_fp8_quantize", "gemm_fp8_run", "gemm_moe_fp8_workspace", "gemm_moe_fp8")))
+            "gemm_fp8_quantize", "gemm_fp8_run", "gemm_moe_fp8_workspace", "gemm_moe_fp8",
+            "gemm_fp4_quantize", "gemm_fp4_dequantize", "gemm_fp4_run",
+            "gemm_orthogonalize_workspace", "gemm_orthogonalize")))
         _native = mod
     return _native
 
@@ -292,6 +324,35 @@ def gemm_moe_fp8_workspace(h, layer: gemm_moe_fp8_t):
 
 def gemm_moe_fp8(h, layer: gemm_moe_fp8_t, ws_ptr, ws_bytes, stream_ptr) -> int:
     return load().gemm_moe_fp8(c_void_p(h), ctypes.byref(layer), ws_ptr, ws_bytes, stream_ptr)
+
+
+def gemm_fp4_scale_bytes(rows, cols, format) -> int:
+    return load().gemm_fp4_scale_bytes(rows, cols, format)
+
+
+def gemm_fp4_quantize(h, rows, cols, src_ptr, ld_src, src_dtype, out, stream_ptr) -> int:
+    return load().gemm_fp4_quantize(c_void_p(h), rows, cols, src_ptr, ld_src, src_dtype,
+                                    ctypes.byref(out), stream_ptr)
+
+
+def gemm_fp4_dequantize(h, rows, cols, m, dst_ptr, ld_dst, dst_dtype, stream_ptr) -> int:
+    return load().gemm_fp4_dequantize(c_void_p(h), rows, cols, ctypes.byref(m), dst_ptr, ld_dst,
+                                      dst_dtype, stream_ptr)
+
+
+def gemm_fp4_run(h, M, N, K, A, Bm, bias_ptr, C_ptr, ldc, out_dtype, stream_ptr) -> int:
+    return load().gemm_fp4_run(c_void_p(h), M, N, K, ctypes.byref(A), ctypes.byref(Bm), bias_ptr,
+                               C_ptr, ldc, out_dtype, stream_ptr)
+
+
+def gemm_orthogonalize_workspace(h, p: gemm_orthogonalize_t):
+    n = c_int64()
+    rc = load().gemm_orthogonalize_workspace(c_void_p(h), ctypes.byref(p), ctypes.byref(n))
+    return rc, n.value
+
+
+def gemm_orthogonalize(h, p: gemm_orthogonalize_t, ws_ptr, ws_bytes, stream_ptr) -> int:
+    return load().gemm_orthogonalize(c_void_p(h), ctypes.byref(p), ws_ptr, ws_bytes, stream_ptr)
 
 
 TRACE_PHASES = ("start", "first_load", "first_data", "mma_done", "last_accum", "end")

@@ -3,7 +3,7 @@
 Each translation unit is compiled for sm_103a only, in parallel, then linked
 with nvcc (static CUDA runtime; the driver is reached at run time through the
 runtime's entry-point query, so the library loads on a machine without a GPU).
-Beside it, _build/_dgemm_native-*.so: the 8-bit operators' tensor-facing calls
+Beside it, _build/_dgemm_native-*.so: the 8- and 4-bit operators' tensor-facing calls
 (csrc/native.cpp) as a Python extension against the installed torch.  Only those
 calls need it: where it cannot be built (no host compiler, Python or torch
 headers), the library is there all the same and they say why.
@@ -40,10 +40,12 @@ NATIVE = os.path.join(OUT_DIR, "_dgemm_native-%s-torch%s.so"
 NATIVE_SOURCE = os.path.join(CSRC, "native.cpp")
 SOURCES = ["api.cu", "simt.cu", "simt_f16.cu", "selftest.cu", "noalloc.cu", "tc2.cu",
            "tc_n256.cu", "tc_n128.cu", "tc_small.cu", "tc_narrow.cu", "tc64.cu",
-           "fp8_api.cu", "fp8_quant.cu", "fp8_simt.cu", "fp8_moe.cu", "fp8_tc.cu"]
+           "fp8_api.cu", "fp8_quant.cu", "fp8_simt.cu", "fp8_moe.cu", "fp8_tc.cu",
+           "fp4_api.cu", "fp4_quant.cu", "fp4_simt.cu", "ortho.cu", "ortho_simt.cu"]
 HEADERS = ["ptx.cuh", "work.cuh", "tc_kernel.cuh", "tc2_kernel.cuh", "tc64_kernel.cuh",
            "tc_launch.cuh", "simt_kernel.cuh", "internal.h", "context.h", "fp8.cuh",
-           "fp8_tc_kernel.cuh", "moe_order.h"]
+           "fp8_tc_kernel.cuh", "moe_order.h", "fp4.cuh", "ortho.cuh"]
+INCLUDES = ["gemm.h", "gemm_fp8.h", "gemm_fp4.h", "gemm_ortho.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-I", os.path.join(ROOT, "include")]
@@ -58,7 +60,7 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files += [os.path.join(ROOT, "include", h) for h in ("gemm.h", "gemm_fp8.h")]
+    files += [os.path.join(ROOT, "include", h) for h in INCLUDES]
     return files
 
 
@@ -74,7 +76,7 @@ def up_to_date() -> bool:
 
 
 def native_up_to_date() -> bool:
-    return _newer(NATIVE, _inputs()[-2:] + [NATIVE_SOURCE])
+    return _newer(NATIVE, _inputs()[-len(INCLUDES):] + [NATIVE_SOURCE])
 
 
 def build_native() -> str:

@@ -11,7 +11,9 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "../../include/gemm_fp4.h"
 #include "../../include/gemm_fp8.h"
+#include "../../include/gemm_ortho.h"
 
 namespace {
 
@@ -22,10 +24,23 @@ using RunFn = int (*)(gemm_handle_t, int64_t, int64_t, int64_t, const gemm_fp8_m
                       void*);
 using MoeSpaceFn = int (*)(gemm_handle_t, const gemm_moe_fp8_t*, int64_t*);
 using MoeFn = int (*)(gemm_handle_t, const gemm_moe_fp8_t*, void*, int64_t, void*);
+using Quantize4Fn = int (*)(gemm_handle_t, int64_t, int64_t, const void*, int64_t, int,
+                            const gemm_fp4_matrix_t*, void*);
+using Dequantize4Fn = int (*)(gemm_handle_t, int64_t, int64_t, const gemm_fp4_matrix_t*, void*,
+                              int64_t, int, void*);
+using Run4Fn = int (*)(gemm_handle_t, int64_t, int64_t, int64_t, const gemm_fp4_matrix_t*,
+                       const gemm_fp4_matrix_t*, const float*, void*, int64_t, int, void*);
+using OrthoSpaceFn = int (*)(gemm_handle_t, const gemm_orthogonalize_t*, int64_t*);
+using OrthoFn = int (*)(gemm_handle_t, const gemm_orthogonalize_t*, void*, int64_t, void*);
 QuantizeFn quantize_fn = nullptr;
 RunFn run_fn = nullptr;
 MoeSpaceFn moe_space_fn = nullptr;
 MoeFn moe_fn = nullptr;
+Quantize4Fn quantize4_fn = nullptr;
+Dequantize4Fn dequantize4_fn = nullptr;
+Run4Fn run4_fn = nullptr;
+OrthoSpaceFn ortho_space_fn = nullptr;
+OrthoFn ortho_fn = nullptr;
 
 constexpr int64_t kBlock = 128;
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
@@ -100,11 +115,16 @@ PyObject* guarded(F&& f) {
 
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    if (n != 4) fail(PyExc_TypeError, "init takes 4 addresses");
+    if (n != 9) fail(PyExc_TypeError, "init takes 9 addresses");
     quantize_fn = reinterpret_cast<QuantizeFn>(address<void>(args[0]));
     run_fn = reinterpret_cast<RunFn>(address<void>(args[1]));
     moe_space_fn = reinterpret_cast<MoeSpaceFn>(address<void>(args[2]));
     moe_fn = reinterpret_cast<MoeFn>(address<void>(args[3]));
+    quantize4_fn = reinterpret_cast<Quantize4Fn>(address<void>(args[4]));
+    dequantize4_fn = reinterpret_cast<Dequantize4Fn>(address<void>(args[5]));
+    run4_fn = reinterpret_cast<Run4Fn>(address<void>(args[6]));
+    ortho_space_fn = reinterpret_cast<OrthoSpaceFn>(address<void>(args[7]));
+    ortho_fn = reinterpret_cast<OrthoFn>(address<void>(args[8]));
     Py_RETURN_NONE;
   });
 }
@@ -346,12 +366,270 @@ PyObject* moe(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ 4 bits --
+int64_t scale_bytes4(int64_t rows, int64_t cols, int64_t kind) {
+  const int64_t per = kind == GEMM_MXFP4 ? 128 : 64;
+  return blocks_of(rows) * ((cols + per - 1) / per) * 512;
+}
+
+at::ScalarType type_of(int64_t code) {
+  return code == GEMM_F16 ? at::kHalf : code == GEMM_BF16 ? at::kBFloat16 : at::kFloat;
+}
+
+// A 4-bit matrix and what it is stored in.
+struct Made4 {
+  gemm_fp4_matrix_t m;
+  at::Tensor buf;
+  int64_t rows, cols, scales_at, rows_at;
+  // values, block scales and row scales in one allocation
+  Made4(const at::TensorOptions& opt, int64_t r, int64_t c, int64_t kind) : rows(r), cols(c) {
+    const int64_t ld = ((c + 1) / 2 + 15) & ~int64_t(15);
+    scales_at = (r * ld + 255) & ~int64_t(255);
+    rows_at = scales_at + scale_bytes4(r, c, kind);  // a multiple of 256
+    buf = at::empty({rows_at + (kind == GEMM_NVFP4 ? 4 * r : 0)}, opt);
+    uint8_t* base = static_cast<uint8_t*>(buf.data_ptr());
+    m = gemm_fp4_matrix_t{base, ld, base + scales_at,
+                          kind == GEMM_NVFP4 ? reinterpret_cast<float*>(base + rows_at) : nullptr,
+                          kind == GEMM_NVFP4, int32_t(kind), 0};
+  }
+};
+
+// The tensors of an Fp4Matrix of `cols` columns, looked at on every call.
+struct Given4 {
+  gemm_fp4_matrix_t m;
+  int64_t rows;
+  Given4(PyObject* data, PyObject* scale, PyObject* row_scale, int64_t cols, int64_t kind,
+         int64_t device) {
+    const at::Tensor& q = tensor(data, "data must be a tensor");
+    const at::Tensor& s = tensor(scale, "scale must be a tensor");
+    if (kind != GEMM_MXFP4 && kind != GEMM_NVFP4) fail(PyExc_ValueError, "unknown format");
+    if (q.element_size() != 1 || s.element_size() != 1)
+      fail(PyExc_TypeError, "data and scale must have one byte an element");
+    if (q.dim() != 2 || cols < 0 || q.size(1) != (cols + 1) / 2)
+      fail(PyExc_ValueError, "data must be (rows, ceil(cols / 2))");
+    rows = q.size(0);
+    if (s.dim() != 1 || s.size(0) != scale_bytes4(rows, cols, kind) || !s.is_contiguous())
+      fail(PyExc_ValueError, "scale must be flat and contiguous, of the format's size");
+    on_device(q, device);
+    on_device(s, device);
+    // a lone row needs no pitch
+    const int64_t pitch = pitch_of(q, "rows of data must be contiguous and not overlap");
+    m = gemm_fp4_matrix_t{q.data_ptr(), rows > 1 ? pitch : (q.size(1) + 15) & ~int64_t(15),
+                          s.data_ptr(), nullptr, 0, int32_t(kind), 0};
+    if (row_scale != Py_None) {
+      const at::Tensor& r = tensor(row_scale, "row_scale must be a tensor or None");
+      if (r.scalar_type() != at::kFloat || r.dim() != 1 || r.size(0) != rows)
+        fail(PyExc_ValueError, "row_scale must be float32 of shape (rows,)");
+      on_device(r, device);
+      m.row_scale = static_cast<float*>(r.data_ptr());
+      m.row_scale_stride = r.stride(0);
+    }
+  }
+};
+
+const float* bias_of(PyObject* o, int64_t N, int64_t device) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, "bias must be a tensor");
+  if (t.scalar_type() != at::kFloat || t.dim() != 1 || t.size(0) != N || !t.is_contiguous())
+    fail(PyExc_ValueError, "bias must be contiguous float32 of shape (N,)");
+  on_device(t, device);
+  return static_cast<const float*>(t.data_ptr());
+}
+
+// A matrix of the caller's: checked, with its type's code and row pitch.
+const at::Tensor& rows_of(PyObject* o, int64_t device, int* code, int64_t* ld) {
+  const at::Tensor& x = tensor(o, "x must be a tensor");
+  *code = code_of(x.scalar_type());
+  if (*code < 0) fail(PyExc_TypeError, "x must be float16, bfloat16 or float32");
+  if (x.dim() != 2) fail(PyExc_ValueError, "x must be 2-D");
+  on_device(x, device);
+  *ld = pitch_of(x, "rows of x must be contiguous and not overlap");
+  return x;
+}
+
+// quantize4(handle, device, x, kind, stream) -> (data, scale, row_scale or None)
+// or a gemm_status_t
+PyObject* quantize4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 5) fail(PyExc_TypeError, "quantize4 takes 5 arguments");
+    int code;
+    int64_t ld;
+    const at::Tensor& x = rows_of(args[2], integer(args[1]), &code, &ld);
+    const int64_t kind = integer(args[3]);
+    const Made4 q(x.options().dtype(at::kByte).requires_grad(false), x.size(0), x.size(1), kind);
+    const int rc = quantize4_fn(address<gemm_ctx>(args[0]), q.rows, q.cols, x.data_ptr(), ld,
+                                code, &q.m, address<void>(args[4]));
+    if (rc != GEMM_OK) return PyLong_FromLong(rc);
+    PyObject* r = PyTuple_New(3);
+    if (!r) throw Raised{};
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(carve(q.buf, at::kByte, 0, q.rows, (q.cols + 1) / 2,
+                                                  q.m.ld, 1)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(q.buf.narrow(0, q.scales_at,
+                                                         q.rows_at - q.scales_at)));
+    if (kind == GEMM_NVFP4) {
+      at::Tensor rows = carve(q.buf, at::kFloat, q.rows_at, 1, q.rows, q.rows, 1);
+      PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(rows.select(0, 0)));
+    } else {
+      Py_INCREF(Py_None);
+      PyTuple_SET_ITEM(r, 2, Py_None);
+    }
+    return r;
+  });
+}
+
+// dequantize4(handle, device, data, scale, row_scale, cols, kind, output type's code,
+// stream) -> a tensor or a gemm_status_t
+PyObject* dequantize4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 9) fail(PyExc_TypeError, "dequantize4 takes 9 arguments");
+    const int64_t cols = integer(args[5]), code = integer(args[7]);
+    const Given4 q(args[2], args[3], args[4], cols, integer(args[6]), integer(args[1]));
+    at::Tensor out = at::empty({q.rows, cols}, THPVariable_Unpack(args[2]).options()
+                                                   .dtype(type_of(code)).requires_grad(false));
+    const int rc = dequantize4_fn(address<gemm_ctx>(args[0]), q.rows, cols, &q.m, out.data_ptr(),
+                                  cols, int(code), address<void>(args[8]));
+    if (rc != GEMM_OK) return PyLong_FromLong(rc);
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
+// What both product calls take: handle, device, A data, scale, row_scale, B data, scale,
+// row_scale, K, kind, bias or None.
+struct Product4 {
+  gemm_ctx* h;
+  int64_t device, K;
+  Given4 a, b;
+  const float* bias;
+  explicit Product4(PyObject* const* args)
+      : h(address<gemm_ctx>(args[0])),
+        device(integer(args[1])),
+        K(integer(args[8])),
+        a(args[2], args[3], args[4], K, integer(args[9]), device),
+        b(args[5], args[6], args[7], K, integer(args[9]), device),
+        bias(bias_of(args[10], b.rows, device)) {}
+};
+
+// matmul4(the product's arguments, output type's code, stream) -> C or a gemm_status_t
+PyObject* matmul4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 13) fail(PyExc_TypeError, "matmul4 takes 13 arguments");
+    const Product4 p(args);
+    const int64_t code = integer(args[11]);
+    at::Tensor C = at::empty({p.a.rows, p.b.rows}, THPVariable_Unpack(args[2]).options()
+                                                       .dtype(type_of(code)).requires_grad(false));
+    const int rc = run4_fn(p.h, p.a.rows, p.b.rows, p.K, &p.a.m, &p.b.m, p.bias, C.data_ptr(),
+                           p.b.rows, int(code), address<void>(args[12]));
+    if (rc != GEMM_OK) return PyLong_FromLong(rc);
+    return THPVariable_Wrap(std::move(C));
+  });
+}
+
+// run4(the product's arguments, C, stream) -> a gemm_status_t
+PyObject* run4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 13) fail(PyExc_TypeError, "run4 takes 13 arguments");
+    const Product4 p(args);
+    const at::Tensor& C = tensor(args[11], "C must be a tensor");
+    const int code = code_of(C.scalar_type());
+    if (code < 0) fail(PyExc_TypeError, "C must be float16, bfloat16 or float32");
+    if (C.dim() != 2 || C.size(0) != p.a.rows || C.size(1) != p.b.rows) {
+      PyErr_Format(PyExc_ValueError, "C must have shape (%lld, %lld)", (long long)p.a.rows,
+                   (long long)p.b.rows);
+      throw Raised{};
+    }
+    on_device(C, p.device);
+    const int64_t ldc = pitch_of(C, "rows of C must be contiguous and not overlap");
+    return PyLong_FromLong(run4_fn(p.h, p.a.rows, p.b.rows, p.K, &p.a.m, &p.b.m, p.bias,
+                                   C.data_ptr(), ldc, code, address<void>(args[12])));
+  });
+}
+
+// linear4(handle, device, x, W data, scale, row_scale, K, kind, bias or None, stream)
+// -> y or a gemm_status_t.  `stream` is the current stream: the quantised x is freed
+// on return, in that stream's order.
+PyObject* linear4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 10) fail(PyExc_TypeError, "linear4 takes 10 arguments");
+    gemm_ctx* h = address<gemm_ctx>(args[0]);
+    const int64_t device = integer(args[1]), K = integer(args[6]), kind = integer(args[7]);
+    int code;
+    int64_t ld;
+    const at::Tensor& x = rows_of(args[2], device, &code, &ld);
+    const Given4 w(args[3], args[4], args[5], K, kind, device);
+    if (x.size(1) != K) {
+      PyErr_Format(PyExc_ValueError, "inner dimensions differ: %lld vs %lld",
+                   (long long)x.size(1), (long long)K);
+      throw Raised{};
+    }
+    const float* bias = bias_of(args[8], w.rows, device);
+    void* stream = address<void>(args[9]);
+    const auto opt = x.options().requires_grad(false);
+    const Made4 q(opt.dtype(at::kByte), x.size(0), K, kind);
+    at::Tensor y = at::empty({x.size(0), w.rows}, opt);
+    int rc = quantize4_fn(h, q.rows, K, x.data_ptr(), ld, code, &q.m, stream);
+    if (rc == GEMM_OK)
+      rc = run4_fn(h, q.rows, w.rows, K, &q.m, &w.m, bias, y.data_ptr(), w.rows, code, stream);
+    if (rc != GEMM_OK) return PyLong_FromLong(rc);
+    return THPVariable_Wrap(std::move(y));
+  });
+}
+
+// orthogonalize(handle, device, G, coefficients as fp32 bytes, eps, stream) -> a tensor or
+// a gemm_status_t.  `stream` is the current stream: the scratch is freed on return, in
+// that stream's order.
+PyObject* orthogonalize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 6) fail(PyExc_TypeError, "orthogonalize takes 6 arguments");
+    gemm_ctx* h = address<gemm_ctx>(args[0]);
+    const at::Tensor& g = tensor(args[2], "G must be a tensor");
+    const int code = code_of(g.scalar_type());
+    if (code < 0) fail(PyExc_TypeError, "G must be float16, bfloat16 or float32");
+    const int64_t d = g.dim();
+    if (d != 2 && d != 3) fail(PyExc_ValueError, "G must be 2-D, or 3-D with a batch");
+    on_device(g, integer(args[1]));
+    if (!PyBytes_Check(args[3]) || PyBytes_GET_SIZE(args[3]) % 12 != 0)
+      fail(PyExc_TypeError, "coefficients must be bytes of three floats a step");
+    gemm_orthogonalize_t p = {};
+    p.batch = d == 3 ? g.size(0) : 1;
+    p.rows = g.size(d - 2);
+    p.cols = g.size(d - 1);
+    p.steps = int32_t(PyBytes_GET_SIZE(args[3]) / 12);
+    p.dtype = code;
+    p.coefficients = reinterpret_cast<const float*>(PyBytes_AS_STRING(args[3]));
+    p.eps = PyFloat_AsDouble(args[4]);
+    if (p.eps == -1 && PyErr_Occurred()) throw Raised{};
+    if ((p.cols > 1 && g.stride(d - 1) != 1) || (p.rows > 1 && g.stride(d - 2) < p.cols))
+      fail(PyExc_ValueError, "rows of G must be contiguous and not overlap");
+    p.g = g.data_ptr();
+    p.ld_g = p.rows > 1 ? g.stride(d - 2) : p.cols;
+    p.stride_g = d == 3 && p.batch > 1 ? g.stride(0) : 0;
+    int64_t bytes = 0;
+    int rc = ortho_space_fn(h, &p, &bytes);
+    if (rc != GEMM_OK) return PyLong_FromLong(rc);
+    const auto opt = g.options().requires_grad(false);
+    at::Tensor out = at::empty(g.sizes(), opt.dtype(at::kBFloat16));
+    at::Tensor space = at::empty({bytes}, opt.dtype(at::kByte));
+    p.out = out.data_ptr();
+    p.ld_out = p.cols;
+    p.stride_out = p.rows * p.cols;
+    rc = ortho_fn(h, &p, space.data_ptr(), bytes, address<void>(args[5]));
+    if (rc != GEMM_OK) return PyLong_FromLong(rc);
+    return THPVariable_Wrap(std::move(out));
+  });
+}
+
 PyMethodDef methods[] = {
     {"init", reinterpret_cast<PyCFunction>(init), METH_FASTCALL, nullptr},
     {"quantize", reinterpret_cast<PyCFunction>(quantize), METH_FASTCALL, nullptr},
     {"matmul", reinterpret_cast<PyCFunction>(matmul), METH_FASTCALL, nullptr},
     {"run", reinterpret_cast<PyCFunction>(run), METH_FASTCALL, nullptr},
     {"moe", reinterpret_cast<PyCFunction>(moe), METH_FASTCALL, nullptr},
+    {"quantize4", reinterpret_cast<PyCFunction>(quantize4), METH_FASTCALL, nullptr},
+    {"dequantize4", reinterpret_cast<PyCFunction>(dequantize4), METH_FASTCALL, nullptr},
+    {"matmul4", reinterpret_cast<PyCFunction>(matmul4), METH_FASTCALL, nullptr},
+    {"run4", reinterpret_cast<PyCFunction>(run4), METH_FASTCALL, nullptr},
+    {"linear4", reinterpret_cast<PyCFunction>(linear4), METH_FASTCALL, nullptr},
+    {"orthogonalize", reinterpret_cast<PyCFunction>(orthogonalize), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dgemm_native", nullptr, -1, methods,

@@ -2,9 +2,12 @@
 the current CUDA stream.  PyTorch supplies device memory and streams only."""
 from __future__ import annotations
 
+import array
+
 import torch
 
 from . import binding as B
+from .fp4 import FORMATS as _FORMATS4, Fp4Matrix
 from .fp8 import Fp8Matrix
 
 _DT = {torch.float16: B.GEMM_F16, torch.float32: B.GEMM_F32}
@@ -245,3 +248,146 @@ class Gemm:
         if r.__class__ is int:
             raise B.GemmError(r, "gemm_moe_fp8")
         return r
+
+    # ---- 4-bit operators (include/gemm_fp4.h)
+    def fp4_quantize(self, x: torch.Tensor, format: str = "nvfp4", stream=None) -> Fp4Matrix:
+        """x (rows, cols; float16, bfloat16 or float32, unit stride along its rows)
+        as an Fp4Matrix, "mxfp4" or "nvfp4".  Streams and gradients, here and in the
+        calls below: as fp8_quantize."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                r = self.fp4_quantize(x, format)
+            _in_use(stream, x)
+            return r
+        kind = _FORMATS4.get(format)
+        if kind is None:
+            raise ValueError("format must be 'mxfp4' or 'nvfp4', got %r" % (format,))
+        native = self._native or self._extension()
+        r = native.quantize4(self.handle, self.device.index, x, kind,
+                             _current_raw(self.device.index))
+        if r.__class__ is int:
+            raise B.GemmError(r, "gemm_fp4_quantize")
+        return Fp4Matrix._wrap(r[0], r[1], r[2], tuple(x.shape), format)
+
+    def fp4_dequantize(self, m: Fp4Matrix, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+        """The values an Fp4Matrix stands for, as a new (rows, cols) tensor."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                r = self.fp4_dequantize(m, dtype)
+            _in_use(stream, m.data, m.scale, m.row_scale)
+            return r
+        code = _DT8.get(dtype)
+        if code is None:
+            raise TypeError("dtype must be float16, bfloat16 or float32, got %s" % dtype)
+        native = self._native or self._extension()
+        r = native.dequantize4(self.handle, self.device.index, m.data, m.scale, m.row_scale,
+                               m.shape[1], m.kind, code, _current_raw(self.device.index))
+        if r.__class__ is int:
+            raise B.GemmError(r, "gemm_fp4_dequantize")
+        return r
+
+    def _fp4_operands(self, A: Fp4Matrix, Bm: Fp4Matrix):
+        if A.kind != Bm.kind:
+            raise ValueError("A is %s, B %s: both have one format" % (A.format, Bm.format))
+        if A.shape[1] != Bm.shape[1]:
+            raise ValueError("inner dimensions differ: %d vs %d" % (A.shape[1], Bm.shape[1]))
+
+    def fp4_run(self, A: Fp4Matrix, Bm: Fp4Matrix, C: torch.Tensor, bias=None,
+                stream=None) -> None:
+        """Enqueues C = A·Bᵀ (+bias) of 4-bit matrices A (M, K) and B (N, K) of one
+        format into C (M, N; float16, bfloat16 or float32, unit stride along its
+        rows)."""
+        self._fp4_operands(A, Bm)
+        native = self._native or self._extension()
+        rc = native.run4(self.handle, self.device.index, A.data, A.scale, A.row_scale, Bm.data,
+                         Bm.scale, Bm.row_scale, A.shape[1], A.kind, bias, C,
+                         self._raw_stream(stream))
+        if rc != B.GEMM_OK:
+            raise B.GemmError(rc, "gemm_fp4_run")
+        if stream is not None:
+            _in_use(stream, A.data, A.scale, A.row_scale, Bm.data, Bm.scale, Bm.row_scale, bias, C)
+
+    def fp4_matmul(self, A: Fp4Matrix, Bm: Fp4Matrix, bias=None, out_dtype=torch.bfloat16,
+                   stream=None) -> torch.Tensor:
+        """A·Bᵀ (+bias) as a new tensor (see fp4_run), which carries no gradient."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                C = self.fp4_matmul(A, Bm, bias, out_dtype)
+            _in_use(stream, A.data, A.scale, A.row_scale, Bm.data, Bm.scale, Bm.row_scale, bias)
+            return C
+        self._fp4_operands(A, Bm)
+        code = _DT8.get(out_dtype)
+        if code is None:
+            raise TypeError("out_dtype must be float16, bfloat16 or float32, got %s" % out_dtype)
+        native = self._native or self._extension()
+        C = native.matmul4(self.handle, self.device.index, A.data, A.scale, A.row_scale, Bm.data,
+                           Bm.scale, Bm.row_scale, A.shape[1], A.kind, bias, code,
+                           _current_raw(self.device.index))
+        if C.__class__ is int:
+            raise B.GemmError(C, "gemm_fp4_run")
+        return C
+
+    def fp4_linear(self, x: torch.Tensor, w: Fp4Matrix, bias=None, stream=None) -> torch.Tensor:
+        """x·wᵀ (+bias) in x's type: x quantised to w's format, then the product
+        (fp4.linear)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                y = self.fp4_linear(x, w, bias)
+            _in_use(stream, x, w.data, w.scale, w.row_scale, bias)
+            return y
+        native = self._native or self._extension()
+        y = native.linear4(self.handle, self.device.index, x, w.data, w.scale, w.row_scale,
+                           w.shape[1], w.kind, bias, _current_raw(self.device.index))
+        if y.__class__ is int:
+            raise B.GemmError(y, "gemm_fp4_run")
+        return y
+
+    # ---- orthogonalising an update (include/gemm_ortho.h)
+    def orthogonalize(self, G: torch.Tensor, steps: int = 5,
+                      coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                      stream=None) -> torch.Tensor:
+        """G (rows, cols) or a batch of them (batch, rows, cols), float16, bfloat16 or
+        float32 with unit stride along the rows, with its singular values driven
+        towards 1 by Newton-Schulz steps: X = G / max(|G|, eps), then X = aX + (bA +
+        cA²)X with A = X·Xᵀ.  coefficients: (a, b, c) for every step, or one such
+        triple per step.  The default takes the singular values to about 0.7 ... 1.2
+        in 5 steps; (1.875, -1.25, 0.375) converges to 1, more slowly.  Returns
+        bfloat16, which carries no gradient.  The products' operands are 16-bit, so
+        the result is right to about 2e-3 of its norm."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                r = self.orthogonalize(G, steps, coefficients, eps)
+            _in_use(stream, G)
+            return r
+        steps = int(steps)
+        if steps < 1 or steps > B.GEMM_ORTHO_MAX_STEPS:
+            raise ValueError("steps must be 1 ... %d, got %d" % (B.GEMM_ORTHO_MAX_STEPS, steps))
+        abc = _coefficients(coefficients, steps)
+        native = self._native or self._extension()
+        r = native.orthogonalize(self.handle, self.device.index, G, abc, float(eps),
+                                 _current_raw(self.device.index))
+        if r.__class__ is int:
+            raise B.GemmError(r, "gemm_orthogonalize")
+        return r
+
+
+_ABC = {}  # (coefficients, steps) -> their fp32 bytes, built once
+
+
+def _coefficients(coefficients, steps: int) -> bytes:
+    """a, b, c of every step as fp32."""
+    try:
+        key = (coefficients, steps)
+        got = _ABC.get(key)
+    except TypeError:  # a list, which is not kept
+        key = got = None
+    if got is None:
+        rows = list(coefficients)
+        if rows and not hasattr(rows[0], "__len__"):
+            rows = [rows] * steps
+        if len(rows) != steps or any(len(r) != 3 for r in rows):
+            raise ValueError("coefficients: one (a, b, c), or one for each of the %d steps" % steps)
+        got = array.array("f", (float(v) for r in rows for v in r)).tobytes()
+        if key is not None and len(_ABC) < 64:
+            _ABC[key] = got
+    return got

@@ -1,0 +1,351 @@
+"""The 4-bit operators on the GPU against a 64-bit reference: quantising bit for bit,
+reading back and products within bounds derived from their fp32 arithmetic, at the
+sizes, strides and values where they can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_reference as R
+from dense_gemm_tmem_gb300 import binding as B
+from dense_gemm_tmem_gb300 import fp4
+from dense_gemm_tmem_gb300.fp4 import Fp4Matrix
+from dense_gemm_tmem_gb300.gemm import Gemm
+
+pytestmark = pytest.mark.gpu
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+FORMATS = ["mxfp4", "nvfp4"]
+
+
+@pytest.fixture(scope="module")
+def g():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+    h = Gemm(torch.device("cuda", 0))
+    yield h
+    h.close()
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def make(rng, rows, cols, spread=1.0):
+    return torch.from_numpy(rng.standard_normal((rows, cols))
+                            * np.exp(spread * rng.standard_normal((1, cols))))
+
+
+def check_quantized(m, x, fmt):
+    code, byte, rows = R.quantize(host(x), fmt)
+    got_code, got_byte = R.stored(m)
+    assert np.array_equal(got_byte, byte), int((got_byte != byte).sum())
+    assert np.array_equal(got_code, code), int((got_code != code).sum())
+    if rows is None:
+        assert m.row_scale is None
+    else:
+        assert np.array_equal(host(m.row_scale), rows)
+    # every byte of a piece past the matrix is 0, and so is the odd column's partner
+    blocks = byte.shape[1]
+    full = np.zeros(m.scale.numel(), np.uint8)
+    r, b = np.arange(m.shape[0])[:, None], np.arange(blocks)[None, :]
+    full[R.place(r, b, blocks)] = byte
+    assert np.array_equal(m.scale.cpu().numpy(), full)
+    assert np.array_equal(m.data.cpu().numpy(), R.pack(code))
+
+
+# ------------------------------------------------------------------ quantise --
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 16), (3, 33), (128, 64), (129, 127), (5, 1025),
+                                       (260, 1000), (1, 4096), (2, 8192), (2, 8209), (3, 20001)])
+def test_quantize(g, rows, cols, dtype, fmt):
+    rng = np.random.default_rng(rows * 1000 + cols)
+    x = make(rng, rows, cols).to(dtype).cuda()
+    check_quantized(g.fp4_quantize(x, fmt), x, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_quantize_values_at_the_ends(g, dtype, fmt):
+    """Zeros, a type's largest and smallest, ties, infinities and NaN, rows of them."""
+    big, tiny = torch.finfo(dtype).max, torch.finfo(dtype).smallest_normal / 4
+    x = torch.zeros(12, 96, dtype=dtype)
+    x[1] = big
+    x[2] = tiny
+    x[3, 5], x[3, 70] = float("inf"), float("nan")
+    x[3, 40] = -2.5
+    x[4, 0::2] = 6.0  # block maximum 6: scales of powers of two, every tie of e2m1 below
+    x[4, 1:32:2] = torch.tensor([.25, .75, 1.25, 1.75, 2.5, 3.5, 5, -.25, -.75, -1.25, -1.75, -2.5,
+                                 -3.5, -5, .2, -.2], dtype=dtype)
+    x[5, 0], x[5, 50] = big, tiny
+    x[6] = -0.0
+    x[7, 33] = tiny
+    x[8] = float("-inf")
+    x[9] = torch.linspace(-7, 7, 96).to(dtype)
+    x[10, 17] = big
+    x[10, 18] = float("nan")
+    x[11] = torch.linspace(0, 1, 96).to(dtype) ** 8
+    x = x.cuda()
+    check_quantized(g.fp4_quantize(x, fmt), x, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("offset,pitch", [(1, 401), (8, 408), (0, 403), (3, 440)])
+def test_quantize_strided_rows(g, dtype, fmt, offset, pitch):
+    rng = np.random.default_rng(offset)
+    buf = make(rng, 37, 450).to(dtype).cuda().reshape(-1)
+    x = torch.as_strided(buf, (37, 390), (pitch, 1), offset)
+    check_quantized(g.fp4_quantize(x, fmt), x, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_quantize_leaves_the_padding_of_rows(g, fmt):
+    rows, cols = 5, 45  # 23 bytes a row
+    buf = torch.full((rows, 32), 0xa5, dtype=torch.uint8, device="cuda")
+    scale = torch.empty(fp4.scale_bytes(rows, cols, fmt), dtype=torch.uint8, device="cuda")
+    r = torch.empty(2 * rows, device="cuda")[::2] if fmt == "nvfp4" else None
+    m = Fp4Matrix(buf[:, :23], scale, r, (rows, cols), fmt)
+    x = torch.randn(rows, cols, device="cuda")
+    rc = B.gemm_fp4_quantize(g.handle, rows, cols, x.data_ptr(), cols, B.GEMM_F32, m.desc(),
+                             torch.cuda.current_stream().cuda_stream)
+    assert rc == B.GEMM_OK
+    check_quantized(m, x, fmt)
+    assert bool((buf[:, 23:] == 0xa5).all())
+
+
+def test_tokens_do_not_depend_on_each_other(g):
+    x = torch.randn(300, 700, device="cuda").bfloat16()
+    for fmt in FORMATS:
+        all_, one = g.fp4_quantize(x, fmt), g.fp4_quantize(x[177:178], fmt)
+        assert torch.equal(all_.data[177:178], one.data)
+        assert np.array_equal(R.stored(all_)[1][177:178], R.stored(one)[1])
+
+
+# ------------------------------------------------------------------ read back --
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 31), (130, 65), (17, 1000), (1, 4096)])
+def test_dequantize(g, rows, cols, dtype, fmt):
+    rng = np.random.default_rng(rows + cols)
+    m = g.fp4_quantize(make(rng, rows, cols).cuda().float(), fmt)
+    got, want = g.fp4_dequantize(m, dtype), R.values(m)
+    assert got.dtype == dtype and got.shape == (rows, cols)
+    # the row scale's product and the last rounding
+    tol = np.abs(want) * (2.0 ** -24 + torch.finfo(dtype).eps / 2) + \
+        torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    assert np.all(np.abs(host(got) - want) <= tol)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_dequantize_every_code_and_scale(g, fmt):
+    """All 16 values under all 256 scale bytes (e4m3's sign bit too), with one scale for the
+    matrix and none."""
+    n = R.BLOCK[fmt]
+    data = torch.arange(n // 2, dtype=torch.int32) % 8
+    data = ((2 * data) + 16 * (2 * data + 1)).to(torch.uint8).repeat(256, 1).cuda()
+    scale = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(256, 1).cuda()
+    for rs in (None, torch.tensor([1.5], device="cuda")):
+        m = Fp4Matrix.from_parts(data, scale, rs, n, fmt)
+        got, want = host(g.fp4_dequantize(m, F32)), R.values(m)
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        ok = np.isfinite(want) & (np.abs(want) < 3e38)
+        assert np.array_equal(got[ok], R.f32(want[ok]))
+
+
+# -------------------------------------------------------------------- product --
+def bound(a, b, ra, rb, want, bias, dtype):
+    """Exact products summed in fp32 in any order and with truncating adders lose at most
+    2^-23 of the sum of magnitudes per addition; then the two row scales, the bias, each
+    rounded, and C's rounding (half a step of its type, subnormals included)."""
+    K = a.shape[1]
+    mag = np.abs(a) @ np.abs(b).T
+    if ra is not None:
+        mag = mag * ra[:, None]
+    if rb is not None:
+        mag = mag * rb[None, :]
+    err = mag * (K * 2.0 ** -23 + 2 * 2.0 ** -24) + 2.0 ** -24 * np.abs(want)
+    if bias is not None:
+        err = err + 2.0 ** -24 * np.abs(bias)[None, :]
+    f = torch.finfo(dtype)
+    return err + np.abs(want) * f.eps / 2 + f.smallest_normal * f.eps
+
+
+def parts(m):
+    code, byte = R.stored(m)
+    rows = None if m.row_scale is None else host(m.row_scale)
+    return R.times_blocks(code, byte, m.format), rows
+
+
+def check_product(C, A, Bm, bias=None):
+    (a, ra), (b, rb) = parts(A), parts(Bm)
+    want = a @ b.T
+    want = want * (1 if ra is None else ra[:, None]) * (1 if rb is None else rb[None, :])
+    bias = None if bias is None else host(bias)
+    if bias is not None:
+        want = want + bias[None, :]
+    got = host(C)
+    assert got.shape == want.shape
+    tol = bound(a, b, ra, rb, want, bias, C.dtype)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), float(np.abs(got - want)[bad].max()),
+                           np.argwhere(bad)[:5])
+
+
+SHAPES = [(1, 1, 1), (1, 16, 16), (1, 128, 64), (2, 3, 5), (5, 130, 63), (128, 128, 256),
+          (127, 129, 255), (1, 4096, 4096), (16, 1000, 2056), (33, 520, 777), (64, 300, 100),
+          (65, 64, 4100), (129, 1, 300), (257, 260, 512), (300, 700, 1025), (515, 1000, 2056),
+          (1001, 514, 260), (256, 512, 64), (1024, 2304, 130)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(g, M, N, K, fmt):
+    rng = np.random.default_rng(M * 7 + N * 3 + K)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    Bm = g.fp4_quantize(make(rng, N, K, 0.2).cuda().float(), fmt)
+    bias = torch.from_numpy(rng.standard_normal(N)).float().cuda() if (M + N) % 2 else None
+    for dtype in (F32, F16, BF16):
+        check_product(g.fp4_matmul(A, Bm, bias, out_dtype=dtype), A, Bm, bias)
+    g.status()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(2048, 2304, 576), (1600, 4000, 320)])
+def test_product_of_many_tiles(g, M, N, K, fmt):
+    """Several tiles a CTA; a sample of rows against doubles."""
+    rng = np.random.default_rng(M)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    check_product(g.fp4_matmul(A, Bm, out_dtype=F16), A, Bm)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(1, 300, 200), (200, 300, 520), (700, 1024, 256)])
+def test_product_into_strided_rows(g, M, N, K, fmt):
+    rng = np.random.default_rng(K)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    for dtype in (F16, F32):
+        for offset, pitch in ((0, N), (1, N + 3), (8, N + 8)):
+            buf = torch.full((M * pitch + offset + 64,), 7.0, dtype=dtype, device="cuda")
+            C = torch.as_strided(buf, (M, N), (pitch, 1), offset)
+            g.fp4_run(A, Bm, C)
+            check_product(C, A, Bm)
+            C.fill_(7.0)
+            assert bool((buf == 7.0).all())  # nothing outside C was written
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_scales_at_the_ends_and_nan(g, M, fmt):
+    """A NaN scale reaches its row or column of C and nothing else; the largest and smallest
+    scales; operands whose rows are padded with bytes that are no part of them."""
+    N, K = 260, 320
+    n = R.BLOCK[fmt]
+    rng = np.random.default_rng(M)
+
+    def operand(rows, lo, hi):
+        data = torch.from_numpy(rng.integers(0, 256, (rows, K // 2)).astype(np.uint8)).cuda()
+        scale = torch.from_numpy(rng.integers(lo, hi, (rows, K // n)).astype(np.uint8)).cuda()
+        buf = torch.full((rows, K // 2 + 32), 0x77, dtype=torch.uint8, device="cuda")
+        buf[:, :K // 2] = data
+        return buf, scale
+
+    lo, hi = (60, 190) if fmt == "mxfp4" else (0, 127)
+    da, sa = operand(M, lo, hi)
+    db, sb = operand(N, 100, 128) if fmt == "mxfp4" else operand(N, 0, 127)
+    for nan in (False, True):
+        if nan:
+            sa[M // 2, 3] = 255 if fmt == "mxfp4" else 127
+            sb[N - 1, K // n - 1] = 255 if fmt == "mxfp4" else 127
+        A = Fp4Matrix(da[:, :K // 2], fp4.pack_scales(sa), None, (M, K), fmt)
+        Bm = Fp4Matrix(db[:, :K // 2], fp4.pack_scales(sb), None, (N, K), fmt)
+        C = g.fp4_matmul(A, Bm, out_dtype=F32)
+        if nan:
+            want = torch.zeros(M, N, dtype=torch.bool)
+            want[M // 2], want[:, N - 1] = True, True
+            assert torch.equal(torch.isnan(C).cpu(), want)
+        else:
+            check_product(C, A, Bm)
+
+
+def test_row_scales(g):
+    """One for all (stride 0), every second of a tensor, on one side only, in mxfp4 too."""
+    rng = np.random.default_rng(0)
+    M, N, K = 150, 200, 256
+    for fmt in FORMATS:
+        A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+        Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+        for ra in (None, torch.tensor([0.3], device="cuda").expand(M),
+                   torch.rand(2 * M, device="cuda")[::2]):
+            A2 = Fp4Matrix(A.data, A.scale, ra, (M, K), fmt)
+            check_product(g.fp4_matmul(A2, Bm, out_dtype=F32), A2, Bm)
+            check_product(g.fp4_matmul(Bm, A2, out_dtype=F32), Bm, A2)
+
+
+def test_empty_sizes(g):
+    z = lambda r, c, f: g.fp4_quantize(torch.zeros(r, c, device="cuda"), f)  # noqa: E731
+    for fmt in FORMATS:
+        assert g.fp4_matmul(z(0, 64, fmt), z(5, 64, fmt)).shape == (0, 5)
+        assert g.fp4_matmul(z(5, 64, fmt), z(0, 64, fmt)).shape == (5, 0)
+        bias = torch.randn(7, device="cuda")
+        C = g.fp4_matmul(z(3, 0, fmt), z(7, 0, fmt), bias, out_dtype=F32)
+        assert torch.equal(C, bias.expand(3, 7))
+        assert float(g.fp4_matmul(z(3, 0, fmt), z(7, 0, fmt), out_dtype=F32).abs().sum()) == 0
+        assert g.fp4_dequantize(z(0, 8, fmt)).shape == (0, 8)
+        assert g.fp4_linear(torch.zeros(0, 64, device="cuda"), z(5, 64, fmt)).shape == (0, 5)
+
+
+# ------------------------------------------------------------------ as a user --
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("T,N,K", [(1, 300, 260), (70, 512, 1000), (300, 257, 512)])
+def test_linear_is_quantising_and_product(g, T, N, K, dtype, fmt):
+    rng = np.random.default_rng(T)
+    x = make(rng, T, K).cuda().to(dtype)
+    w = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    bias = torch.randn(N, device="cuda")
+    for b in (None, bias):
+        y = fp4.linear(g, x, w, b)
+        assert y.dtype == dtype
+        check_product(y, g.fp4_quantize(x, fmt), w, b)
+
+
+def test_streams_graphs_and_repeats(g):
+    """Another stream, a captured and replayed chain, the same bits every time."""
+    torch.manual_seed(0)
+    for fmt in FORMATS:
+        for T in (1, 200, 1030):
+            x = torch.randn(T, 1000, device="cuda").bfloat16()
+            w = g.fp4_quantize(torch.randn(520, 1000, device="cuda"), fmt)
+            want = fp4.linear(g, x, w)
+            for _ in range(3):
+                assert torch.equal(fp4.linear(g, x, w), want)
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            y = fp4.linear(g, x, w, stream=s)
+            q = g.fp4_quantize(x, fmt, stream=s)
+            C = g.fp4_matmul(q, w, stream=s)
+            back = g.fp4_dequantize(q, stream=s)
+            s.synchronize()
+            assert torch.equal(y, want) and torch.equal(C, want)
+            assert torch.equal(back, g.fp4_dequantize(q))
+            graph = torch.cuda.CUDAGraph()
+            static = x.clone()
+            with torch.cuda.graph(graph):
+                out = fp4.linear(g, static, w)
+            x2 = torch.randn_like(x)
+            static.copy_(x2)
+            graph.replay()
+            assert torch.equal(out, fp4.linear(g, x2, w))
+    g.status()
+
+
+def test_from_parts_is_what_quantising_stores(g):
+    for fmt in FORMATS:
+        for rows, cols in ((3, 45), (130, 64), (257, 1000)):
+            m = g.fp4_quantize(torch.randn(rows, cols, device="cuda"), fmt)
+            again = Fp4Matrix.from_parts(m.data.contiguous(), m.block_scales(), m.row_scale, cols,
+                                         fmt)
+            assert torch.equal(again.data, m.data) and torch.equal(again.scale, m.scale)

@@ -1,0 +1,175 @@
+"""Orthogonalising on the GPU against its formula in doubles, and against a simulation in
+doubles of what it rounds."""
+import numpy as np
+import pytest
+import torch
+
+from dense_gemm_tmem_gb300.gemm import Gemm
+
+pytestmark = pytest.mark.gpu
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+FAST, CONVERGENT = (3.4445, -4.7750, 2.0315), (1.875, -1.25, 0.375)
+
+
+@pytest.fixture(scope="module")
+def g():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+    h = Gemm(torch.device("cuda", 0))
+    yield h
+    h.close()
+
+
+def steps_of(abc, steps):
+    return [abc] * steps if not hasattr(abc[0], "__len__") else list(abc)
+
+
+def simulate(G, steps, abc, eps=1e-7, round16=True):
+    """The steps in doubles; with round16, X, A and bA + cA² are rounded to fp16 where the
+    products read them (relative to their magnitude, which is what scaling by powers of two
+    makes of it), the iterate to fp32."""
+    X = G.double()
+    X = X / max(float(torch.linalg.matrix_norm(X)), eps)
+    tall = X.shape[0] > X.shape[1]
+    X = X.mT.contiguous() if tall else X
+    r = (lambda v: (v * 4096).half().double() / 4096) if round16 else (lambda v: v)
+    for a, b, c in steps_of(abc, steps):
+        H = r(X)
+        A = r(H @ H.mT)
+        X = a * X + r(b * A + c * (A @ A)) @ H
+        if round16:
+            X = X.float().double()
+    return X.mT if tall else X
+
+
+def rel(a, b):
+    return float((a - b).norm() / b.norm()) if float(b.norm()) else float(a.norm())
+
+
+def check(got, G, steps, abc, eps=1e-7):
+    """fp32 sums in another order turn over a few of the fp16 roundings, each by one step
+    (2^-11 of an element): less than the roundings themselves, and the result's own rounding
+    to bfloat16 is at most 2^-9 in the mean square (2^-8 at worst for an element)."""
+    assert got.dtype == BF16 and got.shape == G.shape
+    exact = simulate(G, steps, abc, eps, False)
+    rounded = simulate(G, steps, abc, eps)
+    own = rel(rounded, exact)
+    assert rel(got.double(), exact) <= 1.5 * own + 2.0 ** -9 + 1e-6, (own, rel(got.double(), exact))
+
+
+def gradient(rows, cols, dtype, rank=8, noise=0.05):
+    rank = min(rank, rows, cols)
+    fall = 1.0 / torch.arange(1, rank + 1, device="cuda")
+    G = (torch.randn(rows, rank, device="cuda") * fall) @ torch.randn(rank, cols, device="cuda")
+    return ((G + noise * torch.randn(rows, cols, device="cuda")) * 1e-3).to(dtype)
+
+
+SHAPES = [(1, 1), (1, 64), (64, 1), (8, 8), (7, 33), (130, 67), (64, 257), (257, 64), (128, 128),
+          (200, 300), (384, 640), (512, 512), (515, 1000), (1000, 515), (129, 2056), (700, 1000)]
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_shapes(g, rows, cols):
+    torch.manual_seed(rows * 3 + cols)
+    for dtype in (F32, BF16, F16):
+        for G in (gradient(rows, cols, dtype), torch.randn(rows, cols, device="cuda").to(dtype)):
+            check(g.orthogonalize(G), G, 5, FAST)
+    g.status()
+
+
+@pytest.mark.parametrize("rows,cols", [(100, 300), (600, 260), (1024, 1024)])
+@pytest.mark.parametrize("abc,steps", [(FAST, 1), (FAST, 2), (CONVERGENT, 12), ((1.5, -0.5, 0.0), 9),
+                                       ((1.0, 0.0, 0.0), 2), ((0.0, 1.0, 0.0), 1),
+                                       ([(4.0, -6.0, 3.0), FAST, CONVERGENT], 3)])
+def test_coefficients(g, rows, cols, abc, steps):
+    torch.manual_seed(steps)
+    G = torch.randn(rows, cols, device="cuda")
+    check(g.orthogonalize(G, steps, abc), G, steps, abc)
+
+
+def test_converges_to_the_polar_factor(g):
+    torch.manual_seed(1)
+    for rows, cols in ((96, 200), (300, 128)):
+        q = torch.linalg.qr(torch.randn(max(rows, cols), min(rows, cols), device="cuda").double())[0]
+        u = torch.linalg.qr(torch.randn(min(rows, cols), min(rows, cols), device="cuda").double())[0]
+        s = torch.linspace(0.2, 1.0, min(rows, cols), device="cuda").double()
+        P = q @ (u * s) @ u.T
+        want, G = q, P
+        if rows < cols:
+            want, G = want.mT, G.mT
+        got = g.orthogonalize(G.float().contiguous(), 16, CONVERGENT).double()
+        # 16-bit operands in the last steps (2^-11 each) and the result's rounding
+        assert rel(got, want.contiguous()) <= 3 * 2.0 ** -11 + 2.0 ** -9
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 64, 100), (3, 70, 130), (10, 200, 72), (40, 128, 128),
+                                             (5, 300, 260)])
+def test_batch_is_each_by_itself(g, batch, rows, cols):
+    torch.manual_seed(batch)
+    G = torch.randn(batch, rows, cols, device="cuda") * torch.logspace(-6, 6, batch,
+                                                                      device="cuda").view(-1, 1, 1)
+    got = g.orthogonalize(G)
+    for i in range(batch):
+        check(got[i], G[i], 5, FAST)
+        assert torch.equal(got[i], g.orthogonalize(G[i].contiguous())), i
+
+
+def test_strided_input(g):
+    torch.manual_seed(5)
+    buf = torch.randn(4, 150, 260, device="cuda")
+    for G in (buf[1:3, 3:130, 1:200], buf[::2, :100, :256], buf[0, ::3, 5:71],
+              buf[:1].expand(3, 150, 260)):
+        got = g.orthogonalize(G)
+        assert got.is_contiguous() and torch.equal(got, g.orthogonalize(G.contiguous()))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e12, 3e37])
+def test_far_magnitudes(g, dtype, scale):
+    """Squares that leave fp32's range; eps far below."""
+    torch.manual_seed(2)
+    G = (torch.randn(130, 200, device="cuda").clamp(-5, 5).double() * scale).to(dtype)
+    check(g.orthogonalize(G, eps=2.0 ** -100), G, 5, FAST, 2.0 ** -100)
+    G[3, 4] = 3e38
+    check(g.orthogonalize(G, eps=2.0 ** -100), G, 5, FAST, 2.0 ** -100)
+
+
+def test_zero_small_and_non_finite(g):
+    z = torch.zeros(3, 100, 64, device="cuda")
+    assert float(g.orthogonalize(z).abs().max()) == 0
+    z[1] = torch.randn(100, 64, device="cuda") * 1e-9
+    got = g.orthogonalize(z)
+    check(got[1], z[1], 5, FAST)
+    assert float(got[0].abs().max()) == 0 and float(got[2].abs().max()) == 0
+    for bad in (float("nan"), float("inf")):
+        z[2, 99, 63] = bad
+        again = g.orthogonalize(z)
+        assert torch.equal(again[:2], got[:2]) and bool(torch.isnan(again[2]).all())
+
+
+def test_empty(g):
+    for shape in ((0, 5), (5, 0), (0, 4, 4), (3, 0, 4)):
+        assert g.orthogonalize(torch.zeros(shape, device="cuda")).shape == shape
+
+
+def test_streams_graphs_and_repeats(g):
+    torch.manual_seed(3)
+    for shape in ((64, 64), (3, 200, 136), (600, 1030)):
+        G = torch.randn(shape, device="cuda").bfloat16()
+        want = g.orthogonalize(G)
+        for _ in range(4):
+            assert torch.equal(g.orthogonalize(G), want)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        got = g.orthogonalize(G, stream=s)
+        s.synchronize()
+        assert torch.equal(got, want)
+        graph, static = torch.cuda.CUDAGraph(), torch.randn_like(G)
+        with torch.cuda.graph(graph):
+            out = g.orthogonalize(static)
+        static.copy_(G)
+        for _ in range(3):
+            graph.replay()
+            assert torch.equal(out, want)
+    g.status()
