@@ -66,17 +66,6 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t byte, int format) {
   return unpack_e4m3x2(byte).x;
 }
 
-// What the matrix holds in (r, c), without its row scale.
-__device__ __forceinline__ float fp4_element(const gemm_fp4_matrix_t& m, int64_t r, int64_t c,
-                                             int64_t pieces) {
-  const uint32_t byte = static_cast<const uint8_t*>(m.data)[r * m.ld + (c >> 1)];
-  const float2 v = unpack_e2m1x2(byte);
-  const int64_t b = c / fp4_block(m.format);
-  return (c & 1 ? v.y : v.x) *
-         fp4_scale_value(static_cast<const uint8_t*>(m.scale)[fp4_scale_at(r, b, pieces)],
-                         m.format);
-}
-
 struct Fp4Product {
   int64_t M, N, K;
   gemm_fp4_matrix_t A, B;
@@ -90,6 +79,6 @@ cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int
                                 int src_dtype, const gemm_fp4_matrix_t& out, cudaStream_t stream);
 cudaError_t launch_fp4_dequantize(int64_t rows, int64_t cols, const gemm_fp4_matrix_t& m,
                                   void* dst, int64_t ld_dst, int dst_dtype, cudaStream_t stream);
-cudaError_t launch_fp4_simt(const Fp4Product& p, cudaStream_t stream);
+cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream);
 
 }  // namespace dg

@@ -78,7 +78,7 @@ int gemm_fp4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp
   if (!C) return GEMM_ERR_INVALID_ARG;
   const dg::Fp4Product p{M, N, K, *A, *B, bias, C, ldc, out_dtype};
   return dg::on_device(h->device, [&]() -> int {
-    return dg::done(dg::launch_fp4_simt(p, static_cast<cudaStream_t>(stream)));
+    return dg::done(dg::launch_fp4(h, p, static_cast<cudaStream_t>(stream)));
   });
 }
 

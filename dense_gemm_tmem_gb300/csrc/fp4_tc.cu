@@ -1,0 +1,189 @@
+// fp4_tc.cu: plan, tensor maps and launch of the 4-bit product.
+#include <algorithm>
+
+#include "context.h"
+#include "fp4_tc_kernel.cuh"
+
+namespace dg {
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* p, cuuint64_t inner,
+            cuuint64_t outer, cuuint64_t pitch, cuuint32_t box_inner, cuuint32_t box_outer,
+            CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint32_t box[2] = {box_inner, box_outer}, estr[2] = {1, 1};
+  return fn && fn(map, type, 2, const_cast<void*>(p), dims, &pitch, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Values: rows of ceil(K / 2) bytes in boxes of box_rows x 128, zeros outside.  Scales:
+// groups of 128 rows in boxes of box_groups x a k-block's pieces (8-byte elements, as a
+// box has at most 256), zeros past the last piece.
+bool encode_operand(CUtensorMap* values, CUtensorMap* scales, const gemm_fp4_matrix_t& m,
+                    int64_t rows, int64_t K, int box_rows, int box_groups) {
+  const int64_t pieces = ceil_div(K, 4 * fp4_block(m.format));
+  const int per = kF4BlockK / (4 * fp4_block(m.format));
+  return encode(values, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.data, cuuint64_t(ceil_div(K, 2)),
+                cuuint64_t(rows), cuuint64_t(rows > 1 ? m.ld : (m.ld + 15) & ~int64_t(15)), 128,
+                cuuint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, m.scale,
+                cuuint64_t(pieces * (kFp4Piece / 8)), cuuint64_t(ceil_div(rows, 128)),
+                cuuint64_t(pieces * kFp4Piece), cuuint32_t(per * kFp4Piece / 8),
+                cuuint32_t(box_groups), CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Row-major C for the epilogue's TMA stores, as the 8-bit product's: boxes of 32 rows
+// of 128 bytes, only for rows of whole 16-byte pieces.
+bool encode_c(CUtensorMap* map, const Fp4Product& p) {
+  const int size = p.out_dtype == GEMM_F32 ? 4 : 2;
+  const cuuint64_t pitch = cuuint64_t(p.ldc) * size;
+  return pitch < (cuuint64_t(1) << 40) && p.N * size % 16 == 0 &&
+         encode(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                p.C, cuuint64_t(p.N), cuuint64_t(p.M), pitch, cuuint32_t(128 / size), 32,
+                CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int BN, bool PAIR, bool TRANS, int FMT, bool OUT32>
+cudaError_t launch_inst(const Fp4Maps& maps, const CUtensorMap& mC, const Fp4TcArgs& args,
+                        int device, bool pdl, cudaStream_t stream) {
+  auto kern = fp4_tc_kernel<BN, PAIR, TRANS, FMT, OUT32>;
+  constexpr int smem = Fp4TcConfig<BN, PAIR, FMT>::kSmemBytes;
+  static SharedMemoryOnce once;
+  cudaError_t e = once.allow(kern, smem, device);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  const int cluster = PAIR ? 2 : args.work.csplit;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = unsigned(cluster);
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.gridDim = dim3(unsigned(args.work.grid * (PAIR ? 2 : 1)), 1, 1);
+  cfg.blockDim = dim3(kF4Threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = unsigned(n);
+  return cudaLaunchKernelEx(&cfg, kern, maps, mC, args);
+}
+
+template <int FMT, class Launch>
+cudaError_t launch_format(int bn, bool trans, bool out32, Launch&& launch) {
+  if (trans) {
+    if (bn == 32) return launch(launch_inst<32, false, true, FMT, false>);
+    if (bn == 64) return launch(launch_inst<64, false, true, FMT, false>);
+    return launch(launch_inst<128, false, true, FMT, false>);
+  }
+  if (bn == 256)
+    return out32 ? launch(launch_inst<256, true, false, FMT, true>)
+                 : launch(launch_inst<256, true, false, FMT, false>);
+  if (bn == 64)
+    return out32 ? launch(launch_inst<64, false, false, FMT, true>)
+                 : launch(launch_inst<64, false, false, FMT, false>);
+  return out32 ? launch(launch_inst<128, false, false, FMT, true>)
+               : launch(launch_inst<128, false, false, FMT, false>);
+}
+
+// K == 0: C = bias (or 0).
+__global__ void fp4_fill_kernel(int64_t M, int64_t N, const float* bias, void* C, int64_t ldc,
+                                int dtype) {
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < M * N;
+       i += int64_t(gridDim.x) * blockDim.x)
+    store_typed(C, i / N * ldc + i % N, bias ? bias[i % N] : 0.f, dtype);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
+  if (p.K == 0) {
+    fp4_fill_kernel<<<1024, 256, 0, stream>>>(p.M, p.N, p.bias, p.C, p.ldc, p.out_dtype);
+    return cudaGetLastError();
+  }
+  // Few rows of A: operands swapped, so that the other side fills the 128 MMA rows and
+  // A's rows are the MMA's columns, 32, 64 or 128 of them.
+  const bool trans = p.M <= 128 && p.N > p.M;
+  const gemm_fp4_matrix_t& opA = trans ? p.B : p.A;
+  const gemm_fp4_matrix_t& opB = trans ? p.A : p.B;
+  const int64_t Mm = trans ? p.N : p.M, Nm = trans ? p.M : p.N;
+  const int64_t sms = h->num_sms;
+  const int64_t I = ceil_div(p.K, kF4BlockK);
+  const int64_t pairs = h->opt.pair_clusters > 0 ? h->opt.pair_clusters : sms / 2;
+  // Fewer tiles than half the SMs: each tile's k-blocks over a cluster, the largest
+  // whose clusters are all resident at once, if that takes more than kSplitGain
+  // k-blocks off each CTA.
+  constexpr int64_t kSplitGain = 4;
+  const int forced = h->opt.csplit;  // GEMM_OPT_CLUSTER_SPLIT
+  auto split_of = [&](int64_t T) -> int64_t {
+    if (forced < 2 && (forced >= 0 || 2 * T >= sms)) return 1;
+    for (int s : {8, 4, 2}) {
+      if (forced >= 2 ? s == forced && I >= s && T * s <= INT32_MAX
+                      : T <= h->opt.csplit_clusters[s] && T * s <= sms &&
+                            I - ceil_div(I, s) > kSplitGain)
+        return s;
+    }
+    return 1;
+  };
+  int64_t tiles_m = ceil_div(Mm, kBM);
+  int bn;
+  if (trans) {
+    bn = Nm <= 32 ? 32 : Nm <= 64 ? 64 : 128;
+  } else if (ceil_div(Mm, 256) * ceil_div(Nm, 256) >= pairs / 2) {
+    bn = 256;
+    tiles_m = ceil_div(Mm, 256);
+  } else {
+    bn = 2 * tiles_m * ceil_div(Nm, 128) <= sms ? 64 : 128;
+  }
+  const int64_t tiles_n = ceil_div(Nm, bn), T = tiles_m * tiles_n;
+  if (T > INT32_MAX / 2) return cudaErrorInvalidValue;
+  const int64_t split = bn <= 128 ? split_of(T) : 1;
+  Fp4TcArgs a{};
+  a.work.tiles_m = int32_t(tiles_m);
+  a.work.tiles_n = int32_t(tiles_n);
+  a.work.k_iters = int32_t(I);
+  a.work.dp_tiles = int32_t(split > 1 ? 0 : T);
+  a.work.sk_tiles = int32_t(split > 1 ? T : 0);
+  a.work.grid = int32_t(split > 1 ? T * split : std::min(bn == 256 ? pairs : sms, T));
+  a.work.group_m = bn == 256 ? 8 : 16;
+  a.work.csplit = int32_t(split);
+  a.Mm = int32_t(Mm);
+  a.Nm = int32_t(Nm);
+  a.row_scale = opA.row_scale;
+  a.row_stride = opA.row_scale_stride;
+  a.col_scale = opB.row_scale;
+  a.col_stride = opB.row_scale_stride;
+  a.C = p.C;
+  a.ldc = p.ldc;
+  a.bias = p.bias;
+  a.out_dtype = p.out_dtype;
+  const int64_t pitch = p.ldc * (p.out_dtype == GEMM_F32 ? 4 : 2);
+  a.c_vec = (reinterpret_cast<uintptr_t>(p.C) & 15) == 0 && pitch % 16 == 0 ? 1 : 0;
+  a.steps = int32_t(ceil_div(p.K, 64));
+  a.status = h->status;
+  a.wait_limit_ns = h->opt.wait_limit_ns;
+  a.idesc = make_idesc_f4(bn == 256 ? 256 : kBM, bn, p.A.format);
+  Fp4Maps m;
+  if (!encode_operand(&m.a, &m.sa, opA, Mm, p.K, kBM, 1) ||
+      !encode_operand(&m.b, &m.sb, opB, Nm, p.K, bn == 256 ? 128 : bn, bn == 256 ? 2 : 1))
+    return cudaErrorInvalidValue;
+  CUtensorMap mC{};
+  a.c_tma = bn == 256 && a.c_vec && encode_c(&mC, p);
+  const bool pdl = h->opt.pdl != 0, out32 = p.out_dtype == GEMM_F32;
+  auto launch = [&](auto inst) { return inst(m, mC, a, h->device, pdl, stream); };
+  return p.A.format == GEMM_MXFP4 ? launch_format<GEMM_MXFP4>(bn, trans, out32, launch)
+                                  : launch_format<GEMM_NVFP4>(bn, trans, out32, launch);
+}
+
+}  // namespace dg

@@ -445,8 +445,8 @@ __device__ __forceinline__ bool f8_mma(const Fp8TcArgs& args, uint32_t sA, uint3
 // 64 bytes of each row at a time through the warp's shared rows, so that 4 lanes
 // store a row's 64 bytes and an instruction 8 rows.  SIZE: bytes an element.
 // The bias is added in fp32 before the one rounding.
-template <int HC, int SIZE>
-__device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float (&acc)[HC],
+template <int HC, int SIZE, class Args>
+__device__ __forceinline__ void f8_store_rows(const Args& a, const float (&acc)[HC],
                                               float* stage_w, int32_t mrow0, int lane,
                                               int32_t nn0) {
   constexpr int PER = 64 / SIZE;               // columns a pass
@@ -515,11 +515,11 @@ __device__ __forceinline__ void f8_store_rows(const Fp8TcArgs& a, const float (&
 }
 
 // The same by TMA, 128 bytes of the 32 rows (a swizzled box) at a time through two
-// boxes a warp: the stores drain while the next tile is summed (4096^3 73.2 against
+// boxes a warp (or one): the stores drain while the next tile is summed (4096^3 73.2 against
 // 76.7 us with f8_store_rows, a linear step of three such products 317 against 327).
 // Outside the matrix nothing is stored.
-template <int HC, int SIZE>
-__device__ __forceinline__ void f8_store_tma(const Fp8TcArgs& a, const CUtensorMap* map,
+template <int HC, int SIZE, int BOXES = 2, class Args>
+__device__ __forceinline__ void f8_store_tma(const Args& a, const CUtensorMap* map,
                                              const float (&acc)[HC], uint32_t stage,
                                              int32_t mrow0, int lane, int32_t nn0) {
   constexpr int PER = 128 / SIZE;              // columns a box
@@ -528,11 +528,11 @@ __device__ __forceinline__ void f8_store_tma(const Fp8TcArgs& a, const CUtensorM
   for (int c = 0; c < HC; c += PER) {
     if (mrow0 >= a.Mm || nn0 + c >= a.Nm) break;
     if (lane == 0) {                           // the box's last store has been read
-      if (c == 0) bulk_wait_read_all();
+      if (c == 0 || BOXES == 1) bulk_wait_read_all();
       else if (c >= 2 * PER) bulk_wait_read_1();
     }
     __syncwarp();
-    const uint32_t box = stage + uint32_t((c / PER) & 1) * 4096u, row = box + uint32_t(lane) * 128u;
+    const uint32_t box = stage + uint32_t((c / PER) & (BOXES - 1)) * 4096u, row = box + uint32_t(lane) * 128u;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t w[4];
@@ -799,7 +799,8 @@ __device__ __forceinline__ void f8_epilogue(const Fp8TcArgs& args, const CUtenso
 }
 
 // Four neighbouring outputs of a row of C, `valid` of them inside the matrix.
-__device__ __forceinline__ void f8_store4(const Fp8TcArgs& a, int64_t off, const float (&v)[4],
+template <class Args>
+__device__ __forceinline__ void f8_store4(const Args& a, int64_t off, const float (&v)[4],
                                           int valid) {
   if (valid >= 4 && a.c_vec) {
     if (a.out_dtype == GEMM_F32) {
@@ -831,8 +832,8 @@ __device__ __forceinline__ void f8_store4(const Fp8TcArgs& a, int64_t off, const
 // threads; each adds the partials in rank order and stores.  8 remote loads a
 // thread are in flight (one quad at a time cost 6 us of a 128 x 128 tile split
 // in two).
-template <int BN, bool TRANS, int SPLIT>
-__device__ __forceinline__ void f8_cluster_reduce(const Fp8TcArgs& a, uint32_t park) {
+template <int BN, bool TRANS, int SPLIT, int ROLE_WARPS = kF8RoleWarps, class Args>
+__device__ __forceinline__ void f8_cluster_reduce(const Args& a, uint32_t park) {
   using Cfg = Fp8TcConfig<BN>;
   constexpr int kThreads = 32 * kF8EpiWarps, U = 8 / SPLIT;
   const int32_t tile = int32_t(blockIdx.x) / SPLIT;
@@ -846,7 +847,7 @@ __device__ __forceinline__ void f8_cluster_reduce(const Fp8TcArgs& a, uint32_t p
   uint32_t peer[SPLIT];
 #pragma unroll
   for (int r = 0; r < SPLIT; ++r) peer[r] = map_to_rank(park, uint32_t(r));
-  for (int i0 = rank * kThreads + int(threadIdx.x) - 32 * kF8RoleWarps; i0 < total;
+  for (int i0 = rank * kThreads + int(threadIdx.x) - 32 * ROLE_WARPS; i0 < total;
        i0 += U * SPLIT * kThreads) {
     float4 x[U][SPLIT];
 #pragma unroll
