@@ -57,6 +57,7 @@ struct Fp4TcConfig {
   static constexpr int kEpiBytes = kF4EpiWarps * kWarpStage;
   static constexpr int kBarBytes = 256;
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + kBarBytes;
+  static_assert(2 * kHalf * 4 <= kWarpStage, "a warp's column scales and biases");
   static constexpr int kParkRow = BN + 4, kParkCol = kBM + 4;
   static_assert(BN == 256 || (kBM * kParkRow * 4 <= kStages * kStageBytes &&
                               BN * kParkCol * 4 <= kStages * kStageBytes), "the ring holds it");
@@ -257,14 +258,49 @@ __device__ __forceinline__ bool f4_mma(const Fp4TcArgs& args, uint32_t ring, uin
   return any;
 }
 
-// v times both row scales: their product where fp32 holds it, else the smaller first.
-__device__ __forceinline__ float f4_scaled(float v, float a, float b) {
-  const float ab = a * b;
-  if (scale_fits(ab)) return v * ab;
-  float lo, hi;
-  scale_order(a, b, lo, hi);
-  return __fmul_rn(v, lo) * hi;
-}
+// A warp's column scales and biases, HC of each, in its staging memory until the tile is
+// staged there.
+template <int HC>
+struct F4Columns {
+  static constexpr int kPer = (HC + 31) / 32;  // a lane's
+  float s[kPer], b[kPer];
+  bool fits;  // every column's scale times this lane's row scale is a number fp32 holds
+
+  // Sent for before the wait for the tile's sum; columns outside the matrix have 1 and 0.
+  __device__ __forceinline__ void load(const float* scale, int64_t stride, const float* bias,
+                                       int32_t n0, int32_t N, int lane) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = lane + i * 32;
+      const bool in = j < HC && n0 + j < N;
+      s[i] = scale && in ? __ldg(scale + int64_t(n0 + j) * stride) : 1.f;
+      b[i] = bias && in ? __ldg(bias + n0 + j) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void share(float* to, float row, int lane) {
+    float most = 0.f, least = INFINITY;
+    bool nan = false;
+    __syncwarp();  // the last tile's have been read
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (lane + i * 32 < HC) {
+        to[lane + i * 32] = s[i];
+        to[HC + lane + i * 32] = b[i];
+      }
+      const float a = fabsf(s[i]);
+      most = fmaxf(most, a);
+      least = fminf(least, a);
+      nan |= !(a == a);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+      least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
+    }
+    fits = __all_sync(0xffffffffu, !nan && scale_fits(row * most) && scale_fits(row * least));
+    __syncwarp();
+  }
+};
 
 template <int BN, bool PAIR, bool TRANS, int FMT, bool OUT32>
 __device__ __forceinline__ void f4_epilogue(const Fp4TcArgs& args, const CUtensorMap* tmC,
@@ -285,7 +321,13 @@ __device__ __forceinline__ void f4_epilogue(const Fp4TcArgs& args, const CUtenso
   Unit u;
   uint32_t b = 0, bph = 0;
   const uint32_t tlane = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(wg * HC);
-  const bool scaled = args.row_scale != nullptr || args.col_scale != nullptr;
+  // the bias joins the scales, but for a split tile's (added after the partials) and for
+  // a transposed one's (a lane's own)
+  const float* const bias = TRANS || (BN <= 128 && W.csplit > 1) ? nullptr : args.bias;
+  const bool columns = args.row_scale != nullptr || args.col_scale != nullptr || bias != nullptr;
+  F4Columns<HC> C;
+  Fp4TcArgs plain = args;
+  plain.bias = nullptr;
   while (it.next(W, u)) {
     int32_t tm, tn;
     tile_coords(W, u.tile, tm, tn);
@@ -294,6 +336,11 @@ __device__ __forceinline__ void f4_epilogue(const Fp4TcArgs& args, const CUtenso
     const int32_t nn0 = tn * BN + wg * HC;
     const float rs = args.row_scale && mm < args.Mm
                          ? __ldg(args.row_scale + int64_t(mm) * args.row_stride) : 1.f;
+    if (columns) {
+      C.load(args.col_scale, args.col_stride, bias, nn0, args.Nm, lane);
+      if (BN == 256 && lane == 0) bulk_wait_read_all();  // the last tile's store has left
+      C.share(stage_w, rs, lane);
+    }
     const bool ok = wait_bounded(acc_full + 8 * b, bph, wc, kSiteEpilogue);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after();
@@ -324,12 +371,27 @@ __device__ __forceinline__ void f4_epilogue(const Fp4TcArgs& args, const CUtenso
       b = 0;
       bph ^= 1;
     }
-    if (scaled) {
+    if (columns) {
+      // the product of the two scales where fp32 holds it, else the smaller first
+      const float* cs = stage_w;
+      const float* cb = stage_w + HC;
+      if (C.fits) {
 #pragma unroll
-      for (int j = 0; j < HC; ++j) {
-        const float cs = args.col_scale && nn0 + j < args.Nm
-                             ? __ldg(args.col_scale + int64_t(nn0 + j) * args.col_stride) : 1.f;
-        acc[j] = f4_scaled(acc[j], rs, cs);
+        for (int j = 0; j < HC; j += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(cs + j);
+          const float4 b4 = *reinterpret_cast<const float4*>(cb + j);
+          acc[j] = fmaf(acc[j], s4.x * rs, b4.x);
+          acc[j + 1] = fmaf(acc[j + 1], s4.y * rs, b4.y);
+          acc[j + 2] = fmaf(acc[j + 2], s4.z * rs, b4.z);
+          acc[j + 3] = fmaf(acc[j + 3], s4.w * rs, b4.w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+          float lo, hi;
+          scale_order(rs, cs[j], lo, hi);
+          acc[j] = fmaf(__fmul_rn(acc[j], lo), hi, cb[j]);
+        }
       }
     }
     if (BN <= 128 && W.csplit > 1) {
@@ -362,9 +424,9 @@ __device__ __forceinline__ void f4_epilogue(const Fp4TcArgs& args, const CUtenso
     } else {
       constexpr int SIZE = OUT32 ? 4 : 2;
       if (BN == 256 && args.c_tma)
-        f8_store_tma<HC, SIZE, 1>(args, tmC, acc, smem_u32(stage_w), mrow0 + q * 32, lane, nn0);
+        f8_store_tma<HC, SIZE, 1>(plain, tmC, acc, smem_u32(stage_w), mrow0 + q * 32, lane, nn0);
       else
-        f8_store_rows<HC, SIZE>(args, acc, stage_w, mrow0 + q * 32, lane, nn0);
+        f8_store_rows<HC, SIZE>(plain, acc, stage_w, mrow0 + q * 32, lane, nn0);
     }
   }
   // every store this warp issued has landed before the CTA moves on
