@@ -60,7 +60,7 @@ struct PrepArgs {
   int dtype;
   float* parts;  // batch x kNormParts x 3
   double eps;
-  float* x32;    // batch x rows x cols
+  float* x32;
   __half* x16;
   int64_t ld_x, stride_x;
   float scale;   // of the 16-bit copy
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kNormThreads) ortho_norm_kernel(const PrepArgs
 
 // X = G / max(norm, eps) and its 16-bit copy.
 __global__ void __launch_bounds__(kNormThreads) ortho_scale_kernel(const PrepArgs a) {
-  const int64_t z = blockIdx.y, n = a.rows * a.cols;
+  const int64_t z = blockIdx.y;
   Squares s;
   if (threadIdx.x < kNormParts) {
     const float* p = a.parts + (z * kNormParts + threadIdx.x) * 3;
@@ -103,12 +103,13 @@ __global__ void __launch_bounds__(kNormThreads) ortho_scale_kernel(const PrepArg
   const int e = fine ? ilogb(inv) : 0;
   const float p1 = fine ? float(scalbn(1.0, e / 2)) : NAN;
   const float p2 = fine ? float(scalbn(inv, -e) * scalbn(1.0, e - e / 2)) : NAN;
-  for (int64_t i = int64_t(blockIdx.x) * kNormThreads + threadIdx.x; i < n;
+  for (int64_t i = int64_t(blockIdx.x) * kNormThreads + threadIdx.x; i < a.stride_x;
        i += int64_t(gridDim.x) * kNormThreads) {
-    const int64_t r = i / a.cols, c = i - r * a.cols;
-    const float x = load_typed(a.g, z * a.stride_g + r * a.ld_g + c, a.dtype) * p1 * p2;
-    a.x32[z * n + i] = x;
-    a.x16[z * a.stride_x + r * a.ld_x + c] = __float2half_rn(x * a.scale);
+    const int64_t r = i / a.ld_x, c = i - r * a.ld_x;
+    const float x =
+        c < a.cols ? load_typed(a.g, z * a.stride_g + r * a.ld_g + c, a.dtype) * p1 * p2 : 0.f;
+    a.x32[z * a.stride_x + i] = x;
+    a.x16[z * a.stride_x + i] = __float2half_rn(x * a.scale);
   }
 }
 
@@ -121,8 +122,8 @@ OrthoShape shape_of(const gemm_orthogonalize_t& p) {
   s.cols = p.cols;
   s.n = std::min(p.rows, p.cols);
   s.tall = p.rows > p.cols;
-  s.ld_x = round_up(p.cols, 8);
-  s.ld_a = round_up(s.n, 8);
+  s.ld_x = round_up(p.cols, 64);
+  s.ld_a = round_up(s.n, 64);
   s.stride_x = s.rows * s.ld_x;
   s.stride_a = s.n * s.ld_a;
   return s;
@@ -141,7 +142,7 @@ Space space_of(const OrthoShape& s) {
     return here;
   };
   w.parts = take(s.batch * kNormParts * 3 * 4);
-  w.x32 = take(s.batch * s.rows * s.cols * 4);
+  w.x32 = take(s.batch * s.stride_x * 4);
   w.x16 = take(2 * round_up(s.batch * s.stride_x * 2, 256));
   w.a16 = take(s.batch * s.stride_a * 2);
   w.b16 = take(s.batch * s.stride_a * 2);
@@ -215,7 +216,7 @@ int check_sizes(const gemm_orthogonalize_t* p) {
   return GEMM_OK;
 }
 
-cudaError_t enqueue(const gemm_orthogonalize_t& p, const Plan& plan, uint8_t* w,
+cudaError_t enqueue(gemm_ctx* h, const gemm_orthogonalize_t& p, const Plan& plan, uint8_t* w,
                     cudaStream_t stream) {
   const OrthoShape s = shape_of(p);
   const Space at = space_of(s);
@@ -243,7 +244,7 @@ cudaError_t enqueue(const gemm_orthogonalize_t& p, const Plan& plan, uint8_t* w,
     q.alpha = two(plan.a[i] - 2 * plan.x[i]);
     q.a = x16[i & 1];
     q.c = a16;
-    e = launch_ortho_simt(s, q, stream);
+    e = launch_ortho_product(h, s, q, stream);
     if (e != cudaSuccess) break;
     q = {};
     q.kind = kPoly;
@@ -251,7 +252,7 @@ cudaError_t enqueue(const gemm_orthogonalize_t& p, const Plan& plan, uint8_t* w,
     q.beta = std::ldexp(b, plan.b[i] - plan.a[i]);
     q.a = a16;
     q.c = b16;
-    e = launch_ortho_simt(s, q, stream);
+    e = launch_ortho_product(h, s, q, stream);
     if (e != cudaSuccess) break;
     q = {};
     q.kind = kApply;
@@ -268,7 +269,7 @@ cudaError_t enqueue(const gemm_orthogonalize_t& p, const Plan& plan, uint8_t* w,
       q.scale = two(plan.x[i + 1]);
       q.c = x16[(i + 1) & 1];
     }
-    e = launch_ortho_simt(s, q, stream);
+    e = launch_ortho_product(h, s, q, stream);
   }
   return e;
 }
@@ -306,7 +307,7 @@ int gemm_orthogonalize(gemm_handle_t h, const gemm_orthogonalize_t* p, void* wor
       workspace_bytes < dg::space_of(dg::shape_of(*p)).total)
     return GEMM_ERR_INVALID_ARG;
   return dg::on_device(h->device, [&]() -> int {
-    return dg::enqueue(*p, plan, static_cast<uint8_t*>(workspace),
+    return dg::enqueue(h, *p, plan, static_cast<uint8_t*>(workspace),
                        static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GEMM_OK
                : GEMM_ERR_CUDA;

@@ -17,7 +17,9 @@ struct OrthoShape {
   int64_t batch, rows, cols;
   int64_t n;                // min(rows, cols)
   bool tall;                // rows > cols
-  int64_t ld_x, ld_a;       // elements from row to row of the 16-bit copies, multiples of 8
+  // elements from row to row of the iterate and its 16-bit copies, and of A and B:
+  // multiples of 64, zeros past the matrix
+  int64_t ld_x, ld_a;
   int64_t stride_x, stride_a;
 };
 
@@ -32,11 +34,12 @@ struct OrthoProduct {
   const __half* a;   // X16, A16, B16
   const __half* x;   // kApply: X16
   __half* c;         // A16, B16, X16 (not the one that is read)
-  float* x32;        // kApply: the iterate, read and written (rows x cols, dense)
+  float* x32;        // kApply: the iterate, read and written (laid out as X16)
   void* out;         // kApply, last step: bfloat16, else NULL
   int64_t ld_out, stride_out;
 };
 
-cudaError_t launch_ortho_simt(const OrthoShape& s, const OrthoProduct& p, cudaStream_t stream);
+cudaError_t launch_ortho_product(gemm_ctx* h, const OrthoShape& s, const OrthoProduct& p,
+                                 cudaStream_t stream);
 
 }  // namespace dg
