@@ -9,18 +9,19 @@
 namespace dg {
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr int kNormParts = 128;  // CTAs that sum one matrix
+constexpr int kPrepThreads = 256;
+constexpr int kNormParts = 256;  // CTAs that sum one matrix, at most
+constexpr int kUnit = 8;         // neighbours that a thread takes at a time
 
 // Sums of squares as three numbers, so that no element's square leaves fp32's range
 // (J. L. Blue, "A portable Fortran program to find the Euclidean norm of a vector",
-// 1978): magnitudes above 2^50 are taken down by 2^96 first (squares up to 2^64, which any sum of
-// 2^40 holds), those below 2^-50 up by 2^64.
+// 1978): magnitudes above 2^40 are taken down by 2^96 first (squares up to 2^64, which
+// any sum of 2^40 holds), those below 2^-50 up by 2^64.
 struct Squares {
   float big = 0.f, mid = 0.f, small = 0.f;
   __device__ __forceinline__ void add(float x) {
     const float a = fabsf(x);
-    if (a > 0x1p50f) {
+    if (a > 0x1p40f) {
       const float t = a * 0x1p-96f;
       big = fmaf(t, t, big);
     } else if (a < 0x1p-50f) {
@@ -30,87 +31,220 @@ struct Squares {
       mid = fmaf(a, a, mid);
     }
   }
-  __device__ __forceinline__ double norm() const {
-    return sqrt(double(big) * 0x1p192 + double(mid) + double(small) * 0x1p-128);
+  // A unit at once where its largest magnitude is an ordinary one: what then underflows
+  // is 2^-26 of its sum at most.
+  __device__ __forceinline__ void add(const float (&x)[kUnit]) {
+    float most = 0.f, sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) {
+      most = fmaxf(most, fabsf(x[j]));
+      sum = fmaf(x[j], x[j], sum);
+    }
+    if (most <= 0x1p40f && most >= 0x1p-50f) {
+      mid += sum;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) add(x[j]);
+    }
+  }
+  // 1 / max(norm, eps) as two factors, since it may lie outside fp32's range.
+  __device__ __forceinline__ void inverse(float eps, float& p1, float& p2) const {
+    float m, down;  // norm = sqrt(m) / down
+    if (big > 0.f || !(mid + small < INFINITY)) {
+      m = big + mid * 0x1p-96f * 0x1p-96f;
+      down = 0x1p-96f;
+      if (!(mid + small < INFINITY)) m = NAN;
+    } else if (mid > 0.f) {
+      m = mid + small * 0x1p-64f * 0x1p-64f;
+      down = 1.f;
+    } else {
+      m = small;
+      down = 0x1p64f;
+    }
+    float root = sqrtf(m);
+    if (root < eps * down) {
+      root = eps;
+      down = 1.f;
+    }
+    p1 = down;
+    p2 = m < INFINITY ? __fdiv_rn(1.f, root) : NAN;
   }
 };
-
-__device__ __forceinline__ float load_typed(const void* p, int64_t i, int dtype) {
-  if (dtype == GEMM_F32) return static_cast<const float*>(p)[i];
-  if (dtype == GEMM_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float red[kNormThreads / 32];
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-#pragma unroll
-  for (int w = 0; w < kNormThreads / 32; ++w) v += red[w];
-  __syncthreads();
-  return v;
-}
 
 struct PrepArgs {
   const void* g;
   int64_t rows, cols, ld_g, stride_g;
   int dtype;
-  float* parts;  // batch x kNormParts x 3
-  double eps;
+  bool vec;      // 16-byte loads of g
+  int32_t parts; // CTAs of the norm
+  float* sums;   // batch x parts x 3
+  float eps;
   float* x32;
   __half* x16;
   int64_t ld_x, stride_x;
   float scale;   // of the 16-bit copy
 };
 
-__global__ void __launch_bounds__(kNormThreads) ortho_norm_kernel(const PrepArgs a) {
-  const int64_t z = blockIdx.y, n = a.rows * a.cols;
-  Squares s;
-  for (int64_t i = int64_t(blockIdx.x) * kNormThreads + threadIdx.x; i < n;
-       i += int64_t(kNormParts) * kNormThreads) {
-    const int64_t r = i / a.cols, c = i - r * a.cols;
-    s.add(load_typed(a.g, z * a.stride_g + r * a.ld_g + c, a.dtype));
+// Elements c ... c + 7 of a row of g, zeros past its end.
+__device__ __forceinline__ void load_unit(const PrepArgs& a, int64_t row_at, int32_t c,
+                                          float (&x)[kUnit]) {
+  const int64_t at = row_at + c;
+  if (a.vec && c + kUnit <= a.cols) {
+    if (a.dtype == GEMM_F32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.g) + at);
+      const float4 u = __ldg(p), v = __ldg(p + 1);
+      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    } else {
+      const uint4 u =
+          __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.g) + at));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 f;
+        if (a.dtype == GEMM_F16) {
+          __half2 h;
+          __builtin_memcpy(&h, &w[j], 4);
+          f = __half22float2(h);
+        } else {
+          f = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+        }
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+      }
+    }
+    return;
   }
-  const float big = block_sum(s.big), mid = block_sum(s.mid), small = block_sum(s.small);
-  if (threadIdx.x == 0) {
-    float* p = a.parts + (z * kNormParts + blockIdx.x) * 3;
-    p[0] = big;
-    p[1] = mid;
-    p[2] = small;
+#pragma unroll
+  for (int j = 0; j < kUnit; ++j) {
+    x[j] = 0.f;
+    if (c + j >= a.cols) continue;
+    if (a.dtype == GEMM_F32) x[j] = static_cast<const float*>(a.g)[at + j];
+    else if (a.dtype == GEMM_F16) x[j] = __half2float(static_cast<const __half*>(a.g)[at + j]);
+    else x[j] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[at + j]);
   }
 }
 
-// X = G / max(norm, eps) and its 16-bit copy.
-__global__ void __launch_bounds__(kNormThreads) ortho_scale_kernel(const PrepArgs a) {
+// Walks the units of a matrix, `step` threads apart, without a division a unit.
+struct UnitWalk {
+  int32_t r, c, dr, dc, per;  // row and unit, their steps, units a row
+  __device__ __forceinline__ UnitWalk(int64_t start, int64_t step, int32_t per) : per(per) {
+    r = int32_t(start / per);
+    c = int32_t(start - int64_t(r) * per);
+    dr = int32_t(step / per);
+    dc = int32_t(step - int64_t(dr) * per);
+  }
+  __device__ __forceinline__ void next() {
+    r += dr;
+    c += dc;
+    if (c >= per) {
+      c -= per;
+      ++r;
+    }
+  }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// The squares of a CTA's threads, added in a fixed order; every thread has the sum.
+__device__ __forceinline__ Squares block_sum(Squares s) {
+  constexpr int kWarps = kPrepThreads / 32;
+  __shared__ float red[3][kWarps];
+  s.big = warp_sum(s.big);
+  s.mid = warp_sum(s.mid);
+  s.small = warp_sum(s.small);
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = s.big;
+    red[1][threadIdx.x >> 5] = s.mid;
+    red[2][threadIdx.x >> 5] = s.small;
+  }
+  __syncthreads();
+  s = Squares();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    s.big += red[0][w];
+    s.mid += red[1][w];
+    s.small += red[2][w];
+  }
+  return s;
+}
+
+__global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const PrepArgs a) {
   const int64_t z = blockIdx.y;
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
   Squares s;
-  if (threadIdx.x < kNormParts) {
-    const float* p = a.parts + (z * kNormParts + threadIdx.x) * 3;
+  const int32_t per = int32_t((a.cols + kUnit - 1) / kUnit);
+  UnitWalk u(int64_t(blockIdx.x) * kPrepThreads + threadIdx.x, int64_t(a.parts) * kPrepThreads,
+             per);
+#pragma unroll 4
+  for (; u.r < a.rows; u.next()) {
+    float x[kUnit];
+    load_unit(a, z * a.stride_g + int64_t(u.r) * a.ld_g, u.c * kUnit, x);
+    s.add(x);
+  }
+  s = block_sum(s);
+  if (threadIdx.x == 0) {
+    float* p = a.sums + (z * a.parts + blockIdx.x) * 3;
+    p[0] = s.big;
+    p[1] = s.mid;
+    p[2] = s.small;
+  }
+}
+
+// X = G / max(norm, eps) and its 16-bit copy, with zeros up to the rows' padded ends.
+__global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const PrepArgs a) {
+  const int64_t z = blockIdx.y;
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
+  Squares s;
+  if (threadIdx.x < a.parts) {
+    const float* p = a.sums + (z * a.parts + threadIdx.x) * 3;
     s.big = p[0];
     s.mid = p[1];
     s.small = p[2];
   }
-  s.big = block_sum(s.big);
-  s.mid = block_sum(s.mid);
-  s.small = block_sum(s.small);
-  const double norm = s.norm();
-  const double inv = 1.0 / fmax(norm, a.eps);
-  // 1 / norm may lie outside fp32's range: a factor in [1, 2) and two powers of two
-  const bool fine = norm < INFINITY;
-  const int e = fine ? ilogb(inv) : 0;
-  const float p1 = fine ? float(scalbn(1.0, e / 2)) : NAN;
-  const float p2 = fine ? float(scalbn(inv, -e) * scalbn(1.0, e - e / 2)) : NAN;
-  for (int64_t i = int64_t(blockIdx.x) * kNormThreads + threadIdx.x; i < a.stride_x;
-       i += int64_t(gridDim.x) * kNormThreads) {
-    const int64_t r = i / a.ld_x, c = i - r * a.ld_x;
-    const float x =
-        c < a.cols ? load_typed(a.g, z * a.stride_g + r * a.ld_g + c, a.dtype) * p1 * p2 : 0.f;
-    a.x32[z * a.stride_x + i] = x;
-    a.x16[z * a.stride_x + i] = __float2half_rn(x * a.scale);
+  s = block_sum(s);
+  float p1, p2;
+  s.inverse(a.eps, p1, p2);
+  UnitWalk u(int64_t(blockIdx.x) * kPrepThreads + threadIdx.x,
+             int64_t(gridDim.x) * kPrepThreads, int32_t(a.ld_x / kUnit));
+#pragma unroll 2
+  for (; u.r < a.rows; u.next()) {
+    float x[kUnit];
+    load_unit(a, z * a.stride_g + int64_t(u.r) * a.ld_g, u.c * kUnit, x);
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) x[j] = x[j] * p1 * p2;
+    const int64_t at = z * a.stride_x + int64_t(u.r) * a.ld_x + u.c * kUnit;
+    float4* to = reinterpret_cast<float4*>(a.x32 + at);
+    to[0] = make_float4(x[0], x[1], x[2], x[3]);
+    to[1] = make_float4(x[4], x[5], x[6], x[7]);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 h = __floats2half2_rn(x[2 * j] * a.scale, x[2 * j + 1] * a.scale);
+      __builtin_memcpy(&w[j], &h, 4);
+    }
+    *reinterpret_cast<uint4*>(a.x16 + at) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+cudaError_t launch_prep(void (*kern)(PrepArgs), const PrepArgs& a, unsigned ctas, int64_t batch,
+                        bool pdl, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(ctas, unsigned(batch), 1);
+  cfg.blockDim = dim3(kPrepThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1u : 0u;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -227,14 +361,35 @@ cudaError_t enqueue(gemm_ctx* h, const gemm_orthogonalize_t& p, const Plan& plan
   __half* a16 = reinterpret_cast<__half*>(w + at.a16);
   __half* b16 = reinterpret_cast<__half*>(w + at.b16);
   auto two = [](int e) { return std::ldexp(1.f, e); };
-  const PrepArgs prep{p.g,    s.rows, s.cols,  p.ld_g, p.stride_g,
-                      p.dtype, reinterpret_cast<float*>(w + at.parts), p.eps, x32,
-                      x16[0], s.ld_x, s.stride_x, two(plan.x[0])};
-  ortho_norm_kernel<<<dim3(kNormParts, unsigned(s.batch)), kNormThreads, 0, stream>>>(prep);
-  const int64_t per = (s.rows * s.cols + kNormThreads - 1) / kNormThreads;
-  ortho_scale_kernel<<<dim3(unsigned(std::min<int64_t>(per, 1024)), unsigned(s.batch)),
-                       kNormThreads, 0, stream>>>(prep);
-  cudaError_t e = cudaGetLastError();
+  PrepArgs prep{};
+  prep.g = p.g;
+  prep.rows = s.rows;
+  prep.cols = s.cols;
+  prep.ld_g = p.ld_g;
+  prep.stride_g = p.stride_g;
+  prep.dtype = p.dtype;
+  const int64_t size = p.dtype == GEMM_F32 ? 4 : 2;
+  prep.vec = (reinterpret_cast<uintptr_t>(p.g) & 15) == 0 &&
+             (s.rows == 1 || p.ld_g * size % 16 == 0) &&
+             (s.batch == 1 || p.stride_g * size % 16 == 0);
+  // the CTAs that are resident together share the batch; 2 units a thread at least
+  const int64_t units = s.rows * (s.ld_x / kUnit);
+  const int64_t ctas = std::max<int64_t>(
+      1, std::min((units + 2 * kPrepThreads - 1) / (2 * kPrepThreads),
+                  (int64_t(h->num_sms) * 6 + s.batch - 1) / s.batch));
+  prep.parts = int32_t(std::min<int64_t>(ctas, kNormParts));
+  prep.sums = reinterpret_cast<float*>(w + at.parts);
+  prep.eps = float(p.eps);
+  prep.x32 = x32;
+  prep.x16 = x16[0];
+  prep.ld_x = s.ld_x;
+  prep.stride_x = s.stride_x;
+  prep.scale = two(plan.x[0]);
+  const bool pdl = h->opt.pdl != 0;
+  cudaError_t e =
+      launch_prep(ortho_norm_kernel, prep, unsigned(prep.parts), s.batch, pdl, stream);
+  if (e == cudaSuccess)
+    e = launch_prep(ortho_scale_kernel, prep, unsigned(ctas), s.batch, pdl, stream);
   for (int i = 0; i < p.steps && e == cudaSuccess; ++i) {
     const float a = p.coefficients[3 * i], b = p.coefficients[3 * i + 1],
                 c = p.coefficients[3 * i + 2];
@@ -295,7 +450,7 @@ int gemm_orthogonalize(gemm_handle_t h, const gemm_orthogonalize_t* p, void* wor
   int rc = dg::check_sizes(p);
   if (rc != GEMM_OK) return rc;
   if ((p->dtype != GEMM_F16 && p->dtype != GEMM_BF16 && p->dtype != GEMM_F32) ||
-      !p->coefficients || !(p->eps >= 0x1p-100) || !std::isfinite(p->eps) || p->ld_g < p->cols ||
+      !p->coefficients || !(p->eps >= 0x1p-100 && p->eps <= 0x1p100) || p->ld_g < p->cols ||
       p->ld_out < p->cols)
     return GEMM_ERR_INVALID_ARG;
   if (p->batch > 1 && (p->stride_g < 0 || p->stride_out < p->rows * p->ld_out - (p->ld_out - p->cols)))

@@ -228,39 +228,73 @@ struct Turn {
   }
 };
 
-// One chunk of a symmetric result: 32 rows from row0, 32 columns from col0.
-__device__ __forceinline__ void or_store_symmetric(const OrTcArgs& a, float (&v)[32],
-                                                   const Turn& turn, int32_t z, int32_t row0,
-                                                   int32_t col0, bool mirror, int lane) {
-  const OrthoProduct& p = a.p;
-  const int32_t row = row0 + lane;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] *= p.alpha;
-  if (p.kind == kPoly) {
-    // A is symmetric: column col of it, read along row `col`
-    const __half* from = p.a + z * a.stride_a + row;
-    __half h[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      h[j] = row < a.n && col0 + j < a.n ? from[int64_t(col0 + j) * a.ld_a] : __half(0.f);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = fmaf(p.beta, __half2float(h[j]), v[j]);
-  }
-  __half* const to = p.c + z * a.stride_a;
-  if (mirror && row < a.ld_a) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col0 + j < a.n) to[int64_t(col0 + j) * a.ld_a + row] = __float2half_rn(v[j]);
-  }
-  turn.write(v, lane);
+// One chunk of a symmetric result: 32 rows from row0, 32 columns from col0.  `old`: what
+// or_read_symmetric brought of A.  The mirrored chunk goes through shared memory too, as
+// halves in rows of 72 bytes (8-byte pieces read back; the 2-byte stores meet a bank at
+// most twice): 64 bytes a row are stored at a time.  (Stored from registers, 2 bytes a
+// lane, it took 1.7 of a chunk's 2.2 us.)
+constexpr int kMirrorLd = 36;  // halves
+__device__ __forceinline__ void or_read_symmetric(const OrTcArgs& a, uint2 (&old)[8], int32_t z,
+                                                  int32_t row0, int32_t col0, int lane) {
   const int32_t c = col0 + (lane & 7) * 4;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    const int32_t r = row0 + 4 * i + (lane >> 3);
+    old[i] = r < a.n && c < a.ld_a ? *reinterpret_cast<const uint2*>(
+                                         a.p.a + z * a.stride_a + int64_t(r) * a.ld_a + c)
+                                   : make_uint2(0, 0);
+  }
+}
+__device__ __forceinline__ void or_store_symmetric(const OrTcArgs& a, const float (&v)[32],
+                                                   const uint2 (&old)[8], const Turn& turn,
+                                                   int32_t z, int32_t row0, int32_t col0,
+                                                   bool mirror, int lane) {
+  const OrthoProduct& p = a.p;
+  turn.write(v, lane);
+  __half* const to = p.c + z * a.stride_a;
+  const int32_t c = col0 + (lane & 7) * 4;
+  uint2 h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + (lane >> 3);
-    const float4 x = turn.read(r, lane & 7);
+    float4 x = turn.read(r, lane & 7);
+    x.x *= p.alpha;
+    x.y *= p.alpha;
+    x.z *= p.alpha;
+    x.w *= p.alpha;
+    if (p.kind == kPoly) {
+      __half2 lo, hi;
+      __builtin_memcpy(&lo, &old[i].x, 4);
+      __builtin_memcpy(&hi, &old[i].y, 4);
+      const float2 l = __half22float2(lo), u = __half22float2(hi);
+      x.x = fmaf(p.beta, l.x, x.x);
+      x.y = fmaf(p.beta, l.y, x.y);
+      x.z = fmaf(p.beta, u.x, x.z);
+      x.w = fmaf(p.beta, u.y, x.w);
+    }
+    h[i] = make_uint2(pack_half2(x.x, x.y), pack_half2(x.z, x.w));
     if (row0 + r < a.n && c < a.ld_a)
-      *reinterpret_cast<uint2*>(to + int64_t(row0 + r) * a.ld_a + c) =
-          make_uint2(pack_half2(x.x, x.y), pack_half2(x.z, x.w));
+      *reinterpret_cast<uint2*>(to + int64_t(row0 + r) * a.ld_a + c) = h[i];
+  }
+  if (!mirror) return;
+  __syncwarp();
+  uint16_t* const m = reinterpret_cast<uint16_t*>(turn.at);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint16_t* to_s = m + (lane & 7) * 4 * kMirrorLd + 4 * i + (lane >> 3);
+    to_s[0] = uint16_t(h[i].x);
+    to_s[kMirrorLd] = uint16_t(h[i].x >> 16);
+    to_s[2 * kMirrorLd] = uint16_t(h[i].y);
+    to_s[3 * kMirrorLd] = uint16_t(h[i].y >> 16);
+  }
+  __syncwarp();
+  const int32_t r = row0 + (lane & 7) * 4;  // a column of the mirrored rows
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int cc = 4 * i + (lane >> 3);
+    const uint2 x = *reinterpret_cast<const uint2*>(m + cc * kMirrorLd + (lane & 7) * 4);
+    if (col0 + cc < a.n && r < a.ld_a)
+      *reinterpret_cast<uint2*>(to + int64_t(col0 + cc) * a.ld_a + r) = x;
   }
 }
 
@@ -349,7 +383,9 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
     for (int c = 0; c < Cfg::kHalf; c += 32) {
       if (row0 >= row_end || col0 + c >= col_end) break;
       float4 old[8];
+      uint2 old_a[8];
       if (apply) or_read_iterate(args, old, z, row0, col0 + c, lane);
+      else if (args.p.kind == kPoly) or_read_symmetric(args, old_a, z, row0, col0 + c, lane);
       uint32_t r[32];
       float v[32];
       __syncwarp();
@@ -358,7 +394,7 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
       if (apply) or_store_iterate(args, v, old, turn, z, row0, col0 + c, lane);
-      else or_store_symmetric(args, v, turn, z, row0, col0 + c, tm != tn, lane);
+      else or_store_symmetric(args, v, old_a, turn, z, row0, col0 + c, tm != tn, lane);
     }
     tc_fence_before();
     __syncwarp();

@@ -34,7 +34,7 @@ typedef struct {
   int32_t steps;              /* 1 ... GEMM_ORTHO_MAX_STEPS */
   int32_t dtype;              /* of g: GEMM_F16, GEMM_BF16 or GEMM_F32 */
   const float *coefficients;  /* HOST memory: a, b, c of each step, read during the call */
-  double eps;                 /* 2^-100 or more */
+  double eps;                 /* 2^-100 ... 2^100 */
   const void *g;              /* matrix i at g + i * stride_g elements */
   int64_t ld_g, stride_g;
   void *out;                  /* bfloat16; may be g itself where types and strides agree */
@@ -53,7 +53,7 @@ int gemm_orthogonalize_workspace(gemm_handle_t h, const gemm_orthogonalize_t *p,
  * batch, rows or cols == 0: nothing is launched.
  * Errors: INVALID_ARG (negative size, steps out of range, ld < cols, matrices
  * of a batch that overlap in out, NULL pointer, workspace too small or
- * misaligned, unknown enum, eps below 2^-100, coefficients that are not finite
+ * misaligned, unknown enum, eps out of range, coefficients that are not finite
  * or let singular values of [0, 1] grow beyond 10^4, or b A + c A·A beyond
  * 10^8), UNSUPPORTED (rows or cols of 2^20 or more, batch of 2^16 or more), CUDA. */
 int gemm_orthogonalize(gemm_handle_t h, const gemm_orthogonalize_t *p, void *workspace,
