@@ -373,13 +373,12 @@ __device__ __forceinline__ void f4_epilogue(const Fp4TcArgs& args, const CUtenso
     }
     if (columns) {
       // the product of the two scales where fp32 holds it, else the smaller first
-      const float* cs = stage_w;
-      const float* cb = stage_w + HC;
+      const uint32_t cs = smem_u32(stage_w), cb = cs + 4 * HC;
       if (C.fits) {
 #pragma unroll
         for (int j = 0; j < HC; j += 4) {
-          const float4 s4 = *reinterpret_cast<const float4*>(cs + j);
-          const float4 b4 = *reinterpret_cast<const float4*>(cb + j);
+          const float4 s4 = lds4(cs + 4 * j);
+          const float4 b4 = lds4(cb + 4 * j);
           acc[j] = fmaf(acc[j], s4.x * rs, b4.x);
           acc[j + 1] = fmaf(acc[j + 1], s4.y * rs, b4.y);
           acc[j + 2] = fmaf(acc[j + 2], s4.z * rs, b4.z);
@@ -389,8 +388,8 @@ __device__ __forceinline__ void f4_epilogue(const Fp4TcArgs& args, const CUtenso
 #pragma unroll
         for (int j = 0; j < HC; ++j) {
           float lo, hi;
-          scale_order(rs, cs[j], lo, hi);
-          acc[j] = fmaf(__fmul_rn(acc[j], lo), hi, cb[j]);
+          scale_order(rs, stage_w[j], lo, hi);
+          acc[j] = fmaf(__fmul_rn(acc[j], lo), hi, stage_w[HC + j]);
         }
       }
     }

@@ -25,6 +25,9 @@ namespace dg {
 
 constexpr int kOrRoleWarps = 4, kOrEpiWarps = 8;
 constexpr int kOrThreads = 32 * (kOrRoleWarps + kOrEpiWarps);
+// Registers a thread: 3 warpgroups launch with 168 each (504 in all); the roles keep 56,
+// the epilogue's two take 224 each, for the chunk that is sent for ahead.
+constexpr int kOrRoleRegs = 56, kOrEpiRegs = 224;
 constexpr int kOrGroup = 2;   // k-blocks of 64 per stage
 constexpr int kOrStages = 3;
 
@@ -210,22 +213,39 @@ __device__ __forceinline__ uint32_t pack_half2(float x, float y) {
   return w;
 }
 
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // A warp's 32 x 32 floats (lane i holds row i) turned, through shared memory, so that 8
-// lanes hold a row: read(r, c4) is floats 4 c4 ... 4 c4 + 3 of row r.  16-byte pieces are
-// swapped about by row, so that neither side meets a bank twice.
-struct Turn {
-  float* at;
-  __device__ __forceinline__ void write(const float (&v)[32], int lane) const {
-    __syncwarp();  // the last chunk has been read
+// lanes hold a row: x[i] is floats 4 (lane % 8) ... + 3 of row 4 i + lane / 8.  16-byte
+// pieces are swapped about by row, so that neither side meets a bank twice.  (Shared
+// addresses, not pointers: through generic ones a chunk took 1.3 us even alone, as no
+// load passed a store.)
+__device__ __forceinline__ void or_turn(uint32_t at, const float (&v)[32], float4 (&x)[8],
+                                        int lane) {
+  __syncwarp();  // the last chunk has been read
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      *reinterpret_cast<float4*>(at + lane * 32 + ((c ^ (lane & 7)) << 2)) =
-          make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-    __syncwarp();
+  for (int c = 0; c < 8; ++c)
+    st_shared_v4(at + lane * 128 + ((c ^ (lane & 7)) << 4), __float_as_uint(v[4 * c]),
+                 __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                 __float_as_uint(v[4 * c + 3]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    x[i] = lds4(at + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
   }
-  __device__ __forceinline__ float4 read(int r, int c4) const {
-    return *reinterpret_cast<const float4*>(at + r * 32 + ((c4 ^ (r & 7)) << 2));
-  }
+}
+
+// What a chunk adds: 8 x 4 neighbours of the iterate, or of A as halves in x and y.
+struct OrOld {
+  float4 v[8];
 };
 
 // One chunk of a symmetric result: 32 rows from row0, 32 columns from col0.  `old`: what
@@ -234,38 +254,41 @@ struct Turn {
 // most twice): 64 bytes a row are stored at a time.  (Stored from registers, 2 bytes a
 // lane, it took 1.7 of a chunk's 2.2 us.)
 constexpr int kMirrorLd = 36;  // halves
-__device__ __forceinline__ void or_read_symmetric(const OrTcArgs& a, uint2 (&old)[8], int32_t z,
+__device__ __forceinline__ void or_read_symmetric(const OrTcArgs& a, OrOld& old, int32_t z,
                                                   int32_t row0, int32_t col0, int lane) {
   const int32_t c = col0 + (lane & 7) * 4;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int32_t r = row0 + 4 * i + (lane >> 3);
-    old[i] = r < a.n && c < a.ld_a ? *reinterpret_cast<const uint2*>(
-                                         a.p.a + z * a.stride_a + int64_t(r) * a.ld_a + c)
-                                   : make_uint2(0, 0);
+    const uint2 x = r < a.n && c < a.ld_a ? *reinterpret_cast<const uint2*>(
+                                                a.p.a + z * a.stride_a + int64_t(r) * a.ld_a + c)
+                                          : make_uint2(0, 0);
+    old.v[i].x = __uint_as_float(x.x);
+    old.v[i].y = __uint_as_float(x.y);
   }
 }
 __device__ __forceinline__ void or_store_symmetric(const OrTcArgs& a, const float (&v)[32],
-                                                   const uint2 (&old)[8], const Turn& turn,
+                                                   const OrOld& old, uint32_t stage,
                                                    int32_t z, int32_t row0, int32_t col0,
                                                    bool mirror, int lane) {
   const OrthoProduct& p = a.p;
-  turn.write(v, lane);
+  float4 turned[8];
+  or_turn(stage, v, turned, lane);
   __half* const to = p.c + z * a.stride_a;
   const int32_t c = col0 + (lane & 7) * 4;
   uint2 h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + (lane >> 3);
-    float4 x = turn.read(r, lane & 7);
+    float4 x = turned[i];
     x.x *= p.alpha;
     x.y *= p.alpha;
     x.z *= p.alpha;
     x.w *= p.alpha;
     if (p.kind == kPoly) {
       __half2 lo, hi;
-      __builtin_memcpy(&lo, &old[i].x, 4);
-      __builtin_memcpy(&hi, &old[i].y, 4);
+      __builtin_memcpy(&lo, &old.v[i].x, 4);
+      __builtin_memcpy(&hi, &old.v[i].y, 4);
       const float2 l = __half22float2(lo), u = __half22float2(hi);
       x.x = fmaf(p.beta, l.x, x.x);
       x.y = fmaf(p.beta, l.y, x.y);
@@ -278,56 +301,59 @@ __device__ __forceinline__ void or_store_symmetric(const OrTcArgs& a, const floa
   }
   if (!mirror) return;
   __syncwarp();
-  uint16_t* const m = reinterpret_cast<uint16_t*>(turn.at);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint16_t* to_s = m + (lane & 7) * 4 * kMirrorLd + 4 * i + (lane >> 3);
-    to_s[0] = uint16_t(h[i].x);
-    to_s[kMirrorLd] = uint16_t(h[i].x >> 16);
-    to_s[2 * kMirrorLd] = uint16_t(h[i].y);
-    to_s[3 * kMirrorLd] = uint16_t(h[i].y >> 16);
+    const uint32_t at = stage + ((lane & 7) * 4 * kMirrorLd + 4 * i + (lane >> 3)) * 2;
+    st_shared_u16(at, uint16_t(h[i].x));
+    st_shared_u16(at + 2 * kMirrorLd, uint16_t(h[i].x >> 16));
+    st_shared_u16(at + 4 * kMirrorLd, uint16_t(h[i].y));
+    st_shared_u16(at + 6 * kMirrorLd, uint16_t(h[i].y >> 16));
   }
   __syncwarp();
+  uint2 m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    m[i] = ld_shared_v2(stage + ((4 * i + (lane >> 3)) * kMirrorLd + (lane & 7) * 4) * 2);
   const int32_t r = row0 + (lane & 7) * 4;  // a column of the mirrored rows
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int cc = 4 * i + (lane >> 3);
-    const uint2 x = *reinterpret_cast<const uint2*>(m + cc * kMirrorLd + (lane & 7) * 4);
     if (col0 + cc < a.n && r < a.ld_a)
-      *reinterpret_cast<uint2*>(to + int64_t(col0 + cc) * a.ld_a + r) = x;
+      *reinterpret_cast<uint2*>(to + int64_t(col0 + cc) * a.ld_a + r) = m[i];
   }
 }
 
-// One chunk of the new iterate; `old`: what read_iterate brought.
-__device__ __forceinline__ void or_read_iterate(const OrTcArgs& a, float4 (&old)[8], int32_t z,
+// One chunk of the new iterate; `old`: what or_read_iterate brought.
+__device__ __forceinline__ void or_read_iterate(const OrTcArgs& a, OrOld& old, int32_t z,
                                                 int32_t row0, int32_t col0, int lane) {
   const int32_t c = col0 + (lane & 7) * 4;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int32_t r = row0 + 4 * i + (lane >> 3);
-    old[i] = r < a.rows && c < a.ld_x
-                 ? *reinterpret_cast<const float4*>(a.p.x32 + z * a.stride_x +
-                                                    int64_t(r) * a.ld_x + c)
-                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    old.v[i] = r < a.rows && c < a.ld_x
+                   ? *reinterpret_cast<const float4*>(a.p.x32 + z * a.stride_x +
+                                                      int64_t(r) * a.ld_x + c)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 __device__ __forceinline__ void or_store_iterate(const OrTcArgs& a, const float (&v)[32],
-                                                 const float4 (&old)[8], const Turn& turn,
+                                                 const OrOld& old, uint32_t stage,
                                                  int32_t z, int32_t row0, int32_t col0,
                                                  int lane) {
   const OrthoProduct& p = a.p;
-  turn.write(v, lane);
+  float4 turned[8];
+  or_turn(stage, v, turned, lane);
   const int32_t c = col0 + (lane & 7) * 4;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int rr = 4 * i + (lane >> 3);
     const int32_t r = row0 + rr;
-    float4 x = turn.read(rr, lane & 7);
+    float4 x = turned[i];
     if (r >= a.rows) continue;
-    x.x = fmaf(p.alpha, x.x, p.beta * old[i].x);
-    x.y = fmaf(p.alpha, x.y, p.beta * old[i].y);
-    x.z = fmaf(p.alpha, x.z, p.beta * old[i].z);
-    x.w = fmaf(p.alpha, x.w, p.beta * old[i].w);
+    x.x = fmaf(p.alpha, x.x, p.beta * old.v[i].x);
+    x.y = fmaf(p.alpha, x.y, p.beta * old.v[i].y);
+    x.z = fmaf(p.alpha, x.z, p.beta * old.v[i].z);
+    x.w = fmaf(p.alpha, x.w, p.beta * old.v[i].w);
     if (p.out) {
       __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + z * p.stride_out +
                           int64_t(r) * p.ld_out + c;
@@ -361,7 +387,7 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
   using Cfg = OrConfig<PAIR>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = warp & 3, wg = (warp - kOrRoleWarps) >> 2;
-  const Turn turn{reinterpret_cast<float*>(stage) + (warp - kOrRoleWarps) * 1024};
+  const uint32_t stage_w = smem_u32(stage) + uint32_t(warp - kOrRoleWarps) * 4096u;
   const uint32_t tlane = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(wg * Cfg::kHalf);
   int b = 0;
   uint32_t aph = 0;
@@ -376,16 +402,17 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
     // a mirrored tile's rows past the matrix fill the padding of the mirrored rows
     const int32_t row_end = apply || tm == tn ? rows : int32_t(args.ld_a);
     const int32_t col_end = apply ? int32_t(args.ld_x) : int32_t(args.ld_a);
-    if (!__all_sync(0xffffffffu, wait_bounded(smem_u32(&acc_full[b]), aph, wc, kSiteEpilogue)))
-      break;
-    tc_fence_after();
-#pragma unroll 1
-    for (int c = 0; c < Cfg::kHalf; c += 32) {
-      if (row0 >= row_end || col0 + c >= col_end) break;
-      float4 old[8];
-      uint2 old_a[8];
-      if (apply) or_read_iterate(args, old, z, row0, col0 + c, lane);
-      else if (args.p.kind == kPoly) or_read_symmetric(args, old_a, z, row0, col0 + c, lane);
+    // what a chunk adds to its sums is sent for a chunk ahead, the first one's while the
+    // MMAs still run: two chunks a turn, so that registers have fixed names
+    OrOld old[2];
+    auto inside = [&](int c) { return row0 < row_end && col0 + c < col_end; };
+    auto fetch = [&](OrOld& o, int c) {
+      if (c >= Cfg::kHalf || !inside(c)) return;
+      if (apply) or_read_iterate(args, o, z, row0, col0 + c, lane);
+      else if (args.p.kind == kPoly) or_read_symmetric(args, o, z, row0, col0 + c, lane);
+    };
+    auto chunk = [&](const OrOld& o, int c) {
+      if (!inside(c)) return;
       uint32_t r[32];
       float v[32];
       __syncwarp();
@@ -393,8 +420,19 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
       tmem_wait_ld32(r);
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-      if (apply) or_store_iterate(args, v, old, turn, z, row0, col0 + c, lane);
-      else or_store_symmetric(args, v, old_a, turn, z, row0, col0 + c, tm != tn, lane);
+      if (apply) or_store_iterate(args, v, o, stage_w, z, row0, col0 + c, lane);
+      else or_store_symmetric(args, v, o, stage_w, z, row0, col0 + c, tm != tn, lane);
+    };
+    fetch(old[0], 0);
+    if (!__all_sync(0xffffffffu, wait_bounded(smem_u32(&acc_full[b]), aph, wc, kSiteEpilogue)))
+      break;
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < Cfg::kHalf; c += 64) {
+      fetch(old[1], c + 32);
+      chunk(old[0], c);
+      fetch(old[0], c + 64);
+      chunk(old[1], c + 32);
     }
     tc_fence_before();
     __syncwarp();
@@ -469,20 +507,24 @@ __global__ void __launch_bounds__(kOrThreads, 1)
   uint32_t filled = 0;
   bool issued = false;
   if (warp >= kOrRoleWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOrEpiRegs));
     or_epilogue<PAIR>(args, acc_full, acc_empty, wc, tmem_base, stage, rank, owner);
-  } else if (warp == 0 && lane == 0) {
-    filled = or_producer<PAIR>(mA, mB, args, smem_u32(ring), full, empty, wc, rank, owner);
-    if (PAIR && rank != 0) st_dsmem_u32(map_to_rank(smem_u32(peer_filled), 0), filled);
   } else {
-    pdl_wait_prerequisites();
-    if (warp == 1 && lane == 0 && rank == 0) {
-      issued = or_mma<PAIR>(args, smem_u32(ring), full, empty, acc_full, acc_empty, wc, tmem_base,
-                            owner);
-      // every MMA finishes before TMEM is freed, also when an epilogue gave up
-      if (issued) {
-        if constexpr (PAIR) tc_commit_pair_self(smem_u32(drain));
-        else tc_commit(smem_u32(drain));
-        wait_drain(smem_u32(drain), 0, wc);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOrRoleRegs));
+    if (warp == 0 && lane == 0) {
+      filled = or_producer<PAIR>(mA, mB, args, smem_u32(ring), full, empty, wc, rank, owner);
+      if (PAIR && rank != 0) st_dsmem_u32(map_to_rank(smem_u32(peer_filled), 0), filled);
+    } else {
+      pdl_wait_prerequisites();
+      if (warp == 1 && lane == 0 && rank == 0) {
+        issued = or_mma<PAIR>(args, smem_u32(ring), full, empty, acc_full, acc_empty, wc,
+                              tmem_base, owner);
+        // every MMA finishes before TMEM is freed, also when an epilogue gave up
+        if (issued) {
+          if constexpr (PAIR) tc_commit_pair_self(smem_u32(drain));
+          else tc_commit(smem_u32(drain));
+          wait_drain(smem_u32(drain), 0, wc);
+        }
       }
     }
   }
