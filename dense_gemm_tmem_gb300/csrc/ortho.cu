@@ -83,6 +83,8 @@ struct PrepArgs {
   __half* x16;
   int64_t ld_x, stride_x;
   float scale;   // of the 16-bit copy
+  uint32_t* done;  // the products' counters, set to 0
+  int64_t counters;
 };
 
 // Elements c ... c + 7 of a row of g, zeros past its end.
@@ -208,6 +210,9 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const PrepArg
     s.mid = p[1];
     s.small = p[2];
   }
+  for (int64_t i = (z * gridDim.x + blockIdx.x) * kPrepThreads + threadIdx.x; i < a.counters;
+       i += int64_t(gridDim.x) * gridDim.y * kPrepThreads)
+    a.done[i] = 0;
   s = block_sum(s);
   float p1, p2;
   s.inverse(a.eps, p1, p2);
@@ -263,11 +268,11 @@ OrthoShape shape_of(const gemm_orthogonalize_t& p) {
   return s;
 }
 
-// Workspace: the norm's parts, the iterate in fp32, two 16-bit copies of it, A and B.
+// Workspace: the norm's parts, the products' counters, the iterate in fp32, two 16-bit copies of it, A and B.
 struct Space {
-  int64_t parts, x32, x16, a16, b16, total;
+  int64_t parts, done, x32, x16, a16, b16, total;
 };
-Space space_of(const OrthoShape& s) {
+Space space_of(const OrthoShape& s, int32_t steps) {
   Space w{};
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -276,6 +281,7 @@ Space space_of(const OrthoShape& s) {
     return here;
   };
   w.parts = take(s.batch * kNormParts * 3 * 4);
+  w.done = take(ortho_counters(s, steps) * 4);
   w.x32 = take(s.batch * s.stride_x * 4);
   w.x16 = take(2 * round_up(s.batch * s.stride_x * 2, 256));
   w.a16 = take(s.batch * s.stride_a * 2);
@@ -353,13 +359,11 @@ int check_sizes(const gemm_orthogonalize_t* p) {
 cudaError_t enqueue(gemm_ctx* h, const gemm_orthogonalize_t& p, const Plan& plan, uint8_t* w,
                     cudaStream_t stream) {
   const OrthoShape s = shape_of(p);
-  const Space at = space_of(s);
+  const Space at = space_of(s, p.steps);
   float* x32 = reinterpret_cast<float*>(w + at.x32);
   __half* x16[2] = {reinterpret_cast<__half*>(w + at.x16),
                     reinterpret_cast<__half*>(w + at.x16 +
                                               round_up(s.batch * s.stride_x * 2, 256))};
-  __half* a16 = reinterpret_cast<__half*>(w + at.a16);
-  __half* b16 = reinterpret_cast<__half*>(w + at.b16);
   auto two = [](int e) { return std::ldexp(1.f, e); };
   PrepArgs prep{};
   prep.g = p.g;
@@ -385,48 +389,36 @@ cudaError_t enqueue(gemm_ctx* h, const gemm_orthogonalize_t& p, const Plan& plan
   prep.ld_x = s.ld_x;
   prep.stride_x = s.stride_x;
   prep.scale = two(plan.x[0]);
+  prep.done = reinterpret_cast<uint32_t*>(w + at.done);
+  prep.counters = ortho_counters(s, p.steps);
   const bool pdl = h->opt.pdl != 0;
   cudaError_t e =
       launch_prep(ortho_norm_kernel, prep, unsigned(prep.parts), s.batch, pdl, stream);
   if (e == cudaSuccess)
     e = launch_prep(ortho_scale_kernel, prep, unsigned(ctas), s.batch, pdl, stream);
-  for (int i = 0; i < p.steps && e == cudaSuccess; ++i) {
-    const float a = p.coefficients[3 * i], b = p.coefficients[3 * i + 1],
-                c = p.coefficients[3 * i + 2];
-    const bool last = i + 1 == p.steps;
-    OrthoProduct q{};
-    q.kind = kGram;
-    q.alpha = two(plan.a[i] - 2 * plan.x[i]);
-    q.a = x16[i & 1];
-    q.c = a16;
-    e = launch_ortho_product(h, s, q, stream);
-    if (e != cudaSuccess) break;
-    q = {};
-    q.kind = kPoly;
-    q.alpha = std::ldexp(c, plan.b[i] - 2 * plan.a[i]);
-    q.beta = std::ldexp(b, plan.b[i] - plan.a[i]);
-    q.a = a16;
-    q.c = b16;
-    e = launch_ortho_product(h, s, q, stream);
-    if (e != cudaSuccess) break;
-    q = {};
-    q.kind = kApply;
-    q.alpha = two(-plan.b[i] - plan.x[i]);
-    q.beta = a;
-    q.a = b16;
-    q.x = x16[i & 1];
-    q.x32 = x32;
-    if (last) {
-      q.out = p.out;
-      q.ld_out = p.ld_out;
-      q.stride_out = p.stride_out;
-    } else {
-      q.scale = two(plan.x[i + 1]);
-      q.c = x16[(i + 1) & 1];
-    }
-    e = launch_ortho_product(h, s, q, stream);
+  if (e != cudaSuccess) return e;
+  OrthoCall c{};
+  c.shape = s;
+  c.steps = p.steps;
+  for (int i = 0; i < p.steps; ++i) {
+    OrthoStep& q = c.step[i];
+    q.gram_alpha = two(plan.a[i] - 2 * plan.x[i]);
+    q.poly_alpha = std::ldexp(p.coefficients[3 * i + 2], plan.b[i] - 2 * plan.a[i]);
+    q.poly_beta = std::ldexp(p.coefficients[3 * i + 1], plan.b[i] - plan.a[i]);
+    q.apply_alpha = two(-plan.b[i] - plan.x[i]);
+    q.apply_beta = p.coefficients[3 * i];
+    q.scale = i + 1 < p.steps ? two(plan.x[i + 1]) : 0.f;
   }
-  return e;
+  c.x32 = x32;
+  c.x16[0] = x16[0];
+  c.x16[1] = x16[1];
+  c.a16 = reinterpret_cast<__half*>(w + at.a16);
+  c.b16 = reinterpret_cast<__half*>(w + at.b16);
+  c.done = prep.done;
+  c.out = p.out;
+  c.ld_out = p.ld_out;
+  c.stride_out = p.stride_out;
+  return launch_ortho_products(h, c, stream);
 }
 
 }  // namespace
@@ -440,7 +432,7 @@ int gemm_orthogonalize_workspace(gemm_handle_t h, const gemm_orthogonalize_t* p,
   if (!h) return GEMM_ERR_INVALID_ARG;
   const int rc = dg::check_sizes(p);
   if (rc != GEMM_OK) return rc;
-  *bytes = dg::space_of(dg::shape_of(*p)).total;
+  *bytes = dg::space_of(dg::shape_of(*p), p->steps).total;
   return GEMM_OK;
 }
 
@@ -459,7 +451,7 @@ int gemm_orthogonalize(gemm_handle_t h, const gemm_orthogonalize_t* p, void* wor
   if ((rc = dg::plan_scales(*p, &plan)) != GEMM_OK) return rc;
   if (p->batch == 0 || p->rows == 0 || p->cols == 0) return GEMM_OK;
   if (!p->g || !p->out || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
-      workspace_bytes < dg::space_of(dg::shape_of(*p)).total)
+      workspace_bytes < dg::space_of(dg::shape_of(*p), p->steps).total)
     return GEMM_ERR_INVALID_ARG;
   return dg::on_device(h->device, [&]() -> int {
     return dg::enqueue(h, *p, plan, static_cast<uint8_t*>(workspace),

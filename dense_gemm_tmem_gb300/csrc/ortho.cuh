@@ -23,23 +23,29 @@ struct OrthoShape {
   int64_t stride_x, stride_a;
 };
 
-// One product of a step.  kGram: A16 = half(alpha · X16·X16ᵀ); kPoly: B16 = half(alpha
-// · A16·A16ᵀ + beta · A16); kApply: X = alpha · (B16·X16) + beta · X, in fp32 (and
-// X16 = half(X · scale)), or, in the last step, `out` = bfloat16 of it.
+// The products of a step.  kGram: A16 = half(gram_alpha · X16·X16ᵀ); kPoly: B16 =
+// half(poly_alpha · A16·A16ᵀ + poly_beta · A16); kApply: X = apply_alpha · (B16·X16) +
+// apply_beta · X, in fp32 (and X16 = half(X · scale)), or, in the last step, `out` =
+// bfloat16 of it.
 enum OrthoKind : int { kGram = 0, kPoly = 1, kApply = 2 };
+struct OrthoStep {
+  float gram_alpha, poly_alpha, poly_beta, apply_alpha, apply_beta, scale;
+};
 
-struct OrthoProduct {
-  int kind;
-  float alpha, beta, scale;
-  const __half* a;   // X16, A16, B16
-  const __half* x;   // kApply: X16
-  __half* c;         // A16, B16, X16 (not the one that is read)
-  float* x32;        // kApply: the iterate, read and written (laid out as X16)
-  void* out;         // kApply, last step: bfloat16, else NULL
+struct OrthoCall {
+  OrthoShape shape;
+  int32_t steps;
+  OrthoStep step[GEMM_ORTHO_MAX_STEPS];
+  float* x32;          // the iterate (laid out as its 16-bit copies)
+  __half* x16[2];      // step i reads x16[i & 1] and writes the other
+  __half *a16, *b16;
+  uint32_t* done;      // ortho_counters of them, 0 at the start
+  void* out;           // bfloat16
   int64_t ld_out, stride_out;
 };
 
-cudaError_t launch_ortho_product(gemm_ctx* h, const OrthoShape& s, const OrthoProduct& p,
-                                 cudaStream_t stream);
+// Counters that launch_ortho_products needs: one per tile of each product.
+int64_t ortho_counters(const OrthoShape& s, int32_t steps);
+cudaError_t launch_ortho_products(gemm_ctx* h, const OrthoCall& c, cudaStream_t stream);
 
 }  // namespace dg

@@ -9,29 +9,34 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// An operand stored in rows of `ld` fp16 elements, `batch` matrices of `stride`: K along
-// the rows (zeros from `k` to the next multiple of 64) or down them (mn_major).
-bool encode(CUtensorMap* map, const __half* p, int64_t mn, int64_t k, int64_t ld, int64_t batch,
-            int64_t stride, bool mn_major) {
+// The maps of matrices stored in rows of `ld` fp16 elements (zeros from `cols` to the next
+// multiple of 64), `batch` of them `stride` apart: with K along the rows, and down them.
+bool encode(OrOperand* m, const __half* p, int64_t rows, int64_t cols, int64_t ld, int64_t batch,
+            int64_t stride, int b_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const cuuint64_t row = cuuint64_t(ld) * 2, matrix = cuuint64_t(stride) * 2;
-  const cuuint64_t dk[4] = {64, cuuint64_t(mn), cuuint64_t(ceil_div(k, 64)), cuuint64_t(batch)};
+  auto tiled = [&](CUtensorMap* map, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<__half*>(p), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t dk[4] = {64, cuuint64_t(rows), cuuint64_t(ceil_div(cols, 64)),
+                            cuuint64_t(batch)};
   const cuuint64_t sk[3] = {row, 128, matrix};
-  const cuuint32_t bk[4] = {64, 128, kOrGroup, 1};
-  const cuuint64_t dm[3] = {cuuint64_t(mn), cuuint64_t(k), cuuint64_t(batch)};
+  const cuuint32_t ba[4] = {64, 128, kOrGroup, 1}, bb[4] = {64, cuuint32_t(b_rows), kOrGroup, 1};
+  const cuuint64_t dm[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(batch)};
   const cuuint64_t sm[2] = {row, matrix};
   const cuuint32_t bm[3] = {64, 64 * kOrGroup, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, mn_major ? 3 : 4, const_cast<__half*>(p),
-            mn_major ? dm : dk, mn_major ? sm : sk, mn_major ? bm : bk, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tiled(&m->ka, 4, dk, sk, ba) && tiled(&m->kb, 4, dk, sk, bb) &&
+         tiled(&m->mn, 3, dm, sm, bm);
 }
 
 template <bool PAIR>
-cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const OrTcArgs& args,
-                   gemm_ctx* h, cudaStream_t stream) {
+cudaError_t launch(const OrMaps& maps, const OrTcArgs& args, gemm_ctx* h, cudaStream_t stream) {
   auto kern = ortho_tc_kernel<PAIR>;
   constexpr int smem = OrConfig<PAIR>::kSmemBytes;
   static SharedMemoryOnce once;
@@ -40,11 +45,9 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const OrTcArgs&
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   int n = 0;
-  if (h->opt.pdl) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  attr[n].id = cudaLaunchAttributeCooperative;  // tiles wait for tiles of other CTAs
+  attr[n].val.cooperative = 1;
+  ++n;
   if (PAIR) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
     attr[n].val.clusterDim.x = 2;
@@ -58,15 +61,52 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const OrTcArgs&
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = unsigned(n);
-  return cudaLaunchKernelEx(&cfg, kern, mA, mB, args);
+  return cudaLaunchKernelEx(&cfg, kern, maps, args);
+}
+
+struct Tiles {
+  int64_t r, c, sym, apply;  // of X's rows and columns, and in all of a matrix
+};
+template <bool PAIR>
+Tiles tiles_of(const OrthoShape& s) {
+  using Cfg = OrConfig<PAIR>;
+  Tiles t{};
+  t.r = ceil_div(s.rows, Cfg::kTileM);
+  t.c = ceil_div(s.cols, Cfg::kTileN);
+  const int64_t n = ceil_div(s.n, Cfg::kTileM);
+  t.sym = Cfg::kRatio * (n * (n + 1) / 2);
+  t.apply = t.r * t.c;
+  return t;
 }
 
 }  // namespace
 
-cudaError_t launch_ortho_product(gemm_ctx* h, const OrthoShape& s, const OrthoProduct& p,
-                                 cudaStream_t stream) {
+int64_t ortho_counters(const OrthoShape& s, int32_t steps) {
+  const Tiles t = tiles_of<false>(s);
+  return 3 * int64_t(steps) * s.batch * std::max(t.sym, t.apply);
+}
+
+cudaError_t launch_ortho_products(gemm_ctx* h, const OrthoCall& c, cudaStream_t stream) {
+  const OrthoShape& s = c.shape;
+  // Pairs' tiles where kApply's occupy half of the SMs, else eight times as many small
+  // ones.
+  const int64_t pairs = h->opt.pair_clusters > 0 ? h->opt.pair_clusters : h->num_sms / 2;
+  const bool pair = h->opt.pair >= 0 ? h->opt.pair == 1
+                                     : 2 * tiles_of<true>(s).apply * s.batch > pairs;
+  const Tiles t = pair ? tiles_of<true>(s) : tiles_of<false>(s);
+  if (t.sym > INT32_MAX / 16 || t.apply > INT32_MAX / 16) return cudaErrorInvalidValue;
   OrTcArgs a{};
   a.batch = int32_t(s.batch);
+  a.steps = c.steps;
+  a.owners = int32_t(std::min<int64_t>(pair ? pairs : h->num_sms,
+                                       std::max(t.sym, t.apply) * s.batch));
+  a.tall = s.tall;
+  a.tiles_r = int32_t(t.r);
+  a.tiles_c = int32_t(t.c);
+  a.per_sym = int32_t(t.sym);
+  a.per_apply = int32_t(t.apply);
+  a.kb_gram = int32_t(ceil_div(s.tall ? s.rows : s.cols, 64));
+  a.kb_n = int32_t(ceil_div(s.n, 64));
   a.rows = int32_t(s.rows);
   a.cols = int32_t(s.cols);
   a.n = int32_t(s.n);
@@ -74,50 +114,29 @@ cudaError_t launch_ortho_product(gemm_ctx* h, const OrthoShape& s, const OrthoPr
   a.ld_a = s.ld_a;
   a.stride_x = s.stride_x;
   a.stride_a = s.stride_a;
-  a.p = p;
-  a.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 7) == 0 && p.ld_out % 4 == 0 &&
-              (s.batch == 1 || p.stride_out % 4 == 0);
+  a.x16[0] = c.x16[0];
+  a.x16[1] = c.x16[1];
+  a.a16 = c.a16;
+  a.b16 = c.b16;
+  a.x32 = c.x32;
+  a.out = c.out;
+  a.ld_out = c.ld_out;
+  a.stride_out = c.stride_out;
+  a.out_vec = (reinterpret_cast<uintptr_t>(c.out) & 7) == 0 && c.ld_out % 4 == 0 &&
+              (s.batch == 1 || c.stride_out % 4 == 0);
+  a.done = c.done;
+  a.done_stride = std::max(t.sym, t.apply) * s.batch;
   a.status = h->status;
   a.wait_limit_ns = h->opt.wait_limit_ns;
-  const bool symmetric = p.kind != kApply;
-  const int64_t M = symmetric ? s.n : s.rows, N = symmetric ? s.n : s.cols;
-  const int64_t K = p.kind == kGram ? (s.tall ? s.rows : s.cols) : s.n;
-  auto tiles = [&](int64_t tile) {
-    const int64_t m = ceil_div(M, tile), n = ceil_div(N, tile);
-    return symmetric ? m * (m + 1) / 2 : m * n;
-  };
-  // Pairs' tiles where they occupy half of the SMs, else four times as many small ones.
-  const int64_t pairs = h->opt.pair_clusters > 0 ? h->opt.pair_clusters : h->num_sms / 2;
-  const bool pair = h->opt.pair >= 0 ? h->opt.pair == 1 : 2 * tiles(256) * s.batch > pairs;
-  const int64_t tile = pair ? 256 : 128;
-  a.tiles_m = int32_t(ceil_div(M, tile));
-  a.tiles_n = int32_t(ceil_div(N, tile));
-  const int64_t per = tiles(tile);
-  if (per * s.batch > INT32_MAX / 2) return cudaErrorInvalidValue;
-  a.per = int32_t(per);
-  a.group_m = 8;
-  a.k_blocks = int32_t(ceil_div(K, 64));
-  a.owners = int32_t(std::min<int64_t>(pair ? pairs : h->num_sms, per * s.batch));
-  CUtensorMap mA, mB;
-  bool ok;
-  if (p.kind == kGram) {
-    a.a_mn = a.b_mn = s.tall;
-    ok = encode(&mA, p.a, s.n, K, s.ld_x, s.batch, s.stride_x, s.tall);
-    mB = mA;
-  } else if (p.kind == kPoly) {
-    ok = encode(&mA, p.a, s.n, s.n, s.ld_a, s.batch, s.stride_a, false);
-    mB = mA;
-  } else if (s.tall) {  // X·B, B symmetric
-    ok = encode(&mA, p.x, s.rows, s.n, s.ld_x, s.batch, s.stride_x, false) &&
-         encode(&mB, p.a, s.n, s.n, s.ld_a, s.batch, s.stride_a, false);
-  } else {              // B·X, X's rows along K
-    a.b_mn = 1;
-    ok = encode(&mA, p.a, s.n, s.n, s.ld_a, s.batch, s.stride_a, false) &&
-         encode(&mB, p.x, s.cols, s.n, s.ld_x, s.batch, s.stride_x, true);
-  }
+  std::copy(c.step, c.step + c.steps, a.step);
+  OrMaps m{};
+  const int b_rows = pair ? OrConfig<true>::kBRows : OrConfig<false>::kBRows;
+  bool ok = encode(&m.a, c.a16, s.n, s.n, s.ld_a, s.batch, s.stride_a, b_rows) &&
+            encode(&m.b, c.b16, s.n, s.n, s.ld_a, s.batch, s.stride_a, b_rows);
+  for (int i = 0; ok && i < 2; ++i)
+    ok = encode(&m.x[i], c.x16[i], s.rows, s.cols, s.ld_x, s.batch, s.stride_x, b_rows);
   if (!ok) return cudaErrorInvalidValue;
-  a.idesc = make_idesc_f16(int(tile), int(tile), a.a_mn, a.b_mn);
-  return pair ? launch<true>(mA, mB, a, h, stream) : launch<false>(mA, mB, a, h, stream);
+  return pair ? launch<true>(m, a, h, stream) : launch<false>(m, a, h, stream);
 }
 
 }  // namespace dg
