@@ -609,30 +609,33 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
     const OrthoStep& co = args.step[o.step];
     const float alpha = apply ? co.apply_alpha : o.kind == kPoly ? co.poly_alpha : co.gram_alpha;
     const float beta = apply ? co.apply_beta : co.poly_beta, scale = co.scale;
-    // What a chunk adds to its sums is sent for a chunk ahead, the first one's while the
-    // MMAs still run: A's tile once its piece of K may be loaded, the iterate's once any
-    // of B may be.
-    OrOld old, next;
-    auto fetch = [&](OrOld& to, int c) {
-      if (row0 >= rows || col0 + c >= col_end) return;
-      const OrChunk k{row0, col0 + c, rows, col_end};
-      if (apply) or_read_iterate(args, to, o.z, k, lane);
-      else if (o.kind == kPoly) or_read_symmetric(args, to, o.z, k, lane);
-    };
+    // What the tile adds to its sums is sent for while the MMAs still run: A's tile once
+    // its piece of K may be loaded, the iterate's once any of B may be.  (A chunk ahead,
+    // each chunk took 1.4 us, the loads' latency.)
+    constexpr int kChunks = Cfg::kHalf / 32;
+    OrOld old[kChunks];
     bool ok = true;
     if (o.kind != kGram) {
       const uint32_t need = passed + (apply ? 1 : o.tn / Cfg::kRatio + 1);
       ok = __all_sync(0xffffffffu, or_wait_ready(ready, need, wc));
-      if (ok) fetch(old, 0);
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          if (row0 >= rows || col0 + 32 * i >= col_end) break;
+          const OrChunk k{row0, col0 + 32 * i, rows, col_end};
+          if (apply) or_read_iterate(args, old[i], o.z, k, lane);
+          else or_read_symmetric(args, old[i], o.z, k, lane);
+        }
+      }
     }
     passed += or_pieces<PAIR>(args, o.kind);
     ok = ok && wait_bounded(smem_u32(&acc_full[b]), aph, wc, kSiteEpilogue);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after();
-#pragma unroll 1
-    for (int c = 0; c < Cfg::kHalf; c += 32) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = 32 * i;
       if (row0 >= rows || col0 + c >= col_end) break;
-      if (c + 32 < Cfg::kHalf) fetch(next, c + 32);
       uint32_t r[32];
       float v[32];
       __syncwarp();
@@ -641,9 +644,8 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
       const OrChunk k{row0, col0 + c, rows, col_end};
-      if (apply) or_store_iterate(args, v, old, stage_w, o, alpha, beta, scale, k, lane);
-      else or_store_symmetric(args, v, old, stage_w, o, alpha, beta, k, lane);
-      old = next;
+      if (apply) or_store_iterate(args, v, old[i], stage_w, o, alpha, beta, scale, k, lane);
+      else or_store_symmetric(args, v, old[i], stage_w, o, alpha, beta, k, lane);
     }
     // the tile's counter: this warp's stores, for copies and loads of other SMs
     __syncwarp();
