@@ -7,7 +7,10 @@
 // bytes of values, and 4 neighbouring blocks' threads put their scales into one
 // 4-byte word.  nvfp4 needs the row's maximum first: the threads of a row (a warp,
 // or the whole CTA) keep their elements in registers across that reduction; rows
-// too long for that are read twice.
+// too long for that are read twice.  What is left to keep short is the instruction
+// count: 16-bit elements stay packed and maxima are taken of magnitudes as integers
+// (which order like the numbers), and a row's division by its blocks' scales, which
+// have 8 different mantissas, is made once for each of those.
 #include <type_traits>
 
 #include "fp4.cuh"
@@ -42,31 +45,66 @@ struct Unit16 {
       else w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j & 1));
     }
   }
-  __device__ __forceinline__ float get(int j) const {
+  // Elements 2 j and 2 j + 1.
+  __device__ __forceinline__ float2 pair(int j) const {
     if constexpr (sizeof(T) == 4) {
-      return __uint_as_float(w[j]);
+      return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+    } else if constexpr (std::is_same<T, __half>::value) {
+      __half2 h;
+      __builtin_memcpy(&h, &w[j], 4);
+      return __half22float2(h);
     } else {
-      const uint16_t h = uint16_t(w[j / 2] >> (16 * (j & 1)));
-      T v;
-      __builtin_memcpy(&v, &h, 2);
-      if constexpr (std::is_same<T, __half>::value) return __half2float(v);
-      else return __bfloat162float(v);
+      return make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
     }
   }
   // The largest finite magnitude; `odd`: there is a non-finite element.
   __device__ __forceinline__ float amax(bool& odd) const {
-    float m = 0.f;
-    odd = false;
+    float m;
+    if constexpr (sizeof(T) == 4) {
+      uint32_t most = 0;
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) {
-      const float a = fabsf(get(j));
-      const bool fine = a < INFINITY;
-      odd |= !fine;
-      m = fmaxf(m, fine ? a : 0.f);
+      for (int j = 0; j < kUnit; ++j) most = max(most, w[j] & 0x7fffffffu);
+      m = __uint_as_float(most);
+    } else {
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
+      const uint16_t h = uint16_t(max(most & 0xffffu, most >> 16));
+      T v;
+      __builtin_memcpy(&v, &h, 2);
+      if constexpr (std::is_same<T, __half>::value) m = __half2float(v);
+      else m = __bfloat162float(v);
+    }
+    odd = !(m < INFINITY);
+    if (odd) {
+      m = 0.f;
+#pragma unroll
+      for (int j = 0; j < kUnit / 2; ++j) {
+        const float2 x = pair(j);
+        if (fabsf(x.x) < INFINITY) m = fmaxf(m, fabsf(x.x));
+        if (fabsf(x.y) < INFINITY) m = fmaxf(m, fabsf(x.y));
+      }
     }
     return m;
   }
 };
+
+// (x a, y a), one instruction.
+__device__ __forceinline__ float2 mul2(float2 x, float a) {
+  float2 r;
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%2, %3};\n\t"
+      "mov.b64 q, {%4, %4};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(a));
+  return r;
+}
+
+// Launches of up to so many CTAs let the next kernel's CTAs in beside them (and enter
+// beside the last kernel's): of longer ones they would take room.
+constexpr int64_t kEarlyCtas = 256;
 
 struct QuantArgs {
   const void* src;
@@ -74,35 +112,22 @@ struct QuantArgs {
   bool vec;
   gemm_fp4_matrix_t out;
   int64_t pieces;
+  bool early;  // the next kernel may start beside this one
 };
-
-// One unit's block: its scale byte and the factor of its elements.
-template <int FMT>
-__device__ __forceinline__ void block_scale(float amax, bool odd, float a448, float a2688,
-                                            uint32_t& byte, float& factor) {
-  if constexpr (FMT == GEMM_MXFP4) {
-    const int e = int(__float_as_uint(amax) >> 23);
-    byte = uint32_t(max(e - 2, 0));
-    factor = __uint_as_float((254u - byte) << 23);
-    if (odd) byte = 255;
-  } else {
-    byte = pack_e4m3x2(__fmul_rn(amax, a448), 0.f) & 0xffu;
-    const float s = unpack_e4m3x2(byte).x;
-    factor = s > 0.f ? __fdiv_rn(a2688, s) : 0.f;
-    if (odd) byte = 0x7f;
-  }
-}
 
 // A row per TPR threads (32: a warp, or the whole CTA), U units a thread in
 // registers.
 template <typename T, int FMT, int TPR, int U>
-__global__ void __launch_bounds__(kQuantThreads) fp4_quantize_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 6 : 4)
+    fp4_quantize_kernel(const QuantArgs a) {
   constexpr int kRowsPer = kQuantThreads / TPR;
   const int t = threadIdx.x % TPR;
   const int64_t r = int64_t(blockIdx.x) * kRowsPer + threadIdx.x / TPR;
   const int64_t units = a.pieces * (fp4_block(FMT) * 4 / kUnit);  // whole pieces
   uint8_t* const scale = static_cast<uint8_t*>(a.out.scale);
   constexpr int kPer = FMT == GEMM_MXFP4 ? 8 : 4;  // threads of a piece's four blocks
+  if (a.early) pdl_launch_dependents();
+  pdl_wait_prerequisites();
   if (r >= (a.rows + 127) / 128 * 128) return;     // (whole warps, or the whole CTA)
   if (r >= a.rows) {                               // a row that only fills up a piece
     for (int64_t p = t; p < a.pieces; p += TPR)
@@ -111,7 +136,11 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_quantize_kernel(const Quant
   }
   const T* const src = static_cast<const T*>(a.src) + r * a.ld;
   uint8_t* const data = static_cast<uint8_t*>(a.out.data) + r * a.out.ld;
+  // the row's place among the scales; piece p is p * kFp4Piece further on
+  uint8_t* const scale_row = scale + fp4_scale_at(r, 0, a.pieces);
   Unit16<T> x[U];
+  float m[U];
+  bool odd[U];
   auto load = [&](int64_t u0) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -119,21 +148,24 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_quantize_kernel(const Quant
       x[i].load(src + c, int(max(int64_t(0), min(int64_t(kUnit), a.cols - c))), a.vec);
     }
   };
+  auto maxima = [&]() {
+#pragma unroll
+    for (int i = 0; i < U; ++i) m[i] = x[i].amax(odd[i]);
+  };
   load(0);
-  float a448 = 0.f, a2688 = 0.f;
+  maxima();
+  float a448 = 0.f, quotient = 0.f;
   if constexpr (FMT == GEMM_NVFP4) {
     float most = 0.f;
-    bool odd;
     for (int64_t u0 = 0;;) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) most = fmaxf(most, x[i].amax(odd));
+      for (int i = 0; i < U; ++i) most = fmaxf(most, m[i]);
       u0 += TPR * U;
       if (u0 >= units) break;
       load(u0);
+      maxima();
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
     if constexpr (TPR > 32) {
       __shared__ float red[kQuantThreads / 32];
       if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
@@ -143,30 +175,51 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_quantize_kernel(const Quant
     }
     most = fmaxf(most, kAmaxMin);
     a448 = __fdiv_rn(448.f, most);
-    a2688 = __fdiv_rn(2688.f, most);
+    // 2688 / a by each mantissa of an e4m3 number; its exponent then shifts exactly
+    quotient = __fdiv_rn(__fdiv_rn(2688.f, most), 1.f + 0.125f * float(threadIdx.x & 7));
     if (t == 0) a.out.row_scale[r * a.out.row_scale_stride] = __fdiv_rn(most, 2688.f);
-    if (units > TPR * U) load(0);
+    if (units > TPR * U) {
+      load(0);
+      maxima();
+    }
   }
   for (int64_t u0 = 0; u0 < units; u0 += TPR * U) {
-    if (u0 > 0) load(u0);
+    if (u0 > 0) {
+      load(u0);
+      maxima();
+    }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t u = u0 + t + i * TPR, c = u * kUnit;
-      bool odd;
-      float m = x[i].amax(odd);
-      if constexpr (FMT == GEMM_MXFP4) {  // the block's other half
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        odd |= __shfl_xor_sync(0xffffffffu, int(odd), 1) != 0;
-      }
       uint32_t byte;
       float f;
-      block_scale<FMT>(m, odd, a448, a2688, byte, f);
+      bool bad = odd[i];
+      if constexpr (FMT == GEMM_MXFP4) {
+        // the block's other half; 2^e with e = floor(log2 amax) - 2
+        const float most = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+        bad |= __shfl_xor_sync(0xffffffffu, int(bad), 1) != 0;
+        byte = uint32_t(max(int(__float_as_uint(most) >> 23) - 2, 0));
+        f = __uint_as_float((254u - byte) << 23);
+        if (bad) byte = 255;
+      } else {
+        byte = pack_e4m3x2(__fmul_rn(m[i], a448), 0.f) & 0xffu;
+        const uint32_t s = __float_as_uint(unpack_e4m3x2(byte).x);
+        f = __shfl_sync(0xffffffffu, quotient, (s >> 20) & 7) *
+            __uint_as_float((254u << 23) - (s & 0x7f800000u));
+        if (s == 0) f = 0.f;
+        if (bad) byte = 0x7f;
+      }
       // blocks past the matrix have scale 0
       if (c >= (a.cols + fp4_block(FMT) - 1) / fp4_block(FMT) * fp4_block(FMT)) byte = 0;
       float q[kUnit];
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j) q[j] = odd ? 0.f : __fmul_rn(x[i].get(j), f);
-      const uint2 v = make_uint2(pack_e2m1x8(q), pack_e2m1x8(q + 8));
+      for (int j = 0; j < kUnit / 2; ++j) {
+        const float2 y = mul2(x[i].pair(j), f);
+        q[2 * j] = y.x;
+        q[2 * j + 1] = y.y;
+      }
+      uint2 v = make_uint2(pack_e2m1x8(q), pack_e2m1x8(q + 8));
+      if (bad) v = make_uint2(0, 0);
       // the four blocks' scales to the first of their threads
       constexpr int kStep = kPer / 4;
       uint32_t word = byte << (8 * ((threadIdx.x % kPer) / kStep));
@@ -174,7 +227,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_quantize_kernel(const Quant
       word |= __shfl_xor_sync(0xffffffffu, word, 2 * kStep);
       if (u >= units) continue;
       if (threadIdx.x % kPer == 0)
-        *reinterpret_cast<uint32_t*>(scale + fp4_scale_at(r, c / fp4_block(FMT), a.pieces)) = word;
+        *reinterpret_cast<uint32_t*>(scale_row + u / kPer * kFp4Piece) = word;
       const int64_t left = (a.cols - c + 1) / 2;  // bytes
       if (left >= 8) {
         *reinterpret_cast<uint2*>(data + c / 2) = v;
@@ -187,16 +240,23 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_quantize_kernel(const Quant
 }
 
 template <typename T, int FMT>
-cudaError_t launch_format(const QuantArgs& a, cudaStream_t s) {
+cudaError_t launch_format(QuantArgs a, cudaStream_t s) {
   const int64_t rows = (a.rows + 127) / 128 * 128;
-  if (a.cols <= 2 * 32 * kUnit) {
-    constexpr int kPer = kQuantThreads / 32;
-    fp4_quantize_kernel<T, FMT, 32, 2>
-        <<<unsigned((rows + kPer - 1) / kPer), kQuantThreads, 0, s>>>(a);
-  } else {
-    fp4_quantize_kernel<T, FMT, kQuantThreads, 2><<<unsigned(rows), kQuantThreads, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  constexpr int kPer = kQuantThreads / 32;
+  const bool warps = a.cols <= 2 * 32 * kUnit;
+  const int64_t grid = warps ? rows / kPer : rows;
+  a.early = grid <= kEarlyCtas;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(unsigned(grid), 1, 1);
+  cfg.blockDim = dim3(kQuantThreads, 1, 1);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.early ? 1 : 0;
+  if (warps) return cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, FMT, 32, 2>, a);
+  return cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, FMT, kQuantThreads, 2>, a);
 }
 
 template <typename T>
@@ -206,69 +266,98 @@ cudaError_t launch_typed(const QuantArgs& a, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------- reading back --
+// Bytes in 9/16, out 2 or 4 an element.  A thread writes 16 bytes (8 or 4 neighbours), so
+// that a warp's stores are contiguous, for kBackRows rows at once, whose loads are in
+// flight together.
+constexpr int kBackRows = 4;
+
 struct BackArgs {
   gemm_fp4_matrix_t m;
   int64_t rows, cols, ld, pieces;
-  int64_t units;  // 16 elements each, a row
   void* dst;
-  int dtype;
+  int32_t tpr_log2;      // threads of a row
+  int32_t chunks;        // CTAs along a row
   bool vec;
 };
 
-__global__ void __launch_bounds__(256) fp4_dequantize_kernel(const BackArgs a) {
-  const int64_t total = a.rows * a.units;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / a.units, c = (i - r * a.units) * kUnit;
-    const int64_t b = c / fp4_block(a.m.format);
-    const float s = fp4_scale_value(
-        static_cast<const uint8_t*>(a.m.scale)[fp4_scale_at(r, b, a.pieces)], a.m.format);
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kQuantThreads) fp4_dequantize_kernel(const BackArgs a) {
+  constexpr int kPer = 16 / sizeof(T);  // elements a thread
+  const int tpr = 1 << a.tpr_log2, lanes = kQuantThreads >> a.tpr_log2;
+  const int64_t group = blockIdx.x / uint32_t(a.chunks);
+  const int64_t c =
+      (int64_t(blockIdx.x - group * a.chunks) * tpr + (threadIdx.x & (tpr - 1))) * kPer;
+  const int64_t r0 = group * (lanes * kBackRows) + (threadIdx.x >> a.tpr_log2);
+  if (c >= a.cols) return;
+  const int64_t b = c / fp4_block(FMT);
+  const int64_t bytes = min(int64_t(kPer / 2), (a.cols - c + 1) / 2);
+  uint32_t q[kBackRows], s[kBackRows];
+  float g[kBackRows];
+#pragma unroll
+  for (int i = 0; i < kBackRows; ++i) {
+    const int64_t r = r0 + i * lanes;
+    q[i] = 0;
+    s[i] = 0;
+    g[i] = 1.f;
+    if (r >= a.rows) continue;
     const uint8_t* p = static_cast<const uint8_t*>(a.m.data) + r * a.m.ld + c / 2;
-    uint2 q = make_uint2(0, 0);
-    const int64_t bytes = (a.cols - c + 1) / 2;
-    if (bytes >= 8) {
-      q = __ldg(reinterpret_cast<const uint2*>(p));
+    if (bytes == kPer / 2) {
+      if constexpr (kPer == 8) q[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      else q[i] = __ldg(reinterpret_cast<const uint16_t*>(p));
     } else {
-      for (int j = 0; j < bytes; ++j) (j < 4 ? q.x : q.y) |= uint32_t(p[j]) << (8 * (j & 3));
+      for (int j = 0; j < bytes; ++j) q[i] |= uint32_t(p[j]) << (8 * j);
     }
-    const bool has = a.m.row_scale != nullptr;
-    const float g = has ? a.m.row_scale[r * a.m.row_scale_stride] : 1.f;
-    float v[kUnit];
+    s[i] = __ldg(static_cast<const uint8_t*>(a.m.scale) + fp4_scale_at(r, b, a.pieces));
+    if (a.m.row_scale) g[i] = __ldg(a.m.row_scale + r * a.m.row_scale_stride);
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 x = unpack_e2m1x2((j < 4 ? q.x >> (8 * j) : q.y >> (8 * (j - 4))) & 0xff);
-      v[2 * j] = __fmul_rn(x.x, s) * g;
-      v[2 * j + 1] = __fmul_rn(x.y, s) * g;
+  for (int i = 0; i < kBackRows; ++i) {
+    const int64_t r = r0 + i * lanes;
+    if (r >= a.rows) continue;
+    const float f = fp4_scale_value(s[i], FMT);
+    float v[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer / 2; ++j) {
+      const float2 x = unpack_e2m1x2((q[i] >> (8 * j)) & 0xff);
+      v[2 * j] = __fmul_rn(x.x, f) * g[i];
+      v[2 * j + 1] = __fmul_rn(x.y, f) * g[i];
     }
-    const int64_t at = r * a.ld + c;
-    if (a.vec && c + kUnit <= a.cols) {
-      if (a.dtype == GEMM_F32) {
-        float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.dst) + at);
+    T* const d = static_cast<T*>(a.dst) + r * a.ld + c;
+    T out[kPer];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          d[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      } else {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (a.dtype == GEMM_F16) {
-            const __half2 x = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-            __builtin_memcpy(&w[j], &x, 4);
-          } else {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            __builtin_memcpy(&w[j], &x, 4);
-          }
-        }
-        uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dst) + at);
-        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
+    for (int j = 0; j < kPer; ++j) {
+      if constexpr (sizeof(T) == 4) out[j] = v[j];
+      else if constexpr (std::is_same<T, __half>::value) out[j] = __float2half_rn(v[j]);
+      else out[j] = __float2bfloat16_rn(v[j]);
+    }
+    if (a.vec && c + kPer <= a.cols) {
+      uint4 w;
+      __builtin_memcpy(&w, out, 16);
+      *reinterpret_cast<uint4*>(d) = w;
     } else {
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j)
-        if (c + j < a.cols) store_typed(a.dst, at + j, v[j], a.dtype);
+      for (int j = 0; j < kPer; ++j)
+        if (c + j < a.cols) d[j] = out[j];
     }
   }
+}
+
+template <typename T>
+cudaError_t launch_back(BackArgs a, cudaStream_t s) {
+  constexpr int kPer = 16 / sizeof(T);
+  a.tpr_log2 = 5;
+  while (a.tpr_log2 < 8 && (int64_t(kPer) << a.tpr_log2) < a.cols) ++a.tpr_log2;
+  const int64_t tpr = int64_t(1) << a.tpr_log2, rows = (kQuantThreads / tpr) * kBackRows;
+  const int64_t chunks = (a.cols + tpr * kPer - 1) / (tpr * kPer);
+  const int64_t groups = (a.rows + rows - 1) / rows;
+  if (groups > INT32_MAX / chunks) return cudaErrorInvalidValue;
+  a.chunks = int32_t(chunks);
+  const unsigned grid = unsigned(groups * chunks);
+  if (a.m.format == GEMM_MXFP4)
+    fp4_dequantize_kernel<T, GEMM_MXFP4><<<grid, kQuantThreads, 0, s>>>(a);
+  else
+    fp4_dequantize_kernel<T, GEMM_NVFP4><<<grid, kQuantThreads, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 int64_t pieces_of(int64_t cols, int format) {
@@ -284,7 +373,7 @@ cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int
   const int64_t size = src_dtype == GEMM_F32 ? 4 : 2;
   const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 &&
                    (rows == 1 || (ld_src * size) % 16 == 0);
-  const QuantArgs a{src, rows, cols, ld_src, vec, out, pieces_of(cols, out.format)};
+  const QuantArgs a{src, rows, cols, ld_src, vec, out, pieces_of(cols, out.format), false};
   if (src_dtype == GEMM_F32) return launch_typed<float>(a, stream);
   if (src_dtype == GEMM_F16) return launch_typed<__half>(a, stream);
   return launch_typed<__nv_bfloat16>(a, stream);
@@ -293,14 +382,12 @@ cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int
 cudaError_t launch_fp4_dequantize(int64_t rows, int64_t cols, const gemm_fp4_matrix_t& m,
                                   void* dst, int64_t ld_dst, int dst_dtype, cudaStream_t stream) {
   const int64_t size = dst_dtype == GEMM_F32 ? 4 : 2;
-  const int64_t units = (cols + kUnit - 1) / kUnit;
   const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 &&
                    (rows == 1 || (ld_dst * size) % 16 == 0);
-  const BackArgs a{m,     rows, cols,      ld_dst, pieces_of(cols, m.format),
-                   units, dst,  dst_dtype, vec};
-  const int64_t ctas = (rows * units + 255) / 256;
-  fp4_dequantize_kernel<<<unsigned(ctas < (1 << 20) ? ctas : (1 << 20)), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  const BackArgs a{m, rows, cols, ld_dst, pieces_of(cols, m.format), dst, 0, 0, vec};
+  if (dst_dtype == GEMM_F32) return launch_back<float>(a, stream);
+  if (dst_dtype == GEMM_F16) return launch_back<__half>(a, stream);
+  return launch_back<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace dg

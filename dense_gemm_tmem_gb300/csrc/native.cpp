@@ -102,6 +102,16 @@ at::Tensor carve(const at::Tensor& buf, at::ScalarType type, int64_t at, int64_t
   return t;
 }
 
+// The same, flat.
+at::Tensor carve_flat(const at::Tensor& buf, at::ScalarType type, int64_t at, int64_t count) {
+  const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::TensorImpl::VIEW, c10::Storage(buf.storage()), buf.key_set(), meta);
+  t.unsafeGetTensorImpl()->set_storage_offset(at / int64_t(meta.itemsize()));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(count);
+  return t;
+}
+
 template <class F>
 PyObject* guarded(F&& f) {
   try {
@@ -464,11 +474,10 @@ PyObject* quantize4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!r) throw Raised{};
     PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(carve(q.buf, at::kByte, 0, q.rows, (q.cols + 1) / 2,
                                                   q.m.ld, 1)));
-    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(q.buf.narrow(0, q.scales_at,
-                                                         q.rows_at - q.scales_at)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(carve_flat(q.buf, at::kByte, q.scales_at,
+                                                       q.rows_at - q.scales_at)));
     if (kind == GEMM_NVFP4) {
-      at::Tensor rows = carve(q.buf, at::kFloat, q.rows_at, 1, q.rows, q.rows, 1);
-      PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(rows.select(0, 0)));
+      PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(carve_flat(q.buf, at::kFloat, q.rows_at, q.rows)));
     } else {
       Py_INCREF(Py_None);
       PyTuple_SET_ITEM(r, 2, Py_None);
