@@ -35,10 +35,10 @@ bool encode(OrOperand* m, const __half* p, int64_t rows, int64_t cols, int64_t l
          tiled(&m->mn, 3, dm, sm, bm);
 }
 
-template <bool PAIR>
+template <class Cfg>
 cudaError_t launch(const OrMaps& maps, const OrTcArgs& args, gemm_ctx* h, cudaStream_t stream) {
-  auto kern = ortho_tc_kernel<PAIR>;
-  constexpr int smem = OrConfig<PAIR>::kSmemBytes;
+  auto kern = ortho_tc_kernel<Cfg>;
+  constexpr int smem = Cfg::kSmemBytes;
   static SharedMemoryOnce once;
   cudaError_t e = once.allow(kern, smem, h->device);
   if (e != cudaSuccess) return e;
@@ -48,14 +48,14 @@ cudaError_t launch(const OrMaps& maps, const OrTcArgs& args, gemm_ctx* h, cudaSt
   attr[n].id = cudaLaunchAttributeCooperative;  // tiles wait for tiles of other CTAs
   attr[n].val.cooperative = 1;
   ++n;
-  if (PAIR) {
+  if (Cfg::kPair) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
     attr[n].val.clusterDim.x = 2;
     attr[n].val.clusterDim.y = 1;
     attr[n].val.clusterDim.z = 1;
     ++n;
   }
-  cfg.gridDim = dim3(unsigned(args.owners * (PAIR ? 2 : 1)), 1, 1);
+  cfg.gridDim = dim3(unsigned(args.owners * (Cfg::kPair ? 2 : 1)), 1, 1);
   cfg.blockDim = dim3(kOrThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -64,12 +64,15 @@ cudaError_t launch(const OrMaps& maps, const OrTcArgs& args, gemm_ctx* h, cudaSt
   return cudaLaunchKernelEx(&cfg, kern, maps, args);
 }
 
+using Wide = OrConfig<true, 256>;
+using Narrow = OrConfig<true, 128>;
+using Small = OrConfig<false, 64>;
+
 struct Tiles {
   int64_t r, c, sym, apply;  // of X's rows and columns, and in all of a matrix
 };
-template <bool PAIR>
+template <class Cfg>
 Tiles tiles_of(const OrthoShape& s) {
-  using Cfg = OrConfig<PAIR>;
   Tiles t{};
   t.r = ceil_div(s.rows, Cfg::kTileM);
   t.c = ceil_div(s.cols, Cfg::kTileN);
@@ -82,18 +85,32 @@ Tiles tiles_of(const OrthoShape& s) {
 }  // namespace
 
 int64_t ortho_counters(const OrthoShape& s, int32_t steps) {
-  const Tiles t = tiles_of<false>(s);
+  const Tiles t = tiles_of<Small>(s);
   return 3 * int64_t(steps) * s.batch * std::max(t.sym, t.apply);
 }
 
 cudaError_t launch_ortho_products(gemm_ctx* h, const OrthoCall& c, cudaStream_t stream) {
   const OrthoShape& s = c.shape;
-  // Pairs' tiles where kApply's occupy half of the SMs, else eight times as many small
-  // ones.
+  // Which tiles.  256 x 256: 640 cycles a k-block, 8 flops a loaded byte and cycle more
+  // than the others, but each ends with 4 us of epilogue before another product's tile
+  // can start; 256 x 128: 480 cycles and 2 us; 128 x 64 of one CTA: 545 cycles, 1 us.
+  // So the widest ones where kApply has more than 5/3 of them for each pair, the small
+  // ones where it has one for each SM at most and K is so short that its loads take less
+  // than an epilogue.  Measured (us, 256 / 128 / 64): 4096^2 1027 / 1597 / 3979, 8 x
+  // 1024^2 279 / 295 / 614, 10 x 700 x 1000 240 / 227 / 444, 2048^2 309 / 301 / 557, 1000
+  // x 4096 304 / 264 / 367, 1024^2 206 / 159 / 171, 700 x 1000 189 / 143 / 151, 4 x 512^2
+  // 165 / 125 / 119, 512^2 156 / 116 / 113, 128^2 119 / 83 / 70.
+  constexpr int64_t kShortK = 8;  // k-blocks
   const int64_t pairs = h->opt.pair_clusters > 0 ? h->opt.pair_clusters : h->num_sms / 2;
-  const bool pair = h->opt.pair >= 0 ? h->opt.pair == 1
-                                     : 2 * tiles_of<true>(s).apply * s.batch > pairs;
-  const Tiles t = pair ? tiles_of<true>(s) : tiles_of<false>(s);
+  const Tiles wide = tiles_of<Wide>(s), narrow = tiles_of<Narrow>(s), small = tiles_of<Small>(s);
+  const int64_t kb = ceil_div(std::max(s.rows, s.cols), 64);
+  enum { kWide, kNarrow, kSmall } kind;
+  if (h->opt.pair == 0) kind = kSmall;  // GEMM_OPT_PAIR and _FORCE_TILE_N force them
+  else if (h->opt.pair == 1) kind = h->opt.force_tile_n == 128 ? kNarrow : kWide;
+  else if (3 * wide.apply * s.batch > 5 * pairs) kind = kWide;
+  else kind = kb <= kShortK && small.apply * s.batch <= h->num_sms ? kSmall : kNarrow;
+  const Tiles t = kind == kWide ? wide : kind == kNarrow ? narrow : small;
+  const bool pair = kind != kSmall;
   if (t.sym > INT32_MAX / 16 || t.apply > INT32_MAX / 16) return cudaErrorInvalidValue;
   OrTcArgs a{};
   a.batch = int32_t(s.batch);
@@ -130,13 +147,15 @@ cudaError_t launch_ortho_products(gemm_ctx* h, const OrthoCall& c, cudaStream_t 
   a.wait_limit_ns = h->opt.wait_limit_ns;
   std::copy(c.step, c.step + c.steps, a.step);
   OrMaps m{};
-  const int b_rows = pair ? OrConfig<true>::kBRows : OrConfig<false>::kBRows;
+  const int b_rows = kind == kWide ? Wide::kBRows : kind == kNarrow ? Narrow::kBRows
+                                                                     : Small::kBRows;
   bool ok = encode(&m.a, c.a16, s.n, s.n, s.ld_a, s.batch, s.stride_a, b_rows) &&
             encode(&m.b, c.b16, s.n, s.n, s.ld_a, s.batch, s.stride_a, b_rows);
   for (int i = 0; ok && i < 2; ++i)
     ok = encode(&m.x[i], c.x16[i], s.rows, s.cols, s.ld_x, s.batch, s.stride_x, b_rows);
   if (!ok) return cudaErrorInvalidValue;
-  return pair ? launch<true>(m, a, h, stream) : launch<false>(m, a, h, stream);
+  if (kind == kWide) return launch<Wide>(m, a, h, stream);
+  return kind == kNarrow ? launch<Narrow>(m, a, h, stream) : launch<Small>(m, a, h, stream);
 }
 
 }  // namespace dg

@@ -26,9 +26,8 @@
 //   warp 2             watches the counters of what the next loads read
 //   warps 4-11         epilogue, two warpgroups of half the columns each, beside the
 //                      next tile's MMAs
-// PAIR: two CTAs on two SMs own a 256 x 256 tile (cta_group::2).  Matrices too small to
-// fill the SMs with those have tiles of 128 x 64 of one CTA: what bounds a small tile is
-// its loads, some 45 bytes a cycle and SM, and the latency of its epilogue.
+// Two CTAs on two SMs own a 256 x 256 or a 256 x 128 tile (cta_group::2), or one CTA a
+// 128 x 64 tile: ortho_tc.cu says which when.
 #pragma once
 
 #include "fp8_tc_kernel.cuh"
@@ -44,16 +43,17 @@ constexpr int kOrThreads = 32 * (kOrRoleWarps + kOrEpiWarps);
 constexpr int kOrRoleRegs = 56, kOrEpiRegs = 224;
 constexpr int kOrGroup = 2;   // k-blocks of 64 per stage
 
-template <bool PAIR>
+template <bool PAIR_, int TN>
 struct OrConfig {
-  static constexpr int kTileM = PAIR ? 256 : 128, kTileN = PAIR ? 256 : 64;
+  static constexpr bool kPair = PAIR_;
+  static constexpr int kTileM = kPair ? 256 : 128, kTileN = TN;
   static constexpr int kRatio = kTileM / kTileN;          // tiles along a diagonal block's row
-  static constexpr int kBRows = PAIR ? 128 : 64;          // of B that a CTA loads
+  static constexpr int kBRows = kPair ? TN / 2 : TN;      // of B that a CTA loads
   static constexpr int kABlock = 128 * 128;               // bytes of a k-block of A
   static constexpr int kBBlock = kBRows * 128;
   static constexpr int kABytes = kOrGroup * kABlock;
   static constexpr int kStageBytes = kABytes + kOrGroup * kBBlock;
-  static constexpr int kStages = PAIR ? 3 : 4;
+  static constexpr int kStages = kBRows > 64 ? 3 : 4;
   static constexpr int kTmemCols = 2 * kTileN;
   static constexpr int kHalf = kTileN / 2;                // columns per warpgroup
   static constexpr int kPieceBlocks = kTileM / kBK;       // k-blocks of a piece of K
@@ -96,9 +96,9 @@ struct OrMaps {
 struct OrTile {
   int32_t step, kind, z, tm, tn;
 };
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ OrTile or_tile(const OrTcArgs& a, int64_t t) {
-  constexpr int R = OrConfig<PAIR>::kRatio;
+  constexpr int R = Cfg::kRatio;
   OrTile o;
   const int64_t sym = int64_t(a.per_sym) * a.batch, per = 2 * sym + int64_t(a.per_apply) * a.batch;
   o.step = int32_t(t / per);
@@ -126,9 +126,9 @@ __device__ __forceinline__ OrTile or_tile(const OrTcArgs& a, int64_t t) {
 __device__ __forceinline__ int64_t or_total(const OrTcArgs& a) {
   return (2 * int64_t(a.per_sym) + a.per_apply) * a.batch * a.steps;
 }
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ int32_t or_pieces(const OrTcArgs& a, int32_t kind) {
-  constexpr int P = OrConfig<PAIR>::kPieceBlocks;
+  constexpr int P = Cfg::kPieceBlocks;
   return ((kind == kGram ? a.kb_gram : a.kb_n) + P - 1) / P;
 }
 __device__ __forceinline__ int32_t or_k_blocks(const OrTcArgs& a, int32_t kind) {
@@ -141,17 +141,17 @@ __device__ __forceinline__ uint32_t* or_counters(const OrTcArgs& a, int32_t step
          int64_t(z) * (kind == kApply ? a.per_apply : a.per_sym);
 }
 // Tile (tm, tn)'s place among them.
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ int32_t or_index(const OrTcArgs& a, int32_t kind, int32_t tm,
                                             int32_t tn) {
-  if (kind != kApply) return OrConfig<PAIR>::kRatio * (tm * (tm + 1) / 2) + tn;
+  if (kind != kApply) return Cfg::kRatio * (tm * (tm + 1) / 2) + tn;
   return a.tall ? tn * a.tiles_r + tm : tm * a.tiles_c + tn;
 }
 // Which way the MMA's operands of a piece lie: bit 0 A MN-major, bit 1 B.  Block (i, p) of
 // A16 or B16 above the diagonal is the mirrored (p, i).
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ int or_majors(const OrTcArgs& a, const OrTile& o, int32_t p) {
-  constexpr int R = OrConfig<PAIR>::kRatio;
+  constexpr int R = Cfg::kRatio;
   if (o.kind == kGram) return a.tall ? 3 : 0;
   const int i = p > o.tm, j = p > o.tn / R;
   if (o.kind == kPoly) return i | (j << 1);
@@ -189,40 +189,40 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
 }
 
 // Whether block (i, p) of a symmetric result, or the mirrored one, is stored.
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ bool or_block_done(const OrTcArgs& a, const uint32_t* counters,
                                               int32_t i, int32_t p) {
-  constexpr int R = OrConfig<PAIR>::kRatio;
-  constexpr uint32_t kFull = kOrEpiWarps * (PAIR ? 2 : 1);
-  const uint32_t* c = counters + or_index<PAIR>(a, kPoly, max(i, p), R * min(i, p));
+  constexpr int R = Cfg::kRatio;
+  constexpr uint32_t kFull = kOrEpiWarps * (Cfg::kPair ? 2 : 1);
+  const uint32_t* c = counters + or_index<Cfg>(a, kPoly, max(i, p), R * min(i, p));
   bool have = true;
 #pragma unroll
   for (int r = 0; r < R; ++r) have &= ld_relaxed_gpu(c + r) >= kFull;
   return have;
 }
 // Whether X's tiles in row tm, or R of them from column R j on (those there are), are.
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ bool or_x_done(const OrTcArgs& a, const uint32_t* counters, int32_t tm,
                                           int32_t tn, int32_t count) {
-  constexpr uint32_t kFull = kOrEpiWarps * (PAIR ? 2 : 1);
+  constexpr uint32_t kFull = kOrEpiWarps * (Cfg::kPair ? 2 : 1);
   bool have = true;
   for (int r = 0; r < count; ++r)
-    have &= ld_relaxed_gpu(counters + or_index<PAIR>(a, kApply, tm, tn + r)) >= kFull;
+    have &= ld_relaxed_gpu(counters + or_index<Cfg>(a, kApply, tm, tn + r)) >= kFull;
   return have;
 }
 
 // Watches the counters of what this CTA's tiles read (one warp): `ready` counts the tiles'
 // K in pieces of kTileM, as far as they may be loaded.
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ void or_watch(const OrTcArgs& args, volatile uint32_t* ready,
                                          const WaitCtl& wc, int32_t owner) {
-  constexpr int R = OrConfig<PAIR>::kRatio;
+  constexpr int R = Cfg::kRatio;
   const int lane = threadIdx.x & 31;
   uint32_t passed = 0;
   pdl_wait_prerequisites();
   for (int64_t t = owner; t < or_total(args); t += args.owners) {
-    const OrTile o = or_tile<PAIR>(args, t);
-    const int32_t pieces = or_pieces<PAIR>(args, o.kind);
+    const OrTile o = or_tile<Cfg>(args, t);
+    const int32_t pieces = or_pieces<Cfg>(args, o.kind);
     if (o.kind == kGram && o.step == 0) {
       passed += pieces;
       if (lane == 0) *ready = passed;
@@ -236,18 +236,18 @@ __device__ __forceinline__ void or_watch(const OrTcArgs& args, volatile uint32_t
       auto look = [&]() {
         if (o.kind == kGram) {  // the rows (or columns) of X that the tile multiplies
           if (args.tall)
-            return or_x_done<PAIR>(args, counters, p, R * o.tm,
+            return or_x_done<Cfg>(args, counters, p, R * o.tm,
                                    min(R, args.tiles_c - R * o.tm)) &&
-                   or_x_done<PAIR>(args, counters, p, o.tn, o.tn < args.tiles_c);
+                   or_x_done<Cfg>(args, counters, p, o.tn, o.tn < args.tiles_c);
           const int32_t there = min(R, args.tiles_c - R * p);
-          return or_x_done<PAIR>(args, counters, o.tm, R * p, there) &&
-                 or_x_done<PAIR>(args, counters, o.tn / R, R * p, there);
+          return or_x_done<Cfg>(args, counters, o.tm, R * p, there) &&
+                 or_x_done<Cfg>(args, counters, o.tn / R, R * p, there);
         }
         if (o.kind == kPoly)    // the rows of A
-          return or_block_done<PAIR>(args, counters, o.tm, p) &&
-                 or_block_done<PAIR>(args, counters, o.tn / R, p);
+          return or_block_done<Cfg>(args, counters, o.tm, p) &&
+                 or_block_done<Cfg>(args, counters, o.tn / R, p);
         // the rows of B; X is complete where B is
-        return or_block_done<PAIR>(args, counters, args.tall ? o.tn / R : o.tm, p);
+        return or_block_done<Cfg>(args, counters, args.tall ? o.tn / R : o.tm, p);
       };
       bool have = false;
       int32_t seen = 0;
@@ -300,19 +300,18 @@ __device__ __forceinline__ bool or_wait_ready(const volatile uint32_t* ready, ui
 }
 
 // TMA producer (one thread).  Returns how many stages it filled.
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ uint32_t or_producer(const OrMaps& maps, const OrTcArgs& args,
                                                 uint32_t ring, uint64_t* full, uint64_t* empty,
                                                 const volatile uint32_t* ready,
                                                 const WaitCtl& wc, uint32_t rank, int32_t owner) {
-  using Cfg = OrConfig<PAIR>;
   int s = 0;
   uint32_t ph = 0, filled = 0, passed = 0;
   pdl_wait_prerequisites();
   for (int64_t t = owner; t < or_total(args); t += args.owners) {
-    const OrTile o = or_tile<PAIR>(args, t);
+    const OrTile o = or_tile<Cfg>(args, t);
     const int32_t a_row = o.tm * Cfg::kTileM + int32_t(rank) * 128;
-    const int32_t b_row = o.tn * Cfg::kTileN + int32_t(rank) * 128;
+    const int32_t b_row = o.tn * Cfg::kTileN + int32_t(rank) * Cfg::kBRows;
     const int32_t k_blocks = or_k_blocks(args, o.kind);
     const OrOperand& x = maps.x[o.step & 1];
     const OrOperand& mA = o.kind == kGram ? x : o.kind == kPoly ? maps.a : args.tall ? x : maps.b;
@@ -322,18 +321,18 @@ __device__ __forceinline__ uint32_t or_producer(const OrMaps& maps, const OrTcAr
       if (kb % Cfg::kPieceBlocks == 0) {
         if (!or_wait_ready(ready, ++passed, wc)) return filled;
         fence_proxy_async_all();
-        majors = or_majors<PAIR>(args, o, kb / Cfg::kPieceBlocks);
+        majors = or_majors<Cfg>(args, o, kb / Cfg::kPieceBlocks);
       }
       if (!wait_bounded(smem_u32(&empty[s]), ph ^ 1, wc, kSiteProducer)) return filled;
       const uint32_t own = smem_u32(&full[s]);
-      if (rank == 0) mbar_arrive_expect_tx(own, (PAIR ? 2 : 1) * Cfg::kStageBytes);
+      if (rank == 0) mbar_arrive_expect_tx(own, (Cfg::kPair ? 2 : 1) * Cfg::kStageBytes);
       // K-major: the rows' two k-blocks; MN-major: boxes 64 wide and 128 of K deep
       auto load4 = [&](uint32_t dst, const CUtensorMap* map, int32_t row) {
-        if constexpr (PAIR) tma_load_4d_pair(dst, map, map_to_rank(own, 0), 0, row, kb, o.z);
+        if constexpr (Cfg::kPair) tma_load_4d_pair(dst, map, map_to_rank(own, 0), 0, row, kb, o.z);
         else tma_load_4d(dst, map, own, 0, row, kb, o.z);
       };
       auto load3 = [&](uint32_t dst, const CUtensorMap* map, int32_t row) {
-        if constexpr (PAIR) tma_load_3d_pair(dst, map, map_to_rank(own, 0), row, kb * kBK, o.z);
+        if constexpr (Cfg::kPair) tma_load_3d_pair(dst, map, map_to_rank(own, 0), row, kb * kBK, o.z);
         else tma_load_3d(dst, map, own, row, kb * kBK, o.z);
       };
       const uint32_t a_dst = ring + uint32_t(s) * Cfg::kStageBytes, b_dst = a_dst + Cfg::kABytes;
@@ -360,26 +359,25 @@ __device__ __forceinline__ uint32_t or_producer(const OrMaps& maps, const OrTcAr
 }
 
 // MMA issuer (one thread).  Whether it issued anything.
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ bool or_mma(const OrTcArgs& args, uint32_t ring, uint64_t* full,
                                        uint64_t* empty, uint64_t* acc_full, uint64_t* acc_empty,
                                        const WaitCtl& wc, uint32_t tmem_base, int32_t owner) {
-  using Cfg = OrConfig<PAIR>;
   int s = 0, b = 0;
   uint32_t ph = 0, aph = 1;
   bool any = false;
   auto commit = [&](uint64_t* bar) {
-    if constexpr (PAIR) tc_commit_pair_both(smem_u32(bar));
+    if constexpr (Cfg::kPair) tc_commit_pair_both(smem_u32(bar));
     else tc_commit(smem_u32(bar));
   };
   for (int64_t t = owner; t < or_total(args); t += args.owners) {
-    const OrTile o = or_tile<PAIR>(args, t);
+    const OrTile o = or_tile<Cfg>(args, t);
     const int32_t k_blocks = or_k_blocks(args, o.kind);
     if (!wait_bounded(smem_u32(&acc_empty[b]), aph, wc, kSiteMmaAccum)) return any;
     tc_fence_after();
     const uint32_t d = tmem_base + uint32_t(b * Cfg::kTileN);
     for (int32_t kb = 0; kb < k_blocks; kb += kOrGroup) {
-      const int majors = or_majors<PAIR>(args, o, kb / Cfg::kPieceBlocks);
+      const int majors = or_majors<Cfg>(args, o, kb / Cfg::kPieceBlocks);
       const int a_mn = majors & 1, b_mn = majors >> 1;
       const uint32_t idesc = make_idesc_f16(Cfg::kTileM, Cfg::kTileN, a_mn, b_mn);
       // MN-major: 64-wide halves two k-blocks apart, 16 of K 2 KiB apart, a k-block 8
@@ -400,7 +398,7 @@ __device__ __forceinline__ bool or_mma(const OrTcArgs& args, uint32_t ring, uint
 #pragma unroll
         for (int kk = 0; kk < kBK / 16; ++kk) {
           const uint32_t acc = kb > 0 || j > 0 || kk > 0 ? 1u : 0u;
-          if constexpr (PAIR)
+          if constexpr (Cfg::kPair)
             tc_mma_f16_pair(d, adesc + uint64_t(kk * a_step), bdesc + uint64_t(kk * b_step), idesc,
                             acc);
           else
@@ -584,13 +582,12 @@ __device__ __forceinline__ void or_store_iterate(const OrTcArgs& a, const float 
   }
 }
 
-template <bool PAIR>
+template <class Cfg>
 __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_full,
                                             uint64_t* acc_empty, const volatile uint32_t* ready,
                                             const WaitCtl& wc,
                                             uint32_t tmem_base, uint8_t* stage, uint32_t rank,
                                             int32_t owner) {
-  using Cfg = OrConfig<PAIR>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = warp & 3, wg = (warp - kOrRoleWarps) >> 2;
   const uint32_t stage_w = smem_u32(stage) + uint32_t(warp - kOrRoleWarps) * 4096u;
@@ -600,7 +597,7 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
   uint32_t passed = 0;
   pdl_wait_prerequisites();
   for (int64_t t = owner; t < or_total(args); t += args.owners) {
-    const OrTile o = or_tile<PAIR>(args, t);
+    const OrTile o = or_tile<Cfg>(args, t);
     const int32_t row0 = o.tm * Cfg::kTileM + int32_t(rank) * 128 + q * 32;
     const int32_t col0 = o.tn * Cfg::kTileN + wg * Cfg::kHalf;
     const bool apply = o.kind == kApply;
@@ -628,7 +625,7 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
         }
       }
     }
-    passed += or_pieces<PAIR>(args, o.kind);
+    passed += or_pieces<Cfg>(args, o.kind);
     ok = ok && wait_bounded(smem_u32(&acc_full[b]), aph, wc, kSiteEpilogue);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after();
@@ -650,11 +647,11 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
     // the tile's counter: this warp's stores, for copies and loads of other SMs
     __syncwarp();
     if (lane == 0) red_release_gpu(or_counters(args, o.step, o.kind, o.z) +
-                                   or_index<PAIR>(args, o.kind, o.tm, o.tn));
+                                   or_index<Cfg>(args, o.kind, o.tm, o.tn));
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      if constexpr (PAIR) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[b]), 0));
+      if constexpr (Cfg::kPair) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[b]), 0));
       else mbar_arrive(smem_u32(&acc_empty[b]));
     }
     if (++b == 2) {
@@ -664,10 +661,9 @@ __device__ __forceinline__ void or_epilogue(const OrTcArgs& args, uint64_t* acc_
   }
 }
 
-template <bool PAIR>
+template <class Cfg>
 __global__ void __launch_bounds__(kOrThreads, 1)
     ortho_tc_kernel(const __grid_constant__ OrMaps maps, const __grid_constant__ OrTcArgs args) {
-  using Cfg = OrConfig<PAIR>;
   constexpr uint32_t S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
@@ -686,8 +682,8 @@ __global__ void __launch_bounds__(kOrThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0;
-  const int32_t owner = PAIR ? int32_t(blockIdx.x >> 1) : int32_t(blockIdx.x);
+  const uint32_t rank = Cfg::kPair ? cluster_rank() : 0;
+  const int32_t owner = Cfg::kPair ? int32_t(blockIdx.x >> 1) : int32_t(blockIdx.x);
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -695,7 +691,7 @@ __global__ void __launch_bounds__(kOrThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&acc_full[i]), 1);
-      mbar_init(smem_u32(&acc_empty[i]), kOrEpiWarps * (PAIR ? 2 : 1));
+      mbar_init(smem_u32(&acc_empty[i]), kOrEpiWarps * (Cfg::kPair ? 2 : 1));
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -706,7 +702,7 @@ __global__ void __launch_bounds__(kOrThreads, 1)
     tma_prefetch_map(args.tall ? &maps.x[0].mn : &maps.x[0].kb);
   }
   if (warp == 1) {
-    if constexpr (PAIR) {
+    if constexpr (Cfg::kPair) {
       tmem_alloc_pair(smem_u32(tmem_slot), Cfg::kTmemCols);
       tmem_relinquish_pair();
     } else {
@@ -715,7 +711,7 @@ __global__ void __launch_bounds__(kOrThreads, 1)
     }
   }
   tc_fence_before();
-  if constexpr (PAIR) cluster_sync_all();
+  if constexpr (Cfg::kPair) cluster_sync_all();
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
@@ -726,22 +722,22 @@ __global__ void __launch_bounds__(kOrThreads, 1)
   bool issued = false;
   if (warp >= kOrRoleWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOrEpiRegs));
-    or_epilogue<PAIR>(args, acc_full, acc_empty, ready, wc, tmem_base, stage, rank, owner);
+    or_epilogue<Cfg>(args, acc_full, acc_empty, ready, wc, tmem_base, stage, rank, owner);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOrRoleRegs));
     if (warp == 0 && lane == 0) {
-      filled = or_producer<PAIR>(maps, args, smem_u32(ring), full, empty, ready, wc, rank, owner);
-      if (PAIR && rank != 0) st_dsmem_u32(map_to_rank(smem_u32(peer_filled), 0), filled);
+      filled = or_producer<Cfg>(maps, args, smem_u32(ring), full, empty, ready, wc, rank, owner);
+      if (Cfg::kPair && rank != 0) st_dsmem_u32(map_to_rank(smem_u32(peer_filled), 0), filled);
     } else if (warp == 2) {
-      or_watch<PAIR>(args, ready, wc, owner);
+      or_watch<Cfg>(args, ready, wc, owner);
     } else {
       pdl_wait_prerequisites();
       if (warp == 1 && lane == 0 && rank == 0) {
-        issued = or_mma<PAIR>(args, smem_u32(ring), full, empty, acc_full, acc_empty, wc,
+        issued = or_mma<Cfg>(args, smem_u32(ring), full, empty, acc_full, acc_empty, wc,
                               tmem_base, owner);
         // every MMA finishes before TMEM is freed, also when an epilogue gave up
         if (issued) {
-          if constexpr (PAIR) tc_commit_pair_self(smem_u32(drain));
+          if constexpr (Cfg::kPair) tc_commit_pair_self(smem_u32(drain));
           else tc_commit(smem_u32(drain));
           wait_drain(smem_u32(drain), 0, wc);
         }
@@ -750,11 +746,11 @@ __global__ void __launch_bounds__(kOrThreads, 1)
   }
   __syncthreads();
   tc_fence_before();
-  if constexpr (PAIR) cluster_sync_all();
+  if constexpr (Cfg::kPair) cluster_sync_all();
   // after an abort copies may still be in flight: each stage's last one (of a pair, see
   // tc2_drain_loads)
   if (rank == 0 && threadIdx.x == 0) {
-    const uint32_t n0 = filled, n1 = PAIR ? *peer_filled : filled, n = n0 > n1 ? n0 : n1;
+    const uint32_t n0 = filled, n1 = Cfg::kPair ? *peer_filled : filled, n = n0 > n1 ? n0 : n1;
 #pragma unroll 1
     for (uint32_t s = 0; s < S && s < n; ++s) {
       const uint32_t at = s + ((n - 1 - s) / S) * S;
@@ -764,11 +760,11 @@ __global__ void __launch_bounds__(kOrThreads, 1)
       wait_drain(bar, (at / S) & 1, wc);
     }
   }
-  if constexpr (PAIR) cluster_sync_all();
+  if constexpr (Cfg::kPair) cluster_sync_all();
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+    if constexpr (Cfg::kPair) tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
     else tmem_dealloc(tmem_base, Cfg::kTmemCols);
   }
 }

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from dense_gemm_tmem_gb300 import binding as B
 from dense_gemm_tmem_gb300.gemm import Gemm
 
 pytestmark = pytest.mark.gpu
@@ -173,3 +174,40 @@ def test_streams_graphs_and_repeats(g):
             graph.replay()
             assert torch.equal(out, want)
     g.status()
+
+
+@pytest.mark.parametrize("pair,tile_n", [(0, -1), (1, 128), (1, 256)])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 130, 70), (2, 300, 600), (3, 600, 270),
+                                             (1, 700, 700), (5, 64, 40)])
+def test_every_tile_on_every_shape(g, pair, tile_n, batch, rows, cols):
+    """One CTA's tiles, and both of a pair's, whatever the rule would take."""
+    torch.manual_seed(rows)
+    G = torch.randn(batch, rows, cols, device="cuda")
+    g.set_option(B.GEMM_OPT_PAIR, pair)
+    g.set_option(B.GEMM_OPT_FORCE_TILE_N, tile_n)
+    try:
+        for steps, abc in ((5, FAST), (2, CONVERGENT)):
+            got = g.orthogonalize(G, steps, abc)
+            for i in range(batch):
+                check(got[i], G[i], steps, abc)
+            assert torch.equal(g.orthogonalize(G, steps, abc), got)
+        g.status()
+    finally:
+        g.set_option(B.GEMM_OPT_PAIR, -1)
+        g.set_option(B.GEMM_OPT_FORCE_TILE_N, -1)
+
+
+@pytest.mark.parametrize("pair,tile_n", [(0, -1), (1, 128), (1, 256)])
+def test_under_short_wait_limits(g, pair, tile_n):
+    """Limits that run out anywhere in the launch: it ends, gemm_status reports it or the
+    result is right, and the next call is right."""
+    from test_gpu_fp8_limits import limited
+    torch.manual_seed(4)
+    G = torch.randn(2, 520, 600, device="cuda")
+    g.set_option(B.GEMM_OPT_PAIR, pair)
+    g.set_option(B.GEMM_OPT_FORCE_TILE_N, tile_n)
+    try:
+        limited(g, lambda: [g.orthogonalize(G)], [1, 300, 1000, 3000, 10000, 30000], times=3)
+    finally:
+        g.set_option(B.GEMM_OPT_PAIR, -1)
+        g.set_option(B.GEMM_OPT_FORCE_TILE_N, -1)
