@@ -18,8 +18,15 @@
 namespace dg {
 namespace {
 
-constexpr int kQuantThreads = 256;
+constexpr int kQuantThreads = 128;
+constexpr int kBackThreads = 256;
 constexpr int kUnit = 16;  // elements a thread takes at a time
+
+// Where 16-byte blocks may be read: the bytes from a matrix's first element to its last,
+// gaps between its rows among them.
+struct Span {
+  const uint8_t *begin, *end;
+};
 
 // 16 neighbouring elements as loaded.
 template <typename T>
@@ -27,22 +34,47 @@ struct Unit16 {
   static constexpr int kWords = sizeof(T) * kUnit / 4;
   uint32_t w[kWords];
 
-  __device__ __forceinline__ void load(const T* p, int valid, bool vec) {
-    if (vec && valid >= kUnit) {
+  // The first `valid` of the elements at p, zeros after them.  Rows that do not start on
+  // 16 bytes are read in the 16-byte blocks that hold them, shifted into place (element
+  // by element 1000 x 8191 bf16 took 13.4 us instead of 8.8).
+  __device__ __forceinline__ void load(const T* p, int valid, const Span& span) {
+    const uint8_t* const at = reinterpret_cast<const uint8_t*>(p);
+    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
+    const uint4* const block = reinterpret_cast<const uint4*>(at - off);
+    if (valid >= kUnit && off == 0) {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        const uint4 a = __ldg(block + i);
         w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
       }
-      return;
-    }
+    } else if (valid >= kUnit && at - off >= span.begin &&
+               at - off + 4 * kWords + 16 <= span.end) {
+      uint32_t v[kWords + 4];
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0;
+      for (int i = 0; i < kWords / 4 + 1; ++i) {
+        const uint4 a = __ldg(block + i);
+        v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
+      }
+      if (off & 8u) {
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) {
-      if (j >= valid) continue;
-      if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(float(p[j]));
-      else w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j & 1));
+        for (int j = 0; j < kWords + 2; ++j) v[j] = v[j + 2];
+      }
+      if (off & 4u) {
+#pragma unroll
+        for (int j = 0; j < kWords + 1; ++j) v[j] = v[j + 1];
+      }
+#pragma unroll
+      for (int j = 0; j < kWords; ++j)
+        w[j] = sizeof(T) == 2 && (off & 2u) ? __funnelshift_r(v[j], v[j + 1], 16) : v[j];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) {
+        if (j >= valid) continue;
+        if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(float(p[j]));
+        else w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j & 1));
+      }
     }
   }
   // Elements 2 j and 2 j + 1.
@@ -109,16 +141,21 @@ constexpr int64_t kEarlyCtas = 256;
 struct QuantArgs {
   const void* src;
   int64_t rows, cols, ld;
-  bool vec;
+  Span span;
   gemm_fp4_matrix_t out;
   int64_t pieces;
   bool early;  // the next kernel may start beside this one
 };
 
+// CTAs an SM that the registers are cut for.
+constexpr int quant_ctas(size_t size, int units) {
+  return size == 2 ? (units > 2 ? 8 : 10) : (units > 2 ? 5 : 8);
+}
+
 // A row per TPR threads (32: a warp, or the whole CTA), U units a thread in
 // registers.
 template <typename T, int FMT, int TPR, int U>
-__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 6 : 4)
+__global__ void __launch_bounds__(kQuantThreads, quant_ctas(sizeof(T), U))
     fp4_quantize_kernel(const QuantArgs a) {
   constexpr int kRowsPer = kQuantThreads / TPR;
   const int t = threadIdx.x % TPR;
@@ -145,7 +182,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 6 : 4)
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t c = (u0 + t + i * TPR) * kUnit;
-      x[i].load(src + c, int(max(int64_t(0), min(int64_t(kUnit), a.cols - c))), a.vec);
+      x[i].load(src + c, int(max(int64_t(0), min(int64_t(kUnit), a.cols - c))), a.span);
     }
   };
   auto maxima = [&]() {
@@ -242,8 +279,11 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 6 : 4)
 template <typename T, int FMT>
 cudaError_t launch_format(QuantArgs a, cudaStream_t s) {
   const int64_t rows = (a.rows + 127) / 128 * 128;
+  const int64_t units = a.pieces * (fp4_block(FMT) * 4 / kUnit);
   constexpr int kPer = kQuantThreads / 32;
-  const bool warps = a.cols <= 2 * 32 * kUnit;
+  // a warp a row up to 2 units a lane, else the CTA with as few units a thread as hold
+  // the row, 4 at most
+  const bool warps = units <= 2 * 32;
   const int64_t grid = warps ? rows / kPer : rows;
   a.early = grid <= kEarlyCtas;
   cudaLaunchConfig_t cfg = {};
@@ -256,7 +296,14 @@ cudaError_t launch_format(QuantArgs a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = a.early ? 1 : 0;
   if (warps) return cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, FMT, 32, 2>, a);
-  return cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, FMT, kQuantThreads, 2>, a);
+  switch (units <= kQuantThreads ? 1 : units <= 2 * kQuantThreads ? 2
+                                   : units <= 3 * kQuantThreads   ? 3
+                                                                  : 4) {
+    case 1: return cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, FMT, kQuantThreads, 1>, a);
+    case 2: return cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, FMT, kQuantThreads, 2>, a);
+    case 3: return cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, FMT, kQuantThreads, 3>, a);
+    default: return cudaLaunchKernelEx(&cfg, fp4_quantize_kernel<T, FMT, kQuantThreads, 4>, a);
+  }
 }
 
 template <typename T>
@@ -266,7 +313,8 @@ cudaError_t launch_typed(const QuantArgs& a, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------- reading back --
-// Bytes in 9/16, out 2 or 4 an element.  A thread writes 16 bytes (8 or 4 neighbours), so
+// Bytes in 9/16, out 2 or 4 an element.  A thread writes an aligned 16 bytes of a row (8 or
+// 4 neighbours, which may lie in two blocks where the row does not start on 16 bytes), so
 // that a warp's stores are contiguous, for kBackRows rows at once, whose loads are in
 // flight together.
 constexpr int kBackRows = 4;
@@ -275,69 +323,105 @@ struct BackArgs {
   gemm_fp4_matrix_t m;
   int64_t rows, cols, ld, pieces;
   void* dst;
-  int32_t tpr_log2;      // threads of a row
-  int32_t chunks;        // CTAs along a row
-  bool vec;
+  int32_t tpr_log2;  // threads of a row
+  int32_t chunks;    // CTAs along a row
 };
 
-template <typename T, int FMT>
-__global__ void __launch_bounds__(kQuantThreads) fp4_dequantize_kernel(const BackArgs a) {
+// ALIGNED: every row of dst starts on 16 bytes.  (8192^2 bf16 36.8 us, through the general
+// way 73; 1000 x 8191, which has to take it, 15.3, element by element 26.)
+template <typename T, int FMT, bool ALIGNED>
+__global__ void __launch_bounds__(kBackThreads) fp4_dequantize_kernel(const BackArgs a) {
   constexpr int kPer = 16 / sizeof(T);  // elements a thread
-  const int tpr = 1 << a.tpr_log2, lanes = kQuantThreads >> a.tpr_log2;
+  const int tpr = 1 << a.tpr_log2, lanes = kBackThreads >> a.tpr_log2;
   const int64_t group = blockIdx.x / uint32_t(a.chunks);
-  const int64_t c =
-      (int64_t(blockIdx.x - group * a.chunks) * tpr + (threadIdx.x & (tpr - 1))) * kPer;
+  const int64_t place =
+      int64_t(blockIdx.x - group * a.chunks) * tpr + (threadIdx.x & (tpr - 1));
   const int64_t r0 = group * (lanes * kBackRows) + (threadIdx.x >> a.tpr_log2);
-  if (c >= a.cols) return;
-  const int64_t b = c / fp4_block(FMT);
-  const int64_t bytes = min(int64_t(kPer / 2), (a.cols - c + 1) / 2);
-  uint32_t q[kBackRows], s[kBackRows];
+  uint32_t q[kBackRows], s[kBackRows][2];
   float g[kBackRows];
+  int64_t first[kBackRows];  // this thread's first element, below 0 where the row starts later
 #pragma unroll
   for (int i = 0; i < kBackRows; ++i) {
     const int64_t r = r0 + i * lanes;
-    q[i] = 0;
-    s[i] = 0;
+    q[i] = s[i][0] = s[i][1] = 0;
     g[i] = 1.f;
+    first[i] = a.cols;
     if (r >= a.rows) continue;
-    const uint8_t* p = static_cast<const uint8_t*>(a.m.data) + r * a.m.ld + c / 2;
-    if (bytes == kPer / 2) {
-      if constexpr (kPer == 8) q[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
-      else q[i] = __ldg(reinterpret_cast<const uint16_t*>(p));
-    } else {
-      for (int j = 0; j < bytes; ++j) q[i] |= uint32_t(p[j]) << (8 * j);
+    const uint32_t off =
+        ALIGNED ? 0u
+                : uint32_t(reinterpret_cast<uintptr_t>(static_cast<T*>(a.dst) + r * a.ld)) & 15u;
+    const int64_t c = place * kPer - int64_t(off / sizeof(T));
+    first[i] = c;
+    if (c >= a.cols || c + kPer <= 0) continue;
+    // the values from element c on, out of the two words that hold them
+    const uint8_t* const row = static_cast<const uint8_t*>(a.m.data) + r * a.m.ld;
+    if constexpr (ALIGNED) {
+      const int64_t bytes = min(int64_t(kPer / 2), (a.cols - c + 1) / 2);
+      if (bytes == kPer / 2) {
+        if constexpr (kPer == 8) q[i] = __ldg(reinterpret_cast<const uint32_t*>(row + c / 2));
+        else q[i] = __ldg(reinterpret_cast<const uint16_t*>(row + c / 2));
+      } else {
+        for (int j = 0; j < bytes; ++j) q[i] |= uint32_t(row[c / 2 + j]) << (8 * j);
+      }
+      s[i][0] = __ldg(static_cast<const uint8_t*>(a.m.scale) +
+                      fp4_scale_at(r, c / fp4_block(FMT), a.pieces));
+      if (a.m.row_scale) g[i] = __ldg(a.m.row_scale + r * a.m.row_scale_stride);
+      continue;
     }
-    s[i] = __ldg(static_cast<const uint8_t*>(a.m.scale) + fp4_scale_at(r, b, a.pieces));
+    const int64_t word = c >= 0 ? c >> 3 : -1, last = (a.cols - 1) >> 3;
+    auto word_at = [&](int64_t k) -> uint32_t {
+      if (k < 0 || k > last) return 0;
+      const int64_t bytes = (a.cols + 1) / 2 - 4 * k;
+      if (bytes >= 4) return __ldg(reinterpret_cast<const uint32_t*>(row) + k);
+      uint32_t v = 0;
+      for (int j = 0; j < bytes; ++j) v |= uint32_t(row[4 * k + j]) << (8 * j);
+      return v;
+    };
+    const uint32_t shift = uint32_t(c & 7) * 4;
+    const uint32_t lo = word_at(word);
+    q[i] = lo;
+    if (shift + 4 * kPer > 32) q[i] = __funnelshift_r(lo, word_at(word + 1), shift);
+    else q[i] >>= shift;
+    const int64_t b0 = (c > 0 ? c : 0) / fp4_block(FMT);
+    const int64_t b1 = min(c + kPer, a.cols) - 1 >= 0 ? (min(c + kPer, a.cols) - 1) / fp4_block(FMT)
+                                                      : 0;
+    const uint8_t* const scale = static_cast<const uint8_t*>(a.m.scale);
+    s[i][0] = __ldg(scale + fp4_scale_at(r, b0, a.pieces));
+    s[i][1] = b1 == b0 ? s[i][0] : uint32_t(__ldg(scale + fp4_scale_at(r, b1, a.pieces)));
     if (a.m.row_scale) g[i] = __ldg(a.m.row_scale + r * a.m.row_scale_stride);
   }
 #pragma unroll
   for (int i = 0; i < kBackRows; ++i) {
-    const int64_t r = r0 + i * lanes;
-    if (r >= a.rows) continue;
-    const float f = fp4_scale_value(s[i], FMT);
-    float v[kPer];
+    const int64_t r = r0 + i * lanes, c = first[i];
+    if (r >= a.rows || c >= a.cols || c + kPer <= 0) continue;
+    const float f0 = fp4_scale_value(s[i][0], FMT);
+    const float f1 = ALIGNED ? f0 : fp4_scale_value(s[i][1], FMT);
+    // how many of the elements lie in the first of the two blocks
+    const int in0 = ALIGNED ? kPer
+                            : int(fp4_block(FMT) - (c > 0 ? c : 0) % fp4_block(FMT)) +
+                                  (c < 0 ? int(-c) : 0);
+    T out[kPer];
 #pragma unroll
     for (int j = 0; j < kPer / 2; ++j) {
       const float2 x = unpack_e2m1x2((q[i] >> (8 * j)) & 0xff);
-      v[2 * j] = __fmul_rn(x.x, f) * g[i];
-      v[2 * j + 1] = __fmul_rn(x.y, f) * g[i];
+      const float v[2] = {__fmul_rn(x.x, 2 * j < in0 ? f0 : f1) * g[i],
+                          __fmul_rn(x.y, 2 * j + 1 < in0 ? f0 : f1) * g[i]};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if constexpr (sizeof(T) == 4) out[2 * j + k] = v[k];
+        else if constexpr (std::is_same<T, __half>::value) out[2 * j + k] = __float2half_rn(v[k]);
+        else out[2 * j + k] = __float2bfloat16_rn(v[k]);
+      }
     }
     T* const d = static_cast<T*>(a.dst) + r * a.ld + c;
-    T out[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if constexpr (sizeof(T) == 4) out[j] = v[j];
-      else if constexpr (std::is_same<T, __half>::value) out[j] = __float2half_rn(v[j]);
-      else out[j] = __float2bfloat16_rn(v[j]);
-    }
-    if (a.vec && c + kPer <= a.cols) {
+    if ((ALIGNED || c >= 0) && c + kPer <= a.cols) {
       uint4 w;
       __builtin_memcpy(&w, out, 16);
       *reinterpret_cast<uint4*>(d) = w;
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (c + j < a.cols) d[j] = out[j];
+        if (c + j >= 0 && c + j < a.cols) d[j] = out[j];
     }
   }
 }
@@ -345,19 +429,25 @@ __global__ void __launch_bounds__(kQuantThreads) fp4_dequantize_kernel(const Bac
 template <typename T>
 cudaError_t launch_back(BackArgs a, cudaStream_t s) {
   constexpr int kPer = 16 / sizeof(T);
+  const bool aligned = (reinterpret_cast<uintptr_t>(a.dst) & 15) == 0 &&
+                       (a.rows == 1 || a.ld * int64_t(sizeof(T)) % 16 == 0);
+  const int64_t places = (a.cols + kPer - 1) / kPer + (aligned ? 0 : 1);
   a.tpr_log2 = 5;
-  while (a.tpr_log2 < 8 && (int64_t(kPer) << a.tpr_log2) < a.cols) ++a.tpr_log2;
-  const int64_t tpr = int64_t(1) << a.tpr_log2, rows = (kQuantThreads / tpr) * kBackRows;
-  const int64_t chunks = (a.cols + tpr * kPer - 1) / (tpr * kPer);
-  const int64_t groups = (a.rows + rows - 1) / rows;
+  while (a.tpr_log2 < 8 && (int64_t(1) << a.tpr_log2) < places) ++a.tpr_log2;
+  const int64_t tpr = int64_t(1) << a.tpr_log2, rows = (kBackThreads / tpr) * kBackRows;
+  const int64_t chunks = (places + tpr - 1) / tpr, groups = (a.rows + rows - 1) / rows;
   if (groups > INT32_MAX / chunks) return cudaErrorInvalidValue;
   a.chunks = int32_t(chunks);
   const unsigned grid = unsigned(groups * chunks);
+  auto launch = [&](auto kern) {
+    kern<<<grid, kBackThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  };
   if (a.m.format == GEMM_MXFP4)
-    fp4_dequantize_kernel<T, GEMM_MXFP4><<<grid, kQuantThreads, 0, s>>>(a);
-  else
-    fp4_dequantize_kernel<T, GEMM_NVFP4><<<grid, kQuantThreads, 0, s>>>(a);
-  return cudaGetLastError();
+    return aligned ? launch(fp4_dequantize_kernel<T, GEMM_MXFP4, true>)
+                   : launch(fp4_dequantize_kernel<T, GEMM_MXFP4, false>);
+  return aligned ? launch(fp4_dequantize_kernel<T, GEMM_NVFP4, true>)
+                 : launch(fp4_dequantize_kernel<T, GEMM_NVFP4, false>);
 }
 
 int64_t pieces_of(int64_t cols, int format) {
@@ -371,9 +461,9 @@ cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int
                                 int src_dtype, const gemm_fp4_matrix_t& out,
                                 cudaStream_t stream) {
   const int64_t size = src_dtype == GEMM_F32 ? 4 : 2;
-  const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 &&
-                   (rows == 1 || (ld_src * size) % 16 == 0);
-  const QuantArgs a{src, rows, cols, ld_src, vec, out, pieces_of(cols, out.format), false};
+  const uint8_t* const begin = static_cast<const uint8_t*>(src);
+  const Span span{begin, begin + ((rows - 1) * ld_src + cols) * size};
+  const QuantArgs a{src, rows, cols, ld_src, span, out, pieces_of(cols, out.format), false};
   if (src_dtype == GEMM_F32) return launch_typed<float>(a, stream);
   if (src_dtype == GEMM_F16) return launch_typed<__half>(a, stream);
   return launch_typed<__nv_bfloat16>(a, stream);
@@ -381,10 +471,7 @@ cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int
 
 cudaError_t launch_fp4_dequantize(int64_t rows, int64_t cols, const gemm_fp4_matrix_t& m,
                                   void* dst, int64_t ld_dst, int dst_dtype, cudaStream_t stream) {
-  const int64_t size = dst_dtype == GEMM_F32 ? 4 : 2;
-  const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0 &&
-                   (rows == 1 || (ld_dst * size) % 16 == 0);
-  const BackArgs a{m, rows, cols, ld_dst, pieces_of(cols, m.format), dst, 0, 0, vec};
+  const BackArgs a{m, rows, cols, ld_dst, pieces_of(cols, m.format), dst, 0, 0};
   if (dst_dtype == GEMM_F32) return launch_back<float>(a, stream);
   if (dst_dtype == GEMM_F16) return launch_back<__half>(a, stream);
   return launch_back<__nv_bfloat16>(a, stream);

@@ -404,7 +404,8 @@ struct Made4 {
   }
 };
 
-// The tensors of an Fp4Matrix of `cols` columns, looked at on every call.
+// The tensors of an Fp4Matrix of `cols` columns, looked at on every call (and when one is
+// made, wherever they are: device < 0).
 struct Given4 {
   gemm_fp4_matrix_t m;
   int64_t rows;
@@ -413,29 +414,55 @@ struct Given4 {
     const at::Tensor& q = tensor(data, "data must be a tensor");
     const at::Tensor& s = tensor(scale, "scale must be a tensor");
     if (kind != GEMM_MXFP4 && kind != GEMM_NVFP4) fail(PyExc_ValueError, "unknown format");
-    if (q.element_size() != 1 || s.element_size() != 1)
-      fail(PyExc_TypeError, "data and scale must have one byte an element");
+    if (q.scalar_type() != at::kByte && q.scalar_type() != at::ScalarType::Float4_e2m1fn_x2)
+      fail(PyExc_TypeError, "data must be uint8 (or float4_e2m1fn_x2)");
+    if (s.scalar_type() != at::kByte &&
+        s.scalar_type() != (kind == GEMM_MXFP4 ? at::ScalarType::Float8_e8m0fnu
+                                               : at::ScalarType::Float8_e4m3fn))
+      fail(PyExc_TypeError, "scale must be uint8 or the format's scale type");
     if (q.dim() != 2 || cols < 0 || q.size(1) != (cols + 1) / 2)
       fail(PyExc_ValueError, "data must be (rows, ceil(cols / 2))");
     rows = q.size(0);
     if (s.dim() != 1 || s.size(0) != scale_bytes4(rows, cols, kind) || !s.is_contiguous())
       fail(PyExc_ValueError, "scale must be flat and contiguous, of the format's size");
-    on_device(q, device);
-    on_device(s, device);
+    on(q, device);
+    on(s, device < 0 ? place(q) : device);
     // a lone row needs no pitch
     const int64_t pitch = pitch_of(q, "rows of data must be contiguous and not overlap");
     m = gemm_fp4_matrix_t{q.data_ptr(), rows > 1 ? pitch : (q.size(1) + 15) & ~int64_t(15),
                           s.data_ptr(), nullptr, 0, int32_t(kind), 0};
     if (row_scale != Py_None) {
       const at::Tensor& r = tensor(row_scale, "row_scale must be a tensor or None");
-      if (r.scalar_type() != at::kFloat || r.dim() != 1 || r.size(0) != rows)
-        fail(PyExc_ValueError, "row_scale must be float32 of shape (rows,)");
-      on_device(r, device);
+      if (r.scalar_type() != at::kFloat) fail(PyExc_TypeError, "row_scale must be float32");
+      if (r.dim() != 1 || r.size(0) != rows)
+        fail(PyExc_ValueError, "row_scale must have shape (rows,)");
+      on(r, device < 0 ? place(q) : device);
       m.row_scale = static_cast<float*>(r.data_ptr());
       m.row_scale_stride = r.stride(0);
     }
   }
+
+ private:
+  static constexpr int64_t kHost = -2;
+  static int64_t place(const at::Tensor& t) { return t.is_cuda() ? t.get_device() : kHost; }
+  static void on(const at::Tensor& t, int64_t device) {
+    if (device == kHost) {
+      if (t.is_cuda()) fail(PyExc_ValueError, "the scales are on another device than data");
+    } else if (device >= 0) {
+      on_device(t, device);
+    }
+  }
 };
+
+// check4(data, scale, row_scale or None, rows, cols, kind): refuses what is no 4-bit matrix.
+PyObject* check4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 6) fail(PyExc_TypeError, "check4 takes 6 arguments");
+    const Given4 q(args[0], args[1], args[2], integer(args[4]), integer(args[5]), -1);
+    if (q.rows != integer(args[3])) fail(PyExc_ValueError, "data must be (rows, ceil(cols / 2))");
+    Py_RETURN_NONE;
+  });
+}
 
 const float* bias_of(PyObject* o, int64_t N, int64_t device) {
   if (o == Py_None) return nullptr;
@@ -633,6 +660,7 @@ PyMethodDef methods[] = {
     {"matmul", reinterpret_cast<PyCFunction>(matmul), METH_FASTCALL, nullptr},
     {"run", reinterpret_cast<PyCFunction>(run), METH_FASTCALL, nullptr},
     {"moe", reinterpret_cast<PyCFunction>(moe), METH_FASTCALL, nullptr},
+    {"check4", reinterpret_cast<PyCFunction>(check4), METH_FASTCALL, nullptr},
     {"quantize4", reinterpret_cast<PyCFunction>(quantize4), METH_FASTCALL, nullptr},
     {"dequantize4", reinterpret_cast<PyCFunction>(dequantize4), METH_FASTCALL, nullptr},
     {"matmul4", reinterpret_cast<PyCFunction>(matmul4), METH_FASTCALL, nullptr},

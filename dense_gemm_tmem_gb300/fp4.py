@@ -49,6 +49,33 @@ def unpack_scales(scale: torch.Tensor, rows: int, blocks: int) -> torch.Tensor:
     return s.permute(0, 3, 2, 1, 4).reshape(-(-rows // 128) * 128, -1)[:rows, :blocks]
 
 
+def _check(data, scale, row_scale, rows, cols, format):
+    """Refuses what is no 4-bit matrix."""
+    if data.dtype not in _BYTES:
+        raise TypeError("data must be uint8 (or float4_e2m1fn_x2), got %s" % data.dtype)
+    if scale.dtype not in _SCALES[format]:
+        raise TypeError("scale must be uint8 or the format's scale type, got %s" % scale.dtype)
+    if rows < 0 or cols < 0 or data.shape != (rows, (cols + 1) // 2):
+        raise ValueError("data has shape %s, expected (%d, %d)"
+                         % (tuple(data.shape), rows, (cols + 1) // 2))
+    st = data.stride()
+    if (data.shape[1] > 1 and st[1] != 1) or (rows > 1 and st[0] < data.shape[1]):
+        raise ValueError("rows of data must be contiguous and not overlap")
+    if scale.dim() != 1 or scale.shape[0] != scale_bytes(rows, cols, format) or (
+            scale.shape[0] > 1 and scale.stride(0) != 1):
+        raise ValueError("scale must be contiguous and flat, of %d bytes"
+                         % scale_bytes(rows, cols, format))
+    if row_scale is not None:
+        if row_scale.dtype != torch.float32:
+            raise TypeError("row_scale must be float32, got %s" % row_scale.dtype)
+        if row_scale.shape != (rows,):
+            raise ValueError("row_scale has shape %s, expected (%d,)"
+                             % (tuple(row_scale.shape), rows))
+    for t in (scale, row_scale):
+        if t is not None and t.get_device() != data.get_device():
+            raise ValueError("data on %s, scales on %s" % (data.device, t.device))
+
+
 class Fp4Matrix:
     """A (rows, cols) matrix in 4 bits.  ``data`` (rows, ceil(cols / 2)) has the even
     column in the low half of each byte, unit stride along its rows, which start on
@@ -61,32 +88,15 @@ class Fp4Matrix:
     __slots__ = ("data", "scale", "row_scale", "shape", "format", "kind")
 
     def __init__(self, data: torch.Tensor, scale: torch.Tensor, row_scale, shape, format: str):
-        kind = _format(format)
-        if data.dtype not in _BYTES:
-            raise TypeError("data must be uint8, got %s" % data.dtype)
-        if scale.dtype not in _SCALES[format]:
-            raise TypeError("scale must be uint8 or the format's scale type, got %s"
-                            % scale.dtype)
-        rows, cols = (int(n) for n in shape)
-        if rows < 0 or cols < 0 or data.shape != (rows, (cols + 1) // 2):
-            raise ValueError("data has shape %s, expected (%d, %d)"
-                             % (tuple(data.shape), rows, (cols + 1) // 2))
-        st = data.stride()
-        if (data.shape[1] > 1 and st[1] != 1) or (rows > 1 and st[0] < data.shape[1]):
-            raise ValueError("rows of data must be contiguous and not overlap")
-        if scale.dim() != 1 or scale.shape[0] != scale_bytes(rows, cols, format) or (
-                scale.shape[0] > 1 and scale.stride(0) != 1):
-            raise ValueError("scale must be contiguous and flat, of %d bytes"
-                             % scale_bytes(rows, cols, format))
-        if row_scale is not None:
-            if row_scale.dtype != torch.float32:
-                raise TypeError("row_scale must be float32, got %s" % row_scale.dtype)
-            if row_scale.shape != (rows,):
-                raise ValueError("row_scale has shape %s, expected (%d,)"
-                                 % (tuple(row_scale.shape), rows))
-        for t in (scale, row_scale):
-            if t is not None and t.get_device() != data.get_device():
-                raise ValueError("data on %s, scales on %s" % (data.device, t.device))
+        rows, cols = shape
+        kind = FORMATS.get(format)
+        if kind is None:
+            _format(format)
+        # the extension's checks where it is loaded (0.5 us of a decode step's time, not 2)
+        if B._native is not None:
+            B._native.check4(data, scale, row_scale, rows, cols, kind)
+        else:
+            _check(data, scale, row_scale, rows, cols, format)
         self.data, self.scale, self.row_scale = data, scale, row_scale
         self.shape, self.format, self.kind = (rows, cols), format, kind
 

@@ -157,7 +157,10 @@ def test_from_parts(fmt, rows, cols):
         assert torch.equal(again.data, m.data)
 
 
-def test_matrix_refusals():
+@pytest.mark.parametrize("loaded", [False, True])
+def test_matrix_refusals(monkeypatch, loaded):
+    """The same refusals with the extension's checks and without the extension."""
+    monkeypatch.setattr(B, "_native", B.native() if loaded else None)
     data = torch.zeros(4, 32, dtype=torch.uint8)
     scale = torch.zeros(512, dtype=torch.uint8)
     rs = torch.ones(4)

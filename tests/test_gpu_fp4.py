@@ -91,7 +91,8 @@ def test_quantize_values_at_the_ends(g, dtype, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("offset,pitch", [(1, 401), (8, 408), (0, 403), (3, 440)])
+@pytest.mark.parametrize("offset,pitch", [(1, 401), (8, 408), (0, 403), (3, 440), (5, 390),
+                                          (6, 396), (7, 391)])
 def test_quantize_strided_rows(g, dtype, fmt, offset, pitch):
     rng = np.random.default_rng(offset)
     buf = make(rng, 37, 450).to(dtype).cuda().reshape(-1)
@@ -135,6 +136,24 @@ def test_dequantize(g, rows, cols, dtype, fmt):
     tol = np.abs(want) * (2.0 ** -24 + torch.finfo(dtype).eps / 2) + \
         torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
     assert np.all(np.abs(host(got) - want) <= tol)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("cols,pitch,offset", [(37, 37, 0), (200, 201, 1), (300, 303, 5),
+                                               (64, 72, 3), (9, 11, 7), (2100, 2101, 2)])
+def test_dequantize_into_strided_rows(g, dtype, fmt, cols, pitch, offset):
+    """Rows that start anywhere, and nothing written beside them."""
+    rows = 13
+    m = g.fp4_quantize(torch.randn(rows, cols, device="cuda"), fmt)
+    buf = torch.full((rows * pitch + offset + 9,), 7.0, dtype=dtype, device="cuda")
+    out = torch.as_strided(buf, (rows, cols), (pitch, 1), offset)
+    code = B.GEMM_F32 if dtype == F32 else B.GEMM_F16
+    assert B.gemm_fp4_dequantize(g.handle, rows, cols, m.desc(), out.data_ptr(), pitch, code,
+                                 torch.cuda.current_stream().cuda_stream) == B.GEMM_OK
+    assert torch.equal(out, g.fp4_dequantize(m, dtype))
+    out.fill_(7.0)
+    assert bool((buf == 7.0).all())
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
