@@ -83,8 +83,8 @@ struct OrTcArgs {
   OrthoStep step[GEMM_ORTHO_MAX_STEPS];
 };
 
-// An operand's maps: K-major in boxes of 128 rows (the MMA's A) and of OrConfig's kBRows
-// (its B), two k-blocks each, and MN-major in boxes of 64 by 128 of K.
+// An operand's maps: boxes of 128 rows (the MMA's A) and of OrConfig's kBRows (its B) by two
+// blocks of 64 columns, and of 128 rows by one.
 struct OrOperand {
   CUtensorMap ka, kb, mn;
 };
@@ -157,9 +157,9 @@ __device__ __forceinline__ int or_majors(const OrTcArgs& a, const OrTile& o, int
   if (o.kind == kPoly) return i | (j << 1);
   return a.tall ? j << 1 : i | 2;
 }
-__device__ __forceinline__ uint32_t ld_relaxed_gpu(const uint32_t* p) {
+__device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t* p) {
   uint32_t v;
-  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 __device__ __forceinline__ void red_release_gpu(uint32_t* p) {
@@ -197,7 +197,7 @@ __device__ __forceinline__ bool or_block_done(const OrTcArgs& a, const uint32_t*
   const uint32_t* c = counters + or_index<Cfg>(a, kPoly, max(i, p), R * min(i, p));
   bool have = true;
 #pragma unroll
-  for (int r = 0; r < R; ++r) have &= ld_relaxed_gpu(c + r) >= kFull;
+  for (int r = 0; r < R; ++r) have &= ld_acquire_gpu(c + r) >= kFull;
   return have;
 }
 // Whether X's tiles in row tm, or R of them from column R j on (those there are), are.
@@ -207,7 +207,7 @@ __device__ __forceinline__ bool or_x_done(const OrTcArgs& a, const uint32_t* cou
   constexpr uint32_t kFull = kOrEpiWarps * (Cfg::kPair ? 2 : 1);
   bool have = true;
   for (int r = 0; r < count; ++r)
-    have &= ld_relaxed_gpu(counters + or_index<Cfg>(a, kApply, tm, tn + r)) >= kFull;
+    have &= ld_acquire_gpu(counters + or_index<Cfg>(a, kApply, tm, tn + r)) >= kFull;
   return have;
 }
 
@@ -258,8 +258,8 @@ __device__ __forceinline__ void or_watch(const OrTcArgs& args, volatile uint32_t
         const int32_t now = all == 0xffffffffu ? count : min(count, __ffs(~all) - 1);
         if (now > seen) {
           seen = now;
-          __threadfence();  // what the counters stand for is visible from here on
-          __syncwarp();
+          __syncwarp();  // every lane's acquire before the count is published
+          __threadfence_block();
           if (lane == 0) *ready = passed + uint32_t(seen);
           t0 = 0;
         } else if (t0 == 0) {
@@ -326,28 +326,24 @@ __device__ __forceinline__ uint32_t or_producer(const OrMaps& maps, const OrTcAr
       if (!wait_bounded(smem_u32(&empty[s]), ph ^ 1, wc, kSiteProducer)) return filled;
       const uint32_t own = smem_u32(&full[s]);
       if (rank == 0) mbar_arrive_expect_tx(own, (Cfg::kPair ? 2 : 1) * Cfg::kStageBytes);
-      // K-major: the rows' two k-blocks; MN-major: boxes 64 wide and 128 of K deep
-      auto load4 = [&](uint32_t dst, const CUtensorMap* map, int32_t row) {
-        if constexpr (Cfg::kPair) tma_load_4d_pair(dst, map, map_to_rank(own, 0), 0, row, kb, o.z);
-        else tma_load_4d(dst, map, own, 0, row, kb, o.z);
+      // K-major: 128 (or kBRows) rows of two k-blocks; MN-major: two blocks of 64 columns,
+      // 128 rows of K deep, which is the same box, or one block where kBRows is 64
+      auto load4 = [&](uint32_t dst, const CUtensorMap* map, int32_t row, int32_t block) {
+        if constexpr (Cfg::kPair)
+          tma_load_4d_pair(dst, map, map_to_rank(own, 0), 0, row, block, o.z);
+        else
+          tma_load_4d(dst, map, own, 0, row, block, o.z);
       };
       auto load3 = [&](uint32_t dst, const CUtensorMap* map, int32_t row) {
         if constexpr (Cfg::kPair) tma_load_3d_pair(dst, map, map_to_rank(own, 0), row, kb * kBK, o.z);
         else tma_load_3d(dst, map, own, row, kb * kBK, o.z);
       };
       const uint32_t a_dst = ring + uint32_t(s) * Cfg::kStageBytes, b_dst = a_dst + Cfg::kABytes;
-      if (majors & 1) {
-        load3(a_dst, &mA.mn, a_row);
-        load3(a_dst + kOrGroup * 8192, &mA.mn, a_row + 64);
-      } else {
-        load4(a_dst, &mA.ka, a_row);
-      }
-      if (majors & 2) {
-        load3(b_dst, &mB.mn, b_row);
-        if (Cfg::kBRows > 64) load3(b_dst + kOrGroup * 8192, &mB.mn, b_row + 64);
-      } else {
-        load4(b_dst, &mB.kb, b_row);
-      }
+      if (majors & 1) load4(a_dst, &mA.ka, kb * kBK, a_row / 64);
+      else load4(a_dst, &mA.ka, a_row, kb);
+      if (!(majors & 2)) load4(b_dst, &mB.kb, b_row, kb);
+      else if (Cfg::kBRows > 64) load4(b_dst, &mB.kb, kb * kBK, b_row / 64);
+      else load3(b_dst, &mB.mn, b_row);
       ++filled;
       if (++s == Cfg::kStages) {
         s = 0;
@@ -698,8 +694,8 @@ __global__ void __launch_bounds__(kOrThreads, 1)
     *peer_filled = 0;
     *ready = 0;
     fence_barrier_init();
-    tma_prefetch_map(args.tall ? &maps.x[0].mn : &maps.x[0].ka);
-    tma_prefetch_map(args.tall ? &maps.x[0].mn : &maps.x[0].kb);
+    tma_prefetch_map(&maps.x[0].ka);
+    tma_prefetch_map(args.tall && Cfg::kBRows == 64 ? &maps.x[0].mn : &maps.x[0].kb);
   }
   if (warp == 1) {
     if constexpr (Cfg::kPair) {
