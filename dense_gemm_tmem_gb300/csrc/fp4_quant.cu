@@ -10,7 +10,10 @@
 // too long for that are read twice.  What is left to keep short is the instruction
 // count: 16-bit elements stay packed and maxima are taken of magnitudes as integers
 // (which order like the numbers), and a row's division by its blocks' scales, which
-// have 8 different mantissas, is made once for each of those.
+// have 8 different mantissas, is made once for each of those (8192^2 bf16 nvfp4 54 us
+// before, 34 now, 5.1 TB/s; mxfp4, which waits for no row, 31).
+// Reading back is bound by its stores: 8192^2 bf16 40 us, where filling as many bytes
+// takes 35.5; streaming stores, 2 or 8 rows a thread instead of 4: 41 to 44.
 #include <type_traits>
 
 #include "fp4.cuh"

@@ -82,11 +82,7 @@ cudaError_t launch_inst(const Fp4Maps& maps, const CUtensorMap& mC, const Fp4TcA
 
 template <int FMT, class Launch>
 cudaError_t launch_format(int bn, bool trans, bool out32, Launch&& launch) {
-  if (trans) {
-    if (bn == 32) return launch(launch_inst<32, false, true, FMT, false>);
-    if (bn == 64) return launch(launch_inst<64, false, true, FMT, false>);
-    return launch(launch_inst<128, false, true, FMT, false>);
-  }
+  if (trans) return launch(launch_inst<32, false, true, FMT, false>);  // stores any type
   if (bn == 256)
     return out32 ? launch(launch_inst<256, true, false, FMT, true>)
                  : launch(launch_inst<256, true, false, FMT, false>);
@@ -113,8 +109,12 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
     return cudaGetLastError();
   }
   // Few rows of A: operands swapped, so that the other side fills the 128 MMA rows and
-  // A's rows are the MMA's columns, 32, 64 or 128 of them.
-  const bool trans = p.M <= 128 && p.N > p.M;
+  // A's rows are the MMA's columns, 32 of them.  Measured (mxfp4, graph replay, cold
+  // inputs, us, swapped / not), N x K 4096 x 4096: 6.4 / 8.1 for 8 rows, 6.7 / 7.7 for 32,
+  // 7.2 / 7.8 for 48, 7.3 / 7.1 for 64; 8192 x 1024: 4.4 / 4.9, 4.8 / 4.8, 5.5 / 4.7.
+  constexpr int64_t kSwapRows = 32;
+  const int swap = h->opt.force_swap;  // GEMM_OPT_FORCE_SWAP_AB
+  const bool trans = swap != 0 && p.M <= kSwapRows && (swap == 1 || p.N > p.M);
   const gemm_fp4_matrix_t& opA = trans ? p.B : p.A;
   const gemm_fp4_matrix_t& opB = trans ? p.A : p.B;
   const int64_t Mm = trans ? p.N : p.M, Nm = trans ? p.M : p.N;
@@ -123,7 +123,11 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   const int64_t pairs = h->opt.pair_clusters > 0 ? h->opt.pair_clusters : sms / 2;
   // Fewer tiles than half the SMs: each tile's k-blocks over a cluster, the largest
   // whose clusters are all resident at once, if that takes more than kSplitGain
-  // k-blocks off each CTA.
+  // k-blocks off each CTA (adding the partials costs about as long).  Measured (nvfp4, us,
+  // split / whole): 1 x 4096 x 4096 6.4 / 7.6, 1 x 1024 x 8192 5.6 / 11.8, 256 x 1024 x
+  // 4096 7.0 / 7.7, 512 x 512 x 8192 8.0 / 12.0, 16 x 512 x 2048 4.6 / 5.0; not taken: 32 x
+  // 2048 x 1024 4.7 / 4.1, 300 x 700 x 1024 5.5 / 4.6; more CTAs than SMs: 64 x 8192 x
+  // 8192 by 4 18.3, by 2, which fit, 12.4, whole 14.4.
   constexpr int64_t kSplitGain = 4;
   const int forced = h->opt.csplit;  // GEMM_OPT_CLUSTER_SPLIT
   auto split_of = [&](int64_t T) -> int64_t {
@@ -138,13 +142,24 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   };
   int64_t tiles_m = ceil_div(Mm, kBM);
   int bn;
+  // Tiles of 256 x 256 of a pair where there are more than 5/4 of them for each pair and K
+  // is deep enough for what the pair loses between tiles, its one accumulator being read
+  // out (1.2 us): nvfp4, us, 256 / 128: 4096^3 37.4 / 39.5, 8192^3 182 / 253, 4096 x 2048 x
+  // 8192 32 / 41, 6000 x 6000 x 2000 55 / 60, but 2048^3 12.2 / 9.4, 1024 x 4096 x 4096 15.1
+  // / 14.0, 4096 x 4096 x 1024 22.5 / 19.2, 8192 x 8192 x 1024 64 / 58.  Tiles of 64 columns
+  // instead of 128 where both leave half of the SMs idle: 515 x 1000 x 2056 6.4 / 7.6, 1024^3
+  // 4.6 / 5.3, but 1001 x 2050 x 4100 14.7 / 12.0, 1536 x 1536 x 1024 6.2 / 5.3.
+  constexpr int64_t kPairDepth = 8;  // k-blocks
+  const int tile_n = h->opt.force_tile_n;  // GEMM_OPT_FORCE_TILE_N: 64, 128 or 256 (pairs)
+  const int64_t wide = ceil_div(Mm, 256) * ceil_div(Nm, 256);
   if (trans) {
-    bn = Nm <= 32 ? 32 : Nm <= 64 ? 64 : 128;
-  } else if (ceil_div(Mm, 256) * ceil_div(Nm, 256) >= pairs / 2) {
+    bn = 32;
+  } else if (tile_n > 0 ? tile_n >= 256 : 4 * wide >= 5 * pairs && I >= kPairDepth) {
     bn = 256;
     tiles_m = ceil_div(Mm, 256);
   } else {
-    bn = 2 * tiles_m * ceil_div(Nm, 128) <= sms ? 64 : 128;
+    const bool narrow = tile_n > 0 ? tile_n <= 64 : 2 * tiles_m * ceil_div(Nm, 128) <= sms;
+    bn = narrow ? 64 : 128;
   }
   const int64_t tiles_n = ceil_div(Nm, bn), T = tiles_m * tiles_n;
   if (T > INT32_MAX / 2) return cudaErrorInvalidValue;

@@ -17,6 +17,23 @@
 //                      registers, the buffer goes back, row scales, bias, store.
 // PAIR: two CTAs on two SMs own a 256 x 256 tile (cta_group::2), each with its 128
 // rows of A and half of B's rows, both with all of B's scales.
+//
+// What bounds it, 8192^3 nvfp4 in 182 us (6.0 PFLOP/s; mxfp4 172, 6.4): a k-block's MMAs
+// take 512 cycles, a tile's 32 of them 16400 of the 22900 that it takes.  1750 are copies
+// of scales (mxfp4 half of that), 2250 pass between two tiles, because 512 columns of
+// TMEM hold one accumulator and the scales (its 256 columns are read in 1550), and some
+// 4000 are waits for loads, whose latency of 2500 cycles under load five stages do not
+// cover.  Left out in copies made for the purpose: A's and B's loads 169 us, the scales'
+// 177, the stores 166.  Measured and dropped: tiles of 192 columns with two accumulators
+// (mxfp4 178 against 173; in nvfp4 TMEM then holds two k-blocks' scales, 223), the scales
+// copied a k-block ahead (226 and 321), one more thread to send for the scales' loads
+// (188 against 184), polling instead of suspended waits (191), all of the accumulator's
+// reads in flight together (no change), 128 columns (230).
+// tcgen05.mma reads scales from even TMEM columns only: tiles start at multiples of 64
+// rows of B (160-wide ones, whose scales start at odd columns, fault).
+// Small products are bound by latency: launch, first loads, the cluster's exchange.  A
+// matrix-vector kernel of its own was not tried: 1 x 4096 x 4096 takes 6.4 us, of which
+// 1.4 would be its bytes.
 #pragma once
 
 #include "fp4.cuh"
@@ -51,7 +68,7 @@ struct Fp4TcConfig {
   static constexpr int kAccCols = BN * kBuffers;
   static constexpr int kUsedCols = kAccCols + kStages * (kSaCols + kSbCols);
   static constexpr int kTmemCols = kUsedCols <= 256 ? 256 : 512;
-  static_assert(kUsedCols <= 512, "TMEM columns");
+  static_assert(kUsedCols <= 512 && (BN % 64 == 0 || BN == 32), "TMEM columns");
   static constexpr int kHalf = BN / 2;
   static constexpr int kWarpStage = BN == 256 ? 4096 : 32 * 20 * 4;  // a store box, or staged rows
   static constexpr int kEpiBytes = kF4EpiWarps * kWarpStage;

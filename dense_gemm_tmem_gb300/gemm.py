@@ -267,7 +267,7 @@ class Gemm:
                              _current_raw(self.device.index))
         if r.__class__ is int:
             raise B.GemmError(r, "gemm_fp4_quantize")
-        return Fp4Matrix._wrap(r[0], r[1], r[2], tuple(x.shape), format)
+        return Fp4Matrix._wrap(r[0], r[1], r[2], x.shape, format)
 
     def fp4_dequantize(self, m: Fp4Matrix, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """The values an Fp4Matrix stands for, as a new (rows, cols) tensor."""

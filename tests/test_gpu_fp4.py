@@ -230,13 +230,36 @@ def test_product(g, M, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("M,N,K", [(2048, 2304, 576), (1600, 4000, 320)])
+@pytest.mark.parametrize("M,N,K", [(2048, 2304, 576), (1600, 4000, 320), (2560, 2816, 2100)])
 def test_product_of_many_tiles(g, M, N, K, fmt):
     """Several tiles a CTA; a sample of rows against doubles."""
     rng = np.random.default_rng(M)
     A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
     Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
     check_product(g.fp4_matmul(A, Bm, out_dtype=F16), A, Bm)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("swap,tile,split", [(1, -1, 0), (1, -1, 4), (0, 64, 0), (0, 64, 2), (0, 64, 8),
+                                             (0, 128, 0), (0, 128, 4), (0, 256, -1)])
+@pytest.mark.parametrize("M,N,K", [(1, 130, 2100), (32, 300, 2304), (20, 64, 70), (300, 450, 2500)])
+def test_every_tile_on_every_shape(g, M, N, K, swap, tile, split, fmt):
+    """What the rule takes elsewhere, forced: swapped operands, tile widths, CTA pairs, splits."""
+    rng = np.random.default_rng(M)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    bias = torch.from_numpy(rng.standard_normal(N)).float().cuda()
+    forced = {B.GEMM_OPT_FORCE_SWAP_AB: swap, B.GEMM_OPT_FORCE_TILE_N: tile,
+              B.GEMM_OPT_CLUSTER_SPLIT: split}
+    try:
+        for o, v in forced.items():
+            g.set_option(o, v)
+        for dtype in (F32, BF16):
+            check_product(g.fp4_matmul(A, Bm, bias, out_dtype=dtype), A, Bm, bias)
+        g.status()
+    finally:
+        for o in forced:
+            g.set_option(o, -1)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

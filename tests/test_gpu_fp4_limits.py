@@ -20,11 +20,16 @@ def h():
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (300, 700, 2048), (2048, 2048, 2048),
-                                   (4096, 4096, 1024)])
-def test_product_under_short_limits(h, M, N, K, fmt):
+@pytest.mark.parametrize("M,N,K,tile", [(1, 4096, 4096, -1), (300, 700, 2048, -1),
+                                        (2048, 2048, 2048, -1), (1024, 2048, 2048, 256),
+                                        (4096, 4096, 1024, 256)])
+def test_product_under_short_limits(h, M, N, K, tile, fmt):
     """Split over clusters, whole tiles of one CTA, and of CTA pairs, one and several each."""
     torch.manual_seed(M)
     a = h.fp4_quantize(torch.randn(M, K, device="cuda"), fmt)
     b = h.fp4_quantize(torch.randn(N, K, device="cuda"), fmt)
-    limited(h, lambda: [h.fp4_matmul(a, b)], [1, 300, 1000, 3000, 10000, 30000])
+    h.set_option(B.GEMM_OPT_FORCE_TILE_N, tile)
+    try:
+        limited(h, lambda: [h.fp4_matmul(a, b)], [1, 300, 1000, 3000, 10000, 30000])
+    finally:
+        h.set_option(B.GEMM_OPT_FORCE_TILE_N, -1)
