@@ -133,7 +133,8 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   auto split_of = [&](int64_t T) -> int64_t {
     if (forced < 2 && (forced >= 0 || 2 * T >= sms)) return 1;
     for (int s : {8, 4, 2}) {
-      if (forced >= 2 ? s == forced && I >= s && T * s <= INT32_MAX
+      if (I < s) continue;  // a CTA without a k-block has no partial to add
+      if (forced >= 2 ? s == forced && T * s <= INT32_MAX
                       : T <= h->opt.csplit_clusters[s] && T * s <= sms &&
                             I - ceil_div(I, s) > kSplitGain)
         return s;

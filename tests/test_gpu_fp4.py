@@ -263,6 +263,45 @@ def test_every_tile_on_every_shape(g, M, N, K, swap, tile, split, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K", [257, 1281, 1400, 1537, 1790, 2049])
+@pytest.mark.parametrize("M,N", [(1, 300), (3, 64), (70, 200)])
+def test_few_tiles_over_few_k_blocks(g, M, N, K, fmt):
+    """Fewer k-blocks than CTAs that a tile might be split over."""
+    rng = np.random.default_rng(K)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    for _ in range(3):
+        check_product(g.fp4_matmul(A, Bm, out_dtype=F32), A, Bm)
+    g.status()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K", [(7, 100), (130, 1000), (700, 516)])
+def test_a_matrix_by_itself(g, M, K, fmt):
+    rng = np.random.default_rng(M)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    check_product(g.fp4_matmul(A, A, out_dtype=F32), A, A)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_without_programmatic_launches(g, fmt):
+    """GEMM_OPT_PDL changes when kernels start, and nothing else."""
+    rng = np.random.default_rng(11)
+    x = make(rng, 33, 520).cuda().float()
+    w = g.fp4_quantize(make(rng, 300, 520).cuda().float(), fmt)
+    def run():
+        q = g.fp4_quantize(x, fmt)
+        return q.data, q.scale, g.fp4_linear(x, w), g.fp4_dequantize(q)
+    want = run()
+    g.set_option(B.GEMM_OPT_PDL, 0)
+    try:
+        got = run()
+    finally:
+        g.set_option(B.GEMM_OPT_PDL, -1)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N,K", [(1, 300, 200), (200, 300, 520), (700, 1024, 256)])
 def test_product_into_strided_rows(g, M, N, K, fmt):
     rng = np.random.default_rng(K)
