@@ -21,19 +21,8 @@ __host__ __device__ __forceinline__ int64_t fp4_scale_at(int64_t r, int64_t b, i
   return ((r >> 7) * pieces + (b >> 2)) * kFp4Piece + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
-// Two floats to e2m1, round to nearest even, saturating, `a` in the low half of
-// the byte (the other bytes of the result are 0).
-__device__ __forceinline__ uint32_t pack_e2m1x2(float a, float b) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 p, z;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 p, %1, %2;\n\t"
-      "cvt.u8.u32 z, 0;\n\t"
-      "mov.b32 %0, {p, z, z, z};\n\t}"
-      : "=r"(r)
-      : "f"(b), "f"(a));
-  return r;
-}
-// Eight floats to a word, the first in the lowest bits.
+// Eight floats to e2m1, round to nearest even, saturating, the first in the word's
+// lowest bits.
 __device__ __forceinline__ uint32_t pack_e2m1x8(const float* v) {
   uint32_t r;
   asm("{\n\t.reg .b8 p, q, s, t;\n\t"
@@ -76,7 +65,8 @@ struct Fp4Product {
 };
 
 cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int64_t ld_src,
-                                int src_dtype, const gemm_fp4_matrix_t& out, cudaStream_t stream);
+                                int src_dtype, const gemm_fp4_matrix_t& out, bool pdl,
+                                cudaStream_t stream);
 cudaError_t launch_fp4_dequantize(int64_t rows, int64_t cols, const gemm_fp4_matrix_t& m,
                                   void* dst, int64_t ld_dst, int dst_dtype, cudaStream_t stream);
 cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream);

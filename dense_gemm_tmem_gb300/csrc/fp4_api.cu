@@ -46,7 +46,7 @@ int gemm_fp4_quantize(gemm_handle_t h, int64_t rows, int64_t cols, const void* s
   if (!src) return GEMM_ERR_INVALID_ARG;
   return dg::on_device(h->device, [&]() -> int {
     return dg::done(dg::launch_fp4_quantize(rows, cols, src, ld_src, src_dtype, *out,
-                                            static_cast<cudaStream_t>(stream)));
+                                            h->opt.pdl != 0, static_cast<cudaStream_t>(stream)));
   });
 }
 

@@ -147,7 +147,7 @@ struct QuantArgs {
   Span span;
   gemm_fp4_matrix_t out;
   int64_t pieces;
-  bool early;  // the next kernel may start beside this one
+  bool early;  // the next kernel may start beside this one (GEMM_OPT_PDL)
 };
 
 // CTAs an SM that the registers are cut for.
@@ -288,7 +288,7 @@ cudaError_t launch_format(QuantArgs a, cudaStream_t s) {
   // the row, 4 at most
   const bool warps = units <= 2 * 32;
   const int64_t grid = warps ? rows / kPer : rows;
-  a.early = grid <= kEarlyCtas;
+  a.early = a.early && grid <= kEarlyCtas;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -461,12 +461,12 @@ int64_t pieces_of(int64_t cols, int format) {
 }  // namespace
 
 cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int64_t ld_src,
-                                int src_dtype, const gemm_fp4_matrix_t& out,
+                                int src_dtype, const gemm_fp4_matrix_t& out, bool pdl,
                                 cudaStream_t stream) {
   const int64_t size = src_dtype == GEMM_F32 ? 4 : 2;
   const uint8_t* const begin = static_cast<const uint8_t*>(src);
   const Span span{begin, begin + ((rows - 1) * ld_src + cols) * size};
-  const QuantArgs a{src, rows, cols, ld_src, span, out, pieces_of(cols, out.format), false};
+  const QuantArgs a{src, rows, cols, ld_src, span, out, pieces_of(cols, out.format), pdl};
   if (src_dtype == GEMM_F32) return launch_typed<float>(a, stream);
   if (src_dtype == GEMM_F16) return launch_typed<__half>(a, stream);
   return launch_typed<__nv_bfloat16>(a, stream);
