@@ -12,9 +12,16 @@ int check_matrix(const gemm_fp4_matrix_t* m, int64_t rows, int64_t cols) {
   if (!m || bad_format(m->format) || m->ld < (cols + 1) / 2) return GEMM_ERR_INVALID_ARG;
   if (rows > 0 && cols > 0 && (!m->data || !m->scale)) return GEMM_ERR_INVALID_ARG;
   if (rows >= kMaxCoord || cols >= kMaxCoord || m->ld >= (int64_t(1) << 40) || m->ld % 16 != 0 ||
-      ((reinterpret_cast<uintptr_t>(m->data) | reinterpret_cast<uintptr_t>(m->scale)) & 15))
+      ((reinterpret_cast<uintptr_t>(m->data) | reinterpret_cast<uintptr_t>(m->scale)) & 15) ||
+      reinterpret_cast<uintptr_t>(m->row_scale) % 4 != 0)
     return GEMM_ERR_UNSUPPORTED;
   return GEMM_OK;
+}
+
+// Elements of `type` that do not start on a multiple of their size, which no load or store
+// may touch.
+bool misaligned(const void* p, int type) {
+  return reinterpret_cast<uintptr_t>(p) % (type == GEMM_F32 ? 4 : 2) != 0;
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA; }
@@ -44,6 +51,7 @@ int gemm_fp4_quantize(gemm_handle_t h, int64_t rows, int64_t cols, const void* s
     return GEMM_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return GEMM_OK;
   if (!src) return GEMM_ERR_INVALID_ARG;
+  if (dg::misaligned(src, src_dtype)) return GEMM_ERR_UNSUPPORTED;
   return dg::on_device(h->device, [&]() -> int {
     return dg::done(dg::launch_fp4_quantize(rows, cols, src, ld_src, src_dtype, *out,
                                             h->opt.pdl != 0, static_cast<cudaStream_t>(stream)));
@@ -58,6 +66,7 @@ int gemm_fp4_dequantize(gemm_handle_t h, int64_t rows, int64_t cols, const gemm_
   if (rc != GEMM_OK) return rc;
   if (rows == 0 || cols == 0) return GEMM_OK;
   if (!dst) return GEMM_ERR_INVALID_ARG;
+  if (dg::misaligned(dst, dst_dtype)) return GEMM_ERR_UNSUPPORTED;
   return dg::on_device(h->device, [&]() -> int {
     return dg::done(dg::launch_fp4_dequantize(rows, cols, *m, dst, ld_dst, dst_dtype,
                                               static_cast<cudaStream_t>(stream)));
@@ -76,6 +85,7 @@ int gemm_fp4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp
   if (A->format != B->format) return GEMM_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return GEMM_OK;
   if (!C) return GEMM_ERR_INVALID_ARG;
+  if (dg::misaligned(C, out_dtype) || dg::misaligned(bias, GEMM_F32)) return GEMM_ERR_UNSUPPORTED;
   const dg::Fp4Product p{M, N, K, *A, *B, bias, C, ldc, out_dtype};
   return dg::on_device(h->device, [&]() -> int {
     return dg::done(dg::launch_fp4(h, p, static_cast<cudaStream_t>(stream)));

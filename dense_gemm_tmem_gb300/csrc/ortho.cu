@@ -462,6 +462,9 @@ int gemm_orthogonalize(gemm_handle_t h, const gemm_orthogonalize_t* p, void* wor
   dg::Plan plan;
   if ((rc = dg::plan_scales(*p, &plan)) != GEMM_OK) return rc;
   if (p->batch == 0 || p->rows == 0 || p->cols == 0) return GEMM_OK;
+  if ((reinterpret_cast<uintptr_t>(p->g) % (p->dtype == GEMM_F32 ? 4 : 2)) != 0 ||
+      reinterpret_cast<uintptr_t>(p->out) % 2 != 0)
+    return GEMM_ERR_UNSUPPORTED;
   if (!p->g || !p->out || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
       workspace_bytes < dg::space_of(dg::shape_of(*p), p->steps).total)
     return GEMM_ERR_INVALID_ARG;

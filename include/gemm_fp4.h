@@ -65,8 +65,9 @@ int64_t gemm_fp4_scale_bytes(int64_t rows, int64_t cols, int format);
  * rows == 0 or cols == 0: nothing is launched.
  * Errors: INVALID_ARG (negative size, ld_src < cols, ld < ceil(cols / 2), NULL
  * pointer of a non-empty matrix, a row scale that the format does not have or
- * lacks, unknown enum), UNSUPPORTED (misaligned data, scale or ld; rows or cols
- * of 2^31 - 1024 or more), CUDA. */
+ * lacks, unknown enum), UNSUPPORTED (misaligned data, scale or ld; src or
+ * row_scale not on a multiple of its elements' size; rows or cols of 2^31 -
+ * 1024 or more), CUDA. */
 int gemm_fp4_quantize(gemm_handle_t h, int64_t rows, int64_t cols, const void *src,
                       int64_t ld_src, int src_dtype, const gemm_fp4_matrix_t *out, void *stream);
 
@@ -85,7 +86,8 @@ int gemm_fp4_dequantize(gemm_handle_t h, int64_t rows, int64_t cols, const gemm_
  * M == 0 or N == 0: nothing is launched.  K == 0: C = bias (or 0).
  * Errors: INVALID_ARG (negative size, ld < ceil(K / 2), ldc < N, NULL pointer
  * of a non-empty operand, unknown enum, two formats), UNSUPPORTED (misaligned
- * data, scale or ld; M, N or K of 2^31 - 1024 or more), CUDA. */
+ * data, scale or ld; C, bias or row_scale not on a multiple of its elements'
+ * size; M, N or K of 2^31 - 1024 or more), CUDA. */
 int gemm_fp4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp4_matrix_t *A,
                  const gemm_fp4_matrix_t *B, const float *bias, void *C, int64_t ldc,
                  int out_dtype, void *stream);

@@ -37,7 +37,7 @@ typedef struct {
   double eps;                 /* 2^-100 ... 2^100 */
   const void *g;              /* matrix i at g + i * stride_g elements */
   int64_t ld_g, stride_g;
-  void *out;                  /* bfloat16; may be g itself where types and strides agree */
+  void *out;                  /* bfloat16; may be g itself, which is read before it is written */
   int64_t ld_out, stride_out;
 } gemm_orthogonalize_t;
 
@@ -55,7 +55,9 @@ int gemm_orthogonalize_workspace(gemm_handle_t h, const gemm_orthogonalize_t *p,
  * of a batch that overlap in out, NULL pointer, workspace too small or
  * misaligned, unknown enum, eps out of range, coefficients that are not finite
  * or let singular values of [0, 1] grow beyond 10^4, or b A + c A·A beyond
- * 10^8), UNSUPPORTED (rows or cols of 2^20 or more, batch of 2^16 or more), CUDA. */
+ * 10^8),
+ * UNSUPPORTED (rows or cols of 2^20 or more, batch of 2^16 or more, g or out not
+ * on a multiple of its elements' size), CUDA. */
 int gemm_orthogonalize(gemm_handle_t h, const gemm_orthogonalize_t *p, void *workspace,
                        int64_t workspace_bytes, void *stream);
 

@@ -103,6 +103,19 @@ def test_orthogonalize_refusals(handle):
         assert call(coefficients=ctypes.addressof(c)) == ERR, abc
 
 
+def test_addresses_inside_an_element_are_refused(handle):
+    h, _ = handle
+    m, nv = matrix(), matrix(rows=18, fmt=B.GEMM_NVFP4)
+    for dtype, at in ((B.GEMM_F32, 18), (B.GEMM_F16, 17), (B.GEMM_BF16, 33)):
+        assert B.gemm_fp4_quantize(h, 4, 64, at, 64, dtype, m, None) == UNSUPPORTED
+        assert B.gemm_fp4_dequantize(h, 4, 64, m, at, 64, dtype, None) == UNSUPPORTED
+        assert B.gemm_fp4_run(h, 4, 8, 64, m, m, None, at, 8, dtype, None) == UNSUPPORTED
+        assert B.gemm_orthogonalize(h, ortho(g=at, dtype=dtype), 256, 1 << 40, None) == UNSUPPORTED
+    assert B.gemm_fp4_run(h, 4, 8, 64, m, m, 18, 16, 8, B.GEMM_F32, None) == UNSUPPORTED
+    assert B.gemm_fp4_quantize(h, 4, 64, 16, 64, B.GEMM_F32, nv, None) == UNSUPPORTED
+    assert B.gemm_orthogonalize(h, ortho(out=257), 256, 1 << 40, None) == UNSUPPORTED
+
+
 def test_orthogonalize_workspace(handle):
     h, _ = handle
     assert B.gemm_orthogonalize_workspace(None, ortho()) == (ERR, 0)

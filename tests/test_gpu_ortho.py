@@ -1,5 +1,7 @@
 """Orthogonalising on the GPU against its formula in doubles, and against a simulation in
 doubles of what it rounds."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -173,6 +175,78 @@ def test_streams_graphs_and_repeats(g):
         for _ in range(3):
             graph.replay()
             assert torch.equal(out, want)
+    g.status()
+
+
+def run_c(g, p, abc, poison):
+    """The C entry with a workspace of one byte's value throughout."""
+    c = (ctypes.c_float * (3 * p.steps))(*(abc * p.steps))
+    p.coefficients = ctypes.addressof(c)
+    rc, size = B.gemm_orthogonalize_workspace(g.handle, p)
+    assert rc == 0
+    ws = torch.full((size,), poison, dtype=torch.uint8, device="cuda")
+    rc = B.gemm_orthogonalize(g.handle, p, ws.data_ptr(), size,
+                              torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    g.status()
+
+
+@pytest.mark.parametrize("pair,tile_n", [(-1, -1), (0, -1), (1, 128), (1, 256)])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 1, 1), (1, 200, 131), (3, 70, 130), (2, 300, 261)])
+def test_in_place_padded_and_any_workspace(g, pair, tile_n, batch, rows, cols):
+    """out in rows and matrices with gaps, which stay as they were, or over g itself; the
+    workspace's contents do not matter."""
+    torch.manual_seed(cols)
+    G = torch.randn(batch, rows, cols, device="cuda").bfloat16()
+    g.set_option(B.GEMM_OPT_PAIR, pair)
+    g.set_option(B.GEMM_OPT_FORCE_TILE_N, tile_n)
+    try:
+        want = g.orthogonalize(G)
+        for pad, gap, place, poison in ((0, 0, False, 0xff), (5, 7, False, 0x7c), (3, 16, True, 0xff),
+                                        (8, 64, True, 0)):
+            ld = cols + pad
+            stride = rows * ld + gap
+            buf = torch.full((batch * stride + 8,), 7.0, device="cuda").bfloat16()
+            view = buf.as_strided((batch, rows, cols), (stride, ld, 1), 1)
+            src = G
+            if place:
+                view.copy_(G)
+                src = view
+            p = B.gemm_orthogonalize_t(batch=batch, rows=rows, cols=cols, steps=5, dtype=B.GEMM_BF16,
+                                       eps=1e-7, g=src.data_ptr(), ld_g=src.stride(1),
+                                       stride_g=src.stride(0), out=view.data_ptr(), ld_out=ld,
+                                       stride_out=stride)
+            run_c(g, p, FAST, poison)
+            assert torch.equal(view, want)
+            view.fill_(7.0)
+            assert bool((buf == 7.0).all())
+    finally:
+        g.set_option(B.GEMM_OPT_PAIR, -1)
+        g.set_option(B.GEMM_OPT_FORCE_TILE_N, -1)
+
+
+def test_two_graphs_at_once(g):
+    """Each has scratch of its own."""
+    torch.manual_seed(8)
+    G = [torch.randn(300, 520, device="cuda"), torch.randn(2, 260, 200, device="cuda")]
+    want = [g.orthogonalize(x) for x in G]
+    graphs, outs = [], []
+    for x in G:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(g.orthogonalize(x))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in G]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
     g.status()
 
 
