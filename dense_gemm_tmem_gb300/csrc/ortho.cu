@@ -335,7 +335,7 @@ int scale_for(double most) {
   if (!(most > 0)) return 0;
   int e;
   std::frexp(most, &e);  // most <= 2^e
-  return std::min(14 - e, 40);
+  return std::min(14 - e, 100);
 }
 
 struct Plan {
@@ -355,6 +355,8 @@ int plan_scales(const gemm_orthogonalize_t& p, Plan* plan) {
     plan->b[i] = scale_for(most_b);
     u = most_quintic(a, b, c, u);
     if (!(u <= 1e4) || !(most_b <= 1e8)) return GEMM_ERR_INVALID_ARG;
+    // below, the factors between the copies' scales would leave fp32's range
+    if (i + 1 < p.steps && u > 0 && u < 0x1p-20) return GEMM_ERR_INVALID_ARG;
   }
   return GEMM_OK;
 }

@@ -53,9 +53,9 @@ int gemm_orthogonalize_workspace(gemm_handle_t h, const gemm_orthogonalize_t *p,
  * batch, rows or cols == 0: nothing is launched.
  * Errors: INVALID_ARG (negative size, steps out of range, ld < cols, matrices
  * of a batch that overlap in out, NULL pointer, workspace too small or
- * misaligned, unknown enum, eps out of range, coefficients that are not finite
- * or let singular values of [0, 1] grow beyond 10^4, or b A + c A·A beyond
- * 10^8),
+ * misaligned, unknown enum, eps out of range, coefficients that are not finite,
+ * let singular values of [0, 1] grow beyond 10^4 or b A + c A·A beyond 10^8, or
+ * take all of them below 2^-20, but not to 0, before the last step),
  * UNSUPPORTED (rows or cols of 2^20 or more, batch of 2^16 or more, g or out not
  * on a multiple of its elements' size), CUDA. */
 int gemm_orthogonalize(gemm_handle_t h, const gemm_orthogonalize_t *p, void *workspace,

@@ -116,6 +116,22 @@ def test_addresses_inside_an_element_are_refused(handle):
     assert B.gemm_orthogonalize(h, ortho(out=257), 256, 1 << 40, None) == UNSUPPORTED
 
 
+def test_coefficients_that_lose_the_iterate_are_refused(handle):
+    """16-bit copies of an iterate far below 1 have scales that fp32 does not hold."""
+    h, _ = handle
+    def call(*abc):
+        c = (ctypes.c_float * (3 * len(abc)))(*(v for step in abc for v in step))
+        p = ortho(steps=len(abc), coefficients=ctypes.addressof(c), g=None)
+        return B.gemm_orthogonalize(h, p, None, 0, None), \
+            B.gemm_orthogonalize(h, ortho(steps=len(abc), coefficients=ctypes.addressof(c), rows=0),
+                                 None, 0, None)
+    assert call((1e-15, 0, 0), (0, 1e38, 0)) == (ERR, ERR)
+    assert call((2.0 ** -21, 0, 0), (1, 0, 0)) == (ERR, ERR)
+    # accepted, so that only the missing pointers are left: small but held, zero, the last step
+    for ok in (((2.0 ** -20, 0, 0), (1, 0, 0)), ((0, 0, 0), (1, 0, 0)), ((1, 0, 0), (1e-15, 0, 0))):
+        assert call(*ok) == (ERR, 0)
+
+
 def test_orthogonalize_workspace(handle):
     h, _ = handle
     assert B.gemm_orthogonalize_workspace(None, ortho()) == (ERR, 0)

@@ -226,6 +226,23 @@ def test_in_place_padded_and_any_workspace(g, pair, tile_n, batch, rows, cols):
         g.set_option(B.GEMM_OPT_FORCE_TILE_N, -1)
 
 
+@pytest.mark.parametrize("abc", [[(2.0 ** -20, 0.0, 0.0), (2.0 ** 20, 0.0, 0.0), FAST],
+                                 [(2.0 ** -10, 0.0, 0.0), (0.0, 2.0 ** 30, 0.0), FAST],
+                                 [(0.01, 0.0, 0.0), (150.0, -8e5, 1e9), FAST],
+                                 [(1.0, 0.0, 0.0), (2.0 ** -40, 2.0 ** -40, 0.0)]])
+def test_an_iterate_far_below_1(g, abc):
+    """The 16-bit copies' scales follow it.  (The result itself may be far below 1: relative.)"""
+    torch.manual_seed(6)
+    for rows, cols in ((40, 100), (130, 64)):
+        G = torch.randn(rows, cols, device="cuda")
+        got = g.orthogonalize(G, len(abc), abc)
+        exact = simulate(G, len(abc), abc, round16=False)
+        # each copy's 2^-11, up to four of them in a step's product, three steps, whose
+        # coefficients magnify by less than 4; the result's rounding
+        assert rel(got.double(), exact) <= 12 * 4 * 2.0 ** -11 + 2.0 ** -9
+    g.status()
+
+
 def test_two_graphs_at_once(g):
     """Each has scratch of its own."""
     torch.manual_seed(8)
