@@ -41,7 +41,7 @@ NATIVE_SOURCE = os.path.join(CSRC, "native.cpp")
 SOURCES = ["api.cu", "simt.cu", "simt_f16.cu", "selftest.cu", "noalloc.cu", "tc2.cu",
            "tc_n256.cu", "tc_n128.cu", "tc_small.cu", "tc_narrow.cu", "tc64.cu",
            "fp8_api.cu", "fp8_quant.cu", "fp8_simt.cu", "fp8_moe.cu", "fp8_tc.cu",
-           "fp4_api.cu", "fp4_quant.cu", "fp4_tc.cu", "ortho.cu", "ortho_tc.cu"]
+           "fp4_api.cu", "fp4_quant.cu", "fp4_tc.cu", "fp4_row.cu", "ortho.cu", "ortho_tc.cu"]
 HEADERS = ["ptx.cuh", "work.cuh", "tc_kernel.cuh", "tc2_kernel.cuh", "tc64_kernel.cuh",
            "tc_launch.cuh", "simt_kernel.cuh", "internal.h", "context.h", "fp8.cuh",
            "fp8_tc_kernel.cuh", "moe_order.h", "fp4.cuh",

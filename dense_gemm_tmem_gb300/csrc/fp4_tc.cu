@@ -108,6 +108,10 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
     fp4_fill_kernel<<<1024, 256, 0, stream>>>(p.M, p.N, p.bias, p.C, p.ldc, p.out_dtype);
     return cudaGetLastError();
   }
+  // One row: a kernel of its own (4096 x 4096 3.7 us against 6.4, all sizes in fp4_row.cu),
+  // unless an option asks for a form of the tensor cores'.
+  if (p.M == 1 && h->opt.force_swap < 0 && h->opt.csplit < 0 && h->opt.force_tile_n <= 0)
+    return launch_fp4_row(h, p, stream);
   // Few rows of A: operands swapped, so that the other side fills the 128 MMA rows and
   // A's rows are the MMA's columns, 32 of them.  Measured (mxfp4, graph replay, cold
   // inputs, us, swapped / not), N x K 4096 x 4096: 6.4 / 8.1 for 8 rows, 6.7 / 7.7 for 32,
@@ -124,7 +128,7 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   // Fewer tiles than half the SMs: each tile's k-blocks over a cluster, the largest
   // whose clusters are all resident at once, if that takes more than kSplitGain
   // k-blocks off each CTA (adding the partials costs about as long).  Measured (nvfp4, us,
-  // split / whole): 1 x 4096 x 4096 6.4 / 7.6, 1 x 1024 x 8192 5.6 / 11.8, 256 x 1024 x
+  // split / whole): 2 x 4096 x 4096 6.4 / 7.6, 2 x 1024 x 8192 5.6 / 11.8, 256 x 1024 x
   // 4096 7.0 / 7.7, 512 x 512 x 8192 8.0 / 12.0, 16 x 512 x 2048 4.6 / 5.0; not taken: 32 x
   // 2048 x 1024 4.7 / 4.1, 300 x 700 x 1024 5.5 / 4.6; more CTAs than SMs: 64 x 8192 x
   // 8192 by 4 18.3, by 2, which fit, 12.4, whole 14.4.

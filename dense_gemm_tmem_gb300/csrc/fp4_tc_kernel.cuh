@@ -31,9 +31,8 @@
 // reads in flight together (no change), 128 columns (230).
 // tcgen05.mma reads scales from even TMEM columns only: tiles start at multiples of 64
 // rows of B (160-wide ones, whose scales start at odd columns, fault).
-// Small products are bound by latency: launch, first loads, the cluster's exchange.  A
-// matrix-vector kernel of its own was not tried: 1 x 4096 x 4096 takes 6.4 us, of which
-// 1.4 would be its bytes.
+// Small products are bound by latency: launch, first loads, the cluster's exchange; one row
+// of A has a kernel of its own (fp4_row.cu).
 #pragma once
 
 #include "fp4.cuh"

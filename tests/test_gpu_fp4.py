@@ -430,3 +430,105 @@ def test_from_parts_is_what_quantising_stores(g):
             again = Fp4Matrix.from_parts(m.data.contiguous(), m.block_scales(), m.row_scale, cols,
                                          fmt)
             assert torch.equal(again.data, m.data) and torch.equal(again.scale, m.scale)
+
+
+# -------------------------------------------------------------- one row of A --
+def codes(rng, rows, cols, fmt, lo, hi):
+    """A matrix of any codes, its rows' padding full of bytes that are no part of it, and
+    block scales of lo ... hi - 1."""
+    width = (cols + 1) // 2
+    buf = torch.full((rows, -(-width // 16) * 16 + 16), 0x77, dtype=torch.uint8)
+    buf[:, :width] = torch.from_numpy(rng.integers(0, 256, (rows, width)).astype(np.uint8))
+    if cols % 2:
+        buf[:, width - 1] &= 15
+    scale = torch.from_numpy(rng.integers(lo, hi, (rows, -(-cols // R.BLOCK[fmt]))).astype(np.uint8))
+    return Fp4Matrix(buf.cuda()[:, :width], fp4.pack_scales(scale.cuda()), None, (rows, cols), fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K", [1, 2, 15, 16, 17, 33, 63, 65, 129, 2047, 2048, 2050, 4100, 10000,
+                               32770])
+@pytest.mark.parametrize("N", [1, 31, 32, 33, 97, 127, 128, 129, 700])
+def test_one_row(g, N, K, fmt):
+    rng = np.random.default_rng(N * 7 + K)
+    lo, hi = (117, 137) if fmt == "mxfp4" else (0, 127)
+    A, Bm = codes(rng, 1, K, fmt, lo, hi), codes(rng, N, K, fmt, lo, hi)
+    bias = torch.randn(N, device="cuda") if K % 2 else None
+    for dtype in (F32, BF16):
+        out = g.fp4_matmul(A, Bm, bias, out_dtype=dtype)
+        check_product(out, A, Bm, bias)
+        assert torch.equal(g.fp4_matmul(A, Bm, bias, out_dtype=dtype), out)
+    # what follows the row stays as it was
+    C = torch.full((N + 5,), 7.0, device="cuda")
+    g.fp4_run(A, Bm, C[2:N + 2].view(1, N), bias)
+    check_product(C[2:N + 2].view(1, N), A, Bm, bias)
+    assert bool((C[:2] == 7).all()) and bool((C[N + 2:] == 7).all())
+
+
+@pytest.mark.parametrize("N,K", [(40000, 520), (14336, 2048), (300, 40000)])
+def test_one_row_of_many(g, N, K):
+    """More rows than are resident at once, and parts of K that several rounds take."""
+    for fmt in FORMATS:
+        rng = np.random.default_rng(K)
+        lo, hi = (117, 137) if fmt == "mxfp4" else (0, 127)
+        A, Bm = codes(rng, 1, K, fmt, lo, hi), codes(rng, N, K, fmt, lo, hi)
+        check_product(g.fp4_matmul(A, Bm, out_dtype=F32), A, Bm)
+
+
+@pytest.mark.parametrize("ea,eb", [((0, 3), (250, 255)), ((250, 255), (0, 3)), ((0, 2), (126, 130)),
+                                   ((126, 129), (0, 2)), ((127, 128), (225, 230))])
+def test_one_row_of_far_scales(g, ea, eb):
+    """Each scale at fp32's ends, their product inside: no step in between leaves its range."""
+    rng = np.random.default_rng(3)
+    A, Bm = codes(rng, 1, 320, "mxfp4", *ea), codes(rng, 140, 320, "mxfp4", *eb)
+    (a, _), (b, _) = parts(A), parts(Bm)
+    want, got = a @ b.T, host(g.fp4_matmul(A, Bm, out_dtype=F32))
+    # as in bound(), and half of fp32's least step for each addition to a sum near it
+    tol = (np.abs(a) @ np.abs(b).T) * 320 * 2.0 ** -23 + 320 * 2.0 ** -150
+    assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_one_row_scaled(g, fmt):
+    """Row scales: none, one for all, each its own, their product outside fp32's range."""
+    rng = np.random.default_rng(5)
+    A0 = g.fp4_quantize(make(rng, 1, 400).cuda().float(), fmt)
+    B0 = g.fp4_quantize(make(rng, 200, 400).cuda().float(), fmt)
+    one = torch.tensor([0.3], device="cuda")
+    for ra in (None, one, 1e30 * one):
+        for rb in (None, one.expand(200), torch.rand(400, device="cuda")[::2], 1e-30 * torch.rand(
+                200, device="cuda")):
+            A = Fp4Matrix(A0.data, A0.scale, ra, (1, 400), fmt)
+            Bm = Fp4Matrix(B0.data, B0.scale, rb, (200, 400), fmt)
+            check_product(g.fp4_matmul(A, Bm, out_dtype=F32), A, Bm)
+    A = Fp4Matrix(A0.data, A0.scale, 1e30 * one, (1, 400), fmt)
+    Bm = Fp4Matrix(B0.data, B0.scale, 1e30 * one.expand(200), (200, 400), fmt)
+    C = g.fp4_matmul(A, Bm, out_dtype=F32)  # beyond fp32, but for sums of 0
+    assert bool((torch.isinf(C) | (C == 0)).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_one_row_after_its_operands_were_written(g, fmt):
+    """In a chain of launches that start early: the weight quantised just before the product
+    that reads it, again and again into the same memory."""
+    rng = np.random.default_rng(9)
+    ws = [make(rng, 600, 1100).cuda().float() for _ in range(4)]
+    xs = [make(rng, 1, 1100).cuda().float() for _ in range(4)]
+    want = []
+    for x, w in zip(xs, ws):
+        want.append(g.fp4_matmul(g.fp4_quantize(x, fmt), g.fp4_quantize(w, fmt), out_dtype=F32))
+        torch.cuda.synchronize()
+    x, w = xs[0].clone(), ws[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    outs = []
+    with torch.cuda.graph(graph):
+        for i in range(4):
+            x.copy_(xs[i])
+            w.copy_(ws[i])
+            outs.append(g.fp4_matmul(g.fp4_quantize(x, fmt), g.fp4_quantize(w, fmt),
+                                     out_dtype=F32))
+    for _ in range(10):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        assert all(torch.equal(o, v) for o, v in zip(outs, want))
