@@ -163,6 +163,21 @@ __device__ __forceinline__ uint32_t f4_producer(const Fp4Maps& m, const Fp4TcArg
   Unit u;
   int s = 0;
   uint32_t ph = 0, filled = 0;
+  // Swapped operands: what the first stages load of A, the weight, is sent for to L2 before
+  // the kernels ahead in the stream are done: that is no read, so that they may write it.
+  // (A layer of 4096 x 4096 for 16 rows 8.0 us instead of 8.8, the product alone 6.7 / 6.9.
+  // Other tiles, whose loads then follow at once, lose half a microsecond.)
+  if constexpr (BN == 32) {
+    WorkIter first = it;
+    if (first.next(W, u)) {
+      int32_t tm, tn;
+      tile_coords(W, u.tile, tm, tn);
+      for (int32_t kb = u.kb0; kb < u.kb1 && kb < u.kb0 + Cfg::kStages; ++kb) {
+        tma_prefetch_2d(&m.a, kb * 128, tm * kBM);
+        tma_prefetch_2d(&m.sa, kb * (Cfg::kPieces * kFp4Piece / 8), tm);
+      }
+    }
+  }
   pdl_wait_prerequisites();
   while (it.next(W, u)) {
     int32_t tm, tn;

@@ -290,6 +290,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Sends for a 2-D tile to L2, from which a load then takes it.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 // 3-D tiled load: used for a group of consecutive k-blocks of a K-major
 // operand, viewed as {64 (k within the block), rows, k-block}; the box
 // {64, rows, J} lands as J consecutive blocks of rows x 128 bytes.

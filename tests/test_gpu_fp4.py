@@ -508,12 +508,13 @@ def test_one_row_scaled(g, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_one_row_after_its_operands_were_written(g, fmt):
+@pytest.mark.parametrize("rows", [1, 20, 200])
+def test_rows_after_their_operands_were_written(g, rows, fmt):
     """In a chain of launches that start early: the weight quantised just before the product
     that reads it, again and again into the same memory."""
     rng = np.random.default_rng(9)
     ws = [make(rng, 600, 1100).cuda().float() for _ in range(4)]
-    xs = [make(rng, 1, 1100).cuda().float() for _ in range(4)]
+    xs = [make(rng, rows, 1100).cuda().float() for _ in range(4)]
     want = []
     for x, w in zip(xs, ws):
         want.append(g.fp4_matmul(g.fp4_quantize(x, fmt), g.fp4_quantize(w, fmt), out_dtype=F32))
