@@ -82,7 +82,9 @@ cudaError_t launch_inst(const Fp4Maps& maps, const CUtensorMap& mC, const Fp4TcA
 
 template <int FMT, class Launch>
 cudaError_t launch_format(int bn, bool trans, bool out32, Launch&& launch) {
-  if (trans) return launch(launch_inst<32, false, true, FMT, false>);  // stores any type
+  if (trans)  // stores any type
+    return bn == 32 ? launch(launch_inst<32, false, true, FMT, false>)
+                    : launch(launch_inst<64, false, true, FMT, false>);
   if (bn == 256)
     return out32 ? launch(launch_inst<256, true, false, FMT, true>)
                  : launch(launch_inst<256, true, false, FMT, false>);
@@ -112,18 +114,22 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   // unless an option asks for a form of the tensor cores'.
   if (p.M == 1 && h->opt.force_swap < 0 && h->opt.csplit < 0 && h->opt.force_tile_n <= 0)
     return launch_fp4_row(h, p, stream);
+  const int64_t I = ceil_div(p.K, kF4BlockK);
   // Few rows of A: operands swapped, so that the other side fills the 128 MMA rows and
-  // A's rows are the MMA's columns, 32 of them.  Measured (mxfp4, graph replay, cold
-  // inputs, us, swapped / not), N x K 4096 x 4096: 6.4 / 8.1 for 8 rows, 6.7 / 7.7 for 32,
-  // 7.2 / 7.8 for 48, 7.3 / 7.1 for 64; 8192 x 1024: 4.4 / 4.9, 4.8 / 4.8, 5.5 / 4.7.
-  constexpr int64_t kSwapRows = 32;
+  // A's rows are the MMA's columns, 32 or 64 of them.  Measured (mxfp4, graph replay, cold
+  // inputs, us, swapped / not), N x K 4096 x 4096: 6.4 / 8.0 for 16 rows, 6.7 / 7.7 for 32;
+  // 8192 x 1024: 4.4 / 4.9, 4.5 / 4.8.  33 to 63 rows where K is deep and N wide: 48 rows
+  // 4096 x 4096 7.1 / 7.8, 4096 x 2816 6.6 / 7.0, 14336 x 4096 10.1 / 12.1, but 4096 x 2048
+  // 6.2 / 5.4 and 1024 x 2816 5.6 / 5.3; 64 rows, which fill their boxes, 7.3 / 7.2.
+  constexpr int64_t kSwapRows = 32, kSwapMost = 64, kSwapDepth = 8, kSwapWidth = 2048;
   const int swap = h->opt.force_swap;  // GEMM_OPT_FORCE_SWAP_AB
-  const bool trans = swap != 0 && p.M <= kSwapRows && (swap == 1 || p.N > p.M);
+  const bool few = p.M <= kSwapRows ||
+                   (p.M < kSwapMost && I > kSwapDepth && p.N >= kSwapWidth);
+  const bool trans = swap == 1 ? p.M <= kSwapMost : swap != 0 && few && p.N > p.M;
   const gemm_fp4_matrix_t& opA = trans ? p.B : p.A;
   const gemm_fp4_matrix_t& opB = trans ? p.A : p.B;
   const int64_t Mm = trans ? p.N : p.M, Nm = trans ? p.M : p.N;
   const int64_t sms = h->num_sms;
-  const int64_t I = ceil_div(p.K, kF4BlockK);
   const int64_t pairs = h->opt.pair_clusters > 0 ? h->opt.pair_clusters : sms / 2;
   // Fewer tiles than half the SMs: each tile's k-blocks over a cluster, the largest
   // whose clusters are all resident at once, if that takes more than kSplitGain
@@ -158,7 +164,7 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   const int tile_n = h->opt.force_tile_n;  // GEMM_OPT_FORCE_TILE_N: 64, 128 or 256 (pairs)
   const int64_t wide = ceil_div(Mm, 256) * ceil_div(Nm, 256);
   if (trans) {
-    bn = 32;
+    bn = Nm <= 32 ? 32 : 64;
   } else if (tile_n > 0 ? tile_n >= 256 : 4 * wide >= 5 * pairs && I >= kPairDepth) {
     bn = 256;
     tiles_m = ceil_div(Mm, 256);

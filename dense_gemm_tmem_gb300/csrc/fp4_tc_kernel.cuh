@@ -152,7 +152,7 @@ __device__ __forceinline__ uint64_t make_sdesc_rows16(uint32_t saddr) {
 }
 
 // TMA producer (one thread).  Returns how many stages it filled.
-template <int BN, bool PAIR, int FMT>
+template <int BN, bool PAIR, bool TRANS, int FMT>
 __device__ __forceinline__ uint32_t f4_producer(const Fp4Maps& m, const Fp4TcArgs& args,
                                                 uint8_t* ring, uint64_t* full, uint64_t* empty,
                                                 const WaitCtl& wc, uint32_t rank, int32_t owner) {
@@ -167,7 +167,7 @@ __device__ __forceinline__ uint32_t f4_producer(const Fp4Maps& m, const Fp4TcArg
   // the kernels ahead in the stream are done: that is no read, so that they may write it.
   // (A layer of 4096 x 4096 for 16 rows 8.0 us instead of 8.8, the product alone 6.7 / 6.9.
   // Other tiles, whose loads then follow at once, lose half a microsecond.)
-  if constexpr (BN == 32) {
+  if constexpr (TRANS) {
     WorkIter first = it;
     if (first.next(W, u)) {
       int32_t tm, tn;
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   } else {
     if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF4RoleRegs));
     if (warp == 0 && lane == 0) {
-      filled = f4_producer<BN, PAIR, FMT>(maps, args, ring, full, empty, wc, rank, owner);
+      filled = f4_producer<BN, PAIR, TRANS, FMT>(maps, args, ring, full, empty, wc, rank, owner);
       if (PAIR && rank != 0) st_dsmem_u32(map_to_rank(smem_u32(peer_filled), 0), filled);
     } else {
       pdl_wait_prerequisites();

@@ -263,6 +263,29 @@ def test_every_tile_on_every_shape(g, M, N, K, swap, tile, split, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("split", [-1, 0, 2, 4, 8])
+@pytest.mark.parametrize("M,N,K", [(33, 150, 2100), (63, 129, 70), (64, 400, 2304), (48, 2100, 2307)])
+def test_swapped_in_two_widths(g, M, N, K, split, fmt):
+    """33 to 64 rows of A as the MMA's columns."""
+    rng = np.random.default_rng(N)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    bias = torch.from_numpy(rng.standard_normal(N)).float().cuda()
+    g.set_option(B.GEMM_OPT_FORCE_SWAP_AB, 1)
+    g.set_option(B.GEMM_OPT_CLUSTER_SPLIT, split)
+    try:
+        for dtype in (F32, F16, BF16):
+            buf = torch.full((M, N + 3), 7.0, device="cuda").to(dtype)
+            g.fp4_run(A, Bm, buf[:, :N], bias)
+            check_product(buf[:, :N], A, Bm, bias)
+            assert bool((buf[:, N:] == 7).all())
+        g.status()
+    finally:
+        g.set_option(B.GEMM_OPT_FORCE_SWAP_AB, -1)
+        g.set_option(B.GEMM_OPT_CLUSTER_SPLIT, -1)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("K", [257, 1281, 1400, 1537, 1790, 2049])
 @pytest.mark.parametrize("M,N", [(1, 300), (3, 64), (70, 200)])
 def test_few_tiles_over_few_k_blocks(g, M, N, K, fmt):
@@ -508,7 +531,7 @@ def test_one_row_scaled(g, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("rows", [1, 20, 200])
+@pytest.mark.parametrize("rows", [1, 20, 40, 200])
 def test_rows_after_their_operands_were_written(g, rows, fmt):
     """In a chain of launches that start early: the weight quantised just before the product
     that reads it, again and again into the same memory."""
