@@ -21,10 +21,12 @@
 // fp4_tc_kernel.cuh): 4096 x 4096 3.7 / 3.6 (6.4 / 6.1), 1024 x 1024 1.9 / 1.9 (3.7 / 3.5), 1024 x
 // 8192 3.3 / 3.3 (5.6 / 5.4), 8192 x 1024 3.3 / 3.3 (4.4 / 4.3), 8192 x 8192 9.9 / 10.0 (10.8 /
 // 10.5), 4100 x 4100 5.2 / 5.3 (6.7 / 6.4).  An almost empty launch takes 1.8; over that, 4096 x
-// 4096 moves 5.0 TB/s and 8192 x 8192 4.7, where the instructions (3 a value) take as long as
-// the loads.  Dropped: the next piece's loads ahead of this one's sums, in more registers and
+// 4096 moves 5.0 TB/s and 8192 x 8192 4.7.  The loads' latency bounds it: 32 warps an SM, each
+// of which first loads and then computes, fill half of the issue slots, and DRAM a third.
+// Dropped: the next piece's loads ahead of this one's sums, in more registers and
 // so with fewer warps (4.5 and 10.7), nothing sent for ahead of the stream (4.5 and 10.3, both
-// before the row's scales were read at the start), integer dot products of values taken from
+// before the row's scales were read at the start), every next piece sent for to L2 too (3.8
+// and 10.4), integer dot products of values taken from
 // a table by byte permutes (5.0), two rows of A (5.2; 14.2 at 8192 x 8192, where the tensor
 // cores take 11).
 #include "context.h"

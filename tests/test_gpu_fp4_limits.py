@@ -20,7 +20,8 @@ def h():
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("M,N,K,tile", [(1, 4096, 4096, -1), (300, 700, 2048, -1),
+@pytest.mark.parametrize("M,N,K,tile", [(1, 4096, 4096, -1), (20, 4096, 4096, -1),
+                                        (50, 4096, 4096, -1), (300, 700, 2048, -1),
                                         (2048, 2048, 2048, -1), (1024, 2048, 2048, 256),
                                         (4096, 4096, 1024, 256)])
 def test_product_under_short_limits(h, M, N, K, tile, fmt):
