@@ -45,7 +45,7 @@ SOURCES = ["api.cu", "simt.cu", "simt_f16.cu", "selftest.cu", "noalloc.cu", "tc2
 HEADERS = ["ptx.cuh", "work.cuh", "tc_kernel.cuh", "tc2_kernel.cuh", "tc64_kernel.cuh",
            "tc_launch.cuh", "simt_kernel.cuh", "internal.h", "context.h", "fp8.cuh",
            "fp8_tc_kernel.cuh", "moe_order.h", "fp4.cuh",
-           "fp4_tc_kernel.cuh", "ortho.cuh", "ortho_tc_kernel.cuh"]
+           "fp4_quant.cuh", "fp4_tc_kernel.cuh", "ortho.cuh", "ortho_tc_kernel.cuh"]
 INCLUDES = ["gemm.h", "gemm_fp8.h", "gemm_fp4.h", "gemm_ortho.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

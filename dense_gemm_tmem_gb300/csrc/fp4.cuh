@@ -69,7 +69,10 @@ cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int
                                 cudaStream_t stream);
 cudaError_t launch_fp4_dequantize(int64_t rows, int64_t cols, const gemm_fp4_matrix_t& m,
                                   void* dst, int64_t ld_dst, int dst_dtype, cudaStream_t stream);
-cudaError_t launch_fp4_row(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream);
+// One row of A; where `x` is given, K elements of its type, they are quantised on the way and
+// p.A is not looked at.
+cudaError_t launch_fp4_row(gemm_ctx* h, const Fp4Product& p, const void* x, int x_dtype,
+                           cudaStream_t stream);
 cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream);
 
 }  // namespace dg

@@ -92,4 +92,23 @@ int gemm_fp4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp
   });
 }
 
+int gemm_fp4_linear_row(gemm_handle_t h, int64_t N, int64_t K, const void* x, int x_dtype,
+                        const gemm_fp4_matrix_t* W, const float* bias, void* y, int y_dtype,
+                        void* stream) {
+  if (!h || N < 0 || K < 0 || dg::bad_type(x_dtype) || dg::bad_type(y_dtype))
+    return GEMM_ERR_INVALID_ARG;
+  const int rc = dg::check_matrix(W, N, K);
+  if (rc != GEMM_OK) return rc;
+  if (N == 0) return GEMM_OK;
+  if (!y || (K > 0 && !x)) return GEMM_ERR_INVALID_ARG;
+  if (K > GEMM_FP4_ROW_MOST || dg::misaligned(x, x_dtype) || dg::misaligned(y, y_dtype) ||
+      dg::misaligned(bias, GEMM_F32))
+    return GEMM_ERR_UNSUPPORTED;
+  const dg::Fp4Product p{1, N, K, *W, *W, bias, y, N, y_dtype};
+  return dg::on_device(h->device, [&]() -> int {
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dg::done(K == 0 ? dg::launch_fp4(h, p, s) : dg::launch_fp4_row(h, p, x, x_dtype, s));
+  });
+}
+
 }  // extern "C"

@@ -113,7 +113,7 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   // One row: a kernel of its own (4096 x 4096 3.7 us against 6.4, all sizes in fp4_row.cu),
   // unless an option asks for a form of the tensor cores'.
   if (p.M == 1 && h->opt.force_swap < 0 && h->opt.csplit < 0 && h->opt.force_tile_n <= 0)
-    return launch_fp4_row(h, p, stream);
+    return launch_fp4_row(h, p, nullptr, 0, stream);
   const int64_t I = ceil_div(p.K, kF4BlockK);
   // Few rows of A: operands swapped, so that the other side fills the 128 MMA rows and
   // A's rows are the MMA's columns, 32 or 64 of them.  Measured (mxfp4, graph replay, cold

@@ -30,6 +30,8 @@ using Dequantize4Fn = int (*)(gemm_handle_t, int64_t, int64_t, const gemm_fp4_ma
                               int64_t, int, void*);
 using Run4Fn = int (*)(gemm_handle_t, int64_t, int64_t, int64_t, const gemm_fp4_matrix_t*,
                        const gemm_fp4_matrix_t*, const float*, void*, int64_t, int, void*);
+using LinearRow4Fn = int (*)(gemm_handle_t, int64_t, int64_t, const void*, int,
+                             const gemm_fp4_matrix_t*, const float*, void*, int, void*);
 using OrthoSpaceFn = int (*)(gemm_handle_t, const gemm_orthogonalize_t*, int64_t*);
 using OrthoFn = int (*)(gemm_handle_t, const gemm_orthogonalize_t*, void*, int64_t, void*);
 QuantizeFn quantize_fn = nullptr;
@@ -41,6 +43,7 @@ Dequantize4Fn dequantize4_fn = nullptr;
 Run4Fn run4_fn = nullptr;
 OrthoSpaceFn ortho_space_fn = nullptr;
 OrthoFn ortho_fn = nullptr;
+LinearRow4Fn linear_row4_fn = nullptr;
 
 constexpr int64_t kBlock = 128;
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
@@ -125,7 +128,7 @@ PyObject* guarded(F&& f) {
 
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    if (n != 9) fail(PyExc_TypeError, "init takes 9 addresses");
+    if (n != 10) fail(PyExc_TypeError, "init takes 10 addresses");
     quantize_fn = reinterpret_cast<QuantizeFn>(address<void>(args[0]));
     run_fn = reinterpret_cast<RunFn>(address<void>(args[1]));
     moe_space_fn = reinterpret_cast<MoeSpaceFn>(address<void>(args[2]));
@@ -135,6 +138,7 @@ PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
     run4_fn = reinterpret_cast<Run4Fn>(address<void>(args[6]));
     ortho_space_fn = reinterpret_cast<OrthoSpaceFn>(address<void>(args[7]));
     ortho_fn = reinterpret_cast<OrthoFn>(address<void>(args[8]));
+    linear_row4_fn = reinterpret_cast<LinearRow4Fn>(address<void>(args[9]));
     Py_RETURN_NONE;
   });
 }
@@ -600,11 +604,16 @@ PyObject* linear4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const float* bias = bias_of(args[8], w.rows, device);
     void* stream = address<void>(args[9]);
     const auto opt = x.options().requires_grad(false);
-    const Made4 q(opt.dtype(at::kByte), x.size(0), K, kind);
     at::Tensor y = at::empty({x.size(0), w.rows}, opt);
-    int rc = quantize4_fn(h, q.rows, K, x.data_ptr(), ld, code, &q.m, stream);
-    if (rc == GEMM_OK)
-      rc = run4_fn(h, q.rows, w.rows, K, &q.m, &w.m, bias, y.data_ptr(), w.rows, code, stream);
+    int rc;
+    if (x.size(0) == 1 && K <= GEMM_FP4_ROW_MOST) {  // one launch
+      rc = linear_row4_fn(h, w.rows, K, x.data_ptr(), code, &w.m, bias, y.data_ptr(), code, stream);
+    } else {
+      const Made4 q(opt.dtype(at::kByte), x.size(0), K, kind);
+      rc = quantize4_fn(h, q.rows, K, x.data_ptr(), ld, code, &q.m, stream);
+      if (rc == GEMM_OK)
+        rc = run4_fn(h, q.rows, w.rows, K, &q.m, &w.m, bias, y.data_ptr(), w.rows, code, stream);
+    }
     if (rc != GEMM_OK) return PyLong_FromLong(rc);
     return THPVariable_Wrap(std::move(y));
   });

@@ -72,6 +72,21 @@ def test_read_back_and_product_refusals(handle):
     assert run(M=0) == 0 and run(N=0, ldc=0) == 0
 
 
+def test_row_of_a_layer_refusals(handle):
+    h, _ = handle
+    m = matrix()
+    def row(N=8, K=64, x=16, dtype=B.GEMM_BF16, W=m, bias=None, y=16, out=B.GEMM_BF16, handle=h):
+        return B.gemm_fp4_linear_row(handle, N, K, x, dtype, W, bias, y, out, None)
+    assert row(handle=None) == ERR and row(N=-1) == ERR and row(K=-1) == ERR
+    assert row(dtype=9) == ERR and row(out=-1) == ERR and row(x=None) == ERR and row(y=None) == ERR
+    assert row(W=matrix(ld=16)) == ERR and row(W=matrix(data=None)) == ERR
+    assert row(W=matrix(fmt=2)) == ERR
+    assert row(x=17) == UNSUPPORTED and row(y=18, out=B.GEMM_F32) == UNSUPPORTED
+    assert row(bias=18) == UNSUPPORTED and row(W=matrix(ld=40)) == UNSUPPORTED
+    assert row(K=65537, W=matrix(ld=1 << 16)) == UNSUPPORTED
+    assert row(N=2 ** 31) == UNSUPPORTED and row(N=0, x=None, y=None) == 0
+
+
 def ortho(**kw):
     abc = (ctypes.c_float * 192)(*([3.4445, -4.7750, 2.0315] * 64))
     p = dict(batch=1, rows=64, cols=32, steps=5, dtype=B.GEMM_F32,

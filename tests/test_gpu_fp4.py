@@ -556,3 +556,65 @@ def test_rows_after_their_operands_were_written(g, rows, fmt):
             o.zero_()
         graph.replay()
         assert all(torch.equal(o, v) for o, v in zip(outs, want))
+
+
+def same(a, b):
+    """Equal bits, of which NaN is any."""
+    return a.shape == b.shape and bool(((a == b) | (torch.isnan(a) & torch.isnan(b))).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("K", [1, 15, 16, 17, 33, 64, 1000, 4095, 4096, 4100, 10001, 65536, 65600])
+def test_one_row_of_a_layer_is_quantising_and_product(g, K, dtype, fmt):
+    """One launch, the bits of two: values of far magnitudes, zeros, non-finite ones, rows that
+    do not start on 16 bytes."""
+    rng = np.random.default_rng(K)
+    w = g.fp4_quantize(make(rng, 300, K).cuda().float(), fmt)
+    bias = torch.randn(300, device="cuda")
+    buf = make(rng, 1, K + 9, 3.0).cuda().to(dtype)
+    buf[0, 5] = 0
+    rows = [buf[:, :K], buf[:, 1:K + 1], buf[:, 9:], torch.zeros_like(buf[:, :K]),
+            buf[:, :K] * 1e-6, buf[:, :K] * 1e3]
+    for bad in (float("nan"), float("inf")):
+        x = buf[:, :K].clone()
+        x[0, K // 2] = bad
+        rows.append(x)
+    for x in rows:
+        for b in (None, bias):
+            want = g.fp4_matmul(g.fp4_quantize(x, fmt), w, b, out_dtype=dtype)
+            assert same(fp4.linear(g, x, w, b), want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_one_row_of_a_layer_elsewhere(g, fmt):
+    """Odd widths, another result type (the C entry), row scales of the weight, empty sizes, a
+    graph, another stream."""
+    rng = np.random.default_rng(1)
+    x = make(rng, 1, 1100).cuda().bfloat16()
+    for N in (1, 31, 129, 5000):
+        w = g.fp4_quantize(make(rng, N, 1100).cuda().float(), fmt)
+        w = Fp4Matrix(w.data, w.scale, torch.rand(2 * N, device="cuda")[::2], w.shape, fmt)
+        want = g.fp4_matmul(g.fp4_quantize(x, fmt), w, out_dtype=F32)
+        y = torch.full((N + 2,), 7.0, device="cuda")
+        assert B.gemm_fp4_linear_row(g.handle, N, 1100, x.data_ptr(), B.GEMM_BF16, w.desc(), None,
+                                     y[1:].data_ptr(), B.GEMM_F32,
+                                     torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(y[1:N + 1], want[0]) and float(y[0]) == 7 and float(y[N + 1]) == 7
+    want = fp4.linear(g, x, w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = fp4.linear(g, x, w, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    static, graph = torch.zeros_like(x), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fp4.linear(g, fp4.linear(g, static, w)[:, :1100].contiguous(), w)
+    static.copy_(x)
+    graph.replay()
+    assert torch.equal(out, fp4.linear(g, want[:, :1100].contiguous(), w))
+    bias = torch.randn(6, device="cuda")
+    empty = g.fp4_quantize(torch.zeros(6, 0, device="cuda"), fmt)
+    none = g.fp4_quantize(torch.zeros(0, 1100, device="cuda"), fmt)
+    assert torch.equal(fp4.linear(g, torch.zeros(1, 0, device="cuda"), empty, bias)[0], bias)
+    assert fp4.linear(g, x, none).shape == (1, 0)
