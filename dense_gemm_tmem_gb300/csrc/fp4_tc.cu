@@ -133,20 +133,22 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   const int64_t pairs = h->opt.pair_clusters > 0 ? h->opt.pair_clusters : sms / 2;
   // Fewer tiles than half the SMs: each tile's k-blocks over a cluster, the largest
   // whose clusters are all resident at once, if that takes more than kSplitGain
-  // k-blocks off each CTA (adding the partials costs about as long).  Measured (nvfp4, us,
-  // split / whole): 2 x 4096 x 4096 6.4 / 7.6, 2 x 1024 x 8192 5.6 / 11.8, 256 x 1024 x
-  // 4096 7.0 / 7.7, 512 x 512 x 8192 8.0 / 12.0, 16 x 512 x 2048 4.6 / 5.0; not taken: 32 x
-  // 2048 x 1024 4.7 / 4.1, 300 x 700 x 1024 5.5 / 4.6; more CTAs than SMs: 64 x 8192 x
-  // 8192 by 4 18.3, by 2, which fit, 12.4, whole 14.4.
-  constexpr int64_t kSplitGain = 4;
+  // k-blocks off each CTA (adding the partials costs about as long; one more where the tiles
+  // have 64 columns instead of 32).  Measured (nvfp4, us, split / whole), 32 columns: 1 x
+  // 4096 x 4096 6.4 / 7.6, 1 x 1024 x 8192 5.6 / 11.8 (rows forced here), 16 x 512 x 2048 4.6 / 5.0, 20 x 4096 x 2816
+  // 6.2 / 6.4; not taken 20 x 4096 x 2048 5.8 / 5.5, 20 x 1024 x 1792 4.8 / 4.8.  64 columns: 256
+  // x 1024 x 4096 7.0 / 7.7, 512 x 512 x 8192 8.0 / 12.0, 64 x 4096 x 4096 7.6 / 7.8; not taken
+  // 128 x 1024 x 2048 5.6 / 5.1, 64 x 2048 x 2560 6.5 / 6.0, 64 x 4096 x 3328 7.6 / 7.1.  More
+  // CTAs than SMs: 64 x 8192 x 8192 by 4 18.3, by 2, which fit, 12.4, whole 14.4.
+  constexpr int64_t kSplitGain = 6;
   const int forced = h->opt.csplit;  // GEMM_OPT_CLUSTER_SPLIT
-  auto split_of = [&](int64_t T) -> int64_t {
+  auto split_of = [&](int64_t T, int64_t gain) -> int64_t {
     if (forced < 2 && (forced >= 0 || 2 * T >= sms)) return 1;
     for (int s : {8, 4, 2}) {
       if (I < s) continue;  // a CTA without a k-block has no partial to add
       if (forced >= 2 ? s == forced && T * s <= INT32_MAX
                       : T <= h->opt.csplit_clusters[s] && T * s <= sms &&
-                            I - ceil_div(I, s) > kSplitGain)
+                            I - ceil_div(I, s) > gain)
         return s;
     }
     return 1;
@@ -174,7 +176,7 @@ cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   }
   const int64_t tiles_n = ceil_div(Nm, bn), T = tiles_m * tiles_n;
   if (T > INT32_MAX / 2) return cudaErrorInvalidValue;
-  const int64_t split = bn <= 128 ? split_of(T) : 1;
+  const int64_t split = bn <= 128 ? split_of(T, bn == 32 ? kSplitGain : kSplitGain + 1) : 1;
   Fp4TcArgs a{};
   a.work.tiles_m = int32_t(tiles_m);
   a.work.tiles_n = int32_t(tiles_n);

@@ -95,7 +95,7 @@ int gemm_fp4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp
 /* y = x·Wᵀ (+bias) for one row x of K elements (GEMM_F16, GEMM_BF16 or GEMM_F32),
  * quantised to W's format on the way, in one launch: the bits of
  * gemm_fp4_quantize and gemm_fp4_run (with its options at their defaults).
- * y: N elements of y_dtype.  N == 0: nothing is launched.  K == 0: y = bias (or 0).
+ * y: N elements of y_dtype, apart from x.  N == 0: nothing is launched.  K == 0: y = bias (or 0).
  * Errors: as theirs; UNSUPPORTED also for K above GEMM_FP4_ROW_MOST. */
 enum { GEMM_FP4_ROW_MOST = 65536 };
 int gemm_fp4_linear_row(gemm_handle_t h, int64_t N, int64_t K, const void* x, int x_dtype,
