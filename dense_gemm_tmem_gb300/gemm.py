@@ -371,23 +371,13 @@ class Gemm:
         return r
 
 
-_ABC = {}  # (coefficients, steps) -> their fp32 bytes, built once
-
-
 def _coefficients(coefficients, steps: int) -> bytes:
-    """a, b, c of every step as fp32."""
-    try:
-        key = (coefficients, steps)
-        got = _ABC.get(key)
-    except TypeError:  # a list, which is not kept
-        key = got = None
-    if got is None:
-        rows = list(coefficients)
-        if rows and not hasattr(rows[0], "__len__"):
-            rows = [rows] * steps
-        if len(rows) != steps or any(len(r) != 3 for r in rows):
-            raise ValueError("coefficients: one (a, b, c), or one for each of the %d steps" % steps)
-        got = array.array("f", (float(v) for r in rows for v in r)).tobytes()
-        if key is not None and len(_ABC) < 64:
-            _ABC[key] = got
-    return got
+    """a, b, c of every step as fp32, read on every call: a schedule may be changed in place."""
+    rows = list(coefficients)
+    one = bool(rows) and not hasattr(rows[0], "__len__")  # for every step
+    if one:
+        rows = [rows]
+    if len(rows) != (1 if one else steps) or any(len(r) != 3 for r in rows):
+        raise ValueError("coefficients: one (a, b, c), or one for each of the %d steps" % steps)
+    abc = array.array("f", [float(v) for r in rows for v in r]).tobytes()
+    return abc * steps if one else abc

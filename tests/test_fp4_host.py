@@ -297,6 +297,31 @@ def test_coefficients():
     assert np.array_equal(each, [1, 2, 3, 4, 5, 6])
 
 
+def test_coefficients_changed_in_place():
+    """What a caller's object holds now counts, not what it held in an earlier call."""
+    first, then = (3.4445, -4.7750, 2.0315), (1.875, -1.25, 0.375)
+    made = (lambda v: torch.tensor([v] * 3), lambda v: tuple(torch.tensor(v) for _ in range(3)),
+            lambda v: np.array([v] * 3, np.float32), lambda v: [list(v) for _ in range(3)],
+            lambda v: tuple([x for x in v] for _ in range(3)),
+            lambda v: tuple(tuple(torch.tensor(x) for x in v) for _ in range(3)))
+    for make in made:
+        abc = make(first)
+        want = np.tile(np.array(first, np.float32), 3)
+        assert np.array_equal(np.frombuffer(_coefficients(abc, 3), np.float32), want)
+        for row in abc:
+            for i, v in enumerate(then):
+                if isinstance(row, tuple):
+                    row[i].fill_(v)
+                else:
+                    row[i] = v
+        want = np.tile(np.array(then, np.float32), 3)
+        assert np.array_equal(np.frombuffer(_coefficients(abc, 3), np.float32), want)
+    one = [1.0, 2.0, 3.0]
+    _coefficients(one, 2)
+    one[0] = 5.0
+    assert np.array_equal(np.frombuffer(_coefficients(one, 2), np.float32), [5, 2, 3] * 2)
+
+
 def test_reference_rounds_to_the_nearest_value():
     """The oracle's e2m1 and e4m3 against a search of their values."""
     rng = np.random.default_rng(0)

@@ -91,6 +91,17 @@ def test_coefficients(g, rows, cols, abc, steps):
     check(g.orthogonalize(G, steps, abc), G, steps, abc)
 
 
+def test_coefficients_changed_in_place(g):
+    """A schedule held in tensors and changed between two calls."""
+    torch.manual_seed(12)
+    G = torch.randn(70, 130, device="cuda")
+    for abc in (torch.tensor([FAST] * 3), tuple(torch.tensor(FAST) for _ in range(3))):
+        assert torch.equal(g.orthogonalize(G, 3, abc), g.orthogonalize(G, 3, FAST))
+        for row in abc:
+            row.copy_(torch.tensor(CONVERGENT))
+        assert torch.equal(g.orthogonalize(G, 3, abc), g.orthogonalize(G, 3, CONVERGENT))
+
+
 def test_converges_to_the_polar_factor(g):
     torch.manual_seed(1)
     for rows, cols in ((96, 200), (300, 128)):
