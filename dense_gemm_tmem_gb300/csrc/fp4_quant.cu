@@ -215,9 +215,20 @@ struct BackArgs {
   int32_t chunks;    // CTAs along a row
 };
 
+// The largest e8m0 scales take values of 4 and 6 out of fp32, from where a row scale below 1
+// may bring them back: 3 of the block scale's powers of two then go with the row scale,
+// exactly, so that value times block scale stays exact.  FAR below: mxfp4 with a row scale
+// (as a test of the pointer in the kernel it cost mxfp4 without one 1.4 of 39.3 us).
+__device__ __forceinline__ void far_scale(float& block, float& row) {
+  if (block >= 0x1p126f && fabsf(row) < 1.f) {
+    block *= 0.125f;
+    row *= 8.f;
+  }
+}
+
 // ALIGNED: every row of dst starts on 16 bytes.  (8192^2 bf16 36.8 us, through the general
 // way 73; 1000 x 8191, which has to take it, 15.3, element by element 26.)
-template <typename T, int FMT, bool ALIGNED>
+template <typename T, int FMT, bool ALIGNED, bool FAR>
 __global__ void __launch_bounds__(kBackThreads) fp4_dequantize_kernel(const BackArgs a) {
   constexpr int kPer = 16 / sizeof(T);  // elements a thread
   const int tpr = 1 << a.tpr_log2, lanes = kBackThreads >> a.tpr_log2;
@@ -282,8 +293,12 @@ __global__ void __launch_bounds__(kBackThreads) fp4_dequantize_kernel(const Back
   for (int i = 0; i < kBackRows; ++i) {
     const int64_t r = r0 + i * lanes, c = first[i];
     if (r >= a.rows || c >= a.cols || c + kPer <= 0) continue;
-    const float f0 = fp4_scale_value(s[i][0], FMT);
-    const float f1 = ALIGNED ? f0 : fp4_scale_value(s[i][1], FMT);
+    float f0 = fp4_scale_value(s[i][0], FMT), g0 = g[i];
+    float f1 = ALIGNED ? f0 : fp4_scale_value(s[i][1], FMT), g1 = g0;
+    if constexpr (FAR) {
+      far_scale(f0, g0);
+      if constexpr (!ALIGNED) far_scale(f1, g1);
+    }
     // how many of the elements lie in the first of the two blocks
     const int in0 = ALIGNED ? kPer
                             : int(fp4_block(FMT) - (c > 0 ? c : 0) % fp4_block(FMT)) +
@@ -292,8 +307,9 @@ __global__ void __launch_bounds__(kBackThreads) fp4_dequantize_kernel(const Back
 #pragma unroll
     for (int j = 0; j < kPer / 2; ++j) {
       const float2 x = unpack_e2m1x2((q[i] >> (8 * j)) & 0xff);
-      const float v[2] = {__fmul_rn(x.x, 2 * j < in0 ? f0 : f1) * g[i],
-                          __fmul_rn(x.y, 2 * j + 1 < in0 ? f0 : f1) * g[i]};
+      const bool a0 = ALIGNED || 2 * j < in0, a1 = ALIGNED || 2 * j + 1 < in0;
+      const float v[2] = {__fmul_rn(x.x, a0 ? f0 : f1) * (a0 ? g0 : g1),
+                          __fmul_rn(x.y, a1 ? f0 : f1) * (a1 ? g0 : g1)};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if constexpr (sizeof(T) == 4) out[2 * j + k] = v[k];
@@ -331,11 +347,14 @@ cudaError_t launch_back(BackArgs a, cudaStream_t s) {
     kern<<<grid, kBackThreads, 0, s>>>(a);
     return cudaGetLastError();
   };
+  if (a.m.format == GEMM_MXFP4 && a.m.row_scale)
+    return aligned ? launch(fp4_dequantize_kernel<T, GEMM_MXFP4, true, true>)
+                   : launch(fp4_dequantize_kernel<T, GEMM_MXFP4, false, true>);
   if (a.m.format == GEMM_MXFP4)
-    return aligned ? launch(fp4_dequantize_kernel<T, GEMM_MXFP4, true>)
-                   : launch(fp4_dequantize_kernel<T, GEMM_MXFP4, false>);
-  return aligned ? launch(fp4_dequantize_kernel<T, GEMM_NVFP4, true>)
-                 : launch(fp4_dequantize_kernel<T, GEMM_NVFP4, false>);
+    return aligned ? launch(fp4_dequantize_kernel<T, GEMM_MXFP4, true, false>)
+                   : launch(fp4_dequantize_kernel<T, GEMM_MXFP4, false, false>);
+  return aligned ? launch(fp4_dequantize_kernel<T, GEMM_NVFP4, true, false>)
+                 : launch(fp4_dequantize_kernel<T, GEMM_NVFP4, false, false>);
 }
 
 int64_t pieces_of(int64_t cols, int format) {

@@ -172,6 +172,25 @@ def test_dequantize_every_code_and_scale(g, fmt):
         assert np.array_equal(got[ok], R.f32(want[ok]))
 
 
+@pytest.mark.parametrize("row", [0.25, -0.3, 1e-30, 2.0 ** -149, 0.0, 1.0, -1.5])
+def test_dequantize_the_largest_scales_with_a_row_scale(g, row):
+    """Value times block scale may lie beyond fp32 where the row scale brings it back: rows
+    that start on 16 bytes, and rows that start anywhere, whose 16 bytes meet two blocks."""
+    cols = 96
+    data = (torch.arange(48) * 37 % 256).to(torch.uint8).expand(4, 48).contiguous().cuda()
+    scale = torch.tensor([[254, 253, 252], [1, 254, 0], [253, 127, 254], [252, 254, 253]],
+                         dtype=torch.uint8, device="cuda")
+    m = Fp4Matrix.from_parts(data, scale, torch.tensor([row], device="cuda"), cols, "mxfp4")
+    want = R.f32(R.values(m))
+    assert np.array_equal(host(g.fp4_dequantize(m, F32)), want)
+    for pitch, offset in ((97, 3), (98, 1)):
+        buf = torch.zeros(4 * pitch + offset, device="cuda")
+        out = torch.as_strided(buf, (4, cols), (pitch, 1), offset)
+        assert B.gemm_fp4_dequantize(g.handle, 4, cols, m.desc(), out.data_ptr(), pitch, B.GEMM_F32,
+                                     torch.cuda.current_stream().cuda_stream) == B.GEMM_OK
+        assert np.array_equal(host(out), want)
+
+
 # -------------------------------------------------------------------- product --
 def bound(a, b, ra, rb, want, bias, dtype):
     """Exact products summed in fp32 in any order and with truncating adders lose at most
