@@ -637,3 +637,86 @@ def test_one_row_of_a_layer_elsewhere(g, fmt):
     none = g.fp4_quantize(torch.zeros(0, 1100, device="cuda"), fmt)
     assert torch.equal(fp4.linear(g, torch.zeros(1, 0, device="cuda"), empty, bias)[0], bias)
     assert fp4.linear(g, x, none).shape == (1, 0)
+
+
+# ------------------------------------------- splits at their ends, far scales, options --
+class Options:
+    """Options of a handle within a block."""
+
+    def __init__(self, g, **forced):
+        names = {"swap": B.GEMM_OPT_FORCE_SWAP_AB, "tile": B.GEMM_OPT_FORCE_TILE_N,
+                 "split": B.GEMM_OPT_CLUSTER_SPLIT}
+        self.g, self.forced = g, {names[k]: v for k, v in forced.items()}
+
+    def __enter__(self):
+        for o, v in self.forced.items():
+            self.g.set_option(o, v)
+
+    def __exit__(self, *_):
+        for o in self.forced:
+            self.g.set_option(o, -1)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("split", [2, 4, 8])
+@pytest.mark.parametrize("K", [200, 257, 513, 1281, 1400, 1537, 1790, 1793, 2049, 2305])
+@pytest.mark.parametrize("M,N,swap,tile", [(1, 300, 1, -1), (3, 64, 1, -1), (50, 200, 1, -1),
+                                           (70, 200, 0, 64), (70, 200, 0, 128)])
+def test_forced_splits_over_few_k_blocks(g, M, N, swap, tile, K, split, fmt):
+    """1 to 10 k-blocks over 2, 4 and 8 CTAs: as many as CTAs, one more, uneven shares, and
+    fewer, which are not split.  One row stays on the tensor cores."""
+    rng = np.random.default_rng(K + split)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    with Options(g, swap=swap, tile=tile, split=split):
+        for _ in range(2):
+            check_product(g.fp4_matmul(A, Bm, out_dtype=F32), A, Bm)
+    g.status()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K", [1536, 1537, 1792, 1793, 2048, 2049, 2304, 2305, 2560, 2561])
+@pytest.mark.parametrize("M,N", [(3, 64), (20, 1000), (70, 200), (128, 1024)])
+def test_splits_around_their_rule(g, M, N, K, fmt):
+    """No option set: 6 to 11 k-blocks, from which on a split pays, on both sides."""
+    rng = np.random.default_rng(K)
+    A = g.fp4_quantize(make(rng, M, K).cuda().float(), fmt)
+    Bm = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    for _ in range(2):
+        check_product(g.fp4_matmul(A, Bm, out_dtype=F32), A, Bm)
+    g.status()
+
+
+@pytest.mark.parametrize("ea,eb", [((0, 3), (250, 255)), ((250, 255), (0, 3)), ((0, 2), (126, 130)),
+                                   ((126, 129), (0, 2)), ((127, 128), (225, 230)),
+                                   ((60, 70), (180, 190))])
+@pytest.mark.parametrize("M,forced", [(1, {}), (1, dict(swap=1)), (2, {}), (33, {}), (40, {}),
+                                      (40, dict(swap=1, split=2)), (300, {}), (300, dict(tile=64)),
+                                      (300, dict(tile=256)), (70, dict(split=2))])
+def test_products_of_far_scales(g, M, forced, ea, eb):
+    """mxfp4 scales at fp32's ends, their product inside, on the tensor cores too."""
+    rng = np.random.default_rng(3)
+    A, Bm = codes(rng, M, 320, "mxfp4", *ea), codes(rng, 140, 320, "mxfp4", *eb)
+    (a, _), (b, _) = parts(A), parts(Bm)
+    want = a @ b.T
+    with Options(g, **forced):
+        got = host(g.fp4_matmul(A, Bm, out_dtype=F32))
+    # as for one row: truncating additions, and half of fp32's least step for each
+    tol = (np.abs(a) @ np.abs(b).T) * 320 * 2.0 ** -23 + 320 * 2.0 ** -150
+    assert (np.abs(got - want) <= tol).all()
+    g.status()
+
+
+def test_one_row_and_two_agree_on_far_scales(g):
+    """The same row alone (CUDA cores) and twice (tensor cores): each within its bound."""
+    rng = np.random.default_rng(4)
+    for ea, eb in (((0, 3), (250, 255)), ((126, 129), (0, 2)), ((127, 128), (225, 230))):
+        two, Bm = codes(rng, 2, 320, "mxfp4", *ea), codes(rng, 140, 320, "mxfp4", *eb)
+        data = two.data[:1].expand(2, 160).contiguous()
+        byte = two.block_scales()[:1].expand(2, 10).contiguous()
+        two = Fp4Matrix.from_parts(data, byte, None, 320, "mxfp4")
+        one = Fp4Matrix.from_parts(data[:1], byte[:1], None, 320, "mxfp4")
+        (a, _), (b, _) = parts(one), parts(Bm)
+        tol = 2 * ((np.abs(a) @ np.abs(b).T) * 320 * 2.0 ** -23 + 320 * 2.0 ** -150)
+        y1, y2 = (host(g.fp4_matmul(m, Bm, out_dtype=F32)) for m in (one, two))
+        assert np.array_equal(y2[0], y2[1]) and (np.abs(y1 - y2[:1]) <= tol).all()

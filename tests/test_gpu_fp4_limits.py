@@ -34,3 +34,19 @@ def test_product_under_short_limits(h, M, N, K, tile, fmt):
         limited(h, lambda: [h.fp4_matmul(a, b)], [1, 300, 1000, 3000, 10000, 30000])
     finally:
         h.set_option(B.GEMM_OPT_FORCE_TILE_N, -1)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,split", [(1, -1), (1, 2), (20, 8), (50, 4)])
+def test_swapped_product_under_short_limits(h, M, split, fmt):
+    """One row kept on the tensor cores, and splits over 2, 4 and 8 CTAs."""
+    torch.manual_seed(M)
+    a = h.fp4_quantize(torch.randn(M, 4096, device="cuda"), fmt)
+    b = h.fp4_quantize(torch.randn(1500, 4096, device="cuda"), fmt)
+    h.set_option(B.GEMM_OPT_FORCE_SWAP_AB, 1)
+    h.set_option(B.GEMM_OPT_CLUSTER_SPLIT, split)
+    try:
+        limited(h, lambda: [h.fp4_matmul(a, b)], [1, 300, 1000, 3000, 10000, 30000])
+    finally:
+        h.set_option(B.GEMM_OPT_FORCE_SWAP_AB, -1)
+        h.set_option(B.GEMM_OPT_CLUSTER_SPLIT, -1)
