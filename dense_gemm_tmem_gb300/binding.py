@@ -158,6 +158,7 @@ def load(build_if_missing: bool = True):
         "gemm_fp4_run": (c_int, [c_void_p, c_int64, c_int64, c_int64, P(gemm_fp4_matrix_t),
                                  P(gemm_fp4_matrix_t), c_void_p, c_void_p, c_int64, c_int,
                                  c_void_p]),
+        "gemm_fp4_one_row": (c_int, [c_void_p, c_int64, c_int64]),
         "gemm_fp4_linear_row": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int,
                                         P(gemm_fp4_matrix_t), c_void_p, c_void_p, c_int,
                                         c_void_p]),
@@ -190,7 +191,8 @@ def native():
         mod.init(*(ctypes.cast(getattr(lib, f), c_void_p).value for f in (
             "gemm_fp8_quantize", "gemm_fp8_run", "gemm_moe_fp8_workspace", "gemm_moe_fp8",
             "gemm_fp4_quantize", "gemm_fp4_dequantize", "gemm_fp4_run",
-            "gemm_orthogonalize_workspace", "gemm_orthogonalize", "gemm_fp4_linear_row")))
+            "gemm_orthogonalize_workspace", "gemm_orthogonalize", "gemm_fp4_linear_row",
+            "gemm_fp4_one_row")))
         _native = mod
     return _native
 
@@ -346,6 +348,10 @@ def gemm_fp4_dequantize(h, rows, cols, m, dst_ptr, ld_dst, dst_dtype, stream_ptr
 def gemm_fp4_run(h, M, N, K, A, Bm, bias_ptr, C_ptr, ldc, out_dtype, stream_ptr) -> int:
     return load().gemm_fp4_run(c_void_p(h), M, N, K, ctypes.byref(A), ctypes.byref(Bm), bias_ptr,
                                C_ptr, ldc, out_dtype, stream_ptr)
+
+
+def gemm_fp4_one_row(h, N, K) -> int:
+    return load().gemm_fp4_one_row(c_void_p(h), N, K)
 
 
 def gemm_fp4_linear_row(h, N, K, x_ptr, x_dtype, W, bias_ptr, y_ptr, y_dtype, stream_ptr) -> int:

@@ -105,15 +105,18 @@ __global__ void fp4_fill_kernel(int64_t M, int64_t N, const float* bias, void* C
 
 }  // namespace
 
+// One row: a kernel of its own (4096 x 4096 3.7 us against 6.4, all sizes in fp4_row.cu),
+// unless an option asks for a form of the tensor cores'.
+bool fp4_one_row(const gemm_ctx* h, int64_t N, int64_t K) {
+  return h->opt.force_swap < 0 && h->opt.csplit < 0 && h->opt.force_tile_n <= 0;
+}
+
 cudaError_t launch_fp4(gemm_ctx* h, const Fp4Product& p, cudaStream_t stream) {
   if (p.K == 0) {
     fp4_fill_kernel<<<1024, 256, 0, stream>>>(p.M, p.N, p.bias, p.C, p.ldc, p.out_dtype);
     return cudaGetLastError();
   }
-  // One row: a kernel of its own (4096 x 4096 3.7 us against 6.4, all sizes in fp4_row.cu),
-  // unless an option asks for a form of the tensor cores'.
-  if (p.M == 1 && h->opt.force_swap < 0 && h->opt.csplit < 0 && h->opt.force_tile_n <= 0)
-    return launch_fp4_row(h, p, nullptr, 0, stream);
+  if (p.M == 1 && fp4_one_row(h, p.N, p.K)) return launch_fp4_row(h, p, nullptr, 0, stream);
   const int64_t I = ceil_div(p.K, kF4BlockK);
   // Few rows of A: operands swapped, so that the other side fills the 128 MMA rows and
   // A's rows are the MMA's columns, 32 or 64 of them.  Measured (mxfp4, graph replay, cold

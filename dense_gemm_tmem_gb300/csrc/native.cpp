@@ -32,6 +32,7 @@ using Run4Fn = int (*)(gemm_handle_t, int64_t, int64_t, int64_t, const gemm_fp4_
                        const gemm_fp4_matrix_t*, const float*, void*, int64_t, int, void*);
 using LinearRow4Fn = int (*)(gemm_handle_t, int64_t, int64_t, const void*, int,
                              const gemm_fp4_matrix_t*, const float*, void*, int, void*);
+using OneRow4Fn = int (*)(gemm_handle_t, int64_t, int64_t);
 using OrthoSpaceFn = int (*)(gemm_handle_t, const gemm_orthogonalize_t*, int64_t*);
 using OrthoFn = int (*)(gemm_handle_t, const gemm_orthogonalize_t*, void*, int64_t, void*);
 QuantizeFn quantize_fn = nullptr;
@@ -44,6 +45,7 @@ Run4Fn run4_fn = nullptr;
 OrthoSpaceFn ortho_space_fn = nullptr;
 OrthoFn ortho_fn = nullptr;
 LinearRow4Fn linear_row4_fn = nullptr;
+OneRow4Fn one_row4_fn = nullptr;
 
 constexpr int64_t kBlock = 128;
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
@@ -128,7 +130,7 @@ PyObject* guarded(F&& f) {
 
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    if (n != 10) fail(PyExc_TypeError, "init takes 10 addresses");
+    if (n != 11) fail(PyExc_TypeError, "init takes 11 addresses");
     quantize_fn = reinterpret_cast<QuantizeFn>(address<void>(args[0]));
     run_fn = reinterpret_cast<RunFn>(address<void>(args[1]));
     moe_space_fn = reinterpret_cast<MoeSpaceFn>(address<void>(args[2]));
@@ -139,6 +141,7 @@ PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
     ortho_space_fn = reinterpret_cast<OrthoSpaceFn>(address<void>(args[7]));
     ortho_fn = reinterpret_cast<OrthoFn>(address<void>(args[8]));
     linear_row4_fn = reinterpret_cast<LinearRow4Fn>(address<void>(args[9]));
+    one_row4_fn = reinterpret_cast<OneRow4Fn>(address<void>(args[10]));
     Py_RETURN_NONE;
   });
 }
@@ -606,7 +609,7 @@ PyObject* linear4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const auto opt = x.options().requires_grad(false);
     at::Tensor y = at::empty({x.size(0), w.rows}, opt);
     int rc;
-    if (x.size(0) == 1 && K <= GEMM_FP4_ROW_MOST) {  // one launch
+    if (x.size(0) == 1 && K <= GEMM_FP4_ROW_MOST && one_row4_fn(h, w.rows, K)) {  // one launch
       rc = linear_row4_fn(h, w.rows, K, x.data_ptr(), code, &w.m, bias, y.data_ptr(), code, stream);
     } else {
       const Made4 q(opt.dtype(at::kByte), x.size(0), K, kind);

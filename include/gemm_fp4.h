@@ -92,9 +92,16 @@ int gemm_fp4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp
                  const gemm_fp4_matrix_t *B, const float *bias, void *C, int64_t ldc,
                  int out_dtype, void *stream);
 
+/* 1 where gemm_fp4_run takes one row of A on the CUDA cores, whose bits
+ * gemm_fp4_linear_row gives; 0 where it takes it on the tensor cores: an option
+ * asks for one of their forms (GEMM_OPT_FORCE_SWAP_AB, _FORCE_TILE_N,
+ * _CLUSTER_SPLIT).  Also 0 for no handle or a negative size. */
+int gemm_fp4_one_row(gemm_handle_t h, int64_t N, int64_t K);
+
 /* y = x·Wᵀ (+bias) for one row x of K elements (GEMM_F16, GEMM_BF16 or GEMM_F32),
- * quantised to W's format on the way, in one launch: the bits of
- * gemm_fp4_quantize and gemm_fp4_run (with its options at their defaults).
+ * quantised to W's format on the way, in one launch on the CUDA cores whatever
+ * the options: the bits of gemm_fp4_quantize and gemm_fp4_run where
+ * gemm_fp4_one_row is 1.
  * y: N elements of y_dtype, apart from x.  N == 0: nothing is launched.  K == 0: y = bias (or 0).
  * Errors: as theirs; UNSUPPORTED also for K above GEMM_FP4_ROW_MOST. */
 enum { GEMM_FP4_ROW_MOST = 65536 };

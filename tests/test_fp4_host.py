@@ -87,6 +87,12 @@ def test_row_of_a_layer_refusals(handle):
     assert row(N=2 ** 31) == UNSUPPORTED and row(N=0, x=None, y=None) == 0
 
 
+def test_one_row_asks_for_a_handle_and_sizes(handle):
+    h, _ = handle
+    assert B.gemm_fp4_one_row(None, 8, 64) == 0
+    assert B.gemm_fp4_one_row(h, -1, 64) == 0 and B.gemm_fp4_one_row(h, 8, -1) == 0
+
+
 def ortho(**kw):
     abc = (ctypes.c_float * 192)(*([3.4445, -4.7750, 2.0315] * 64))
     p = dict(batch=1, rows=64, cols=32, steps=5, dtype=B.GEMM_F32,

@@ -720,3 +720,22 @@ def test_one_row_and_two_agree_on_far_scales(g):
         tol = 2 * ((np.abs(a) @ np.abs(b).T) * 320 * 2.0 ** -23 + 320 * 2.0 ** -150)
         y1, y2 = (host(g.fp4_matmul(m, Bm, out_dtype=F32)) for m in (one, two))
         assert np.array_equal(y2[0], y2[1]) and (np.abs(y1 - y2[:1]) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("forced", [{}, dict(swap=1), dict(swap=0), dict(tile=64), dict(tile=128),
+                                    dict(split=4), dict(swap=1, split=0)])
+def test_one_row_of_a_layer_follows_the_options(g, forced, dtype, fmt):
+    """The layer's bits are those of the two calls on the same handle, whatever is forced."""
+    rng = np.random.default_rng(8)
+    x = make(rng, 1, 2500).cuda().to(dtype)
+    w = g.fp4_quantize(make(rng, 300, 2500).cuda().float(), fmt)
+    bias = torch.randn(300, device="cuda")
+    with Options(g, **forced):
+        assert B.gemm_fp4_one_row(g.handle, 300, 2500) == (not forced)
+        for b in (None, bias):
+            want = g.fp4_matmul(g.fp4_quantize(x, fmt), w, b, out_dtype=dtype)
+            assert torch.equal(fp4.linear(g, x, w, b), want)
+            check_product(want, g.fp4_quantize(x, fmt), w, b)
+    g.status()
