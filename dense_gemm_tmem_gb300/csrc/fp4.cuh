@@ -70,7 +70,7 @@ cudaError_t launch_fp4_quantize(int64_t rows, int64_t cols, const void* src, int
 cudaError_t launch_fp4_dequantize(int64_t rows, int64_t cols, const gemm_fp4_matrix_t& m,
                                   void* dst, int64_t ld_dst, int dst_dtype, cudaStream_t stream);
 // Whether gemm_fp4_run takes one row of A on the CUDA cores.
-bool fp4_one_row(const gemm_ctx* h, int64_t N, int64_t K);
+bool fp4_one_row(const gemm_ctx* h, int64_t N);
 // One row of A; where `x` is given, K elements of its type, they are quantised on the way and
 // p.A is not looked at.
 cudaError_t launch_fp4_row(gemm_ctx* h, const Fp4Product& p, const void* x, int x_dtype,

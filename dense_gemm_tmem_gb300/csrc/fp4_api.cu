@@ -93,7 +93,7 @@ int gemm_fp4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp
 }
 
 int gemm_fp4_one_row(gemm_handle_t h, int64_t N, int64_t K) {
-  return h && N >= 0 && K >= 0 && dg::fp4_one_row(h, N, K);
+  return h && N >= 0 && K >= 0 && dg::fp4_one_row(h, N);
 }
 
 int gemm_fp4_linear_row(gemm_handle_t h, int64_t N, int64_t K, const void* x, int x_dtype,

@@ -93,9 +93,9 @@ int gemm_fp4_run(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const gemm_fp
                  int out_dtype, void *stream);
 
 /* 1 where gemm_fp4_run takes one row of A on the CUDA cores, whose bits
- * gemm_fp4_linear_row gives; 0 where it takes it on the tensor cores: an option
- * asks for one of their forms (GEMM_OPT_FORCE_SWAP_AB, _FORCE_TILE_N,
- * _CLUSTER_SPLIT).  Also 0 for no handle or a negative size. */
+ * gemm_fp4_linear_row gives; 0 where it takes it on the tensor cores: N is 2^15
+ * or more, or an option asks for one of their forms (GEMM_OPT_FORCE_SWAP_AB,
+ * _FORCE_TILE_N, _CLUSTER_SPLIT).  Also 0 for no handle or a negative size. */
 int gemm_fp4_one_row(gemm_handle_t h, int64_t N, int64_t K);
 
 /* y = x·Wᵀ (+bias) for one row x of K elements (GEMM_F16, GEMM_BF16 or GEMM_F32),

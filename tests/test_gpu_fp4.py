@@ -739,3 +739,27 @@ def test_one_row_of_a_layer_follows_the_options(g, forced, dtype, fmt):
             assert torch.equal(fp4.linear(g, x, w, b), want)
             check_product(want, g.fp4_quantize(x, fmt), w, b)
     g.status()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("N", [24576, 32767, 32768, 32769, 65536])
+def test_one_row_on_both_sides_of_its_rule(g, N, fmt):
+    """Up to 2^15 rows of B on the CUDA cores, in several rounds of CTAs; more on the tensor
+    cores; a layer's row the same bits as two calls on both."""
+    K = 150
+    assert B.gemm_fp4_one_row(g.handle, N, K) == (N < 32768)
+    rng = np.random.default_rng(N)
+    w = g.fp4_quantize(make(rng, N, K).cuda().float(), fmt)
+    x = make(rng, 1, K).cuda().bfloat16()
+    bias = torch.randn(N, device="cuda")
+    for b in (None, bias):
+        q = g.fp4_quantize(x, fmt)
+        C = g.fp4_matmul(q, w, b, out_dtype=F32)
+        check_product(C, q, w, b)
+        assert torch.equal(fp4.linear(g, x, w, b), g.fp4_matmul(q, w, b, out_dtype=BF16))
+    y = torch.empty(1, N, device="cuda")  # the row's kernel itself
+    assert B.gemm_fp4_linear_row(g.handle, N, K, x.data_ptr(), B.GEMM_BF16, w.desc(),
+                                 bias.data_ptr(), y.data_ptr(), B.GEMM_F32,
+                                 torch.cuda.current_stream().cuda_stream) == 0
+    check_product(y, q, w, bias)
+    g.status()
