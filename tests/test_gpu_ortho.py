@@ -313,3 +313,42 @@ def test_under_short_wait_limits(g, pair, tile_n):
     finally:
         g.set_option(B.GEMM_OPT_PAIR, -1)
         g.set_option(B.GEMM_OPT_FORCE_TILE_N, -1)
+
+
+def check_elements(got, G, steps, abc):
+    """Every element by itself.  Its error is a sum of hundreds of roundings to fp16, as the
+    simulation's is, whose rms over the element's row or column (the larger) is s; the two
+    need not round alike, but a sum of independent bounded roundings is beyond 10 s once in
+    e^50 (Hoeffding).  Truncating fp32 sums of 5000 products lose 2^-23 of themselves for each
+    16, a tenth of what 2^-12 of each operand makes of them.  The result's rounding to bfloat16
+    comes on top, half a step, 2^-8.  An element that is missing or another's is off by its
+    own size: some 500 s."""
+    exact = simulate(G, steps, abc, round16=False)
+    e = (simulate(G, steps, abc) - exact).square()
+    s = torch.maximum(e.mean(1, keepdim=True).sqrt(), e.mean(0, keepdim=True).sqrt())
+    tol = 2.0 ** -8 * exact.abs() + 10 * (1 + 2.0 ** -8) * s
+    off = (got.double() - exact).abs()
+    bad = ~(off <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:5].tolist(), float((off / tol).max()))
+
+
+@pytest.mark.parametrize("pair,tile_n", [(-1, -1), (0, -1), (1, 128), (1, 256)])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 130, 70), (1, 64, 257), (1, 257, 64), (2, 300, 600),
+                                             (3, 600, 270), (1, 515, 1000), (1, 1000, 515),
+                                             (2, 700, 1000), (1, 129, 2056), (1, 40, 5000)])
+def test_every_element_on_every_tile(g, pair, tile_n, batch, rows, cols):
+    """Tile corners, ragged ends and mirrored blocks, of which a matrix's norm says little."""
+    torch.manual_seed(rows + 2 * cols)
+    G = torch.randn(batch, rows, cols, device="cuda")
+    G[-1] = gradient(rows, cols, F32)
+    g.set_option(B.GEMM_OPT_PAIR, pair)
+    g.set_option(B.GEMM_OPT_FORCE_TILE_N, tile_n)
+    try:
+        for steps, abc in ((5, FAST), (3, CONVERGENT)):
+            got = g.orthogonalize(G, steps, abc)
+            for i in range(batch):
+                check_elements(got[i], G[i], steps, abc)
+        g.status()
+    finally:
+        g.set_option(B.GEMM_OPT_PAIR, -1)
+        g.set_option(B.GEMM_OPT_FORCE_TILE_N, -1)
