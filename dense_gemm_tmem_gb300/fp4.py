@@ -81,7 +81,7 @@ class Fp4Matrix:
     column in the low half of each byte, unit stride along its rows, which start on
     16 bytes (rows padded to 16, as ``fp4_quantize`` pads them); the high half of an
     odd row's last byte is 0.  ``scale`` is the flat tensor of block scales in their
-    stored order (see ``pack_scales``), ``row_scale`` None or float32 (rows,), of any
+    stored order (see ``pack_scales``), nvfp4's with no sign bit set, ``row_scale`` None or float32 (rows,), of any
     stride (``scale.expand(rows)`` for one scale of the whole matrix).  The tensors
     are referenced, not copied; replacing them in place is seen by later calls."""
 
@@ -148,7 +148,8 @@ class Fp4Matrix:
 
 def linear(g, x: torch.Tensor, w: Fp4Matrix, bias: torch.Tensor | None = None, stream=None):
     """x·wᵀ (+bias) in x's type on handle ``g``, x (tokens, inputs) float16, bfloat16 or
-    float32 quantised to w's format row by row (a token's result does not depend on
-    the others), w an Fp4Matrix (outputs, inputs), bias float32 (outputs,).  It carries
-    no gradient.  With a stream: as `Gemm.fp4_matmul`."""
+    float32 quantised to w's format row by row (what a token is quantised to does not
+    depend on the others; its sums are made in an order that depends on how many there
+    are, so that their last fp32 bits may), w an Fp4Matrix (outputs, inputs), bias
+    float32 (outputs,).  It carries no gradient.  With a stream: as `Gemm.fp4_matmul`."""
     return g.fp4_linear(x, w, bias, stream)

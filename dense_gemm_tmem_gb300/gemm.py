@@ -350,7 +350,7 @@ class Gemm:
         float32 with unit stride along the rows, with its singular values driven
         towards 1 by Newton-Schulz steps: X = G / max(|G|, eps), then X = aX + (bA +
         cA²)X with A = X·Xᵀ.  coefficients: (a, b, c) for every step, or one such
-        triple per step.  The default takes the singular values to about 0.7 ... 1.2
+        triple per step, read on the host during the call.  The default takes the singular values to about 0.7 ... 1.2
         in 5 steps; (1.875, -1.25, 0.375) converges to 1, more slowly.  Returns
         bfloat16, which carries no gradient.  The products' operands are 16-bit, so
         the result is right to about 2e-3 of its norm."""

@@ -42,7 +42,8 @@ enum { GEMM_MXFP4 = 0, GEMM_NVFP4 = 1 };
  *   scale[((r / 128) * ceil(blocks / 4) + b / 4) * 512
  *         + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4],
  * blocks = ceil(cols / 32 or 16); bytes of a piece past the matrix are 0
- * (gemm_fp4_scale_bytes gives the size).  data and scale are 16-byte aligned
+ * (gemm_fp4_scale_bytes gives the size).  A product's e4m3 scales have a sign
+ * bit of 0: the tensor cores have no sign there (reading back takes either).  data and scale are 16-byte aligned
  * and ld is a multiple of 16. */
 typedef struct {
   void *data;
