@@ -11,9 +11,9 @@
 // count: 16-bit elements stay packed and maxima are taken of magnitudes as integers
 // (which order like the numbers), and a row's division by its blocks' scales, which
 // have 8 different mantissas, is made once for each of those (8192^2 bf16 nvfp4 54 us
-// before, 34 now, 5.1 TB/s; mxfp4, which waits for no row, 31).
-// Reading back is bound by its stores: 8192^2 bf16 40 us, where filling as many bytes
-// takes 35.5; streaming stores, 2 or 8 rows a thread instead of 4: 41 to 44.
+// before, 32 now, 5.4 TB/s; mxfp4, which waits for no row, 30; graph replay, as below).
+// Reading back is bound by its stores: 8192^2 bf16 38 us (mxfp4 39), where filling as many
+// bytes takes 35.4; streaming stores, 2 or 8 rows a thread instead of 4: 3 to 10 % more.
 #include "fp4_quant.cuh"
 
 namespace dg {
@@ -226,8 +226,8 @@ __device__ __forceinline__ void far_scale(float& block, float& row) {
   }
 }
 
-// ALIGNED: every row of dst starts on 16 bytes.  (8192^2 bf16 36.8 us, through the general
-// way 73; 1000 x 8191, which has to take it, 15.3, element by element 26.)
+// ALIGNED: every row of dst starts on 16 bytes.  (8192^2 bf16 38 us, through the general
+// way twice that; 1000 x 8191, which has to take it, 14, element by element 26.)
 template <typename T, int FMT, bool ALIGNED, bool FAR>
 __global__ void __launch_bounds__(kBackThreads) fp4_dequantize_kernel(const BackArgs a) {
   constexpr int kPer = 16 / sizeof(T);  // elements a thread

@@ -18,11 +18,13 @@
 // exact in fp32, and its scale and the sum along K are applied there.
 //
 // Measured (graph replay, cold B, us, N x K, nvfp4 / mxfp4; in brackets on the tensor cores,
-// fp4_tc_kernel.cuh): 4096 x 4096 3.7 / 3.6 (6.4 / 6.1), 1024 x 1024 1.9 / 1.9 (3.7 / 3.5), 1024 x
-// 8192 3.3 / 3.3 (5.6 / 5.4), 8192 x 1024 3.3 / 3.3 (4.4 / 4.3), 8192 x 8192 9.9 / 10.0 (10.8 /
-// 10.5), 4100 x 4100 5.2 / 5.3 (6.7 / 6.4).  An almost empty launch takes 1.8; over that, 4096 x
-// 4096 moves 5.0 TB/s and 8192 x 8192 4.7.  The loads' latency bounds it: 32 warps an SM, each
-// of which first loads and then computes, fill half of the issue slots, and DRAM a third.
+// fp4_tc_kernel.cuh): 4096 x 4096 3.7 / 3.7 (6.2 / 5.9), 1024 x 1024 2.2 / 2.3 (3.7 / 3.5), 1024 x
+// 8192 3.2 / 3.2 (5.5 / 5.2), 8192 x 1024 3.3 / 3.3 (4.4 / 4.3), 8192 x 8192 9.9 / 9.8 (11.2 /
+// 10.7), 4100 x 4100 5.1 / 5.2 (6.7 / 6.4); more, and where the tensor cores take over, in
+// fp4_tc.cu.  An almost empty launch takes 1.8; over that, 4096 x 4096 moves 5.0 TB/s and 8192 x
+// 8192 4.7.  The loads' latency bounds it: 32 warps an SM, each of which first loads and then
+// computes, use 21 % of the issue slots and 17 % of DRAM's time at 4096 x 4096, 34 and 37 % at
+// 8192 x 8192 (of a profiled launch with cold caches, 7.0 and 12.8 us).
 // Dropped: the next piece's loads ahead of this one's sums, in more registers and
 // so with fewer warps (4.5 and 10.7), nothing sent for ahead of the stream (4.5 and 10.3, both
 // before the row's scales were read at the start), every next piece sent for to L2 too (3.8
@@ -31,8 +33,8 @@
 // cores take 11).
 // A layer's row, quantised on the way: every CTA quantises all of it for itself, the steps of
 // fp4_quant.cu, into shared memory, which spares a launch and its latency.  One launch / two
-// (us, bf16 in and out, nvfp4, mxfp4): 4096 x 4096 4.7 / 5.8, 4.5 / 5.5, 1024 x 1024 2.5 / 3.9, 2.4 /
-// 3.8, 8192 x 8192 12.5 / 12.9, 11.7 / 12.3, 1024 x 65536 31 / 32, 25 / 28, and 3.8 of the host's
+// (us, bf16 in and out, nvfp4, mxfp4): 4096 x 4096 4.5 / 5.3, 4.3 / 5.0, 1024 x 1024 2.9 / 4.1, 2.6 /
+// 3.9, 8192 x 8192 12.1 / 12.8, 11.0 / 12.0, 1024 x 65536 27 / 29, 23 / 25, and 3.8 of the host's
 // time instead of 6.5.  (Quantised by every warp in registers: they spill.)
 #include "context.h"
 #include "fp4_quant.cuh"

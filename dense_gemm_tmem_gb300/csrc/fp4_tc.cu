@@ -105,18 +105,19 @@ __global__ void fp4_fill_kernel(int64_t M, int64_t N, const float* bias, void* C
 
 }  // namespace
 
-// One row: a kernel of its own, unless an option asks for a form of the tensor cores' or B
-// has so many rows that its warps, four rows each, come in 1.7 rounds or more.
-// Measured (graph replay, cold B, us, own kernel / tensor cores, nvfp4, mxfp4; in brackets a
-// layer, one launch / quantising and tensor cores).  N x K, its own: 4096 x 4096 3.7 / 6.2, 3.7 /
-// 5.9 [4.5 / 7.2, 4.3 / 6.7], 16 x 4096 1.8 / 4.0, 1.9 / 3.8, 64 x 65536 9.4 / 12.4, 9.5 / 11.5,
-// 8192 x 8192 9.9 / 11.2, 9.8 / 10.7 [12.1 / 13.3, 11.0 / 11.8], 14336 x 4096 9.1 / 9.0, 9.3 / 8.6
-// [10.0 / 10.5, 10.0 / 10.0], 24576 x 4096 15.5 / 15.7, 15.9 / 14.6 [16.0 / 17.6, 16.2 / 16.5], 2048
-// x 65536 17 / 24, 18 / 22.  The tensor cores': 32768 x 4096 18.2 / 16.4, 18.2 / 15.7 [18.7 / 18.6,
-// 18.7 / 17.6], 65536 x 1024 11.7 / 11.1, 11.8 / 10.1 [14.0 / 13.2, 12.2 / 12.1], 128256 x 4096 53 /
-// 48, 55 / 45 [57 / 50, 59 / 47].  Between them the rule misses up to a fifth where the warps
-// leave half of the SMs' places empty (10240 x 8192 15.4 / 13.6, 16.2 / 12.8 [17.4 / 16.5, 17.4 /
-// 14.4]) and where K is deep (1024 x 100000 20.7 / 19.6, 21.8 / 18.6).
+// One row: a kernel of its own, unless an option asks for a form of the tensor cores' or B has
+// so many rows that its warps, four rows each, come in 1.7 rounds or more. Measured (graph
+// replay, cold B, us, own kernel / tensor cores, nvfp4, mxfp4; in brackets a layer, one launch
+// / quantising and tensor cores).  N x K, its own: 4096 x 4096 3.7 / 6.2, 3.7 / 5.9 [4.5 /
+// 7.2, 4.3 / 6.7], 16 x 4096 1.8 / 4.0, 1.9 / 3.8, 64 x 65536 9.4 / 12.4, 9.5 / 11.5, 8192 x
+// 8192 9.9 / 11.2, 9.8 / 10.7 [12.1 / 13.3, 11.0 / 11.8], 14336 x 4096 9.1 / 9.0, 9.3 / 8.6
+// [10.0 / 10.5, 10.0 / 10.0], 24576 x 4096 15.5 / 15.7, 15.9 / 14.6 [16.0 / 17.6, 16.2 /
+// 16.5], 2048 x 65536 17 / 24, 18 / 22.  The tensor cores': 32768 x 4096 18.2 / 16.4, 18.2 /
+// 15.7 [18.7 / 18.6, 18.7 / 17.6], 65536 x 1024 11.7 / 11.1, 11.8 / 10.1 [14.0 / 13.2, 12.2 /
+// 12.1], 128256 x 4096 53 / 48, 55 / 45 [57 / 50, 59 / 47].  Between them the rule misses up
+// to a quarter where the warps leave half of the SMs' places empty (10240 x 8192 15.4 / 13.6,
+// 16.2 / 12.8 [17.4 / 16.5, 17.4 / 14.4]) and where K is deep (1024 x 100000 20.7 / 19.6, 21.8
+// / 18.6).
 bool fp4_one_row(const gemm_ctx* h, int64_t N) {
   constexpr int64_t kRowMostN = int64_t(1) << 15;
   return N < kRowMostN && h->opt.force_swap < 0 && h->opt.csplit < 0 && h->opt.force_tile_n <= 0;

@@ -47,7 +47,9 @@ constexpr int kF4Threads = 32 * (kF4RoleWarps + kF4EpiWarps);
 constexpr int kF4BlockK = 256;  // values of K per k-block: 128 bytes
 // Registers: 3 warpgroups launch with 168 each.  A pair's epilogue holds 128 sums a
 // thread: the role warpgroup gives up all but 40, the epilogue's two take 232 (40 + 2 *
-// 232 = 504 = 3 * 168).
+// 232 = 504 = 3 * 168).  A pair's kernel is still compiled for the 168 of the launch and
+// spills (-Xptxas -v: 324 bytes stored and 360 loaded where C has 16 bits, 76 and 200 in
+// fp32); the other tiles do not.
 constexpr int kF4RoleRegs = 40, kF4EpiRegs = 232;
 
 template <int BN, bool PAIR, int FMT>

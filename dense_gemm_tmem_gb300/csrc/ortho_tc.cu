@@ -96,10 +96,12 @@ cudaError_t launch_ortho_products(gemm_ctx* h, const OrthoCall& c, cudaStream_t 
   // can start; 256 x 128: 480 cycles and 2 us; 128 x 64 of one CTA: 545 cycles, 1 us.
   // So the widest ones where kApply has more than 5/3 of them for each pair, the small
   // ones where it has one for each SM at most and K is so short that its loads take less
-  // than an epilogue.  Measured (us, 256 / 128 / 64): 4096^2 1027 / 1597 / 3979, 8 x
-  // 1024^2 279 / 295 / 614, 10 x 700 x 1000 240 / 227 / 444, 2048^2 309 / 301 / 557, 1000
-  // x 4096 304 / 264 / 367, 1024^2 206 / 159 / 171, 700 x 1000 189 / 143 / 151, 4 x 512^2
-  // 165 / 125 / 119, 512^2 156 / 116 / 113, 128^2 119 / 83 / 70.
+  // than an epilogue.  Measured (us, 256 / 128 / 64, each forced, one after the other):
+  // 4096^2 1023 / 1504 / 3799 (by itself 988), 8 x 1024^2 286 / 286 / 596, 10 x 700 x 1000
+  // 234 / 224 / 433, 2048^2 293 / 284 / 532, 1000 x 4096 282 / 252 / 352, 1024^2 196 / 157
+  // / 166, 700 x 1000 180 / 140 / 147, 4 x 512^2 159 / 123 / 117, 512^2 151 / 114 / 111,
+  // 128^2 112 / 83 / 67, 64 x 4096 193 / 165 / 189, 4096 x 128 212 / 172 / 179, 16 x 16384
+  // 476 / 433 / 566.
   constexpr int64_t kShortK = 8;  // k-blocks
   const int64_t pairs = h->opt.pair_clusters > 0 ? h->opt.pair_clusters : h->num_sms / 2;
   const Tiles wide = tiles_of<Wide>(s), narrow = tiles_of<Narrow>(s), small = tiles_of<Small>(s);

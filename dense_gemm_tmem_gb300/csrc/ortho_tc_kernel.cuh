@@ -29,17 +29,18 @@
 // Two CTAs on two SMs own a 256 x 256 or a 256 x 128 tile (cta_group::2), or one CTA a
 // 128 x 64 tile: ortho_tc.cu says which when.
 //
-// What bounds it.  4096^2 (1002 us, 1.37 PFLOP/s of the flops counted): the MMAs, 640 cycles
+// What bounds it.  4096^2 (988 us, 1.39 PFLOP/s of the flops counted): the MMAs, 640 cycles
 // a k-block of 256 x 256 as in the library's other products, 23 to 26 us a tile beside the
 // last one's epilogue; 528 tiles a step on 76 pairs are 6.95 each, 8 us a step are waits.
 // Smaller matrices: the chain of 15 products, each of which costs, after its MMAs, the
 // epilogue (1.1 us for 32 columns a warp), 0.8 to 1.7 us until its stores are acknowledged,
 // 0.9 until another SM has seen the counter and 0.9 for the first loads: 7 us a product for
-// 512^2, 15 for 2048^2.  (A launch a product took 8 and 17, 4096^2 1030.)  Measured and
-// dropped: results stored twice instead of read mirrored (512^2 149 us against 113), 16
-// bytes a lane straight from registers (10 x 700 x 1000 251 against 228), TMA stores (235),
-// two copies for an MN-major operand (228 against 225), a fence after relaxed polls (225
-// against 223).
+// 512^2, 15 for 2048^2.  With one short side kGram has a tile or a few, each of which
+// walks all of the long side alone: 64 x 4096 165 us, 128 x 4096 176, 16 x 16384 433.  (A
+// launch a product took 8 and 17, 4096^2 1030.)  Measured and dropped: results stored
+// twice instead of read mirrored (512^2 149 us against 113), 16 bytes a lane straight from
+// registers (10 x 700 x 1000 251 against 228), TMA stores (235), two copies for an
+// MN-major operand (228 against 225), a fence after relaxed polls (225 against 223).
 #pragma once
 
 #include "fp8_tc_kernel.cuh"
@@ -51,7 +52,9 @@ namespace dg {
 constexpr int kOrRoleWarps = 4, kOrEpiWarps = 8;
 constexpr int kOrThreads = 32 * (kOrRoleWarps + kOrEpiWarps);
 // Registers a thread: 3 warpgroups launch with 168 each (504 in all); the roles keep 56,
-// the epilogue's two take 224 each, for the chunk that is sent for ahead.
+// the epilogue's two take 224 each, for the chunk that is sent for ahead.  (Compiled for
+// 168, the kernels spill a little, -Xptxas -v: 88 bytes stored and 72 loaded in 256-wide
+// tiles, 32 and 56 in 128-wide, 24 and 48 in 64-wide ones.)
 constexpr int kOrRoleRegs = 56, kOrEpiRegs = 224;
 constexpr int kOrGroup = 2;   // k-blocks of 64 per stage
 
