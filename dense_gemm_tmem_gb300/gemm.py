@@ -374,7 +374,8 @@ class Gemm:
 def _coefficients(coefficients, steps: int) -> bytes:
     """a, b, c of every step as fp32, read on every call: a schedule may be changed in place."""
     rows = list(coefficients)
-    one = bool(rows) and not hasattr(rows[0], "__len__")  # for every step
+    # one triple for every step: numbers, tensors without dimensions among them
+    one = bool(rows) and (getattr(rows[0], "ndim", 1) == 0 or not hasattr(rows[0], "__len__"))
     if one:
         rows = [rows]
     if len(rows) != (1 if one else steps) or any(len(r) != 3 for r in rows):

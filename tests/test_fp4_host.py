@@ -303,6 +303,20 @@ def test_coefficients():
     assert np.array_equal(each, [1, 2, 3, 4, 5, 6])
 
 
+@pytest.mark.parametrize("steps", [1, 2, 3, 5])
+def test_one_triple_in_any_numbers(steps):
+    """A triple for every step, as a tensor, an array or numbers without dimensions, also where
+    there are three steps."""
+    want = np.tile(np.array([1, 2, 3], np.float32), steps)
+    for abc in ((1, 2, 3), [1.0, 2.0, 3.0], torch.tensor([1.0, 2.0, 3.0]), np.arange(1.0, 4.0),
+                tuple(torch.tensor([1.0, 2.0, 3.0])), [np.array(v) for v in (1, 2, 3)],
+                (v for v in (1, 2, 3))):
+        assert np.array_equal(np.frombuffer(_coefficients(abc, steps), np.float32), want)
+    for bad in ((1, 2), (1, 2, 3, 4), torch.ones(4), torch.ones(steps + 1, 3), torch.ones(steps, 2)):
+        with pytest.raises(ValueError, match="coefficients"):
+            _coefficients(bad, steps)
+
+
 def test_coefficients_changed_in_place():
     """What a caller's object holds now counts, not what it held in an earlier call."""
     first, then = (3.4445, -4.7750, 2.0315), (1.875, -1.25, 0.375)
